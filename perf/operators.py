@@ -234,7 +234,7 @@ def prepare(case, seed):
             s["batch"] = q.PagedBatch(s["starts"], s["lens"], s["table"], T, s["max_new"], s["max_len"])
             if c["op"] == "attend":
                 n = q.qmm_paged_attention_workspace_size(s["batch"], H, KV, D)
-                s["workspace"] = torch.empty(n, dtype=torch.uint8, device=DEV)
+                s["workspace"] = torch.zeros(n, dtype=torch.uint8, device=DEV)
         return s
 
     P, n, ps = c["pages"], c["count"], c["page"]
@@ -275,7 +275,7 @@ def prepare(case, seed):
     if own:
         q = qmm()
         s["pool"] = q.PagePool(s["data"], s["refs"], s["table"], s["lens"], ps)
-        s["workspace"] = torch.empty(q.qmm_pages_workspace_size(s["pool"], n), dtype=torch.uint8, device=DEV)
+        s["workspace"] = torch.zeros(q.qmm_pages_workspace_size(s["pool"], n), dtype=torch.uint8, device=DEV)
     return s
 
 
