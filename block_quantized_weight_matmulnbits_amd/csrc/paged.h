@@ -1,0 +1,114 @@
+// paged.h -- host-side interface between the validated entry points of the
+// paged cache (paged_api.cpp) and their kernel launchers (rope.hip,
+// paged_attn*.hip, pages.hip).  Not installed.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace qmm {
+
+// Division of a 32-bit index by a number fixed per launch: a multiply-high
+// and two shifts (round-up reciprocal of 33 bits, exact for every n < 2^32).
+struct FastDiv {
+  uint32_t d = 1, mul = 0, s1 = 0, s2 = 0;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f;
+  f.d = d;
+  uint32_t l = 0;
+  while (l < 32 && ((uint64_t)1 << l) < d) ++l;
+  f.mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1);
+  f.s1 = l < 1 ? l : 1;
+  f.s2 = l > 1 ? l - 1 : 0;
+  return f;
+}
+#ifdef __HIPCC__
+__host__ __device__ inline uint32_t div_by(uint32_t n, const FastDiv& f) {
+  const uint32_t t = (uint32_t)(((uint64_t)n * f.mul) >> 32);
+  return (t + ((n - t) >> f.s1)) >> f.s2;
+}
+#endif
+
+// The cache's pages and the batch (device pointers; strides in elements).
+struct CacheArgs {
+  char* k = nullptr;              // [pages, kv_heads, page, dim]
+  char* v = nullptr;
+  int64_t k_page = 0, k_head = 0, k_token = 0;
+  int64_t v_page = 0, v_head = 0, v_token = 0;
+  int pages = 0, kv_heads = 0, page = 0, dim = 0;
+  FastDiv by_page;
+  const int32_t* starts = nullptr;  // [seqs + 1]
+  const int32_t* lens = nullptr;    // [seqs]
+  const int32_t* table = nullptr;   // [seqs, width]
+  int64_t table_stride = 0;
+  int seqs = 0, tokens = 0, width = 0, max_new = 0, max_len = 0;
+};
+
+struct RopeArgs {
+  CacheArgs c;
+  const char *q = nullptr, *k = nullptr, *v = nullptr;  // [tokens, heads, dim]
+  char* out = nullptr;
+  int64_t q_token = 0, q_head = 0, k_token = 0, k_head = 0, v_token = 0, v_head = 0;
+  int64_t out_token = 0, out_head = 0;
+  const double* inv_freq = nullptr;  // [half]
+  const int32_t* positions = nullptr;
+  double factor = 1.0;
+  int q_heads = 0, half = 0, interleaved = 0, dtype = 0;
+  hipStream_t stream = nullptr;
+};
+hipError_t launch_rope_append(const RopeArgs& a);
+
+struct AttnArgs {
+  CacheArgs c;
+  const char* q = nullptr;
+  char* out = nullptr;
+  float* lse = nullptr;              // [tokens, q_heads] or null
+  int64_t q_token = 0, q_head = 0, out_token = 0, out_head = 0, lse_token = 0, lse_head = 0;
+  float scale = 1.f, softcap = 0.f;
+  int q_heads = 0, group = 0, causal = 1, window = 0, dtype = 0;
+  int q_wide = 0, out_wide = 0;      // 16-byte rows of q; four elements at once of out
+  FastDiv by_group;
+  char* workspace = nullptr;
+  hipStream_t stream = nullptr;
+};
+size_t attn_workspace_bytes(int seqs, int tokens, int max_new, int max_len, int q_heads,
+                            int kv_heads, int dim);
+hipError_t launch_paged_attention(const AttnArgs& a);
+
+// A few rows of queries a workgroup (paged_attn_rows.h): keys are split over
+// `splits` workgroups in runs of `chunk`, rows over `row_tiles`.
+struct RowsPlan {
+  int splits, chunk, row_tiles;
+};
+// One instance file a type; blocks of 16 rows a tile, 1 or 2.  Sequences with
+// more than skip_above new tokens are left to another kernel.
+hipError_t launch_rows_f32(const AttnArgs& a, const RowsPlan& plan, int blocks, int skip_above);
+hipError_t launch_rows_f16(const AttnArgs& a, const RowsPlan& plan, int blocks, int skip_above);
+hipError_t launch_rows_bf16(const AttnArgs& a, const RowsPlan& plan, int blocks, int skip_above);
+
+// The bookkeeping of the pages (strides and sizes of `data` in bytes).
+struct PoolArgs {
+  char* data = nullptr;             // [planes, pages, page_bytes]
+  int64_t planes = 0, plane_stride = 0, page_stride = 0, page_bytes = 0;
+  int32_t *refs = nullptr, *table = nullptr, *lens = nullptr;
+  int64_t table_stride = 0;
+  int pages = 0, slots = 0, width = 0, page = 0;
+  FastDiv by_page;
+  char* workspace = nullptr;
+  hipStream_t stream = nullptr;
+};
+// Slots that one list may name (a bit each in LDS, to find repeated ones).
+constexpr int64_t POOL_MAX_SLOTS = 1 << 18;
+size_t pages_workspace_bytes(int64_t pages, int64_t count);
+hipError_t launch_pages_free(const PoolArgs& p, const int32_t* seqs, int count);
+hipError_t launch_pages_fork(const PoolArgs& p, const int32_t* parents, const int32_t* children,
+                             int count, int32_t* status);
+hipError_t launch_pages_reserve(const PoolArgs& p, const int32_t* seqs, const int32_t* grow,
+                                int count, int32_t* status);
+hipError_t launch_pages_copy(const PoolArgs& p, const int32_t* src, const int32_t* dst, int count);
+hipError_t launch_pages_compact(const PoolArgs& p, int32_t* refs_out, int32_t* table_out,
+                                int64_t table_out_stride, int32_t* live);
+
+}  // namespace qmm

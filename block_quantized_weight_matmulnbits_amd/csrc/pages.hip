@@ -1,0 +1,399 @@
+// pages.hip -- the bookkeeping of a paged cache on the device: pages are given
+// back, shared with a forked sequence, reserved for tokens to come, copied,
+// and moved together at the front of the pool.
+//
+// A pool is `planes` arrays of `pages` pages (say the keys and the values of
+// every layer), one reference count a page, and a table of slots: slot s
+// holds ceil(lens[s] / page) pages, in order, then -1.  Counts and tables are
+// whole numbers and new pages are the lowest free ones in list order, so a
+// result does not depend on the order in which workgroups run.
+//
+// Tables and counts are small (kilobytes) and their steps depend on one
+// another: one workgroup plans, through LDS and block-wide scans, and leaves
+// the pages to copy in the workspace.  The copies are bound by HBM (each
+// moved page read and written once in every plane) and run on the whole chip.
+#include <hip/hip_runtime.h>
+
+#include "../../include/qmm.h"
+#include "paged.h"
+#include "qmm_device.h"
+
+namespace qmm {
+namespace {
+
+constexpr int PLAN_THREADS = 1024;
+constexpr int COPY_THREADS = 256;
+
+// Workspace: the number of pages to copy, then the lists.
+struct Plan {
+  int32_t* moves;   // [1]
+  int32_t* src;     // [max(count, pages)]
+  int32_t* dst;
+  int32_t* first;   // [count]: an entry's first new page in `fresh`
+  int32_t* length;  // [count]: an entry's new length
+  int32_t* fresh;   // [pages]: the pages taken
+};
+__host__ __device__ inline int64_t plan_round(int64_t n) { return (n + 63) / 64 * 64; }
+__host__ __device__ inline Plan plan_of(char* ws, int64_t pages, int64_t count) {
+  const int64_t most = plan_round(pages > count ? pages : count), n = plan_round(count);
+  int32_t* w = (int32_t*)ws;
+  Plan p;
+  p.moves = w;
+  p.src = w + 64;
+  p.dst = p.src + most;
+  p.first = p.dst + most;
+  p.length = p.first + n;
+  p.fresh = p.length + n;
+  return p;
+}
+
+// Sum over the workgroup and the sum of the threads before this one.  Every
+// thread calls it; `part` is LDS of one entry a wave.
+__device__ __forceinline__ int block_scan(int v, int* part, int& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();
+  if (lane == 63) part[wave] = x;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) {
+    const int n = part[w];
+    before += w < wave ? n : 0;
+    all += n;
+  }
+  total = all;
+  return before + x - v;
+}
+
+__device__ __forceinline__ int pages_for(int length, const PoolArgs& p) {
+  return length <= 0 ? 0 : (int)div_by((uint32_t)length - 1u, p.by_page) + 1;
+}
+
+__global__ __launch_bounds__(256) void free_kernel(PoolArgs p, const int32_t* seqs) {
+  const int s = seqs[blockIdx.x];
+  if (s < 0 || s >= p.slots) return;
+  int32_t* row = p.table + (int64_t)s * p.table_stride;
+  for (int c = threadIdx.x; c < p.width; c += 256) {
+    // Exchanged, so that a slot listed twice gives its pages back once.
+    const int page = atomicExch(row + c, -1);
+    if (page >= 0 && page < p.pages) atomicSub(p.refs + page, 1);
+  }
+  if (threadIdx.x == 0) p.lens[s] = 0;
+}
+
+// Fork (FORK) or reserve.  Nothing is changed unless the whole list can be
+// served: everything is checked and counted before the first write.
+template <bool FORK>
+__global__ __launch_bounds__(PLAN_THREADS) void take_kernel(PoolArgs p, const int32_t* parents,
+                                                            const int32_t* seqs,
+                                                            const int32_t* grow, int count,
+                                                            int32_t* status) {
+  __shared__ uint32_t seen[POOL_MAX_SLOTS / 32];
+  __shared__ int part[PLAN_THREADS / 64];
+  __shared__ int bad;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Plan w = plan_of(p.workspace, p.pages, count);
+  if (tid == 0) {
+    *w.moves = 0;
+    bad = status[0] != 0 ? -1 : 0;   // an earlier call failed: nothing is done
+  }
+  for (int i = tid; i < (p.slots + 31) / 32; i += PLAN_THREADS) seen[i] = 0;
+  __syncthreads();
+  const bool stop = bad != 0;
+  __syncthreads();   // everyone has read it before anyone below sets it
+  if (stop) return;
+
+  // Check the list and count the pages that each entry needs.
+  int64_t needed = 0;
+  for (int base = 0; base < count; base += PLAN_THREADS) {
+    const int i = base + tid;
+    int need = 0, code = 0, length = 0;
+    if (i < count) {
+      const int s = seqs[i];
+      if (s < 0 || s >= p.slots) {
+        code = QMM_PAGES_BAD_ENTRY;
+      } else {
+        const uint32_t bit = 1u << (s & 31);
+        if (atomicOr(&seen[s >> 5], bit) & bit) code = QMM_PAGES_BAD_ENTRY;
+        const int have = p.lens[s];
+        if (FORK) {
+          const int parent = parents[i];
+          if (have != 0 || parent < 0 || parent >= p.slots) {
+            code = QMM_PAGES_BAD_ENTRY;
+          } else {
+            length = p.lens[parent];
+            const int held = pages_for(length, p);
+            if (length < 0 || held > p.width) code = QMM_PAGES_BAD_ENTRY;
+            need = (int64_t)held * p.page != length;
+          }
+        } else {
+          const int64_t more = grow[i], after = have + more;
+          length = (int)after;
+          if (have < 0 || more < 0 || after > INT32_MAX) {
+            code = QMM_PAGES_BAD_ENTRY;
+          } else {
+            const int to = pages_for(length, p);
+            if (to > p.width) code = QMM_PAGES_TOO_LONG;
+            need = to - pages_for(have, p);
+          }
+        }
+      }
+      if (code) atomicMax(&bad, code);
+    }
+    if (code) need = 0;
+    int sum;
+    const int before = block_scan(need, part, sum);
+    if (i < count) {
+      w.length[i] = code ? 0 : length;
+      if (needed + before <= p.pages) w.first[i] = (int)(needed + before);
+    }
+    needed += sum;
+  }
+  __syncthreads();
+  if (FORK && !bad) {
+    for (int i = wave; i < count; i += PLAN_THREADS / 64) {
+      const int32_t* row = p.table + (int64_t)parents[i] * p.table_stride;
+      const int held = pages_for(w.length[i], p);
+      for (int c = lane; c < held; c += 64)
+        if (row[c] < 0 || row[c] >= p.pages) bad = QMM_PAGES_BAD_ENTRY;
+    }
+  }
+  __syncthreads();
+  if (bad) {
+    if (tid == 0) status[0] = bad;
+    return;
+  }
+
+  // The lowest free pages, as many as are needed.
+  int found = 0;
+  if (needed <= p.pages) {
+    for (int base = 0; base < p.pages && found < needed; base += PLAN_THREADS) {
+      const int page = base + tid;
+      const int open = page < p.pages && p.refs[page] <= 0;
+      int sum;
+      const int rank = found + block_scan(open, part, sum);
+      if (open && rank < needed) w.fresh[rank] = page;
+      found += sum;
+    }
+  }
+  if (found < needed) {
+    if (tid == 0) {
+      const int64_t lack = needed - found;
+      status[0] = QMM_PAGES_NONE_FREE;
+      status[1] = (int)(lack > INT32_MAX ? INT32_MAX : lack);
+    }
+    return;
+  }
+  __syncthreads();
+
+  for (int i = tid; i < (int)needed; i += PLAN_THREADS) p.refs[w.fresh[i]] = 1;
+  // A wave an entry.  The lengths are those that were counted above: a slot
+  // that another entry fills here was empty then, and none of its row is read.
+  for (int i = wave; i < count; i += PLAN_THREADS / 64) {
+    const int s = seqs[i], length = w.length[i], first = w.first[i];
+    int32_t* row = p.table + (int64_t)s * p.table_stride;
+    const int held = pages_for(length, p);
+    if (FORK) {
+      // Full pages are shared, a part-filled last one is copied into a new one.
+      const int full = (int)div_by((uint32_t)length, p.by_page);
+      const int32_t* from = p.table + (int64_t)parents[i] * p.table_stride;
+      for (int c = lane; c < p.width; c += 64) {
+        int page = -1;
+        if (c < full) {
+          page = from[c];
+          atomicAdd(p.refs + page, 1);
+        } else if (c < held) {
+          page = w.fresh[first];
+          w.src[first] = from[c];
+          w.dst[first] = page;
+        }
+        row[c] = page;
+      }
+    } else {
+      const int have = pages_for(p.lens[s], p);
+      for (int c = have + lane; c < held; c += 64) row[c] = w.fresh[first + c - have];
+    }
+    if (lane == 0) p.lens[s] = length;
+  }
+  if (FORK && tid == 0) *w.moves = (int)needed;
+}
+
+// The used pages at or past `live` (the number of used pages) move to the
+// holes before it, the k-th to the k-th.  Leaves the moves and the map of
+// every page in the workspace.
+__global__ __launch_bounds__(PLAN_THREADS) void compact_kernel(PoolArgs p, int32_t* live_out) {
+  __shared__ int part[PLAN_THREADS / 64];
+  const int tid = threadIdx.x;
+  const Plan w = plan_of(p.workspace, p.pages, 0);
+  int mine = 0, live;
+  for (int page = tid; page < p.pages; page += PLAN_THREADS) mine += p.refs[page] > 0;
+  block_scan(mine, part, live);
+  int holes = 0, moves = 0;
+  for (int base = 0; base < p.pages; base += PLAN_THREADS) {
+    const int page = base + tid;
+    const bool in = page < p.pages, used = in && p.refs[page] > 0;
+    const int hole = in && !used && page < live, move = used && page >= live;
+    int sum;
+    // At most 1024 of each, so both counts travel in one scan.
+    const int before = block_scan(hole | move << 16, part, sum);
+    if (hole) w.dst[holes + (before & 0xFFFF)] = page;
+    if (move) w.src[moves + (before >> 16)] = page;
+    else if (in) w.fresh[page] = page;
+    holes += sum & 0xFFFF;
+    moves += sum >> 16;
+  }
+  __syncthreads();
+  for (int k = tid; k < moves; k += PLAN_THREADS) w.fresh[w.src[k]] = w.dst[k];
+  if (tid == 0) {
+    *w.moves = moves;
+    *live_out = live;
+  }
+}
+
+// Pages src[i] -> dst[i] in every plane.  Work is cut into runs of 1024
+// vectors over (move, plane, vector), four a thread in flight; a workgroup
+// divides once for its run and by a launch constant from there.
+template <typename V>
+__device__ __forceinline__ void copy_pages(const PoolArgs& p, const int32_t* src,
+                                           const int32_t* dst, int64_t moves, uint32_t per_page,
+                                           const FastDiv& by_vectors, const FastDiv& by_planes) {
+  constexpr int RUN = 4 * COPY_THREADS;
+  const int64_t total = moves * p.planes * per_page;
+  for (int64_t base = (int64_t)blockIdx.x * RUN; base < total; base += (int64_t)gridDim.x * RUN) {
+    const int64_t pair0 = base / per_page;
+    const uint32_t off0 = (uint32_t)(base - pair0 * per_page);
+    V x[4];
+    V* to[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t k = u * COPY_THREADS + threadIdx.x;
+      to[u] = nullptr;
+      if (base + k >= total) continue;
+      const uint32_t more = div_by(off0 + k, by_vectors), off = off0 + k - more * per_page;
+      const uint32_t pair = (uint32_t)(pair0 + more), m = div_by(pair, by_planes);
+      const uint32_t plane = pair - m * (uint32_t)p.planes;
+      const int a = src[m], b = dst[m];
+      if (a < 0 || a >= p.pages || b < 0 || b >= p.pages || a == b) continue;
+      char* at = p.data + plane * p.plane_stride;
+      x[u] = ((const V*)(at + a * p.page_stride))[off];
+      to[u] = (V*)(at + b * p.page_stride) + off;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (to[u] != nullptr) *to[u] = x[u];
+  }
+}
+
+template <typename V>
+__global__ __launch_bounds__(COPY_THREADS) void copy_kernel(PoolArgs p, const int32_t* src,
+                                                            const int32_t* dst,
+                                                            const int32_t* moves, int count,
+                                                            uint32_t per_page, FastDiv by_vectors,
+                                                            FastDiv by_planes) {
+  copy_pages<V>(p, src, dst, moves ? *moves : count, per_page, by_vectors, by_planes);
+}
+
+// The copies of a compaction, with its counts and table written out anew.
+template <typename V>
+__global__ __launch_bounds__(COPY_THREADS) void move_kernel(PoolArgs p, int32_t* refs_out,
+                                                            int32_t* table_out,
+                                                            int64_t table_out_stride,
+                                                            const int32_t* live,
+                                                            uint32_t per_page, FastDiv by_vectors,
+                                                            FastDiv by_planes, FastDiv by_width) {
+  const Plan w = plan_of(p.workspace, p.pages, 0);
+  const int64_t threads = (int64_t)gridDim.x * COPY_THREADS;
+  const int64_t id = (int64_t)blockIdx.x * COPY_THREADS + threadIdx.x;
+  const int n = *live;
+  for (int64_t page = id; page < p.pages; page += threads) {
+    const int refs = p.refs[page];
+    if (refs > 0) refs_out[w.fresh[page]] = refs;
+    if (page >= n) refs_out[page] = 0;
+  }
+  const int64_t entries = (int64_t)p.slots * p.width;
+  for (int64_t e = id; e < entries; e += threads) {
+    const int64_t s = div_by((uint32_t)e, by_width), c = e - s * p.width;
+    const int page = p.table[s * p.table_stride + c];
+    table_out[s * table_out_stride + c] = page >= 0 && page < p.pages ? w.fresh[page] : page;
+  }
+  copy_pages<V>(p, w.src, w.dst, *w.moves, per_page, by_vectors, by_planes);
+}
+
+// Calls f with a value of the widest vector that the pages' bytes allow.
+template <typename F>
+hipError_t by_vector(const PoolArgs& p, F f) {
+  const uint64_t all = (uint64_t)(uintptr_t)p.data | (uint64_t)p.plane_stride |
+                       (uint64_t)p.page_stride | (uint64_t)p.page_bytes;
+  if (all % 16 == 0) return f(u32x4{});
+  if (all % 4 == 0) return f(uint32_t{});
+  return f(uint8_t{});
+}
+
+int copy_grid(const PoolArgs& p, int64_t moves, int64_t per_page) {
+  const int64_t runs = (moves * p.planes * per_page + 4 * COPY_THREADS - 1) / (4 * COPY_THREADS);
+  return (int)(runs < 1 ? 1 : runs > 8192 ? 8192 : runs);
+}
+
+hipError_t launch_copy(const PoolArgs& p, const int32_t* src, const int32_t* dst,
+                       const int32_t* moves, int count) {
+  return by_vector(p, [&](auto v) {
+    const int64_t per = p.page_bytes / (int64_t)sizeof(v);
+    copy_kernel<decltype(v)><<<copy_grid(p, count, per), COPY_THREADS, 0, p.stream>>>(
+        p, src, dst, moves, count, (uint32_t)per, fast_div((uint32_t)per),
+        fast_div((uint32_t)p.planes));
+    return hipGetLastError();
+  });
+}
+
+}  // namespace
+
+size_t pages_workspace_bytes(int64_t pages, int64_t count) {
+  const int64_t most = plan_round(pages > count ? pages : count);
+  return (size_t)(64 + 2 * most + 2 * plan_round(count) + plan_round(pages)) * 4;
+}
+
+hipError_t launch_pages_free(const PoolArgs& p, const int32_t* seqs, int count) {
+  free_kernel<<<count, 256, 0, p.stream>>>(p, seqs);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_fork(const PoolArgs& p, const int32_t* parents, const int32_t* children,
+                             int count, int32_t* status) {
+  take_kernel<true><<<1, PLAN_THREADS, 0, p.stream>>>(p, parents, children, nullptr, count, status);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const Plan w = plan_of(p.workspace, p.pages, count);
+  return launch_copy(p, w.src, w.dst, w.moves, count);
+}
+
+hipError_t launch_pages_reserve(const PoolArgs& p, const int32_t* seqs, const int32_t* grow,
+                                int count, int32_t* status) {
+  take_kernel<false><<<1, PLAN_THREADS, 0, p.stream>>>(p, nullptr, seqs, grow, count, status);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_copy(const PoolArgs& p, const int32_t* src, const int32_t* dst, int count) {
+  return launch_copy(p, src, dst, nullptr, count);
+}
+
+hipError_t launch_pages_compact(const PoolArgs& p, int32_t* refs_out, int32_t* table_out,
+                                int64_t table_out_stride, int32_t* live) {
+  compact_kernel<<<1, PLAN_THREADS, 0, p.stream>>>(p, live);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return by_vector(p, [&](auto v) {
+    const int64_t per = p.page_bytes / (int64_t)sizeof(v);
+    int grid = copy_grid(p, p.pages / 2 + 1, per);
+    move_kernel<decltype(v)><<<grid, COPY_THREADS, 0, p.stream>>>(
+        p, refs_out, table_out, table_out_stride, live, (uint32_t)per, fast_div((uint32_t)per),
+        fast_div((uint32_t)p.planes), fast_div((uint32_t)(p.width > 0 ? p.width : 1)));
+    return hipGetLastError();
+  });
+}
+
+}  // namespace qmm

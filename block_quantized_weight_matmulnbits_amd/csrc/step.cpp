@@ -1,5 +1,5 @@
-// step.cpp -- a fixed sequence of matmul calls (for example the projections
-// of one decode step) recorded once and replayed as one HIP graph.
+// step.cpp -- a fixed sequence of calls (for example the projections and the
+// attention of one decode step) recorded once and replayed as one HIP graph.
 //
 // The pages' end-to-end decode measurements put the time lost outside the
 // kernels: per-operator fork/join and dispatch, not the matmul itself, made
@@ -90,6 +90,50 @@ int qmm_step_add_gemm_compint8(qmm_step* step, const void* A, int a_dtype, const
     return qmm_gemm_compint8(A, a_dtype, B, b_layout, scales, s_dtype, zero_points, g_idx,
                              g_idx_len, bias, Y, M, K, N, block_size, bits, accuracy_level,
                              workspace, workspace_bytes, s);
+  });
+}
+
+// The structs are copied into the recorded call; the arrays are not.
+int qmm_step_add_rope_append(qmm_step* step, const qmm_heads* q, const qmm_heads* k,
+                             const qmm_heads* v, const qmm_heads* out, const qmm_paged_kv* kv,
+                             const qmm_paged_batch* batch, const double* inv_freq, int half,
+                             int interleaved, double factor, const int32_t* positions) {
+  if (!q || !k || !v || !out || !kv || !batch)
+    return qmm::set_error(QMM_ERR_INVALID_ARG, "qmm_step_add_rope_append: q, k, v, out, kv and "
+                          "batch must be non-null.");
+  const qmm_heads hq = *q, hk = *k, hv = *v, ho = *out;
+  const qmm_paged_kv c = *kv;
+  const qmm_paged_batch b = *batch;
+  return add_call(step, [=](void* s) {
+    return qmm_rope_append(&hq, &hk, &hv, &ho, &c, &b, inv_freq, half, interleaved, factor,
+                           positions, s);
+  });
+}
+
+int qmm_step_add_paged_attention(qmm_step* step, const qmm_heads* q, const qmm_paged_kv* kv,
+                                 const qmm_paged_batch* batch, const qmm_heads* out, float* lse,
+                                 float scale, int causal, int64_t window, float softcap,
+                                 void* workspace, size_t workspace_bytes) {
+  if (!q || !out || !kv || !batch)
+    return qmm::set_error(QMM_ERR_INVALID_ARG, "qmm_step_add_paged_attention: q, kv, batch and out "
+                          "must be non-null.");
+  const qmm_heads hq = *q, ho = *out;
+  const qmm_paged_kv c = *kv;
+  const qmm_paged_batch b = *batch;
+  return add_call(step, [=](void* s) {
+    return qmm_paged_attention(&hq, &c, &b, &ho, lse, scale, causal, window, softcap, workspace,
+                               workspace_bytes, s);
+  });
+}
+
+int qmm_step_add_pages_reserve(qmm_step* step, const qmm_page_pool* pool, const int32_t* seqs,
+                               const int32_t* grow, int64_t count, int32_t* status,
+                               void* workspace, size_t workspace_bytes) {
+  if (!pool)
+    return qmm::set_error(QMM_ERR_INVALID_ARG, "qmm_step_add_pages_reserve: pool must be non-null.");
+  const qmm_page_pool p = *pool;
+  return add_call(step, [=](void* s) {
+    return qmm_pages_reserve(&p, seqs, grow, count, status, workspace, workspace_bytes, s);
   });
 }
 

@@ -30,6 +30,7 @@ if not os.path.exists(LIB_PATH):
 lib = ctypes.CDLL(LIB_PATH)
 
 _vp, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+_f64 = ctypes.c_double
 _SIGS = {
     "qmm_last_error": ([], ctypes.c_char_p),
     "qmm_gemv": ([_vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i32, _i32,
@@ -58,6 +59,19 @@ _SIGS = {
                            _i64, _i32, _i32, _i32], _i32),
     "qmm_step_add_gemm_compint8": ([_vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _i64, _vp, _vp,
                                     _i64, _i64, _i64, _i32, _i32, _i32, _vp, _sz], _i32),
+    "qmm_rope_append": ([_vp] * 6 + [_vp, _i32, _i32, _f64, _vp, _vp], _i32),
+    "qmm_paged_attention_workspace_size": ([_vp, _i32, _i32, _i32], _sz),
+    "qmm_paged_attention": ([_vp, _vp, _vp, _vp, _vp, _f32, _i32, _i64, _f32, _vp, _sz, _vp], _i32),
+    "qmm_pages_workspace_size": ([_vp, _i64], _sz),
+    "qmm_pages_free": ([_vp, _vp, _i64, _vp], _i32),
+    "qmm_pages_fork": ([_vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp], _i32),
+    "qmm_pages_reserve": ([_vp, _vp, _vp, _i64, _vp, _vp, _sz, _vp], _i32),
+    "qmm_pages_copy": ([_vp, _vp, _vp, _i64, _vp], _i32),
+    "qmm_pages_compact": ([_vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "qmm_step_add_rope_append": ([_vp] * 7 + [_vp, _i32, _i32, _f64, _vp], _i32),
+    "qmm_step_add_paged_attention": ([_vp, _vp, _vp, _vp, _vp, _vp, _f32, _i32, _i64, _f32, _vp, _sz],
+                                     _i32),
+    "qmm_step_add_pages_reserve": ([_vp, _vp, _vp, _vp, _i64, _vp, _vp, _sz], _i32),
     "qmm_step_finalize": ([_vp], _i32),
     "qmm_step_launch": ([_vp, _vp], _i32),
     "qmm_step_size": ([_vp], _i32),
@@ -262,9 +276,9 @@ def qmm_gemm_fp4(A, W, scales, fmt, global_scale, bias, Y, M, K, N, stream=None)
 
 
 class Step:
-    """A recorded sequence of matmul calls replayed as one HIP graph
-    (qmm_step_* in include/qmm.h).  add_gemv / add_gemm / add_gemm_compint8
-    take the arguments of the functions of the same name (without a stream);
+    """A recorded sequence of calls replayed as one HIP graph (qmm_step_* in
+    include/qmm.h).  add_gemv / add_gemm / add_gemm_compint8 /
+    add_rope_append / add_paged_attention / add_pages_reserve take the arguments of the functions of the same name (without a stream);
     finalize() validates and captures; launch(stream) replays.  The tensors
     passed are kept referenced for the step's life, since the graph holds
     their device addresses."""
@@ -303,6 +317,23 @@ class Step:
                   (A, B, scales, zero_points, bias, Y, g_idx, workspace), _ptr(A), _dt(A), b,
                   layout, s, sdt, _ptr(zero_points), gp, gn, _ptr(bias), _ptr(Y), M, K, N,
                   block_size, bits, accuracy_level, _ptr(workspace),
+                  workspace.numel() * workspace.element_size())
+
+    def add_rope_append(self, q, k, v, out, kv, batch, inv_freq, interleaved=False, factor=1.0,
+                        positions=None):
+        args = _rope_args(q, k, v, out, kv, batch, inv_freq, interleaved, factor, positions)
+        self._add(lib.qmm_step_add_rope_append, (q, k, v, out, kv, batch, inv_freq, positions),
+                  *args)
+
+    def add_paged_attention(self, q, kv, batch, out, workspace, scale=None, causal=True, window=0,
+                            softcap=0.0, lse=None):
+        args = _attention_args(q, kv, batch, out, workspace, scale, causal, window, softcap, lse)
+        self._add(lib.qmm_step_add_paged_attention, (q, kv, batch, out, workspace, lse), *args)
+
+    def add_pages_reserve(self, pool, seqs, grow, status, workspace):
+        _lists(pool, seqs=seqs, grow=grow, status=status)
+        self._add(lib.qmm_step_add_pages_reserve, (pool, seqs, grow, status, workspace), pool._ref,
+                  _ptr(seqs), _ptr(grow), seqs.numel(), _ptr(status), _ptr(workspace),
                   workspace.numel() * workspace.element_size())
 
     def finalize(self):
@@ -386,3 +417,235 @@ def qmm_lowp_quantize(x, codes, scales, rows, cols, fmt, layout, stream=None):
     f = LOWP_FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
     _check(lib.qmm_lowp_quantize(_ptr(x), _dt(x), rows, cols, f, lay, _ptr(codes), _ptr(scales),
                                  _stream(stream)))
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", _vp), ("token_stride", _i64), ("head_stride", _i64), ("heads", _i32)]
+
+
+class _PagedKV(ctypes.Structure):
+    _fields_ = ([("k_pages", _vp), ("v_pages", _vp)]
+                + [(f"{t}_{d}_stride", _i64) for t in "kv" for d in ("page", "head", "token")]
+                + [("pages", _i64)]
+                + [(n, _i32) for n in ("dtype", "kv_heads", "page_size", "head_dim")])
+
+
+class _PagedBatch(ctypes.Structure):
+    _fields_ = ([(n, _vp) for n in ("starts", "lens", "table")]
+                + [(n, _i64) for n in ("table_stride", "seqs", "tokens", "width", "max_new",
+                                       "max_len")])
+
+
+class _PagePool(ctypes.Structure):
+    _fields_ = ([("data", _vp)]
+                + [(n, _i64) for n in ("planes", "pages", "page_bytes", "plane_stride",
+                                       "page_stride")]
+                + [(n, _vp) for n in ("refs", "table", "lens")]
+                + [(n, _i64) for n in ("table_stride", "slots", "width")]
+                + [("page_size", _i32)])
+
+
+def _int32(name, t, shape=None):
+    if t.dtype != torch.int32 or not t.is_contiguous() or (shape and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be a dense int32 tensor"
+                         f"{f' of shape {list(shape)}' if shape else ''}, got {t.dtype} "
+                         f"{list(t.shape)}")
+
+
+def _rows(name, t):
+    if t.dtype != torch.int32 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be an int32 tensor [rows, width] with dense rows, got "
+                         f"{t.dtype} {list(t.shape)}")
+
+
+class PagedKV:
+    """The pages of one layer's keys and values, each [pages, kv_heads,
+    page_size, head_dim] with any strides as long as head_dim is dense (a
+    cache laid out token by token is passed as a transposed view)."""
+
+    def __init__(self, k_pages, v_pages):
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+            raise ValueError(f"k_pages and v_pages must share one shape [pages, kv_heads, page_size, "
+                             f"head_dim] and dtype, got {list(k_pages.shape)} {k_pages.dtype} and "
+                             f"{list(v_pages.shape)} {v_pages.dtype}")
+        if k_pages.dtype not in _TORCH_TO_QMM:
+            raise ValueError(f"pages of {k_pages.dtype} are not supported: use float32, float16 or "
+                             "bfloat16")
+        if k_pages.device != v_pages.device:
+            raise ValueError("k_pages and v_pages must be on one device")
+        pages, self.kv_heads, self.page_size, self.head_dim = k_pages.shape
+        if self.head_dim > 1 and (k_pages.stride(3) != 1 or v_pages.stride(3) != 1):
+            raise ValueError("head_dim must be the dense dimension of k_pages and v_pages")
+        self.k_pages, self.v_pages, self.dtype = k_pages, v_pages, k_pages.dtype
+        self._c = _PagedKV(_ptr(k_pages), _ptr(v_pages), *k_pages.stride()[:3],
+                           *v_pages.stride()[:3], pages, _dt(k_pages), self.kv_heads,
+                           self.page_size, self.head_dim)
+        self._ref = ctypes.byref(self._c)
+
+
+class PagedBatch:
+    """Sequences over a paged cache: ``starts`` [seqs + 1] and ``lens`` [seqs]
+    (the new tokens included), ``table`` [seqs, width] of page numbers, int32 on
+    the device; ``tokens`` rows in all, at most ``max_new`` of one sequence, and
+    at most ``max_len`` keys.  The bounds stay; the arrays may change in place."""
+
+    def __init__(self, starts, lens, table, tokens, max_new, max_len):
+        _rows("table", table)
+        seqs = table.shape[0]
+        _int32("starts", starts, (seqs + 1,))
+        _int32("lens", lens, (seqs,))
+        if not starts.device == lens.device == table.device:
+            raise ValueError("starts, lens and table must be on one device")
+        self.starts, self.lens, self.table, self.tokens = starts, lens, table, int(tokens)
+        self._c = _PagedBatch(_ptr(starts), _ptr(lens), _ptr(table), table.stride(0), seqs,
+                              self.tokens, table.shape[1], int(max_new), int(max_len))
+        self._ref = ctypes.byref(self._c)
+
+
+class PagePool:
+    """The pages of a whole cache, ``data`` [planes, pages, ...] (each page
+    dense), with ``refs`` [pages], ``table`` [slots, width] and ``lens`` [slots]
+    (int32) for the calls that keep them; qmm_pages_copy needs the data alone."""
+
+    def __init__(self, data, refs=None, table=None, lens=None, page_size=0):
+        if data.dim() < 2 or (data.numel() and not data[0, 0].is_contiguous()):
+            raise ValueError(f"data must be [planes, pages, ...] with dense pages, got "
+                             f"{list(data.shape)} with strides {list(data.stride())}")
+        size, slots, width, stride = data.element_size(), 0, 0, 0
+        if refs is not None:
+            _int32("refs", refs, (data.shape[1],))
+            _rows("table", table)
+            slots, width = table.shape
+            stride = table.stride(0)
+            _int32("lens", lens, (slots,))
+            if not data.device == refs.device == table.device == lens.device:
+                raise ValueError("data, refs, table and lens must be on one device")
+        elems = 1
+        for n in data.shape[2:]:
+            elems *= n
+        self.data, self.refs, self.table, self.lens = data, refs, table, lens
+        self.page_size = int(page_size)
+        self._c = _PagePool(_ptr(data), data.shape[0], data.shape[1], elems * size,
+                            data.stride(0) * size, data.stride(1) * size, _ptr(refs), _ptr(table),
+                            _ptr(lens), stride, slots, width, self.page_size)
+        self._ref = ctypes.byref(self._c)
+
+
+def _heads(name, t, kv, batch, heads=None):
+    """The struct of rows [tokens, heads, head_dim], with the checks that need
+    the tensor's shape."""
+    shape = t.shape
+    if (len(shape) != 3 or shape[0] != batch.tokens or shape[2] != kv.head_dim
+            or (heads is not None and shape[1] != heads) or t.dtype != kv.dtype):
+        raise ValueError(f"{name} must be {kv.dtype} [{batch.tokens}, "
+                         f"{'heads' if heads is None else heads}, {kv.head_dim}], got {t.dtype} "
+                         f"{list(shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and shape[2] > 1:
+        raise ValueError(f"head_dim must be the dense dimension of {name}")
+    return _Heads(t.data_ptr(), s0, s1, shape[1])
+
+
+def _rope_args(q, k, v, out, kv, batch, inv_freq, interleaved, factor, positions):
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be a dense float64 vector, got {inv_freq.dtype} "
+                         f"{list(inv_freq.shape)}")
+    if positions is not None:
+        _int32("positions", positions, (batch.tokens,))
+    byref = ctypes.byref
+    return (byref(_heads("q", q, kv, batch)), byref(_heads("k", k, kv, batch, kv.kv_heads)),
+            byref(_heads("v", v, kv, batch, kv.kv_heads)),
+            byref(_heads("out", out, kv, batch, q.shape[1])), kv._ref, batch._ref,
+            inv_freq.data_ptr(), inv_freq.shape[0], interleaved, factor, _ptr(positions))
+
+
+def qmm_rope_append(q, k, v, out, kv, batch, inv_freq, interleaved=False, factor=1.0,
+                    positions=None, stream=None):
+    """Turn q [tokens, heads, head_dim] into ``out`` and append the turned k and
+    v [tokens, kv_heads, head_dim] to the cache ``kv``; ``inv_freq`` [half] is
+    float64, ``positions`` [tokens] int32 or None (a token's key number)."""
+    _check(lib.qmm_rope_append(*_rope_args(q, k, v, out, kv, batch, inv_freq, interleaved, factor,
+                                           positions), _stream(stream)))
+
+
+def qmm_paged_attention_workspace_size(batch, q_heads, kv_heads, head_dim) -> int:
+    """Bytes of the workspace, which starts zeroed."""
+    return int(lib.qmm_paged_attention_workspace_size(batch._ref, q_heads, kv_heads, head_dim))
+
+
+def _attention_args(q, kv, batch, out, workspace, scale, causal, window, softcap, lse):
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous()
+                            or lse.shape != q.shape[:2]):
+        raise ValueError(f"lse must be a dense float32 tensor {list(q.shape[:2])}, got {lse.dtype} "
+                         f"{list(lse.shape)}")
+    if scale is None:
+        scale = kv.head_dim ** -0.5
+    byref = ctypes.byref
+    return (byref(_heads("q", q, kv, batch)), kv._ref, batch._ref,
+            byref(_heads("out", out, kv, batch, q.shape[1])), _ptr(lse), scale, causal, window,
+            softcap, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def qmm_paged_attention(q, kv, batch, out, workspace, scale=None, causal=True, window=0,
+                        softcap=0.0, lse=None, stream=None):
+    """Attention of q [tokens, heads, head_dim] over the cache, into ``out`` and,
+    where given, ``lse`` [tokens, heads] float32; ``scale`` defaults to
+    head_dim ** -0.5."""
+    _check(lib.qmm_paged_attention(*_attention_args(q, kv, batch, out, workspace, scale, causal,
+                                                    window, softcap, lse), _stream(stream)))
+
+
+def qmm_pages_workspace_size(pool, count=0) -> int:
+    """Bytes of workspace for lists of ``count`` entries (0: a compaction)."""
+    return int(lib.qmm_pages_workspace_size(pool._ref, count))
+
+
+def _lists(pool, **lists):
+    """int32 lists of one length, but for the status word pair."""
+    n = None
+    for name, t in lists.items():
+        if name == "status":
+            _int32(name, t, (2,))
+            continue
+        _int32(name, t)
+        if n is not None and t.numel() != n:
+            raise ValueError(f"{', '.join(k for k in lists if k != 'status')} must have one length")
+        n = t.numel()
+
+
+def qmm_pages_free(pool, seqs, stream=None):
+    _lists(pool, seqs=seqs)
+    _check(lib.qmm_pages_free(pool._ref, seqs.data_ptr(), seqs.numel(), _stream(stream)))
+
+
+def qmm_pages_fork(pool, parents, children, status, workspace, stream=None):
+    """``status`` [2] int32, zeroed by the caller, tells on the device whether
+    the list was served (qmm_pages_status)."""
+    _lists(pool, parents=parents, children=children, status=status)
+    _check(lib.qmm_pages_fork(pool._ref, parents.data_ptr(), children.data_ptr(), parents.numel(),
+                              status.data_ptr(), workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def qmm_pages_reserve(pool, seqs, grow, status, workspace, stream=None):
+    _lists(pool, seqs=seqs, grow=grow, status=status)
+    _check(lib.qmm_pages_reserve(pool._ref, seqs.data_ptr(), grow.data_ptr(), seqs.numel(),
+                                 status.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def qmm_pages_copy(pool, src, dst, stream=None):
+    _lists(pool, src=src, dst=dst)
+    _check(lib.qmm_pages_copy(pool._ref, src.data_ptr(), dst.data_ptr(), src.numel(),
+                              _stream(stream)))
+
+
+def qmm_pages_compact(pool, refs_out, table_out, live, workspace, stream=None):
+    """``refs_out`` and ``table_out`` take the new counts and table, ``live`` [1]
+    the number of used pages, now the first ones."""
+    _int32("refs_out", refs_out, tuple(pool.refs.shape))
+    _int32("table_out", table_out, tuple(pool.table.shape))
+    _int32("live", live)
+    _check(lib.qmm_pages_compact(pool._ref, refs_out.data_ptr(), table_out.data_ptr(),
+                                 live.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)))

@@ -301,8 +301,157 @@ int qmm_lowp_quantize(const void *x, int x_dtype, int64_t rows, int64_t cols, in
                       int layout, uint8_t *codes, void *scales, void *stream);
 
 /*
- * A step: a fixed sequence of matmul calls (say the projections of one
- * decode step) recorded once and replayed as one HIP graph.  The pages find
+ * A paged cache of keys and values, and a batch of sequences over it.  All
+ * strides are in elements; the last dimension of every head is dense.  The
+ * structs are read during the call only; their pointers are device pointers.
+ *
+ * Sequence s of the batch has the tokens starts[s] .. starts[s + 1] - 1 of the
+ * call's rows: the newest of its lens[s] keys.  Token t is its key
+ *   slot = lens[s] - starts[s + 1] + t,
+ * and key j lies in page table[s * table_stride + j / page_size] at position
+ * j % page_size.  starts [seqs + 1] does not decrease.  max_new and max_len
+ * bound the tokens and keys of every sequence: they size the launches (and a
+ * recorded step), and counts past them are cut to them.  A table entry outside
+ * 0 .. pages - 1 gives wrong results, never an access out of bounds: nothing
+ * is appended to it, and attention reads the first or last page for it.
+ */
+typedef struct qmm_paged_kv {
+    void *k_pages;               /* [pages, kv_heads, page_size, head_dim] */
+    void *v_pages;
+    int64_t k_page_stride, k_head_stride, k_token_stride;
+    int64_t v_page_stride, v_head_stride, v_token_stride;
+    int64_t pages;
+    int dtype, kv_heads, page_size, head_dim;
+} qmm_paged_kv;
+
+typedef struct qmm_paged_batch {
+    const int32_t *starts;       /* [seqs + 1] */
+    const int32_t *lens;         /* [seqs], the new tokens included */
+    const int32_t *table;        /* [seqs, width] */
+    int64_t table_stride;
+    int64_t seqs, tokens, width;
+    int64_t max_new, max_len;
+} qmm_paged_batch;
+
+/* Rows of heads [tokens, heads, head_dim] with strides of their own, as a
+ * stacked projection leaves them. */
+typedef struct qmm_heads {
+    void *data;
+    int64_t token_stride, head_stride;
+    int heads;
+} qmm_heads;
+
+/*
+ * Rotary positions, and the append of keys and values to the cache.
+ *   q, k, v   rows of q_heads, kv_heads and kv_heads heads, of kv's dtype
+ *   out       q's heads, turned (may be q itself)
+ *   inv_freq  [half] float64: radians a position turns each pair by, in which
+ *             a stretched context is already accounted for
+ *   positions [tokens] int32, or NULL: token t's position is its slot
+ * The first 2 half elements of every q and k head are half pairs: elements
+ * (i, half + i), or (2 i, 2 i + 1) where interleaved is non-zero; the rest of
+ * the head is copied.  At position p pair i becomes
+ *   factor * (a cos(p f) - b sin(p f), b cos(p f) + a sin(p f)),  f = inv_freq[i];
+ * the angle, its sine and cosine are formed in 64 bits, the products in 32.
+ * The turned keys and the values are written to their slots; a token whose
+ * slot has no page is not appended.  tokens = 0 is a no-op.
+ */
+int qmm_rope_append(const qmm_heads *q, const qmm_heads *k, const qmm_heads *v,
+                    const qmm_heads *out, const qmm_paged_kv *kv,
+                    const qmm_paged_batch *batch, const double *inv_freq, int half,
+                    int interleaved, double factor, const int32_t *positions, void *stream);
+
+/*
+ * Attention of the batch's tokens over the cache, the tokens themselves
+ * included (append them first): with z = scale * q . k, capped to
+ * softcap * tanh(z / softcap) where softcap > 0,
+ *   out = sum_j softmax(z)_j v_j,   lse = log sum_j exp(z_j)
+ * over the keys j < lens[s] that the token sees: j <= slot where causal is
+ * non-zero, j > slot - window where window > 0.  Query head h reads
+ * key/value head h / (heads / kv_heads).  A token that sees no key gets 0 and
+ * an lse of minus infinity; a key that is not seen has no influence, whatever
+ * it holds.  Sums and the softmax are kept in fp32.
+ *   q, out    rows of heads of kv's dtype; head_dim <= 256, a multiple of
+ *             8 (4 for f32); k_pages, v_pages and their strides 16-byte aligned
+ *   lse       [tokens, heads] float32 (dense), or NULL
+ *   workspace qmm_paged_attention_workspace_size bytes, 256-byte aligned,
+ *             zero before its first use; a call leaves its counters zero, so
+ *             calls on one stream may share it, whatever their sizes
+ */
+size_t qmm_paged_attention_workspace_size(const qmm_paged_batch *batch, int q_heads,
+                                          int kv_heads, int head_dim);
+
+int qmm_paged_attention(const qmm_heads *q, const qmm_paged_kv *kv,
+                        const qmm_paged_batch *batch, const qmm_heads *out, float *lse,
+                        float scale, int causal, int64_t window, float softcap,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The pages of a cache.  `data` holds planes x pages pages of page_bytes (say
+ * the keys and values of every layer; page_bytes of a page are dense, strides
+ * in bytes); refs[p] counts the table entries that hold page p (<= 0: free);
+ * slot s of the table holds ceil(lens[s] / page_size) pages in order, then -1.
+ * Lists (seqs, parents, children, grow, src, dst) are device arrays of count
+ * int32 values.  The results do not depend on timing: new pages are the lowest
+ * free ones in list order.
+ *   free     gives back the pages of every listed slot, whose row becomes -1
+ *            and whose length 0; entries out of range are passed over
+ *   fork     children[i], an empty slot, becomes a copy of slot parents[i]:
+ *            its full pages are shared, a part-filled last page is copied into
+ *            a new one (the copy runs over all planes)
+ *   reserve  slot seqs[i] grows by grow[i] >= 0 tokens and gets the pages for them
+ *   copy     page src[i] -> dst[i] in every plane, no page being both; pairs
+ *            that name a page out of range are passed over
+ *   compact  the n used pages move to pages 0 .. n - 1: the k-th used page past
+ *            n to the k-th free one before; counts and table are written anew
+ *            to refs_out [pages] and table_out [slots, width] (dense), n to
+ *            live[0]; free pages' contents are left as they are
+ * fork and reserve serve a list as a whole or not at all: status[0] (int32,
+ * set to 0 by the caller) becomes a qmm_pages_status, and with
+ * QMM_PAGES_NONE_FREE status[1] is the number of pages lacking.  Where
+ * status[0] is not 0 before a call, the call does nothing.
+ * workspace: qmm_pages_workspace_size bytes, 256-byte aligned.
+ */
+typedef struct qmm_page_pool {
+    void *data;
+    int64_t planes, pages, page_bytes, plane_stride, page_stride;
+    int32_t *refs;               /* [pages] */
+    int32_t *table;              /* [slots, width] */
+    int32_t *lens;               /* [slots] */
+    int64_t table_stride, slots, width;
+    int page_size;
+} qmm_page_pool;
+
+typedef enum qmm_pages_status {
+    QMM_PAGES_OK = 0,
+    QMM_PAGES_NONE_FREE = 1,     /* fewer free pages than are needed */
+    QMM_PAGES_TOO_LONG = 2,      /* a sequence would pass the table's width */
+    QMM_PAGES_BAD_ENTRY = 3      /* a slot out of range, listed twice or (a child)
+                                    not empty, or a parent without its pages */
+} qmm_pages_status;
+
+size_t qmm_pages_workspace_size(const qmm_page_pool *pool, int64_t count);
+
+int qmm_pages_free(const qmm_page_pool *pool, const int32_t *seqs, int64_t count,
+                   void *stream);
+
+int qmm_pages_fork(const qmm_page_pool *pool, const int32_t *parents,
+                   const int32_t *children, int64_t count, int32_t *status,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+int qmm_pages_reserve(const qmm_page_pool *pool, const int32_t *seqs, const int32_t *grow,
+                      int64_t count, int32_t *status, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+int qmm_pages_copy(const qmm_page_pool *pool, const int32_t *src, const int32_t *dst,
+                   int64_t count, void *stream);
+
+int qmm_pages_compact(const qmm_page_pool *pool, int32_t *refs_out, int32_t *table_out,
+                      int32_t *live, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * A step: a fixed sequence of calls (say the projections and the attention of
+ * one decode step) recorded once and replayed as one HIP graph.  The pages find
  * the decode step's cost outside the kernels -- per-operator dispatch and
  * fork/join made decode 2.3x slower, and a persistent pool took it from 6 to
  * 28 tok/s (matmul_nbits.rs, module notes on the decode step and the
@@ -354,6 +503,26 @@ int qmm_step_add_gemm_compint8(qmm_step *step, const void *A, int a_dtype,
                                int64_t K, int64_t N, int block_size,
                                int bits, int accuracy_level, void *workspace,
                                size_t workspace_bytes);
+
+/* The operators of the paged cache record the same way; the structs are copied
+ * (the arrays that they point to are not). */
+int qmm_step_add_rope_append(qmm_step *step, const qmm_heads *q,
+                             const qmm_heads *k, const qmm_heads *v,
+                             const qmm_heads *out, const qmm_paged_kv *kv,
+                             const qmm_paged_batch *batch, const double *inv_freq,
+                             int half, int interleaved, double factor,
+                             const int32_t *positions);
+
+int qmm_step_add_paged_attention(qmm_step *step, const qmm_heads *q,
+                                 const qmm_paged_kv *kv,
+                                 const qmm_paged_batch *batch,
+                                 const qmm_heads *out, float *lse, float scale,
+                                 int causal, int64_t window, float softcap, void *workspace,
+                                 size_t workspace_bytes);
+
+int qmm_step_add_pages_reserve(qmm_step *step, const qmm_page_pool *pool,
+                               const int32_t *seqs, const int32_t *grow, int64_t count,
+                               int32_t *status, void *workspace, size_t workspace_bytes);
 
 int qmm_step_finalize(qmm_step *step);
 

@@ -1,0 +1,242 @@
+"""qmm_paged_attention against the definition in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+from tests import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+
+def qmm():
+    from block_quantized_weight_matmulnbits_amd import qmm as q
+    return q
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def run(dtype, counts, lens, H, KV, D, page=16, causal=True, window=0, cap=0.0, scale=None,
+        token_major=False, seed=0, spoil=None, q_offset=0, max_new=None, max_len=None,
+        workspace=None, positive=False):
+    print(f"[attend] {dtype} counts={counts} lens={lens} H={H} KV={KV} D={D} page={page} "
+          f"causal={causal} window={window} cap={cap}", flush=True)
+    q = qmm()
+    g = torch.Generator().manual_seed(seed)
+    starts, lens, table, total = ref.make_batch(counts, lens, page, seed)
+    T = int(starts[-1])
+    shape = (total, page, KV, D) if token_major else (total, KV, page, D)
+    pages = [torch.randn(shape, generator=g).to(dtype) for _ in range(2)]
+    if token_major:
+        pages = [p.transpose(1, 2) for p in pages]
+    if spoil:
+        spoil(*pages, table, lens)
+    kp, vp = (p.to(DEV) for p in pages)
+    flat = (1.7 * torch.randn(T * H * D + q_offset, generator=g)).to(dtype)
+    if positive:
+        flat = flat.abs()
+    x = flat[q_offset:].view(T, H, D)
+    scale = ref.default_scale(D) if scale is None else scale
+    want = ref.attention(x, *pages, starts, lens, table, scale, causal, window, cap)
+    kv = q.PagedKV(kp, vp)
+    batch = q.PagedBatch(dev(starts), dev(lens), dev(table), T,
+                         max(counts, default=0) if max_new is None else max_new,
+                         int(max(lens)) if max_len is None else max_len)
+    out = torch.full((T, H, D), 7.0, dtype=dtype, device=DEV)
+    lse = torch.full((T, H), 7.0, device=DEV)
+    if workspace is None:
+        workspace = torch.zeros(q.qmm_paged_attention_workspace_size(batch, H, KV, D),
+                                dtype=torch.uint8, device=DEV)
+    xd = flat.to(DEV)[q_offset:].view(T, H, D)
+    for again in range(2):   # the workspace serves the next call as it is left
+        out.fill_(7.0)
+        q.qmm_paged_attention(xd, kv, batch, out, workspace, scale=scale, causal=causal,
+                              window=window, softcap=cap, lse=lse)
+        torch.cuda.synchronize()
+        ref.assert_close(out, want[0], ref.rounded(want[0], want[2], dtype), f"out {again}")
+        ref.assert_close(lse, want[1], want[3], f"lse {again}")
+    return out
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [8, 64, 80, 96, 128, 192, 256])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_types_and_widths(dtype, D, cap):
+    run(dtype, [1, 1, 1], [1, 37, 200], 4, 2, D, cap=cap, seed=D)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H,KV", [(1, 1), (7, 1), (8, 8), (16, 1), (28, 4), (40, 2)])
+def test_groups_of_heads(dtype, H, KV):
+    run(dtype, [2, 1], [70, 33], H, KV, 64, seed=H)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("counts,lens", [([5, 12, 1], [5, 300, 140]), ([33], [33]), ([70, 1], [131, 515]),
+                                         ([129, 3, 0, 64], [400, 3, 17, 64])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_chunks(dtype, counts, lens, causal):
+    run(dtype, counts, lens, 6, 2, 64, causal=causal, seed=len(counts))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [80, 128, 192, 256])
+def test_chunks_of_wide_heads(dtype, D):
+    run(dtype, [40, 150], [100, 333], 4, 1, D, page=8, seed=D)
+
+
+@pytest.mark.parametrize("window", [1, 7, 64, 200])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_windows(dtype, window, causal):
+    run(dtype, [1, 9, 100], [400, 90, 230], 4, 2, 64, causal=causal, window=window, seed=window)
+
+
+@pytest.mark.parametrize("page", [1, 3, 8, 64, 128])
+@pytest.mark.parametrize("token_major", [False, True])
+def test_pages_and_layouts_of_the_cache(page, token_major):
+    run(torch.bfloat16, [1, 20], [261, 77], 4, 2, 96, page=page, token_major=token_major, seed=page)
+    run(torch.float16, [140], [260], 4, 1, 128, page=page, token_major=token_major, seed=page)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_empty_rows_and_sequences(dtype):
+    # No keys at all, more tokens than keys, no tokens.
+    run(dtype, [1, 5, 0, 2], [0, 3, 9, 2], 4, 2, 64)
+    run(dtype, [0, 200, 1], [4, 120, 0], 4, 2, 128)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("counts,lens", [([1, 1], [2000, 5]), ([3], [1500])])
+def test_long_sequences_in_parts(dtype, counts, lens):
+    run(dtype, counts, lens, 4, 1, 128, seed=1)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_what_masked_keys_hold_does_not_matter(dtype, bad):
+    """Places past a sequence's end, pages it does not hold, keys later than a
+    token and keys before its window."""
+    def spoil(kp, vp, table, lens):
+        page = kp.shape[2]
+        held = set()
+        for s, n in enumerate(lens):
+            for c in range(-(-int(n) // page)):
+                held.add(int(table[s, c]))
+                keep = min(page, int(n) - c * page)
+                kp[table[s, c], :, keep:] = bad
+                vp[table[s, c], :, keep:] = bad
+        for p in set(range(kp.shape[0])) - held:
+            kp[p] = bad
+            vp[p] = bad
+    run(dtype, [1, 6, 150], [21, 40, 203], 4, 2, 64, spoil=spoil)
+
+    def spoil_window(kp, vp, table, lens):
+        # The first 30 keys are before every token's window.
+        for c in range(30):
+            kp[table[0, c // 8], :, c % 8] = bad
+            vp[table[0, c // 8], :, c % 8] = bad
+    run(dtype, [2], [75], 4, 2, 64, page=8, window=40, spoil=spoil_window)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [7, 150])
+def test_a_bad_value_reaches_only_the_tokens_that_see_it(dtype, n):
+    def spoil(kp, vp, table, lens):
+        j = int(lens[0]) - 3   # seen by the last three tokens alone
+        vp[table[0, j // 16], 0, j % 16, 5] = float("inf")
+        vp[table[0, j // 16], 1, j % 16, 9] = float("nan")
+    run(dtype, [n], [210], 4, 2, 64, spoil=spoil)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_negative_and_equal_scores(dtype):
+    run(dtype, [1, 40], [3, 90], 2, 1, 64, scale=4.0)
+    run(dtype, [1], [50], 2, 1, 64, scale=-0.3)
+    run(dtype, [2], [50], 2, 1, 64, scale=0.0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_seen_scores_of_minus_infinity(dtype):
+    """Keys that a token sees but whose score is minus infinity; then all of them."""
+    def some(kp, vp, table, lens):
+        kp[table[0, 0], :, :, 0] = -float("inf")
+    def every(kp, vp, table, lens):
+        kp[..., 0] = -float("inf")
+    for spoil in (some, every):
+        run(dtype, [1], [40], 2, 1, 64, spoil=spoil, positive=True)
+        run(dtype, [70], [100], 2, 1, 64, spoil=spoil, positive=True)
+
+
+@pytest.mark.parametrize("offset", [1, 4])
+def test_queries_off_alignment(offset):
+    run(torch.bfloat16, [3, 40], [30, 80], 4, 2, 64, q_offset=offset)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_bounds_above_the_batch(dtype):
+    run(dtype, [1, 3], [40, 600], 4, 2, 64, max_new=5, max_len=4000)
+    run(dtype, [1, 70], [40, 600], 4, 2, 64, max_new=200, max_len=3000)
+
+
+def test_one_workspace_for_batches_of_any_size():
+    q = qmm()
+    z = torch.zeros(8, dtype=torch.int32, device=DEV)
+    sizes = [([1] * 6, [300 * i + 1 for i in range(6)]), ([1], [3000]), ([40, 2], [90, 700]), ([1], [1500])]
+    need = 0
+    for counts, lens in sizes:
+        b = q.PagedBatch(z[:len(lens) + 1], z[:len(lens)], z[:len(lens), None], sum(counts),
+                         max(counts), max(lens))
+        need = max(need, q.qmm_paged_attention_workspace_size(b, 4, 2, 64))
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    for counts, lens in sizes:
+        run(torch.bfloat16, counts, lens, 4, 2, 64, workspace=ws)
+
+
+def test_results_do_not_depend_on_timing():
+    outs = [run(torch.bfloat16, [1, 1, 2], [2900, 811, 1700], 8, 2, 128, seed=4) for _ in range(3)]
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_bad_table_entries_stay_in_bounds():
+    q = qmm()
+    kp = torch.randn(4, 1, 16, 64, device=DEV).bfloat16()
+    table = torch.tensor([[0, -7, 1 << 30], [2, 4, -1]], dtype=torch.int32, device=DEV)
+    starts = torch.tensor([0, 1, 41], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([48, 1000], dtype=torch.int32, device=DEV)   # past the table's width too
+    batch = q.PagedBatch(starts, lens, table, 41, 40, 1000)
+    x = torch.randn(41, 4, 64, device=DEV).bfloat16()
+    out = torch.empty_like(x)
+    ws = torch.zeros(q.qmm_paged_attention_workspace_size(batch, 4, 1, 64), dtype=torch.uint8, device=DEV)
+    q.qmm_paged_attention(x, q.PagedKV(kp, kp), batch, out, ws)
+    torch.cuda.synchronize()
+    assert torch.isfinite(out.float()).all()
+
+
+def test_another_stream_and_replays_in_a_step():
+    q = qmm()
+    starts, lens, table, total = ref.make_batch([1, 1, 1], [400, 33, 900], 16)
+    kp, vp = (torch.randn(total, 2, 16, 128, device=DEV).bfloat16() for _ in range(2))
+    x = torch.randn(3, 8, 128, device=DEV).bfloat16()
+    ln = dev(lens)
+    batch = q.PagedBatch(dev(starts), ln, dev(table), 3, 1, 1000)
+    ws = torch.zeros(q.qmm_paged_attention_workspace_size(batch, 8, 2, 128), dtype=torch.uint8, device=DEV)
+    out, direct = torch.empty_like(x), torch.empty_like(x)
+    kv = q.PagedKV(kp, vp)
+    step = q.Step()
+    step.add_paged_attention(x, kv, batch, out, ws)
+    step.finalize()
+    side = torch.cuda.Stream()
+    for i in range(4):
+        x.normal_()
+        ln.copy_(torch.tensor([400 - 50 * i, 33 - i, 900 - 7 * i], dtype=torch.int32))
+        step.launch()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            q.qmm_paged_attention(x, kv, batch, direct, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, direct)
+    step.close()
