@@ -88,6 +88,15 @@ hipError_t launch_rows_f32(const AttnArgs& a, const RowsPlan& plan, int blocks, 
 hipError_t launch_rows_f16(const AttnArgs& a, const RowsPlan& plan, int blocks, int skip_above);
 hipError_t launch_rows_bf16(const AttnArgs& a, const RowsPlan& plan, int blocks, int skip_above);
 
+// Many rows of queries a workgroup (paged_attn_tile.h), 16-bit types: 128 or
+// 256 rows (blocks 1 or 2), at most `tiles` tiles over all sequences with
+// more than skip_upto new tokens.
+struct TilePlan {
+  int splits, chunk, tiles, blocks, skip_upto;
+};
+hipError_t launch_tile_f16(const AttnArgs& a, const TilePlan& plan);
+hipError_t launch_tile_bf16(const AttnArgs& a, const TilePlan& plan);
+
 // The bookkeeping of the pages (strides and sizes of `data` in bytes).
 struct PoolArgs {
   char* data = nullptr;             // [planes, pages, page_bytes]

@@ -1,0 +1,554 @@
+// paged_attn_tile.h -- attention of many new tokens over a paged cache, for
+// 16-bit types: the bound is the matrix cores.
+//
+// A workgroup of four waves takes 128 or 256 query rows (new tokens times the
+// heads of a group, packed) of one key/value head; every wave owns 32 NQ of
+// them from the first key to the last and keeps their queries, running
+// statistics and outputs in registers.  Keys come in steps of 32.  A step's
+// three parts have nothing to wait for in one another: the scores of the next
+// step (matrix cores), the exponentials of this one (vector units) and the
+// product of the last one's probabilities with V (matrix cores).
+//
+// K and V pass through LDS in groups of two steps, two groups of each: the
+// global loads of a group are in flight for a whole group's work before they
+// are written to LDS.  Rows are padded there (K by 16 bytes, V by 32) so that
+// the 16-byte operand reads of K and the transposing reads of V meet no bank
+// twice.  V is one group behind K, as its use is.
+#pragma once
+
+#include "paged_attn.h"
+#include "qmm_internal.h"
+
+namespace qmm {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <int DT> struct Mfma32;
+template <> struct Mfma32<DT_BF16> {
+  static __device__ __forceinline__ f32x16 run(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+};
+template <> struct Mfma32<DT_F16> {
+  static __device__ __forceinline__ f32x16 run(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+};
+
+// Maximum and sum over the two lanes that share a column (lane mod 32).
+__device__ __forceinline__ float pair_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float pair_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+constexpr int TILE_WAVES = 4, TILE_THREADS = 64 * TILE_WAVES;
+
+// DK: the head's width in scores (16s), DV: in outputs (32s).
+template <int DK, int DV> struct TileLds {
+  static constexpr int KROW = DK * 2 + 16, VROW = DV * 2 + 32;
+  static constexpr int KBUF = 64 * KROW, VBUF = 64 * VROW;
+  static constexpr int BYTES = 2 * (KBUF + VBUF);
+};
+
+// The statistics rise above the reference maximum by at most this (log2)
+// before outputs are rescaled to a new one: probabilities stay below 2^8.
+constexpr float TILE_SLACK = 8.f;
+
+template <int DT, int DK, int DV, int NQ, bool CAP>
+__global__ __launch_bounds__(TILE_THREADS, 1) void attn_tile_kernel(AttnArgs a, TilePlan plan,
+                                                                    ScoreScale scale) {
+  using T = typename dt<DT>::T;
+  using L = TileLds<DK, DV>;
+  using Op = MfmaOp<DT>;
+  constexpr int KS = DK / 16, DB = DV / 32, CH = DK / 8;   // score steps, output blocks, chunks
+  constexpr int IT = (16 * CH + 63) / 64;                  // loads of a wave's 16 rows
+  constexpr int ROWS = TILE_WAVES * 32 * NQ;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  __shared__ int found[4];
+  __shared__ int last, odd;
+
+  const CacheArgs& c = a.c;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l31 = lane & 31, half = lane >> 5, l15 = lane & 15;
+
+  // Heads fastest, so that one head's tiles meet in one L2; then parts; the
+  // tiles of the sequences follow one another without gaps.
+  uint32_t id = blockIdx.x;
+  const int kvh = id % c.kv_heads;
+  id /= c.kv_heads;
+  const int split = id % plan.splits, want = id / plan.splits;
+  if (wave == 0) {
+    int base = 0, seq = -1, tile = 0;
+    for (int s0 = 0; s0 < c.seqs && seq < 0; s0 += 64) {
+      int mine = 0;
+      if (s0 + lane < c.seqs) {
+        const Seq q = seq_of(c, s0 + lane);
+        if (q.n > plan.skip_upto) mine = (q.n * a.group + ROWS - 1) / ROWS;
+      }
+      int sum = mine;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int y = __shfl_up(sum, d);
+        if (lane >= d) sum += y;
+      }
+      const bool here = want >= base + sum - mine && want < base + sum;
+      const uint64_t who = __ballot(here);
+      if (who) {
+        const int w = __builtin_ctzll(who);
+        seq = s0 + w;
+        tile = want - base - (__shfl(sum, w) - __shfl(mine, w));
+      }
+      base += __shfl(sum, 63);
+    }
+    if (lane == 0) {
+      found[0] = seq;
+      found[1] = tile;
+      odd = 0;
+    }
+  }
+  __syncthreads();
+  const int seq = __builtin_amdgcn_readfirstlane(found[0]);
+  const int tile = __builtin_amdgcn_readfirstlane(found[1]);
+  if (seq < 0) return;
+  const Seq sq = seq_of(c, seq);
+  const int rows = sq.n * a.group, row0 = tile * ROWS;
+  const int row1 = rows < row0 + ROWS ? rows : row0 + ROWS;
+  const int pos0 = sq.len - sq.n;
+  auto clip = [&](int j) { return j < 0 ? 0 : j > sq.len ? sq.len : j; };
+  auto pos_of = [&](int r) { return pos0 + (int)div_by(r, a.by_group); };
+  const int kmin = a.window ? clip(pos_of(row0) - a.window + 1) : 0;
+  const int kmax = a.causal ? clip(pos_of(row1 - 1) + 1) : sq.len;
+  int active = kmax > kmin ? (kmax - kmin + plan.chunk - 1) / plan.chunk : 1;
+  active = active > plan.splits ? plan.splits : active;
+  if (split >= active) return;
+  // Steps start at multiples of 16, so that a wave's 16 rows of a group lie
+  // in one page wherever pages hold a multiple of 16 keys.
+  const int first = (kmin & ~15) + split * plan.chunk;
+  const int end = split == active - 1 ? kmax : first + plan.chunk;
+  const int begin = split == 0 ? kmin : first;
+  const int steps = end > first ? (end - first + 31) / 32 : 0;
+
+  // The wave's rows: what all of them see, and each lane's own limits.
+  const int wrow0 = row0 + wave * 32 * NQ;
+  int all0 = begin, all1 = end;
+  if (wrow0 < row1) {
+    const int wrow1 = row1 < wrow0 + 32 * NQ ? row1 : wrow0 + 32 * NQ;
+    if (a.window) all0 = max(all0, pos_of(wrow1 - 1) - a.window + 1);
+    if (a.causal) all1 = min(all1, clip(pos_of(wrow0) + 1));
+  }
+  all0 = __builtin_amdgcn_readfirstlane(all0);
+  all1 = __builtin_amdgcn_readfirstlane(all1);
+
+  u32x4 qf[NQ][KS];
+  int lo[NQ], hi[NQ];
+#pragma unroll
+  for (int b = 0; b < NQ; ++b) {
+    const int r = wrow0 + 32 * b + l31;
+    const bool ok = r < row1;
+    const int i = ok ? (int)div_by(r, a.by_group) : 0, h = ok ? r - i * a.group : 0;
+    const int pos = pos0 + i;
+    lo[b] = max(begin, a.window ? pos - a.window + 1 : 0);
+    hi[b] = !ok ? 0 : min(end, a.causal ? clip(pos + 1) : sq.len);
+    const T* from = (const T*)a.q + (int64_t)(sq.t0 + i) * a.q_token +
+                    (int64_t)(kvh * a.group + h) * a.q_head;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int d = (2 * s + half) * 8;
+      T e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = T(0);
+      if (ok && d < c.dim) {
+        if (a.q_wide) {
+          __builtin_memcpy(e, __builtin_assume_aligned(from + d, 16), 16);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[j] = from[d + j];
+        }
+      }
+      __builtin_memcpy(&qf[b][s], e, 16);
+      // A negative scale is its amount and a turned sign of q.
+      if (a.scale < 0.f) qf[b][s] ^= 0x80008000u;
+    }
+  }
+
+  // Staging.  Group n holds the keys of steps 2 n - 1 and 2 n; this wave
+  // loads its rows 16 wave .. 16 wave + 15.
+  const int32_t* table = c.table + (int64_t)seq * c.table_stride;
+  const bool paged16 = c.page % 16 == 0;
+  const int chunks = c.dim / 8;
+  int srow[IT], sch[IT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int x = i * 64 + lane;
+    srow[i] = x / CH;
+    sch[i] = x % CH;
+  }
+  struct Place {
+    int page[IT], at[IT];
+  };
+  auto group_key = [&](int n) { return first + 64 * n - 32 + 16 * wave; };
+  auto place_of = [&](int n) {
+    Place p;
+    const int j0 = group_key(n), top = sq.len > 0 ? sq.len - 1 : 0;
+    if (paged16) {
+      const int j = j0 < 0 ? 0 : j0 > (top & ~15) ? (top & ~15) : j0;
+      int at = 0;
+      const int page = sq.len > 0 ? page_of(c, table, j, at) : 0;
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        p.page[i] = page;
+        p.at[i] = at + srow[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int j = j0 + srow[i];
+        p.at[i] = 0;
+        p.page[i] = sq.len > 0 ? page_of(c, table, j < 0 ? 0 : j > top ? top : j, p.at[i]) : 0;
+      }
+    }
+    return p;
+  };
+  struct Stage {
+    u32x4 x[IT];
+  };
+  auto load = [&](const char* base, int64_t s_page, int64_t s_head, int64_t s_token, const Place& p) {
+    Stage st;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+      st.x[i] = u32x4{0, 0, 0, 0};
+      if ((IT * 64 == 16 * CH || srow[i] < 16) && sch[i] < chunks)
+        st.x[i] = *(const u32x4*)(base + (p.page[i] * s_page + kvh * s_head + p.at[i] * s_token) * 2 +
+                                  sch[i] * 16);
+    }
+    return st;
+  };
+  auto load_k = [&](const Place& p) { return load(c.k, c.k_page, c.k_head, c.k_token, p); };
+  auto load_v = [&](const Place& p) { return load(c.v, c.v_page, c.v_head, c.v_token, p); };
+  auto kbuf = [&](int n) { return lds + (n & 1) * L::KBUF; };
+  auto vbuf = [&](int n) { return lds + 2 * L::KBUF + (n & 1) * L::VBUF; };
+  auto store_k = [&](int n, const Stage& st) {
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+      if (IT * 64 == 16 * CH || srow[i] < 16)
+        *(u32x4*)(kbuf(n) + (16 * wave + srow[i]) * L::KROW + sch[i] * 16) = st.x[i];
+  };
+  // Keys that not every row of the workgroup sees: a value that is not finite
+  // would make NaN of a probability of 0.  It goes in as 0, and is added at
+  // the end to the rows that see it.
+  const int safe0 = a.window ? clip(pos_of(row1 - 1) - a.window + 1) : begin;
+  const int safe1 = a.causal ? clip(pos_of(row0) + 1) : end;
+  auto store_v = [&](int n, Stage st) {
+    const int j0 = group_key(n);
+    if (j0 < max(safe0, begin) || j0 + 16 > min(safe1, end)) {
+      bool any = false;
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int j = j0 + srow[i];
+        const bool in = j >= begin && j < end, safe = in && j >= safe0 && j < safe1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          constexpr uint32_t E = DT == DT_BF16 ? 0x7F80u : 0x7C00u;
+          uint32_t x = in ? st.x[i][e] : 0u;
+          const bool o0 = (x & E) == E, o1 = ((x >> 16) & E) == E;
+          if (o0 && !safe) x &= 0xFFFF0000u;
+          if (o1 && !safe) x &= 0x0000FFFFu;
+          any |= !safe && (o0 || o1);
+          st.x[i][e] = x;
+        }
+      }
+      if (__any(any)) odd = 1;
+    }
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+      if (IT * 64 == 16 * CH || srow[i] < 16)
+        *(u32x4*)(vbuf(n) + (16 * wave + srow[i]) * L::VROW + sch[i] * 16) = st.x[i];
+  };
+
+  f32x16 o[NQ][DB], s[NQ];
+  u32x4 p[NQ][2];
+  float m[NQ], sub[NQ], l[NQ], top[NQ];
+#pragma unroll
+  for (int b = 0; b < NQ; ++b) {
+    m[b] = -INFINITY;
+    sub[b] = 0.f;
+    l[b] = 0.f;
+    p[b][0] = p[b][1] = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[b][d][i] = 0.f;
+  }
+
+  // The scores of a step from rows `row` .. of a K buffer.
+  auto scores = [&](const char* buf, int row, f32x16 (&out)[NQ]) {
+    const char* at = buf + (row + l31) * L::KROW + half * 16;
+#pragma unroll
+    for (int b = 0; b < NQ; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) out[b][i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const u32x4 kf = *(const u32x4*)(at + k * 32);
+#pragma unroll
+      for (int b = 0; b < NQ; ++b) out[b] = Mfma32<DT>::run(kf, qf[b][k], out[b]);
+    }
+  };
+  auto values = [&](const char* buf, int row) {
+    const char* at = buf + (row + 4 * half + l15 / 4) * L::VROW + (lane & 16) * 2 + (l15 % 4) * 8;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        const s16x4 x0 = lds_read_tr(at + 16 * u * L::VROW + d * 64);
+        const s16x4 x1 = lds_read_tr(at + (16 * u + 8) * L::VROW + d * 64);
+        const auto v = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+        for (int b = 0; b < NQ; ++b)
+          o[b][d] = Mfma32<DT>::run(__builtin_bit_cast(u32x4, v), p[b][u], o[b][d]);
+      }
+  };
+  auto tops = [&](const f32x16 (&x)[NQ]) {
+#pragma unroll
+    for (int b = 0; b < NQ; ++b) {
+      float t = fmaxf(fmaxf(x[b][0], x[b][1]), x[b][2]);
+#pragma unroll
+      for (int i = 3; i < 15; i += 2) t = fmaxf(fmaxf(t, x[b][i]), x[b][i + 1]);
+      top[b] = pair_max(fmaxf(t, x[b][15]));
+    }
+  };
+  const float mul = CAP ? 1.f : fabsf(scale.mul);
+  // Cap and mask the scores of step n, where it needs either.
+  auto finish = [&](int n, f32x16 (&x)[NQ]) {
+    const int j0 = first + 32 * n;
+    const bool part = j0 < all0 || j0 + 32 > all1;
+    if (!CAP && !part) return;
+#pragma unroll
+    for (int b = 0; b < NQ; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if constexpr (CAP) x[b][i] = score<true, false>(x[b][i], ScoreScale{fabsf(scale.mul), scale.cap});
+        const int j = j0 + 8 * (i / 4) + 4 * half + i % 4;
+        if (part && !(j >= lo[b] && j < hi[b])) x[b][i] = -INFINITY;
+      }
+    tops(x);
+  };
+  // A new reference maximum where a row passed the old one by the slack; what
+  // is still to be added of the last step is added first.
+  auto renew = [&](const char* buf, int row) {
+    bool past = false;
+#pragma unroll
+    for (int b = 0; b < NQ; ++b) {
+      top[b] *= mul;
+      past |= top[b] > m[b] + TILE_SLACK;
+    }
+    if (!__any(past)) return;
+    values(buf, row);
+#pragma unroll
+    for (int b = 0; b < NQ; ++b) {
+      p[b][0] = p[b][1] = u32x4{0, 0, 0, 0};
+      const float was = m[b];
+      m[b] = fmaxf(was, top[b]);
+      sub[b] = m[b] == -INFINITY ? 0.f : m[b];
+      const float back = exp2_fast(was - sub[b]);
+      l[b] *= back;
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[b][d] *= back;
+    }
+  };
+
+  // A step: scores of the next, probabilities of this, output of the last.
+  auto step = [&](int n, const char* kb, const char* vb, int row) {
+    f32x16 next[NQ];
+    scores(kb, row, next);
+    u32x4 q[NQ][2];
+#pragma unroll
+    for (int b = 0; b < NQ; ++b) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[b][i] = exp2_fast(__builtin_fmaf(s[b][i], mul, -sub[b]));
+        l[b] += s[b][i];
+      }
+      // Rounded to the values' type: the matrix cores take no other pair.
+      // The sum above keeps them in 32 bits.
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[b][u][e] = Op::pack(s[b][8 * u + 2 * e], s[b][8 * u + 2 * e + 1]);
+    }
+    values(vb, row);
+    tops(next);
+#pragma unroll
+    for (int b = 0; b < NQ; ++b) {
+      p[b][0] = q[b][0];
+      p[b][1] = q[b][1];
+      s[b] = next[b];
+    }
+    finish(n + 1, s);
+  };
+
+  Place at_v, at_k = place_of(0);
+  store_k(0, load_k(at_k));
+  store_v(0, load_v(at_k));
+  at_v = place_of(1);
+  store_k(1, load_k(at_v));
+  at_k = place_of(2);
+  Stage gv = load_v(at_v), gk = load_k(at_k);
+  at_v = at_k;
+  at_k = place_of(3);
+  __syncthreads();
+  scores(kbuf(0), 32, s);
+  tops(s);
+  finish(0, s);
+  __syncthreads();
+  const int iters = (steps + 2) / 2;
+  for (int t = 0; t < iters; ++t) {
+    store_k(t + 2, gk);
+    store_v(t + 1, gv);
+    gk = load_k(at_k);
+    gv = load_v(at_v);
+    at_v = at_k;
+    at_k = place_of(t + 4);
+    const char *kb = kbuf(t + 1), *vb = vbuf(t);
+    renew(vb, 0);
+    step(2 * t, kb, vb, 0);
+    renew(vb, 32);
+    step(2 * t + 1, kb, vb, 32);
+    __syncthreads();
+  }
+
+  // Values that were left out, for the rows that see them.
+  if (odd) {
+    for (int j = begin; j < end; ++j) {
+      if (j >= safe0 && j < safe1) continue;
+      int at;
+      const int64_t page = page_of(c, table, j, at);
+      const T* from = (const T*)c.v + page * c.v_page + kvh * c.v_head + at * c.v_token;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int col = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
+          const float x = col < c.dim ? dt<DT>::to_f32(from[col]) : 0.f;
+          if (!(fabsf(x) < INFINITY))
+#pragma unroll
+            for (int b = 0; b < NQ; ++b)
+              if (j >= lo[b] && j < hi[b]) o[b][d][i] += x;
+        }
+    }
+  }
+
+  // Write, or park this part of the keys.
+  char* ws = a.workspace + ATTN_COUNTERS * 4;
+  const int64_t tile_id = ((int64_t)want * c.kv_heads + kvh);
+  const int64_t parts = (int64_t)plan.tiles * c.kv_heads * plan.splits;
+  float2* part_ml = (float2*)ws + tile_id * plan.splits * ROWS;
+  float* part_o = (float*)(ws + parts * ROWS * 8) + tile_id * plan.splits * ROWS * DV;
+#pragma unroll
+  for (int b = 0; b < NQ; ++b) {
+    const int r = wrow0 + 32 * b + l31;
+    const float sum = pair_sum(l[b]);
+    if (r >= row1) continue;
+    const int i = (int)div_by(r, a.by_group), h = kvh * a.group + r - i * a.group;
+    const int64_t tok = sq.t0 + i;
+    if (active == 1) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      T* to = (T*)a.out + tok * a.out_token + (int64_t)h * a.out_head;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = 32 * d + 8 * e + 4 * half;
+          if (col >= c.dim) continue;
+          const u32x2 w = {Op::pack(o[b][d][4 * e] * inv, o[b][d][4 * e + 1] * inv),
+                           Op::pack(o[b][d][4 * e + 2] * inv, o[b][d][4 * e + 3] * inv)};
+          if (a.out_wide) *(u32x2*)(to + col) = w;
+          else __builtin_memcpy(to + col, &w, 8);
+        }
+      if (a.lse != nullptr && half == 0)
+        a.lse[tok * a.lse_token + (int64_t)h * a.lse_head] =
+            sum == 0.f ? -INFINITY : (m[b] + log2f(sum)) * LN2;
+    } else {
+      const int64_t row = (int64_t)split * ROWS + r - row0;
+      if (half == 0) part_ml[row] = make_float2(m[b], sum);
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *(f32x4*)(part_o + row * DV + 32 * d + 8 * e + 4 * half) =
+              f32x4{o[b][d][4 * e], o[b][d][4 * e + 1], o[b][d][4 * e + 2], o[b][d][4 * e + 3]};
+    }
+  }
+  if (active == 1) return;
+  uint32_t* counter = (uint32_t*)a.workspace + ATTN_COUNTERS / 2 + tile_id;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(counter, 1u) == (uint32_t)(active - 1);
+    __threadfence();
+  }
+  __syncthreads();
+  if (!last) return;
+  if (threadIdx.x == 0) *counter = 0;
+  for (int e = threadIdx.x; e < (row1 - row0) * (DV / 4); e += TILE_THREADS) {
+    const int q = e / (DV / 4), col = e % (DV / 4) * 4, r = row0 + q;
+    if (col >= c.dim) continue;
+    float high = -INFINITY, total = 0.f;
+    for (int k = 0; k < active; ++k) high = fmaxf(high, part_ml[k * ROWS + q].x);
+    const float ref = high == -INFINITY ? 0.f : high;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < active; ++k) {
+      const float2 ml = part_ml[k * ROWS + q];
+      const float f = exp2_fast(ml.x - ref);
+      total += f * ml.y;
+      x += f * *(const f32x4*)(part_o + ((int64_t)k * ROWS + q) * DV + col);
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const int i = (int)div_by(r, a.by_group), h = kvh * a.group + r - i * a.group;
+    const int64_t tok = sq.t0 + i;
+    T* to = (T*)a.out + tok * a.out_token + (int64_t)h * a.out_head + col;
+    const u32x2 w = {Op::pack(x[0] * inv, x[1] * inv), Op::pack(x[2] * inv, x[3] * inv)};
+    if (a.out_wide) *(u32x2*)to = w;
+    else __builtin_memcpy(to, &w, 8);
+    if (a.lse != nullptr && col == 0)
+      a.lse[tok * a.lse_token + (int64_t)h * a.lse_head] =
+          total == 0.f ? -INFINITY : (high + log2f(total)) * LN2;
+  }
+}
+
+template <int DT, int DK, int DV, int NQ>
+hipError_t launch_tile(const AttnArgs& a, const TilePlan& plan) {
+  const bool cap = a.softcap > 0.f;
+  const ScoreScale k = cap ? ScoreScale{a.scale / a.softcap, a.softcap * LOG2E}
+                           : ScoreScale{a.scale * LOG2E, 0.f};
+  constexpr int bytes = TileLds<DK, DV>::BYTES;
+  const void* fn = cap ? (const void*)attn_tile_kernel<DT, DK, DV, NQ, true>
+                       : (const void*)attn_tile_kernel<DT, DK, DV, NQ, false>;
+  const hipError_t e = ensure_dynamic_lds(fn, bytes);
+  if (e != hipSuccess) return e;
+  const dim3 grid((uint32_t)plan.tiles * plan.splits * a.c.kv_heads);
+  if (cap) attn_tile_kernel<DT, DK, DV, NQ, true><<<grid, TILE_THREADS, bytes, a.stream>>>(a, plan, k);
+  else attn_tile_kernel<DT, DK, DV, NQ, false><<<grid, TILE_THREADS, bytes, a.stream>>>(a, plan, k);
+  return hipGetLastError();
+}
+
+// Two blocks of 32 rows a wave where their registers fit.
+template <int DT>
+hipError_t launch_tile_type(const AttnArgs& a, const TilePlan& plan) {
+  const int d = a.c.dim;
+#define QMM_TILE(DK, DV)                                        \
+  if (d <= DK) return plan.blocks == 2 ? launch_tile<DT, DK, DV, 2>(a, plan) \
+                                       : launch_tile<DT, DK, DV, 1>(a, plan);
+  QMM_TILE(64, 64) QMM_TILE(80, 96) QMM_TILE(96, 96) QMM_TILE(128, 128)
+#undef QMM_TILE
+  if (d <= 192) return launch_tile<DT, 192, 192, 1>(a, plan);
+  return launch_tile<DT, 256, 256, 1>(a, plan);
+}
+
+}  // namespace qmm

@@ -1,0 +1,10 @@
+// paged_attn_tile_f16.hip -- paged attention of many new tokens, f16 caches.
+#include "paged_attn_tile.h"
+
+namespace qmm {
+
+hipError_t launch_tile_f16(const AttnArgs& a, const TilePlan& plan) {
+  return launch_tile_type<DT_F16>(a, plan);
+}
+
+}  // namespace qmm

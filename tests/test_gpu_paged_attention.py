@@ -116,6 +116,14 @@ def test_long_sequences_in_parts(dtype, counts, lens):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("counts,lens", [([70, 1], [2500, 900]), ([150, 3, 40], [1300, 2000, 700])])
+def test_chunks_of_long_sequences_in_parts(dtype, window, counts, lens):
+    run(dtype, counts, lens, 2, 1, 64, window=window, seed=2)
+    run(dtype, counts, lens, 4, 1, 128, window=window, page=12, seed=3)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_what_masked_keys_hold_does_not_matter(dtype, bad):
     """Places past a sequence's end, pages it does not hold, keys later than a
