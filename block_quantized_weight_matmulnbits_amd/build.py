@@ -32,10 +32,17 @@ COMMON = [
     "-Wall", "-Wno-unused-function",
 ]
 
+# Flags of single sources.  The tiled attention keeps scores, which the vector
+# units work on, and outputs in accumulators at once: matrix instructions that
+# write vector registers save it a copy of every score.
+EXTRA = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+         for name in ("paged_attn_tile_f16.hip", "paged_attn_tile_bf16.hip")}
+
 
 def _compile(src: str) -> str:
-    obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-    cmd = [HIPCC, *COMMON, "-c", src, "-o", obj]
+    name = os.path.basename(src)
+    obj = os.path.join(BUILD, name + ".o")
+    cmd = [HIPCC, *COMMON, *EXTRA.get(name, []), "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")

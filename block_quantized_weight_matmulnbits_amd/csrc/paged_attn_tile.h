@@ -47,7 +47,7 @@ __device__ __forceinline__ float pair_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-constexpr int TILE_WAVES = 4, TILE_THREADS = 64 * TILE_WAVES;
+#define QMM_INLINE __attribute__((always_inline))
 
 // DK: the head's width in scores (16s), DV: in outputs (32s).
 template <int DK, int DV> struct TileLds {
@@ -60,15 +60,16 @@ template <int DK, int DV> struct TileLds {
 // before outputs are rescaled to a new one: probabilities stay below 2^8.
 constexpr float TILE_SLACK = 8.f;
 
-template <int DT, int DK, int DV, int NQ, bool CAP>
-__global__ __launch_bounds__(TILE_THREADS, 1) void attn_tile_kernel(AttnArgs a, TilePlan plan,
+template <int DT, int DK, int DV, int WAVES, bool CAP>
+__global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kernel(AttnArgs a, TilePlan plan,
                                                                     ScoreScale scale) {
   using T = typename dt<DT>::T;
   using L = TileLds<DK, DV>;
   using Op = MfmaOp<DT>;
   constexpr int KS = DK / 16, DB = DV / 32, CH = DK / 8;   // score steps, output blocks, chunks
-  constexpr int IT = (16 * CH + 63) / 64;                  // loads of a wave's 16 rows
-  constexpr int ROWS = TILE_WAVES * 32 * NQ;
+  constexpr int NQ = 1;
+  constexpr int SR = 64 / WAVES, IT = (SR * CH + 63) / 64;   // rows of a group that a wave loads
+  constexpr int THREADS = 64 * WAVES, ROWS = 32 * NQ * WAVES;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   __shared__ int found[4];
   __shared__ int last, odd;
@@ -127,12 +128,9 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void attn_tile_kernel(AttnArgs a, 
   int active = kmax > kmin ? (kmax - kmin + plan.chunk - 1) / plan.chunk : 1;
   active = active > plan.splits ? plan.splits : active;
   if (split >= active) return;
-  // Steps start at multiples of 16, so that a wave's 16 rows of a group lie
-  // in one page wherever pages hold a multiple of 16 keys.
-  const int first = (kmin & ~15) + split * plan.chunk;
-  const int end = split == active - 1 ? kmax : first + plan.chunk;
-  const int begin = split == 0 ? kmin : first;
-  const int steps = end > first ? (end - first + 31) / 32 : 0;
+  const int begin = kmin + split * plan.chunk;
+  const int end = split == active - 1 ? kmax : begin + plan.chunk;
+  const int steps = end > begin ? (end - begin + 31) / 32 : 0;
 
   // The wave's rows: what all of them see, and each lane's own limits.
   const int wrow0 = row0 + wave * 32 * NQ;
@@ -177,76 +175,65 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void attn_tile_kernel(AttnArgs a, 
     }
   }
 
-  // Staging.  Group n holds the keys of steps 2 n - 1 and 2 n; this wave
-  // loads its rows 16 wave .. 16 wave + 15.
+  // Staging.  Group n of V holds the keys of steps 2 n and 2 n + 1, group n of
+  // K those three steps on, 2 n + 3 and 2 n + 4; this wave loads rows 16 wave
+  // .. 16 wave + 15 of each.
   const int32_t* table = c.table + (int64_t)seq * c.table_stride;
-  const bool paged16 = c.page % 16 == 0;
   const int chunks = c.dim / 8;
+  auto v_key = [&](int n) { return begin + 64 * n + SR * wave; };
+  auto k_key = [&](int n) { return v_key(n) + 96; };
   int srow[IT], sch[IT];
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int x = i * 64 + lane;
-    srow[i] = x / CH;
-    sch[i] = x % CH;
+    srow[i] = (i * 64 + lane) / CH;
+    sch[i] = (i * 64 + lane) % CH;
   }
-  struct Place {
-    int page[IT], at[IT];
-  };
-  auto group_key = [&](int n) { return first + 64 * n - 32 + 16 * wave; };
-  auto place_of = [&](int n) {
-    Place p;
-    const int j0 = group_key(n), top = sq.len > 0 ? sq.len - 1 : 0;
-    if (paged16) {
-      const int j = j0 < 0 ? 0 : j0 > (top & ~15) ? (top & ~15) : j0;
-      int at = 0;
-      const int page = sq.len > 0 ? page_of(c, table, j, at) : 0;
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        p.page[i] = page;
-        p.at[i] = at + srow[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const int j = j0 + srow[i];
-        p.at[i] = 0;
-        p.page[i] = sq.len > 0 ? page_of(c, table, j < 0 ? 0 : j > top ? top : j, p.at[i]) : 0;
-      }
-    }
-    return p;
+  // Where the rows of K group nk and V group nv lie: lanes 0 .. 15 look the
+  // first up, lanes 16 .. 31 the second, a row each; the loads take them from
+  // there.  Keys outside the sequence read its first or last one.
+  auto rows_of = [&](int nk, int nv) QMM_INLINE {
+    const int j0 = (lane & 16) ? v_key(nv) : k_key(nk), top = sq.len - 1;
+    int j = j0 + l15, at = 0, page = 0;
+    j = j > top ? top : j;
+    if (sq.len > 0) page = page_of(c, table, j < 0 ? 0 : j, at);
+    const int64_t off = (lane & 16) ? page * c.v_page + kvh * c.v_head + at * c.v_token
+                                    : page * c.k_page + kvh * c.k_head + at * c.k_token;
+    return off * 2;
   };
   struct Stage {
     u32x4 x[IT];
   };
-  auto load = [&](const char* base, int64_t s_page, int64_t s_head, int64_t s_token, const Place& p) {
+  auto load = [&](const char* base, int64_t rows, int from) QMM_INLINE {
     Stage st;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
+      const int who = (from + (IT * 64 == SR * CH ? srow[i] : srow[i] % SR)) * 4;
+      const uint32_t x = __builtin_amdgcn_ds_bpermute(who, (int)(uint32_t)rows);
+      const uint32_t y = __builtin_amdgcn_ds_bpermute(who, (int)(uint32_t)(rows >> 32));
+      const char* at = base + (((uint64_t)y << 32) | x) + sch[i] * 16;
       st.x[i] = u32x4{0, 0, 0, 0};
-      if ((IT * 64 == 16 * CH || srow[i] < 16) && sch[i] < chunks)
-        st.x[i] = *(const u32x4*)(base + (p.page[i] * s_page + kvh * s_head + p.at[i] * s_token) * 2 +
-                                  sch[i] * 16);
+      if (sch[i] < chunks) st.x[i] = *(const u32x4*)at;
     }
     return st;
   };
-  auto load_k = [&](const Place& p) { return load(c.k, c.k_page, c.k_head, c.k_token, p); };
-  auto load_v = [&](const Place& p) { return load(c.v, c.v_page, c.v_head, c.v_token, p); };
+  auto load_k = [&](int64_t rows) QMM_INLINE { return load(c.k, rows, 0); };
+  auto load_v = [&](int64_t rows) QMM_INLINE { return load(c.v, rows, 16); };
   auto kbuf = [&](int n) { return lds + (n & 1) * L::KBUF; };
   auto vbuf = [&](int n) { return lds + 2 * L::KBUF + (n & 1) * L::VBUF; };
-  auto store_k = [&](int n, const Stage& st) {
+  auto store_k = [&](int n, const Stage& st) QMM_INLINE {
 #pragma unroll
     for (int i = 0; i < IT; ++i)
-      if (IT * 64 == 16 * CH || srow[i] < 16)
-        *(u32x4*)(kbuf(n) + (16 * wave + srow[i]) * L::KROW + sch[i] * 16) = st.x[i];
+      if (IT * 64 == SR * CH || srow[i] < SR)
+        *(u32x4*)(kbuf(n) + (SR * wave + srow[i]) * L::KROW + sch[i] * 16) = st.x[i];
   };
   // Keys that not every row of the workgroup sees: a value that is not finite
   // would make NaN of a probability of 0.  It goes in as 0, and is added at
   // the end to the rows that see it.
   const int safe0 = a.window ? clip(pos_of(row1 - 1) - a.window + 1) : begin;
   const int safe1 = a.causal ? clip(pos_of(row0) + 1) : end;
-  auto store_v = [&](int n, Stage st) {
-    const int j0 = group_key(n);
-    if (j0 < max(safe0, begin) || j0 + 16 > min(safe1, end)) {
+  auto store_v = [&](int n, Stage st) QMM_INLINE {
+    const int j0 = v_key(n);
+    if (j0 < max(safe0, begin) || j0 + SR > min(safe1, end)) {
       bool any = false;
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
@@ -267,40 +254,47 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void attn_tile_kernel(AttnArgs a, 
     }
 #pragma unroll
     for (int i = 0; i < IT; ++i)
-      if (IT * 64 == 16 * CH || srow[i] < 16)
-        *(u32x4*)(vbuf(n) + (16 * wave + srow[i]) * L::VROW + sch[i] * 16) = st.x[i];
+      if (IT * 64 == SR * CH || srow[i] < SR)
+        *(u32x4*)(vbuf(n) + (SR * wave + srow[i]) * L::VROW + sch[i] * 16) = st.x[i];
   };
 
-  f32x16 o[NQ][DB], s[NQ];
-  u32x4 p[NQ][2];
+  struct Keys {
+    u32x4 x[KS];
+  };
+  f32x16 o[NQ][DB], s0[NQ], s1[NQ];   // scores of even and odd steps
+  u32x4 p0[NQ][2], p1[NQ][2];         // probabilities of even and odd steps
   float m[NQ], sub[NQ], l[NQ], top[NQ];
 #pragma unroll
   for (int b = 0; b < NQ; ++b) {
     m[b] = -INFINITY;
     sub[b] = 0.f;
     l[b] = 0.f;
-    p[b][0] = p[b][1] = u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[b][d][i] = 0.f;
   }
 
-  // The scores of a step from rows `row` .. of a K buffer.
-  auto scores = [&](const char* buf, int row, f32x16 (&out)[NQ]) {
+  // K operands of a step from rows `row` .. of a buffer, and its scores.
+  auto keys = [&](const char* buf, int row) QMM_INLINE {
     const char* at = buf + (row + l31) * L::KROW + half * 16;
+    Keys r;
 #pragma unroll
-    for (int b = 0; b < NQ; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) out[b][i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const u32x4 kf = *(const u32x4*)(at + k * 32);
-#pragma unroll
-      for (int b = 0; b < NQ; ++b) out[b] = Mfma32<DT>::run(kf, qf[b][k], out[b]);
-    }
+    for (int k = 0; k < KS; ++k) r.x[k] = *(const u32x4*)(at + k * 32);
+    return r;
   };
-  auto values = [&](const char* buf, int row) {
+  auto scores = [&](const Keys& kf, f32x16 (&out)[NQ]) QMM_INLINE {
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int b = 0; b < NQ; ++b) {
+        if (k == 0)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) out[b][i] = 0.f;
+        out[b] = Mfma32<DT>::run(kf.x[k], qf[b][k], out[b]);
+      }
+  };
+  auto values = [&](const char* buf, int row, const u32x4 (&p)[NQ][2]) QMM_INLINE {
     const char* at = buf + (row + 4 * half + l15 / 4) * L::VROW + (lane & 16) * 2 + (l15 % 4) * 8;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -314,7 +308,7 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void attn_tile_kernel(AttnArgs a, 
           o[b][d] = Mfma32<DT>::run(__builtin_bit_cast(u32x4, v), p[b][u], o[b][d]);
       }
   };
-  auto tops = [&](const f32x16 (&x)[NQ]) {
+  auto tops = [&](const f32x16 (&x)[NQ]) QMM_INLINE {
 #pragma unroll
     for (int b = 0; b < NQ; ++b) {
       float t = fmaxf(fmaxf(x[b][0], x[b][1]), x[b][2]);
@@ -325,31 +319,34 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void attn_tile_kernel(AttnArgs a, 
   };
   const float mul = CAP ? 1.f : fabsf(scale.mul);
   // Cap and mask the scores of step n, where it needs either.
-  auto finish = [&](int n, f32x16 (&x)[NQ]) {
-    const int j0 = first + 32 * n;
-    const bool part = j0 < all0 || j0 + 32 > all1;
+  auto whole = [&](int n) { return begin + 32 * n >= all0 && begin + 32 * n + 32 <= all1; };
+  auto finish = [&](int n, f32x16 (&x)[NQ]) QMM_INLINE {
+    const int j0 = begin + 32 * n;
+    const bool part = !whole(n);
     if (!CAP && !part) return;
+    int base = j0 + 4 * half;
+    asm volatile("" : "+v"(base));   // a branch, not selects in every step
 #pragma unroll
     for (int b = 0; b < NQ; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         if constexpr (CAP) x[b][i] = score<true, false>(x[b][i], ScoreScale{fabsf(scale.mul), scale.cap});
-        const int j = j0 + 8 * (i / 4) + 4 * half + i % 4;
+        const int j = base + 8 * (i / 4) + i % 4;
         if (part && !(j >= lo[b] && j < hi[b])) x[b][i] = -INFINITY;
       }
     tops(x);
   };
   // A new reference maximum where a row passed the old one by the slack; what
   // is still to be added of the last step is added first.
-  auto renew = [&](const char* buf, int row) {
+  auto renew = [&](const char* buf, int row, u32x4 (&p)[NQ][2]) QMM_INLINE {
     bool past = false;
 #pragma unroll
     for (int b = 0; b < NQ; ++b) {
       top[b] *= mul;
       past |= top[b] > m[b] + TILE_SLACK;
     }
-    if (!__any(past)) return;
-    values(buf, row);
+    if (__builtin_expect(!__any(past), 1)) return;
+    values(buf, row, p);
 #pragma unroll
     for (int b = 0; b < NQ; ++b) {
       p[b][0] = p[b][1] = u32x4{0, 0, 0, 0};
@@ -363,11 +360,7 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void attn_tile_kernel(AttnArgs a, 
     }
   };
 
-  // A step: scores of the next, probabilities of this, output of the last.
-  auto step = [&](int n, const char* kb, const char* vb, int row) {
-    f32x16 next[NQ];
-    scores(kb, row, next);
-    u32x4 q[NQ][2];
+  auto exps = [&](f32x16 (&s)[NQ], u32x4 (&q)[NQ][2]) QMM_INLINE {
 #pragma unroll
     for (int b = 0; b < NQ; ++b) {
 #pragma unroll
@@ -382,45 +375,69 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void attn_tile_kernel(AttnArgs a, 
 #pragma unroll
         for (int e = 0; e < 4; ++e) q[b][u][e] = Op::pack(s[b][8 * u + 2 * e], s[b][8 * u + 2 * e + 1]);
     }
-    values(vb, row);
+  };
+  // Step n: scores of step n + 1 (to `next`), probabilities of this one (s to
+  // q), output of step n - 1 (p, V rows `row` ..), K operands of step n + 2.
+  auto step = [&](Keys& kf, const char* kb, const char* vb, int row, f32x16 (&s)[NQ],
+                  f32x16 (&next)[NQ], const u32x4 (&p)[NQ][2], u32x4 (&q)[NQ][2]) QMM_INLINE {
+    scores(kf, next);
+    exps(s, q);
+    values(vb, row, p);
+    kf = keys(kb, row);
     tops(next);
 #pragma unroll
-    for (int b = 0; b < NQ; ++b) {
-      p[b][0] = q[b][0];
-      p[b][1] = q[b][1];
-      s[b] = next[b];
+    for (int i = 0; i < KS * NQ + 2 * DB * NQ; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a matrix instruction
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // an LDS read
+      __builtin_amdgcn_sched_group_barrier(0x400, 1, 0);   // an exponential
+      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // vector work
     }
-    finish(n + 1, s);
+    // Held here: the compiler would move the exponentials past the branch.
+#pragma unroll
+    for (int b = 0; b < NQ; ++b) asm volatile("" : "+v"(q[b][0]), "+v"(q[b][1]), "+v"(next[b]), "+v"(top[b]), "+v"(l[b]));
   };
 
-  Place at_v, at_k = place_of(0);
-  store_k(0, load_k(at_k));
-  store_v(0, load_v(at_k));
-  at_v = place_of(1);
-  store_k(1, load_k(at_v));
-  at_k = place_of(2);
-  Stage gv = load_v(at_v), gk = load_k(at_k);
-  at_v = at_k;
-  at_k = place_of(3);
+  // K groups -2 and -1 hold steps 0, 1 and 2.
+  int64_t at = rows_of(-2, 0);
+  store_k(-2, load_k(at));
+  store_v(0, load_v(at));
+  store_k(-1, load_k(rows_of(-1, 0)));
+  at = rows_of(0, 1);
+  Stage gk = load_k(at), gv = load_v(at);
   __syncthreads();
-  scores(kbuf(0), 32, s);
-  tops(s);
-  finish(0, s);
+  scores(keys(kbuf(-2), 32), s0);
+  tops(s0);
+  finish(0, s0);
+#pragma unroll
+  for (int b = 0; b < NQ; ++b) {
+    m[b] = top[b] * mul;
+    if (!(m[b] > -INFINITY)) m[b] = -INFINITY;   // none, or a NaN: the sum tells
+    sub[b] = m[b] == -INFINITY ? 0.f : m[b];
+  }
+  exps(s0, p0);
+  scores(keys(kbuf(-1), 0), s1);
+  tops(s1);
+  finish(1, s1);
+  Keys kf = keys(kbuf(-1), 32);
   __syncthreads();
-  const int iters = (steps + 2) / 2;
+  store_k(0, gk);
+  gk = load_k(rows_of(1, 1));
+  at = rows_of(2, 2);
+  const int iters = (steps + 1) / 2;
   for (int t = 0; t < iters; ++t) {
-    store_k(t + 2, gk);
-    store_v(t + 1, gv);
-    gk = load_k(at_k);
-    gv = load_v(at_v);
-    at_v = at_k;
-    at_k = place_of(t + 4);
-    const char *kb = kbuf(t + 1), *vb = vbuf(t);
-    renew(vb, 0);
-    step(2 * t, kb, vb, 0);
-    renew(vb, 32);
-    step(2 * t + 1, kb, vb, 32);
     __syncthreads();
+    store_k(t + 1, gk);
+    store_v(t + 1, gv);
+    gk = load_k(at);
+    gv = load_v(at);
+    at = rows_of(t + 3, t + 3);
+    const char *kb = kbuf(t), *vb = vbuf(t);
+    renew(vb, 0, p0);
+    step(kf, kb, vb, 0, s1, s0, p0, p1);
+    if (CAP || !whole(2 * t + 2)) finish(2 * t + 2, s0);
+    renew(vb, 32, p1);
+    step(kf, kb, vb, 32, s0, s1, p1, p0);
+    if (CAP || !whole(2 * t + 3)) finish(2 * t + 3, s1);
   }
 
   // Values that were left out, for the rows that see them.
@@ -496,7 +513,7 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void attn_tile_kernel(AttnArgs a, 
   __syncthreads();
   if (!last) return;
   if (threadIdx.x == 0) *counter = 0;
-  for (int e = threadIdx.x; e < (row1 - row0) * (DV / 4); e += TILE_THREADS) {
+  for (int e = threadIdx.x; e < (row1 - row0) * (DV / 4); e += THREADS) {
     const int q = e / (DV / 4), col = e % (DV / 4) * 4, r = row0 + q;
     if (col >= c.dim) continue;
     float high = -INFINITY, total = 0.f;
@@ -522,33 +539,33 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void attn_tile_kernel(AttnArgs a, 
   }
 }
 
-template <int DT, int DK, int DV, int NQ>
+template <int DT, int DK, int DV, int WAVES>
 hipError_t launch_tile(const AttnArgs& a, const TilePlan& plan) {
+  constexpr int THREADS = 64 * WAVES;
   const bool cap = a.softcap > 0.f;
   const ScoreScale k = cap ? ScoreScale{a.scale / a.softcap, a.softcap * LOG2E}
                            : ScoreScale{a.scale * LOG2E, 0.f};
   constexpr int bytes = TileLds<DK, DV>::BYTES;
-  const void* fn = cap ? (const void*)attn_tile_kernel<DT, DK, DV, NQ, true>
-                       : (const void*)attn_tile_kernel<DT, DK, DV, NQ, false>;
+  const void* fn = cap ? (const void*)attn_tile_kernel<DT, DK, DV, WAVES, true>
+                       : (const void*)attn_tile_kernel<DT, DK, DV, WAVES, false>;
   const hipError_t e = ensure_dynamic_lds(fn, bytes);
   if (e != hipSuccess) return e;
   const dim3 grid((uint32_t)plan.tiles * plan.splits * a.c.kv_heads);
-  if (cap) attn_tile_kernel<DT, DK, DV, NQ, true><<<grid, TILE_THREADS, bytes, a.stream>>>(a, plan, k);
-  else attn_tile_kernel<DT, DK, DV, NQ, false><<<grid, TILE_THREADS, bytes, a.stream>>>(a, plan, k);
+  if (cap) attn_tile_kernel<DT, DK, DV, WAVES, true><<<grid, THREADS, bytes, a.stream>>>(a, plan, k);
+  else attn_tile_kernel<DT, DK, DV, WAVES, false><<<grid, THREADS, bytes, a.stream>>>(a, plan, k);
   return hipGetLastError();
 }
 
-// Two blocks of 32 rows a wave where their registers fit.
 template <int DT>
 hipError_t launch_tile_type(const AttnArgs& a, const TilePlan& plan) {
   const int d = a.c.dim;
-#define QMM_TILE(DK, DV)                                        \
-  if (d <= DK) return plan.blocks == 2 ? launch_tile<DT, DK, DV, 2>(a, plan) \
-                                       : launch_tile<DT, DK, DV, 1>(a, plan);
+#define QMM_TILE(DK, DV)                                                     \
+  if (d <= DK) return plan.blocks == 2 ? launch_tile<DT, DK, DV, 8>(a, plan) \
+                                       : launch_tile<DT, DK, DV, 4>(a, plan);
   QMM_TILE(64, 64) QMM_TILE(80, 96) QMM_TILE(96, 96) QMM_TILE(128, 128)
 #undef QMM_TILE
-  if (d <= 192) return launch_tile<DT, 192, 192, 1>(a, plan);
-  return launch_tile<DT, 256, 256, 1>(a, plan);
+  if (d <= 192) return launch_tile<DT, 192, 192, 4>(a, plan);
+  return launch_tile<DT, 256, 256, 4>(a, plan);
 }
 
 }  // namespace qmm
