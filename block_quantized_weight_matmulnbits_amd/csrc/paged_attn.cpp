@@ -2,6 +2,12 @@
 // workspace that this takes.
 #include "paged.h"
 
+#ifndef V_FILL
+#define V_FILL 512
+#endif
+#ifndef V_NO8
+#define V_NO8 0
+#endif
 namespace qmm {
 
 namespace {
@@ -37,7 +43,7 @@ RowsPlan plan_rows(int seqs, int max_new, int64_t keys, int group, int kv_heads,
 
 // Workgroups of the tiles kernel that fill the chip, one a compute unit, twice;
 // its smallest part of the keys; the rows of a sequence that it takes.
-constexpr int64_t TILE_FILL = 512, TILE_MIN_CHUNK = 512, TILE_ROWS = 32;
+constexpr int64_t TILE_FILL = V_FILL, TILE_MIN_CHUNK = 512, TILE_ROWS = 32;
 
 // Whole rows are counted where the host knows them: the tokens of the batch.
 TilePlan plan_tile(int seqs, int tokens, int max_new, int64_t keys, int group, int kv_heads, int dim,
@@ -45,7 +51,7 @@ TilePlan plan_tile(int seqs, int tokens, int max_new, int64_t keys, int group, i
   TilePlan p;
   // Two blocks a wave halve what is read from LDS; one where registers end
   // (wide heads) or rows would be left over.
-  p.blocks = dim <= 128 && (int64_t)max_new * group > 128 ? 2 : 1;
+  p.blocks = V_NO8 ? 1 : dim <= 128 && (int64_t)max_new * group > 128 ? 2 : 1;
   const int64_t rows = 128 * p.blocks, whole = ceil_div((int64_t)tokens * group, rows);
   p.tiles = (int)(whole + seqs);
   // A single sequence is taken whatever it has; of several, those with few

@@ -19,6 +19,9 @@
 #include "paged_attn.h"
 #include "qmm_internal.h"
 
+#ifndef V_LEAD
+#define V_LEAD 2
+#endif
 namespace qmm {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -176,8 +179,8 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   }
 
   // Staging.  Group n of V holds the keys of steps 2 n and 2 n + 1, group n of
-  // K those three steps on, 2 n + 3 and 2 n + 4; this wave loads rows 16 wave
-  // .. 16 wave + 15 of each.
+  // K those three steps on, 2 n + 3 and 2 n + 4; this wave loads SR rows of
+  // each, from SR wave on.
   const int32_t* table = c.table + (int64_t)seq * c.table_stride;
   const int chunks = c.dim / 8;
   auto v_key = [&](int n) { return begin + 64 * n + SR * wave; };
@@ -258,12 +261,10 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
         *(u32x4*)(vbuf(n) + (SR * wave + srow[i]) * L::VROW + sch[i] * 16) = st.x[i];
   };
 
-  struct Keys {
-    u32x4 x[KS];
-  };
+  u32x4 kf[KS];                        // the next step's K operands
   f32x16 o[NQ][DB], s0[NQ], s1[NQ];   // scores of even and odd steps
   u32x4 p0[NQ][2], p1[NQ][2];         // probabilities of even and odd steps
-  float m[NQ], sub[NQ], l[NQ], top[NQ];
+  float m[NQ], mo[NQ], sub[NQ], l[NQ], top[NQ];
 #pragma unroll
   for (int b = 0; b < NQ; ++b) {
     m[b] = -INFINITY;
@@ -275,38 +276,28 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
       for (int i = 0; i < 16; ++i) o[b][d][i] = 0.f;
   }
 
-  // K operands of a step from rows `row` .. of a buffer, and its scores.
-  auto keys = [&](const char* buf, int row) QMM_INLINE {
-    const char* at = buf + (row + l31) * L::KROW + half * 16;
-    Keys r;
-#pragma unroll
-    for (int k = 0; k < KS; ++k) r.x[k] = *(const u32x4*)(at + k * 32);
-    return r;
+  // One operand of a step's products from rows `row` .. of a buffer: K for 16
+  // columns of the head, V for 16 keys u and 32 columns d.
+  auto key = [&](const char* buf, int row, int k) QMM_INLINE {
+    return *(const u32x4*)(buf + (row + l31) * L::KROW + half * 16 + k * 32);
   };
-  auto scores = [&](const Keys& kf, f32x16 (&out)[NQ]) QMM_INLINE {
+  auto value = [&](const char* buf, int row, int u, int d) QMM_INLINE {
+    const char* at = buf + (row + 4 * half + l15 / 4) * L::VROW + (lane & 16) * 2 + (l15 % 4) * 8 +
+                     16 * u * L::VROW + d * 64;
+    const s16x4 x0 = lds_read_tr(at), x1 = lds_read_tr(at + 8 * L::VROW);
+    return __builtin_bit_cast(u32x4, __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto zero = [&](f32x16& x) QMM_INLINE {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = 0.f;
+  };
+  auto scores = [&](const char* buf, int row, f32x16 (&out)[NQ]) QMM_INLINE {
+#pragma unroll
+    for (int b = 0; b < NQ; ++b) zero(out[b]);
 #pragma unroll
     for (int k = 0; k < KS; ++k)
 #pragma unroll
-      for (int b = 0; b < NQ; ++b) {
-        if (k == 0)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) out[b][i] = 0.f;
-        out[b] = Mfma32<DT>::run(kf.x[k], qf[b][k], out[b]);
-      }
-  };
-  auto values = [&](const char* buf, int row, const u32x4 (&p)[NQ][2]) QMM_INLINE {
-    const char* at = buf + (row + 4 * half + l15 / 4) * L::VROW + (lane & 16) * 2 + (l15 % 4) * 8;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        const s16x4 x0 = lds_read_tr(at + 16 * u * L::VROW + d * 64);
-        const s16x4 x1 = lds_read_tr(at + (16 * u + 8) * L::VROW + d * 64);
-        const auto v = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-        for (int b = 0; b < NQ; ++b)
-          o[b][d] = Mfma32<DT>::run(__builtin_bit_cast(u32x4, v), p[b][u], o[b][d]);
-      }
+      for (int b = 0; b < NQ; ++b) out[b] = Mfma32<DT>::run(key(buf, row, k), qf[b][k], out[b]);
   };
   auto tops = [&](const f32x16 (&x)[NQ]) QMM_INLINE {
 #pragma unroll
@@ -336,65 +327,103 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
       }
     tops(x);
   };
-  // A new reference maximum where a row passed the old one by the slack; what
-  // is still to be added of the last step is added first.
-  auto renew = [&](const char* buf, int row, u32x4 (&p)[NQ][2]) QMM_INLINE {
+  // A new reference maximum where a row passed the old one by the slack.  It is
+  // a whole number, so that the factor that sums, outputs and probabilities
+  // not yet multiplied are taken down by is a power of two and rounds none of
+  // them.  The output follows (mo) only where `all` is set, at one place of
+  // the loop: until then it meets probabilities of its own reference alone.
+  auto renew = [&](bool all, u32x4 (&p)[NQ][2]) QMM_INLINE {
     bool past = false;
 #pragma unroll
     for (int b = 0; b < NQ; ++b) {
       top[b] *= mul;
-      past |= top[b] > m[b] + TILE_SLACK;
+      past |= top[b] > m[b] + TILE_SLACK || (all && mo[b] != m[b]);
     }
     if (__builtin_expect(!__any(past), 1)) return;
-    values(buf, row, p);
 #pragma unroll
     for (int b = 0; b < NQ; ++b) {
-      p[b][0] = p[b][1] = u32x4{0, 0, 0, 0};
       const float was = m[b];
-      m[b] = fmaxf(was, top[b]);
+      m[b] = ceilf(fmaxf(was, top[b]));
       sub[b] = m[b] == -INFINITY ? 0.f : m[b];
       const float back = exp2_fast(was - sub[b]);
       l[b] *= back;
-#pragma unroll
-      for (int d = 0; d < DB; ++d) o[b][d] *= back;
-    }
-  };
-
-  auto exps = [&](f32x16 (&s)[NQ], u32x4 (&q)[NQ][2]) QMM_INLINE {
-#pragma unroll
-    for (int b = 0; b < NQ; ++b) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[b][i] = exp2_fast(__builtin_fmaf(s[b][i], mul, -sub[b]));
-        l[b] += s[b][i];
-      }
-      // Rounded to the values' type: the matrix cores take no other pair.
-      // The sum above keeps them in 32 bits.
+      if (!all) continue;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) q[b][u][e] = Op::pack(s[b][8 * u + 2 * e], s[b][8 * u + 2 * e + 1]);
+        for (int e = 0; e < 4; ++e)
+          p[b][u][e] = Op::pack(bits16_to_f32<DT>((uint16_t)p[b][u][e]) * back,
+                                bits16_to_f32<DT>((uint16_t)(p[b][u][e] >> 16)) * back);
+      const float down = exp2_fast(mo[b] - sub[b]);
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[b][d] *= down;
+      mo[b] = m[b];
+    }
+  };
+  // One score a lane, s[b][i], to its probability.  Pairs are rounded to the
+  // values' type for the product: the matrix cores take no other pair.  The
+  // sum keeps them in 32 bits.
+  auto prob = [&](f32x16 (&s)[NQ], u32x4 (&q)[NQ][2], int i) QMM_INLINE {
+#pragma unroll
+    for (int b = 0; b < NQ; ++b) {
+      s[b][i] = exp2_fast(__builtin_fmaf(s[b][i], mul, -sub[b]));
+      l[b] += s[b][i];
+      if (i & 1) q[b][i / 8][i % 8 / 2] = Op::pack(s[b][i - 1], s[b][i]);
     }
   };
   // Step n: scores of step n + 1 (to `next`), probabilities of this one (s to
-  // q), output of step n - 1 (p, V rows `row` ..), K operands of step n + 2.
-  auto step = [&](Keys& kf, const char* kb, const char* vb, int row, f32x16 (&s)[NQ],
-                  f32x16 (&next)[NQ], const u32x4 (&p)[NQ][2], u32x4 (&q)[NQ][2]) QMM_INLINE {
-    scores(kf, next);
-    exps(s, q);
-    values(vb, row, p);
-    kf = keys(kb, row);
-    tops(next);
+  // q), output of step n - 1 (p).  The K operands were read during the step
+  // before; as they are used, V's take their registers, and as those are used
+  // the next step's K.  The order is the one written: a matrix instruction,
+  // then the vector work that hides behind it.
+  auto step = [&](const char* kb, const char* vb, int row, f32x16 (&s)[NQ], f32x16 (&next)[NQ],
+                  const u32x4 (&p)[NQ][2], u32x4 (&q)[NQ][2]) QMM_INLINE {
+    constexpr int VS = 2 * DB, SLOTS = KS + VS, LEAD = V_LEAD;
+    u32x4 vf[VS];
+    float t[NQ];
 #pragma unroll
-    for (int i = 0; i < KS * NQ + 2 * DB * NQ; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a matrix instruction
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // an LDS read
-      __builtin_amdgcn_sched_group_barrier(0x400, 1, 0);   // an exponential
-      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // vector work
+    for (int b = 0; b < NQ; ++b) zero(next[b]);
+#pragma unroll
+    for (int v = 0; v < LEAD && v < VS; ++v) vf[v] = value(vb, row, v / DB, v % DB);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) {
+      if (j < KS) {
+#pragma unroll
+        for (int b = 0; b < NQ; ++b) next[b] = Mfma32<DT>::run(kf[j], qf[b][j], next[b]);
+      } else {
+        const int v = j - KS;
+#pragma unroll
+        for (int b = 0; b < NQ; ++b) o[b][v % DB] = Mfma32<DT>::run(vf[v], p[b][v / DB], o[b][v % DB]);
+      }
+      if (j + LEAD < VS) vf[j + LEAD] = value(vb, row, (j + LEAD) / DB, (j + LEAD) % DB);
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        if (j == KS + (k + LEAD < VS ? k + LEAD : k + LEAD - VS)) kf[k] = key(kb, row, k);
+#pragma unroll
+      for (int i = 16 * j / SLOTS; i < 16 * (j + 1) / SLOTS; ++i) prob(s, q, i);
+      // The maximum of the next scores, in the last three slots.
+#pragma unroll
+      for (int b = 0; b < NQ; ++b) {
+        if (j == SLOTS - 3) {
+          t[b] = fmaxf(fmaxf(next[b][0], next[b][1]), next[b][2]);
+          t[b] = fmaxf(fmaxf(t[b], next[b][3]), next[b][4]);
+          t[b] = fmaxf(fmaxf(t[b], next[b][5]), next[b][6]);
+        } else if (j == SLOTS - 2) {
+          t[b] = fmaxf(fmaxf(t[b], next[b][7]), next[b][8]);
+          t[b] = fmaxf(fmaxf(t[b], next[b][9]), next[b][10]);
+          t[b] = fmaxf(fmaxf(t[b], next[b][11]), next[b][12]);
+        } else if (j == SLOTS - 1) {
+          t[b] = fmaxf(fmaxf(t[b], next[b][13]), next[b][14]);
+          top[b] = pair_max(fmaxf(t[b], next[b][15]));
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
     // Held here: the compiler would move the exponentials past the branch.
 #pragma unroll
-    for (int b = 0; b < NQ; ++b) asm volatile("" : "+v"(q[b][0]), "+v"(q[b][1]), "+v"(next[b]), "+v"(top[b]), "+v"(l[b]));
+    for (int b = 0; b < NQ; ++b)
+      asm volatile("" : "+v"(q[b][0]), "+v"(q[b][1]), "+v"(l[b]));
   };
 
   // K groups -2 and -1 hold steps 0, 1 and 2.
@@ -405,20 +434,23 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   at = rows_of(0, 1);
   Stage gk = load_k(at), gv = load_v(at);
   __syncthreads();
-  scores(keys(kbuf(-2), 32), s0);
+  scores(kbuf(-2), 32, s0);
   tops(s0);
   finish(0, s0);
 #pragma unroll
   for (int b = 0; b < NQ; ++b) {
-    m[b] = top[b] * mul;
-    if (!(m[b] > -INFINITY)) m[b] = -INFINITY;   // none, or a NaN: the sum tells
+    // A NaN is left to the sum.
+    m[b] = ceilf(fmaxf(top[b] * mul, -INFINITY));
+    mo[b] = m[b];
     sub[b] = m[b] == -INFINITY ? 0.f : m[b];
   }
-  exps(s0, p0);
-  scores(keys(kbuf(-1), 0), s1);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) prob(s0, p0, i);
+  scores(kbuf(-1), 0, s1);
   tops(s1);
   finish(1, s1);
-  Keys kf = keys(kbuf(-1), 32);
+#pragma unroll
+  for (int k = 0; k < KS; ++k) kf[k] = key(kbuf(-1), 32, k);
   __syncthreads();
   store_k(0, gk);
   gk = load_k(rows_of(1, 1));
@@ -432,12 +464,20 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
     gv = load_v(at);
     at = rows_of(t + 3, t + 3);
     const char *kb = kbuf(t), *vb = vbuf(t);
-    renew(vb, 0, p0);
-    step(kf, kb, vb, 0, s1, s0, p0, p1);
+    renew(true, p0);
+    step(kb, vb, 0, s1, s0, p0, p1);
     if (CAP || !whole(2 * t + 2)) finish(2 * t + 2, s0);
-    renew(vb, 32, p1);
-    step(kf, kb, vb, 32, s0, s1, p1, p0);
+    renew(false, p1);
+    step(kb, vb, 32, s0, s1, p1, p0);
     if (CAP || !whole(2 * t + 3)) finish(2 * t + 3, s1);
+  }
+
+  // The output may still be a reference behind the sum.
+#pragma unroll
+  for (int b = 0; b < NQ; ++b) {
+    const float down = exp2_fast(mo[b] - sub[b]);
+#pragma unroll
+    for (int d = 0; d < DB; ++d) o[b][d] *= down;
   }
 
   // Values that were left out, for the rows that see them.
