@@ -19,9 +19,6 @@
 #include "paged_attn.h"
 #include "qmm_internal.h"
 
-#ifndef V_LEAD
-#define V_LEAD 2
-#endif
 namespace qmm {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -182,83 +179,110 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   // K those three steps on, 2 n + 3 and 2 n + 4; this wave loads SR rows of
   // each, from SR wave on.
   const int32_t* table = c.table + (int64_t)seq * c.table_stride;
+  //
+  // A lane moves 16 bytes of IT rows of each.  Lanes past the rows, or past the
+  // head's own width, repeat the first row or piece, so that nothing in the
+  // loop is conditional.
   const int chunks = c.dim / 8;
-  auto v_key = [&](int n) { return begin + 64 * n + SR * wave; };
-  auto k_key = [&](int n) { return v_key(n) + 96; };
-  int srow[IT], sch[IT];
+  int srow[IT], kw[IT], vw[IT];
+  uint32_t piece[IT];
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    srow[i] = (i * 64 + lane) / CH;
-    sch[i] = (i * 64 + lane) % CH;
+    const int x = i * 64 + lane;
+    srow[i] = IT * 64 == SR * CH || x < SR * CH ? x / CH : 0;
+    const int ch = x < SR * CH && x % CH < chunks ? x % CH : 0;
+    piece[i] = ch * 16;
+    kw[i] = (SR * wave + srow[i]) * L::KROW + ch * 16;
+    vw[i] = 2 * L::KBUF + (SR * wave + srow[i]) * L::VROW + ch * 16;
   }
-  // Where the rows of K group nk and V group nv lie: lanes 0 .. 15 look the
-  // first up, lanes 16 .. 31 the second, a row each; the loads take them from
-  // there.  Keys outside the sequence read its first or last one.
-  auto rows_of = [&](int nk, int nv) QMM_INLINE {
-    const int j0 = (lane & 16) ? v_key(nv) : k_key(nk), top = sq.len - 1;
-    int j = j0 + l15, at = 0, page = 0;
-    j = j > top ? top : j;
-    if (sq.len > 0) page = page_of(c, table, j < 0 ? 0 : j, at);
-    const int64_t off = (lane & 16) ? page * c.v_page + kvh * c.v_head + at * c.v_token
-                                    : page * c.k_page + kvh * c.k_head + at * c.k_token;
-    return off * 2;
+  // Every row's place in the cache is looked up by one lane, K's and V's, and
+  // handed to those that load it: where 16 lanes load a row, it is one of
+  // them, and the address comes by a broadcast among 16.
+  constexpr bool BY16 = CH == 16;
+  const bool isv = BY16 ? (l15 / IT) & 1 : (lane & 16) != 0;
+  const int key0 = begin + SR * wave + (BY16 ? 4 * (l15 % IT) + (lane >> 4) : l15 % SR) + (isv ? 0 : 96);
+  const uint32_t page_bytes = (uint32_t)(isv ? c.v_page : c.k_page) * 2u;
+  const uint32_t token_bytes = (uint32_t)(isv ? c.v_token : c.k_token) * 2u;
+  const uint64_t head = (uint64_t)(isv ? c.v : c.k) + (uint64_t)(kvh * (isv ? c.v_head : c.k_head) * 2);
+  int page, at;   // of the lane's row in the groups that are looked up next
+  // Keys outside the sequence read its first or last one.
+  auto look_up = [&](int n) QMM_INLINE {
+    int j = key0 + 64 * n;
+    j = j > sq.len - 1 ? sq.len - 1 : j;
+    j = j < 0 ? 0 : j;
+    const int col = (int)div_by((uint32_t)j, c.by_page);
+    at = j - col * c.page;
+    page = table[col];
+  };
+  auto row_address = [&]() QMM_INLINE {
+    const int p = page < 0 ? 0 : page >= c.pages ? c.pages - 1 : page;
+    return head + (uint64_t)(uint32_t)p * page_bytes + (uint64_t)(uint32_t)at * token_bytes;
+  };
+  auto bring = [&](uint64_t rows, int i, int v) QMM_INLINE {   // the address of load i of K or V
+    uint32_t x, y;
+    if constexpr (BY16) {
+      constexpr int BCAST = 0x150;   // row_newbcast
+      const int lo32 = (int)(uint32_t)rows, hi32 = (int)(uint32_t)(rows >> 32);
+      if (v * IT + i == 0) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 0, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 0, 0xF, 0xF, true); }
+      else if (v * IT + i == 1) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 1, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 1, 0xF, 0xF, true); }
+      else if (v * IT + i == 2) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 2, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 2, 0xF, 0xF, true); }
+      else if (v * IT + i == 3) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 3, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 3, 0xF, 0xF, true); }
+      else if (v * IT + i == 4) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 4, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 4, 0xF, 0xF, true); }
+      else if (v * IT + i == 5) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 5, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 5, 0xF, 0xF, true); }
+      else if (v * IT + i == 6) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 6, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 6, 0xF, 0xF, true); }
+      else { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 7, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 7, 0xF, 0xF, true); }
+    } else {
+      const int who = (16 * v + srow[i]) * 4;
+      x = __builtin_amdgcn_ds_bpermute(who, (int)(uint32_t)rows);
+      y = __builtin_amdgcn_ds_bpermute(who, (int)(uint32_t)(rows >> 32));
+    }
+    return ((uint64_t)y << 32 | x) + piece[i];
   };
   struct Stage {
     u32x4 x[IT];
   };
-  auto load = [&](const char* base, int64_t rows, int from) QMM_INLINE {
-    Stage st;
+  auto load = [&](uint64_t rows, int v, Stage& st) QMM_INLINE {
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-      const int who = (from + (IT * 64 == SR * CH ? srow[i] : srow[i] % SR)) * 4;
-      const uint32_t x = __builtin_amdgcn_ds_bpermute(who, (int)(uint32_t)rows);
-      const uint32_t y = __builtin_amdgcn_ds_bpermute(who, (int)(uint32_t)(rows >> 32));
-      const char* at = base + (((uint64_t)y << 32) | x) + sch[i] * 16;
-      st.x[i] = u32x4{0, 0, 0, 0};
-      if (sch[i] < chunks) st.x[i] = *(const u32x4*)at;
-    }
-    return st;
+    for (int i = 0; i < IT; ++i) st.x[i] = *(const __attribute__((address_space(1))) u32x4*)bring(rows, i, v);
   };
-  auto load_k = [&](int64_t rows) QMM_INLINE { return load(c.k, rows, 0); };
-  auto load_v = [&](int64_t rows) QMM_INLINE { return load(c.v, rows, 16); };
   auto kbuf = [&](int n) { return lds + (n & 1) * L::KBUF; };
   auto vbuf = [&](int n) { return lds + 2 * L::KBUF + (n & 1) * L::VBUF; };
   auto store_k = [&](int n, const Stage& st) QMM_INLINE {
 #pragma unroll
-    for (int i = 0; i < IT; ++i)
-      if (IT * 64 == SR * CH || srow[i] < SR)
-        *(u32x4*)(kbuf(n) + (SR * wave + srow[i]) * L::KROW + sch[i] * 16) = st.x[i];
+    for (int i = 0; i < IT; ++i) *(u32x4*)(lds + (n & 1) * L::KBUF + kw[i]) = st.x[i];
+  };
+  auto store_v = [&](int n, const Stage& st) QMM_INLINE {
+#pragma unroll
+    for (int i = 0; i < IT; ++i) *(u32x4*)(lds + (n & 1) * L::VBUF + vw[i]) = st.x[i];
   };
   // Keys that not every row of the workgroup sees: a value that is not finite
-  // would make NaN of a probability of 0.  It goes in as 0, and is added at
-  // the end to the rows that see it.
-  const int safe0 = a.window ? clip(pos_of(row1 - 1) - a.window + 1) : begin;
-  const int safe1 = a.causal ? clip(pos_of(row0) + 1) : end;
-  auto store_v = [&](int n, Stage st) QMM_INLINE {
-    const int j0 = v_key(n);
-    if (j0 < max(safe0, begin) || j0 + SR > min(safe1, end)) {
-      bool any = false;
+  // would make NaN of a probability of 0.  It is replaced by 0 (as are keys
+  // past the end), and added at the end to the rows that see it.
+  const int safe0 = a.window ? max(begin, clip(pos_of(row1 - 1) - a.window + 1)) : begin;
+  const int safe1 = a.causal ? min(end, clip(pos_of(row0) + 1)) : end;
+  auto mend_v = [&](int n) QMM_INLINE {
+    const int j0 = begin + 64 * n + SR * wave;
+    if (j0 >= safe0 && j0 + SR <= safe1) return;
+    bool any = false;
 #pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const int j = j0 + srow[i];
-        const bool in = j >= begin && j < end, safe = in && j >= safe0 && j < safe1;
+    for (int i = 0; i < IT; ++i) {
+      char* to = lds + (n & 1) * L::VBUF + vw[i];
+      u32x4 x = *(const u32x4*)to;
+      const int j = j0 + srow[i];
+      const bool in = j >= begin && j < end, safe = j >= safe0 && j < safe1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          constexpr uint32_t E = DT == DT_BF16 ? 0x7F80u : 0x7C00u;
-          uint32_t x = in ? st.x[i][e] : 0u;
-          const bool o0 = (x & E) == E, o1 = ((x >> 16) & E) == E;
-          if (o0 && !safe) x &= 0xFFFF0000u;
-          if (o1 && !safe) x &= 0x0000FFFFu;
-          any |= !safe && (o0 || o1);
-          st.x[i][e] = x;
-        }
+      for (int e = 0; e < 4; ++e) {
+        constexpr uint32_t E = DT == DT_BF16 ? 0x7F80u : 0x7C00u;
+        uint32_t y = in ? x[e] : 0u;
+        const bool o0 = !safe && (y & E) == E, o1 = !safe && ((y >> 16) & E) == E;
+        if (o0) y &= 0xFFFF0000u;
+        if (o1) y &= 0x0000FFFFu;
+        any |= o0 || o1;
+        x[e] = y;
       }
-      if (__any(any)) odd = 1;
+      *(u32x4*)to = x;
     }
-#pragma unroll
-    for (int i = 0; i < IT; ++i)
-      if (IT * 64 == SR * CH || srow[i] < SR)
-        *(u32x4*)(vbuf(n) + (SR * wave + srow[i]) * L::VROW + sch[i] * 16) = st.x[i];
+    if (__any(any)) odd = 1;
   };
 
   u32x4 kf[KS];                        // the next step's K operands
@@ -376,11 +400,16 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   // before; as they are used, V's take their registers, and as those are used
   // the next step's K.  The order is the one written: a matrix instruction,
   // then the vector work that hides behind it.
-  auto step = [&](const char* kb, const char* vb, int row, f32x16 (&s)[NQ], f32x16 (&next)[NQ],
+  // A step with `stage` also moves the groups: those in registers (t + 1) to
+  // LDS, the next ones' loads and the look-up of the ones after.
+  Stage gk, gv;
+  auto step = [&](bool stage, int t, int row, f32x16 (&s)[NQ], f32x16 (&next)[NQ],
                   const u32x4 (&p)[NQ][2], u32x4 (&q)[NQ][2]) QMM_INLINE {
-    constexpr int VS = 2 * DB, SLOTS = KS + VS, LEAD = V_LEAD;
+    constexpr int VS = 2 * DB, SLOTS = KS + VS, LEAD = 2;
+    const char *kb = kbuf(t), *vb = vbuf(t);
+    uint64_t rows = 0;
     u32x4 vf[VS];
-    float t[NQ];
+    float high[NQ];
 #pragma unroll
     for (int b = 0; b < NQ; ++b) zero(next[b]);
 #pragma unroll
@@ -402,20 +431,28 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
         if (j == KS + (k + LEAD < VS ? k + LEAD : k + LEAD - VS)) kf[k] = key(kb, row, k);
 #pragma unroll
       for (int i = 16 * j / SLOTS; i < 16 * (j + 1) / SLOTS; ++i) prob(s, q, i);
+      if (stage) {
+        if (j == SLOTS / 16) rows = row_address();
+        if (j == SLOTS * 4 / 16) store_k(t + 1, gk);
+        if (j == SLOTS * 5 / 16) store_v(t + 1, gv);
+        if (j == SLOTS * 6 / 16) look_up(t + 3);
+        if (j == SLOTS * 8 / 16) load(rows, 0, gk);
+        if (j == SLOTS * 10 / 16) load(rows, 1, gv);
+      }
       // The maximum of the next scores, in the last three slots.
 #pragma unroll
       for (int b = 0; b < NQ; ++b) {
         if (j == SLOTS - 3) {
-          t[b] = fmaxf(fmaxf(next[b][0], next[b][1]), next[b][2]);
-          t[b] = fmaxf(fmaxf(t[b], next[b][3]), next[b][4]);
-          t[b] = fmaxf(fmaxf(t[b], next[b][5]), next[b][6]);
+          high[b] = fmaxf(fmaxf(next[b][0], next[b][1]), next[b][2]);
+          high[b] = fmaxf(fmaxf(high[b], next[b][3]), next[b][4]);
+          high[b] = fmaxf(fmaxf(high[b], next[b][5]), next[b][6]);
         } else if (j == SLOTS - 2) {
-          t[b] = fmaxf(fmaxf(t[b], next[b][7]), next[b][8]);
-          t[b] = fmaxf(fmaxf(t[b], next[b][9]), next[b][10]);
-          t[b] = fmaxf(fmaxf(t[b], next[b][11]), next[b][12]);
+          high[b] = fmaxf(fmaxf(high[b], next[b][7]), next[b][8]);
+          high[b] = fmaxf(fmaxf(high[b], next[b][9]), next[b][10]);
+          high[b] = fmaxf(fmaxf(high[b], next[b][11]), next[b][12]);
         } else if (j == SLOTS - 1) {
-          t[b] = fmaxf(fmaxf(t[b], next[b][13]), next[b][14]);
-          top[b] = pair_max(fmaxf(t[b], next[b][15]));
+          high[b] = fmaxf(fmaxf(high[b], next[b][13]), next[b][14]);
+          top[b] = pair_max(fmaxf(high[b], next[b][15]));
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -426,13 +463,27 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
       asm volatile("" : "+v"(q[b][0]), "+v"(q[b][1]), "+v"(l[b]));
   };
 
-  // K groups -2 and -1 hold steps 0, 1 and 2.
-  int64_t at = rows_of(-2, 0);
-  store_k(-2, load_k(at));
-  store_v(0, load_v(at));
-  store_k(-1, load_k(rows_of(-1, 0)));
-  at = rows_of(0, 1);
-  Stage gk = load_k(at), gv = load_v(at);
+  // Columns that pad K's rows are not loaded.
+  for (int x = threadIdx.x; x < 128 * (CH - chunks); x += THREADS)
+    *(u32x4*)(lds + x % 128 / 64 * L::KBUF + x % 64 * L::KROW + (chunks + x / 128) * 16) =
+        u32x4{0, 0, 0, 0};
+  // K groups -2 and -1 hold steps 0, 1 and 2; V group 0 belongs to the first
+  // look-up of its own.
+  if (sq.len > 0) {
+    look_up(-2);
+    load(row_address(), 0, gk);
+    store_k(-2, gk);
+    look_up(-1);
+    load(row_address(), 0, gk);
+    store_k(-1, gk);
+    look_up(0);
+    const uint64_t rows = row_address();
+    load(rows, 0, gk);
+    load(rows, 1, gv);
+    store_v(0, gv);
+    mend_v(0);
+    look_up(1);
+  }
   __syncthreads();
   scores(kbuf(-2), 32, s0);
   tops(s0);
@@ -453,22 +504,21 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   for (int k = 0; k < KS; ++k) kf[k] = key(kbuf(-1), 32, k);
   __syncthreads();
   store_k(0, gk);
-  gk = load_k(rows_of(1, 1));
-  at = rows_of(2, 2);
+  if (sq.len > 0) {
+    const uint64_t rows = row_address();
+    look_up(2);
+    load(rows, 0, gk);
+    load(rows, 1, gv);
+  }
   const int iters = (steps + 1) / 2;
   for (int t = 0; t < iters; ++t) {
     __syncthreads();
-    store_k(t + 1, gk);
-    store_v(t + 1, gv);
-    gk = load_k(at);
-    gv = load_v(at);
-    at = rows_of(t + 3, t + 3);
-    const char *kb = kbuf(t), *vb = vbuf(t);
     renew(true, p0);
-    step(kb, vb, 0, s1, s0, p0, p1);
+    step(true, t, 0, s1, s0, p0, p1);
+    mend_v(t + 1);
     if (CAP || !whole(2 * t + 2)) finish(2 * t + 2, s0);
     renew(false, p1);
-    step(kb, vb, 32, s0, s1, p1, p0);
+    step(false, t, 32, s0, s1, p1, p0);
     if (CAP || !whole(2 * t + 3)) finish(2 * t + 3, s1);
   }
 
