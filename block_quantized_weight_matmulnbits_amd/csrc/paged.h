@@ -70,17 +70,24 @@ struct AttnArgs {
   int q_heads = 0, group = 0, causal = 1, window = 0, dtype = 0;
   int q_wide = 0, out_wide = 0;      // 16-byte rows of q; four elements at once of out
   FastDiv by_group;
-  char* workspace = nullptr;
+  // Parts of the keys, where there is more than one (attn_parts in
+  // paged_attn.cpp): by row (token x head), the number of its parts; by part
+  // and row, maximum (log2), sum, and the output before its division.
+  int32_t* part_count = nullptr;
+  float* part_stats = nullptr;       // [splits, rows, 2]
+  float* part_out = nullptr;         // [splits, rows, padded dim]
   hipStream_t stream = nullptr;
 };
 size_t attn_workspace_bytes(int seqs, int tokens, int max_new, int max_len, int q_heads,
                             int kv_heads, int dim);
-hipError_t launch_paged_attention(const AttnArgs& a);
+hipError_t launch_paged_attention(AttnArgs a, char* workspace);
+// Joins the parts of every row that has several (paged_attn_join.hip).
+hipError_t launch_join(const AttnArgs& a, int padded_dim, int splits);
 
 // A few rows of queries a workgroup (paged_attn_rows.h): keys are split over
 // `splits` workgroups in runs of `chunk`, rows over `row_tiles`.
 struct RowsPlan {
-  int splits, chunk, row_tiles;
+  int splits, chunk, row_tiles, note;   // note: leave each row's number of parts
 };
 // One instance file a type; blocks of 16 rows a tile, 1 or 2.  Sequences with
 // more than skip_above new tokens are left to another kernel.
@@ -92,7 +99,7 @@ hipError_t launch_rows_bf16(const AttnArgs& a, const RowsPlan& plan, int blocks,
 // 256 rows (blocks 1 or 2), at most `tiles` tiles over all sequences with
 // more than skip_upto new tokens.
 struct TilePlan {
-  int splits, chunk, tiles, blocks, skip_upto;
+  int splits, chunk, tiles, blocks, skip_upto, note;
 };
 hipError_t launch_tile_f16(const AttnArgs& a, const TilePlan& plan);
 hipError_t launch_tile_bf16(const AttnArgs& a, const TilePlan& plan);

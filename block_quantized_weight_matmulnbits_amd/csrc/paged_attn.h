@@ -23,9 +23,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 
-// Counters of the joins, at the front of the workspace: zero between calls.
-constexpr int ATTN_COUNTERS = 16384;
-
 // What stands in for keys past a sequence's end and for the columns that pad
 // a head to the kernel's width: a row of zeros.
 __device__ __attribute__((aligned(256))) const uint32_t zero_row[256] = {};

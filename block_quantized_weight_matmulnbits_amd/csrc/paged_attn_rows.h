@@ -9,8 +9,7 @@
 // running maximum, sum and output, loads K straight into matrix-core operands
 // (16 bytes a lane) and V through its own LDS (16 bytes a lane, asynchronous),
 // from where 16-bit values are read back transposed.  The waves join through
-// LDS, the workgroups through the workspace: the last one to arrive sums the
-// parts in the order of the keys, so a result does not depend on which that is.
+// LDS; parts of the keys are left in the workspace for the join.
 #pragma once
 
 #include "paged_attn.h"
@@ -47,7 +46,6 @@ __global__ __launch_bounds__(ROWS_THREADS, (RowsWaves<DT, DP, NB>::N)) void attn
   constexpr int OSTRIDE = DP + 4;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   __shared__ float2 wave_ml[ROWS_WAVES][16];
-  __shared__ int last;
 
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l15 = lane & 15, g = lane >> 4;
@@ -58,7 +56,6 @@ __global__ __launch_bounds__(ROWS_THREADS, (RowsWaves<DT, DP, NB>::N)) void attn
   const int kvh = id % c.kv_heads;
   id /= c.kv_heads;
   const int tile = id % plan.row_tiles, seq = id / plan.row_tiles;
-  const int tile_id = (seq * plan.row_tiles + tile) * c.kv_heads + kvh;
 
   const Seq sq = seq_of(c, seq);
   const int rows = sq.n * a.group, row0 = tile * 16 * NB;
@@ -333,15 +330,6 @@ __global__ __launch_bounds__(ROWS_THREADS, (RowsWaves<DT, DP, NB>::N)) void attn
 
   // Join the waves, one block of 16 rows at a time, and write or park it.
   float* ol = (float*)lds;
-  char* ws = a.workspace;
-  float2* part_ml = nullptr;
-  float* part_o = nullptr;
-  if (active > 1) {
-    const int64_t all = (int64_t)c.seqs * plan.row_tiles * c.kv_heads * plan.splits;
-    const int64_t mine = (int64_t)tile_id * plan.splits;
-    part_ml = (float2*)(ws + ATTN_COUNTERS * 4) + mine * 16 * NB;
-    part_o = (float*)(ws + ATTN_COUNTERS * 4 + all * 16 * NB * 8) + mine * 16 * NB * DP;
-  }
   auto emit = [&](int r, int d, f32x4 x, float inv) {
     const int i = (int)div_by(r, a.by_group), h = r - i * a.group;
     T* to = (T*)a.out + (int64_t)(sq.t0 + i) * a.out_token +
@@ -383,43 +371,20 @@ __global__ __launch_bounds__(ROWS_THREADS, (RowsWaves<DT, DP, NB>::N)) void attn
         total += f * wave_ml[w][q].y;
         x += f * *(const f32x4*)(ol + (w * 16 + q) * OSTRIDE + d);
       }
-      if (active > 1) {
-        const int64_t row = (int64_t)split * 16 * NB + 16 * b + q;
-        *(f32x4*)(part_o + row * DP + d) = x;
-        if (d == 0) part_ml[row] = make_float2(top, total);
-      } else {
-        emit(r, d, x, total == 0.f ? 0.f : 1.f / total);
-        if (d == 0) emit_lse(r, top, total);
+      if (plan.note) {
+        const int i = (int)div_by(r, a.by_group);
+        const int64_t row = (int64_t)(sq.t0 + i) * a.q_heads + kvh * a.group + r - i * a.group;
+        const int64_t at = (int64_t)split * c.tokens * a.q_heads + row;
+        if (split == 0 && d == 0) a.part_count[row] = active;
+        if (active > 1) {
+          *(f32x4*)(a.part_out + at * DP + d) = x;
+          if (d == 0) ((float2*)a.part_stats)[at] = make_float2(top, total);
+          continue;
+        }
       }
+      emit(r, d, x, total == 0.f ? 0.f : 1.f / total);
+      if (d == 0) emit_lse(r, top, total);
     }
-  }
-  if (active == 1) return;
-
-  uint32_t* counter = (uint32_t*)ws + tile_id;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    last = atomicAdd(counter, 1u) == (uint32_t)(active - 1);
-    __threadfence();
-  }
-  __syncthreads();
-  if (!last) return;
-  if (threadIdx.x == 0) *counter = 0;
-  for (int e = threadIdx.x; e < (row1 - row0) * (DP / 4); e += ROWS_THREADS) {
-    const int q = e / (DP / 4), d = e % (DP / 4) * 4;
-    if (d >= c.dim) continue;
-    float top = -INFINITY, total = 0.f;
-    for (int k = 0; k < active; ++k) top = fmaxf(top, part_ml[k * 16 * NB + q].x);
-    const float ref = top == -INFINITY ? 0.f : top;
-    f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < active; ++k) {
-      const float2 ml = part_ml[k * 16 * NB + q];
-      const float f = exp2_fast(ml.x - ref);
-      total += f * ml.y;
-      x += f * *(const f32x4*)(part_o + ((int64_t)k * 16 * NB + q) * DP + d);
-    }
-    emit(row0 + q, d, x, total == 0.f ? 0.f : 1.f / total);
-    if (d == 0) emit_lse(row0 + q, top, total);
   }
 }
 

@@ -73,7 +73,7 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   constexpr int THREADS = 64 * WAVES, ROWS = 32 * NQ * WAVES;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   __shared__ int found[4];
-  __shared__ int last, odd;
+  __shared__ int odd;
 
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -553,11 +553,6 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   }
 
   // Write, or park this part of the keys.
-  char* ws = a.workspace + ATTN_COUNTERS * 4;
-  const int64_t tile_id = ((int64_t)want * c.kv_heads + kvh);
-  const int64_t parts = (int64_t)plan.tiles * c.kv_heads * plan.splits;
-  float2* part_ml = (float2*)ws + tile_id * plan.splits * ROWS;
-  float* part_o = (float*)(ws + parts * ROWS * 8) + tile_id * plan.splits * ROWS * DV;
 #pragma unroll
   for (int b = 0; b < NQ; ++b) {
     const int r = wrow0 + 32 * b + l31;
@@ -565,6 +560,7 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
     if (r >= row1) continue;
     const int i = (int)div_by(r, a.by_group), h = kvh * a.group + r - i * a.group;
     const int64_t tok = sq.t0 + i;
+    if (plan.note && split == 0 && half == 0) a.part_count[tok * a.q_heads + h] = active;
     if (active == 1) {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       T* to = (T*)a.out + tok * a.out_token + (int64_t)h * a.out_head;
@@ -583,50 +579,15 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
         a.lse[tok * a.lse_token + (int64_t)h * a.lse_head] =
             sum == 0.f ? -INFINITY : (m[b] + log2f(sum)) * LN2;
     } else {
-      const int64_t row = (int64_t)split * ROWS + r - row0;
-      if (half == 0) part_ml[row] = make_float2(m[b], sum);
+      const int64_t at = (int64_t)split * c.tokens * a.q_heads + tok * a.q_heads + h;
+      if (half == 0) ((float2*)a.part_stats)[at] = make_float2(m[b], sum);
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          *(f32x4*)(part_o + row * DV + 32 * d + 8 * e + 4 * half) =
+          *(f32x4*)(a.part_out + at * DV + 32 * d + 8 * e + 4 * half) =
               f32x4{o[b][d][4 * e], o[b][d][4 * e + 1], o[b][d][4 * e + 2], o[b][d][4 * e + 3]};
     }
-  }
-  if (active == 1) return;
-  uint32_t* counter = (uint32_t*)a.workspace + ATTN_COUNTERS / 2 + tile_id;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    last = atomicAdd(counter, 1u) == (uint32_t)(active - 1);
-    __threadfence();
-  }
-  __syncthreads();
-  if (!last) return;
-  if (threadIdx.x == 0) *counter = 0;
-  for (int e = threadIdx.x; e < (row1 - row0) * (DV / 4); e += THREADS) {
-    const int q = e / (DV / 4), col = e % (DV / 4) * 4, r = row0 + q;
-    if (col >= c.dim) continue;
-    float high = -INFINITY, total = 0.f;
-    for (int k = 0; k < active; ++k) high = fmaxf(high, part_ml[k * ROWS + q].x);
-    const float ref = high == -INFINITY ? 0.f : high;
-    f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < active; ++k) {
-      const float2 ml = part_ml[k * ROWS + q];
-      const float f = exp2_fast(ml.x - ref);
-      total += f * ml.y;
-      x += f * *(const f32x4*)(part_o + ((int64_t)k * ROWS + q) * DV + col);
-    }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    const int i = (int)div_by(r, a.by_group), h = kvh * a.group + r - i * a.group;
-    const int64_t tok = sq.t0 + i;
-    T* to = (T*)a.out + tok * a.out_token + (int64_t)h * a.out_head + col;
-    const u32x2 w = {Op::pack(x[0] * inv, x[1] * inv), Op::pack(x[2] * inv, x[3] * inv)};
-    if (a.out_wide) *(u32x2*)to = w;
-    else __builtin_memcpy(to, &w, 8);
-    if (a.lse != nullptr && col == 0)
-      a.lse[tok * a.lse_token + (int64_t)h * a.lse_head] =
-          total == 0.f ? -INFINITY : (high + log2f(total)) * LN2;
   }
 }
 

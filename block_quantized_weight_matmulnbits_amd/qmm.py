@@ -569,7 +569,7 @@ def qmm_rope_append(q, k, v, out, kv, batch, inv_freq, interleaved=False, factor
 
 
 def qmm_paged_attention_workspace_size(batch, q_heads, kv_heads, head_dim) -> int:
-    """Bytes of the workspace, which starts zeroed."""
+    """Bytes of the workspace; calls on one stream may share it."""
     return int(lib.qmm_paged_attention_workspace_size(batch._ref, q_heads, kv_heads, head_dim))
 
 

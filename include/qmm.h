@@ -374,9 +374,9 @@ int qmm_rope_append(const qmm_heads *q, const qmm_heads *k, const qmm_heads *v,
  *   q, out    rows of heads of kv's dtype; head_dim <= 256, a multiple of
  *             8 (4 for f32); k_pages, v_pages and their strides 16-byte aligned
  *   lse       [tokens, heads] float32 (dense), or NULL
- *   workspace qmm_paged_attention_workspace_size bytes, 256-byte aligned,
- *             zero before its first use; a call leaves its counters zero, so
+ *   workspace qmm_paged_attention_workspace_size bytes, 256-byte aligned;
  *             calls on one stream may share it, whatever their sizes
+ * Rows of out and lse that belong to no sequence are left undefined.
  */
 size_t qmm_paged_attention_workspace_size(const qmm_paged_batch *batch, int q_heads,
                                           int kv_heads, int head_dim);

@@ -48,8 +48,8 @@ def run(dtype, counts, lens, H, KV, D, page=16, causal=True, window=0, cap=0.0, 
     out = torch.full((T, H, D), 7.0, dtype=dtype, device=DEV)
     lse = torch.full((T, H), 7.0, device=DEV)
     if workspace is None:
-        workspace = torch.zeros(q.qmm_paged_attention_workspace_size(batch, H, KV, D),
-                                dtype=torch.uint8, device=DEV)
+        workspace = torch.full((q.qmm_paged_attention_workspace_size(batch, H, KV, D),), 0xA5,
+                               dtype=torch.uint8, device=DEV)
     xd = flat.to(DEV)[q_offset:].view(T, H, D)
     for again in range(2):   # the workspace serves the next call as it is left
         out.fill_(7.0)

@@ -204,7 +204,7 @@ def test_a_batch_without_tokens_is_a_noop(qmm):
 def test_attention_workspace_size(qmm, seqs, max_new, max_len, H, KV, D):
     _, batch, _, _, _ = structs(qmm, seqs=seqs, tokens=seqs * max_new, max_new=max_new, max_len=max_len)
     n = qmm.lib.qmm_paged_attention_workspace_size(ctypes.byref(batch), H, KV, D)
-    assert n >= 4096 and n % 256 == 0 and n < 1 << 30
+    assert n >= 256 and n % 256 == 0 and n < 1 << 30
     assert qmm.lib.qmm_paged_attention_workspace_size(ctypes.byref(batch), H, H + 1, D) == 0
 
 
