@@ -10,25 +10,18 @@ namespace {
 
 constexpr int DT_F32 = 0, DT_F16 = 1;
 
-#ifndef V_FILL
-#define V_FILL 2048
-#endif
-#ifndef V_MIN
-#define V_MIN 128
-#endif
-// Rows kernel: workgroups that fill the chip (256 compute units, four on each,
-// twice over), and the keys of the smallest part, a block of 32 for each wave.
-constexpr int64_t ROWS_FILL = V_FILL, ROWS_MIN_CHUNK = V_MIN;
-#ifndef V_TF
-#define V_TF 512
-#endif
-#ifndef V_TM
-#define V_TM 512
-#endif
+// Rows kernel.  Parts of a few hundred keys keep sequences of uneven lengths
+// from leaving the chip half empty (64 sequences of 17 to 8191 keys: 288 us in
+// parts of 2048, 235 of 1024, 229 of 512; two of 131071 and 90001: 199 of 1024,
+// 205 of 512), so none is longer than ROWS_MAX_CHUNK; few rows are spread over
+// more, shorter ones until the chip is filled, down to a block of 32 for each of
+// the four waves.  Filled it is by three workgroups a compute unit, two times
+// and a half over (as many tiles of rows are not split), or by one where a lane's registers leave room for no more.
+constexpr int64_t ROWS_FILL = 2048, ROWS_FILL_WIDE = 256, ROWS_MIN_CHUNK = 128, ROWS_MAX_CHUNK = 1024;
 // Tiles kernel: whole tiles from TILE_WHOLE on are enough (one a compute unit,
-// twice); fewer are split to about TILE_FILL parts of TILE_MIN_CHUNK keys or
+// twice); fewer are split to about as many parts, of TILE_MIN_CHUNK keys or
 // more.  Sequences with up to TILE_ROWS rows are left to the rows kernel.
-constexpr int64_t TILE_WHOLE = 512, TILE_FILL = V_TF, TILE_MIN_CHUNK = V_TM, TILE_ROWS = 32;
+constexpr int64_t TILE_WHOLE = 512, TILE_MIN_CHUNK = 512, TILE_ROWS = 32;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -45,10 +38,13 @@ void cut(int64_t keys, int64_t parts, int64_t step, int* chunk, int* splits) {
   *splits = (int)ceil_div(keys, *chunk);
 }
 
-int64_t rows_parts(int seqs, int max_new, int64_t keys, int group, int kv_heads, int blocks) {
+int64_t rows_parts(int seqs, int max_new, int64_t keys, int group, int kv_heads, int blocks,
+                   bool wide) {
   const int64_t tiles = seqs * kv_heads * ceil_div((int64_t)max_new * group, 16 * blocks);
-  return std::max<int64_t>(1, std::min(ceil_div(ROWS_FILL, std::max<int64_t>(tiles, 1)),
-                                       ceil_div(keys, ROWS_MIN_CHUNK)));
+  if (tiles >= ROWS_FILL) return 1;
+  const int64_t fill = ceil_div(wide ? ROWS_FILL_WIDE : ROWS_FILL, std::max<int64_t>(tiles, 1));
+  return std::max(ceil_div(keys, ROWS_MAX_CHUNK),
+                  std::max<int64_t>(1, std::min(fill, ceil_div(keys, ROWS_MIN_CHUNK))));
 }
 
 // Rows are counted over the whole batch where the host knows them: tokens.
@@ -66,7 +62,7 @@ TilePlan plan_tile(int seqs, int tokens, int max_new, int group, int dim) {
 int64_t tile_parts(int tokens, int64_t keys, int group, int kv_heads, int blocks) {
   const int64_t whole = ceil_div((int64_t)tokens * group, 128 * blocks) * kv_heads;
   if (whole >= TILE_WHOLE) return 1;
-  return std::max<int64_t>(1, std::min(ceil_div(TILE_FILL, whole), keys / TILE_MIN_CHUNK));
+  return std::max<int64_t>(1, std::min(ceil_div(TILE_WHOLE, whole), keys / TILE_MIN_CHUNK));
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -93,13 +89,13 @@ size_t attn_workspace_bytes(int seqs, int tokens, int max_new, int max_len, int 
   const int64_t rows = (int64_t)tokens * q_heads;
   int64_t parts = 1;
   for (int blocks = 1; blocks <= 2; ++blocks)
-    parts = std::max(parts, rows_parts(seqs, max_new, max_len, group, kv_heads, blocks));
+    parts = std::max(parts, rows_parts(seqs, max_new, max_len, group, kv_heads, blocks, false));
   if ((int64_t)max_new * group > TILE_ROWS) {
     const TilePlan t = plan_tile(seqs, tokens, max_new, group, dim);
     parts = std::max(parts, tile_parts(tokens, max_len, group, kv_heads, t.blocks));
     if (t.skip_upto > 0)
       for (int blocks = 1; blocks <= 2; ++blocks)
-        parts = std::max(parts, rows_parts(seqs, t.skip_upto, max_len, group, kv_heads, blocks));
+        parts = std::max(parts, rows_parts(seqs, t.skip_upto, max_len, group, kv_heads, blocks, false));
   }
   return 256 + (parts > 1 ? align256(parts_bytes(rows, parts, dim)) : 0);
 }
@@ -127,11 +123,13 @@ hipError_t launch_paged_attention(AttnArgs a, char* workspace) {
     few = t.skip_upto;
   }
   if (few > 0) {
-    blocks = (int64_t)few * a.group <= 16 ? 1 : 2;
+    // Next to many-row sequences most of the others have one token.
+    blocks = tiles || (int64_t)few * a.group <= 16 ? 1 : 2;
     const int64_t keys = seen(16 * blocks);
     r.row_tiles = (int)ceil_div((int64_t)few * a.group, 16 * blocks);
-    cut(keys, rows_parts(c.seqs, few, keys, a.group, c.kv_heads, blocks), ROWS_MIN_CHUNK, &r.chunk,
-        &r.splits);
+    const bool wide = padded(c.dim) * (a.dtype == DT_F32 ? 4 : 2) * blocks > 256;
+    cut(keys, rows_parts(c.seqs, few, keys, a.group, c.kv_heads, blocks, wide), ROWS_MIN_CHUNK,
+        &r.chunk, &r.splits);
   }
   const int splits = std::max(t.splits, r.splits);
   if (splits > 1) attn_parts(&a, workspace, splits);

@@ -9,15 +9,15 @@
 namespace qmm {
 namespace {
 
-constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_THREADS = 256, JOIN_SHARED_THREADS = 1024;
 
 // LANES lanes a row, four values each.  SHARED: a workgroup takes one row, its
 // groups of lanes every so-many-th part; else every group takes a row.
 template <int DT, int LANES, bool SHARED>
-__global__ __launch_bounds__(JOIN_THREADS) void join_kernel(AttnArgs a, int padded,
+__global__ __launch_bounds__(SHARED ? JOIN_SHARED_THREADS : JOIN_THREADS) void join_kernel(AttnArgs a, int padded,
                                                             int splits) {
   using T = typename dt<DT>::T;
-  constexpr int GROUPS = JOIN_THREADS / LANES;
+  constexpr int GROUPS = (SHARED ? JOIN_SHARED_THREADS : JOIN_THREADS) / LANES;
   __shared__ f32x4 part[SHARED ? GROUPS : 1][LANES];
   __shared__ float sums[SHARED ? GROUPS : 1];
   const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
@@ -50,8 +50,7 @@ __global__ __launch_bounds__(JOIN_THREADS) void join_kernel(AttnArgs a, int padd
     if (lane == 0) sums[group] = total;
     __syncthreads();
     if (group != 0) return;
-#pragma unroll
-    for (int g = 1; g < GROUPS; ++g) {
+    for (int g = 1; g < GROUPS && g < count; ++g) {
       x += part[g][lane];
       total += sums[g];
     }
@@ -78,7 +77,7 @@ hipError_t launch(const AttnArgs& a, int padded, int splits) {
   const int64_t rows = (int64_t)a.c.tokens * a.q_heads;
   // Few rows: a workgroup each, which reads its parts side by side.
   if (rows <= 2048)
-    join_kernel<DT, LANES, true><<<dim3((uint32_t)rows), JOIN_THREADS, 0, a.stream>>>(a, padded, splits);
+    join_kernel<DT, LANES, true><<<dim3((uint32_t)rows), JOIN_SHARED_THREADS, 0, a.stream>>>(a, padded, splits);
   else
     join_kernel<DT, LANES, false><<<dim3((uint32_t)((rows + JOIN_THREADS / LANES - 1) / (JOIN_THREADS / LANES))),
                                     JOIN_THREADS, 0, a.stream>>>(a, padded, splits);

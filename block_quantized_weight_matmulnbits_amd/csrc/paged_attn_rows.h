@@ -49,9 +49,12 @@ __global__ __launch_bounds__(ROWS_THREADS, (RowsWaves<DT, DP, NB>::N)) void attn
 
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l15 = lane & 15, g = lane >> 4;
-  // Splits fastest, then heads: the parts of a sequence spread over the chip.
+  // Parts fastest, then heads.  Workgroups go round the eight XCDs by number,
+  // and the last parts of short sequences have no work: turned by the rest of
+  // the number, every XCD gets first parts and last ones alike (64 sequences
+  // of 17 to 8191 keys, in parts of 1024: 296 us without, 235 with).
   uint32_t id = blockIdx.x;
-  const int split = id % plan.splits;
+  const int split = (id % plan.splits + id / plan.splits) % plan.splits;
   id /= plan.splits;
   const int kvh = id % c.kv_heads;
   id /= c.kv_heads;

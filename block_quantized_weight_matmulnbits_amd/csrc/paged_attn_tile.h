@@ -79,12 +79,13 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l31 = lane & 31, half = lane >> 5, l15 = lane & 15;
 
-  // Heads fastest, so that one head's tiles meet in one L2; then parts; the
-  // tiles of the sequences follow one another without gaps.
+  // Heads fastest, so that one head's tiles meet in one L2; then parts, turned
+  // by the tile's number as in the rows kernel; the tiles of the sequences
+  // follow one another without gaps.
   uint32_t id = blockIdx.x;
   const int kvh = id % c.kv_heads;
   id /= c.kv_heads;
-  const int split = id % plan.splits, want = id / plan.splits;
+  const int want = id / plan.splits, split = (id % plan.splits + want) % plan.splits;
   if (wave == 0) {
     int base = 0, seq = -1, tile = 0;
     for (int s0 = 0; s0 < c.seqs && seq < 0; s0 += 64) {

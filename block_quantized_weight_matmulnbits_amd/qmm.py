@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -117,6 +118,18 @@ def _stream(stream):
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
+
+
+# The current stream's handle without a Stream object around it, where torch
+# has the call (the object costs a microsecond of every small operator).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_at(t, stream):
+    """``stream``, or the current one of t's device."""
+    if stream is None and _raw_stream is not None and t.is_cuda:
+        return _raw_stream(t.get_device())
+    return _stream(stream)
 
 
 def qmm_last_error() -> str:
@@ -331,10 +344,9 @@ class Step:
         self._add(lib.qmm_step_add_paged_attention, (q, kv, batch, out, workspace, lse), *args)
 
     def add_pages_reserve(self, pool, seqs, grow, status, workspace):
-        _lists(pool, seqs=seqs, grow=grow, status=status)
+        n = _lists("seqs", seqs, "grow", grow, status)
         self._add(lib.qmm_step_add_pages_reserve, (pool, seqs, grow, status, workspace), pool._ref,
-                  _ptr(seqs), _ptr(grow), seqs.numel(), _ptr(status), _ptr(workspace),
-                  workspace.numel() * workspace.element_size())
+                  _ptr(seqs), _ptr(grow), n, _ptr(status), _ptr(workspace), workspace.nbytes)
 
     def finalize(self):
         _check(lib.qmm_step_finalize(self._h))
@@ -419,8 +431,8 @@ def qmm_lowp_quantize(x, codes, scales, rows, cols, fmt, layout, stream=None):
                                  _stream(stream)))
 
 
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", _vp), ("token_stride", _i64), ("head_stride", _i64), ("heads", _i32)]
+# struct qmm_heads, as bytes: data, token_stride, head_stride, heads.
+_pack_heads = struct.Struct("@Pqqi4x").pack
 
 
 class _PagedKV(ctypes.Structure):
@@ -446,7 +458,7 @@ class _PagePool(ctypes.Structure):
 
 
 def _int32(name, t, shape=None):
-    if t.dtype != torch.int32 or not t.is_contiguous() or (shape and tuple(t.shape) != shape):
+    if t.dtype is not torch.int32 or not t.is_contiguous() or (shape and t.shape != shape):
         raise ValueError(f"{name} must be a dense int32 tensor"
                          f"{f' of shape {list(shape)}' if shape else ''}, got {t.dtype} "
                          f"{list(t.shape)}")
@@ -531,19 +543,16 @@ class PagePool:
         self._ref = ctypes.byref(self._c)
 
 
-def _heads(name, t, kv, batch, heads=None):
+def _heads(name, t, kv, batch, heads):
     """The struct of rows [tokens, heads, head_dim], with the checks that need
     the tensor's shape."""
-    shape = t.shape
-    if (len(shape) != 3 or shape[0] != batch.tokens or shape[2] != kv.head_dim
-            or (heads is not None and shape[1] != heads) or t.dtype != kv.dtype):
-        raise ValueError(f"{name} must be {kv.dtype} [{batch.tokens}, "
-                         f"{'heads' if heads is None else heads}, {kv.head_dim}], got {t.dtype} "
-                         f"{list(shape)}")
-    s0, s1, s2 = t.stride()
-    if s2 != 1 and shape[2] > 1:
-        raise ValueError(f"head_dim must be the dense dimension of {name}")
-    return _Heads(t.data_ptr(), s0, s1, shape[1])
+    shape, strides = t.shape, t.stride()
+    if (shape != (batch.tokens, heads, kv.head_dim) or t.dtype is not kv.dtype
+            or (strides[2] != 1 and shape[2] > 1)):
+        raise ValueError(f"{name} must be {kv.dtype} [{batch.tokens}, {heads}, {kv.head_dim}] with "
+                         f"dense rows of head_dim, got {t.dtype} {list(shape)} with strides "
+                         f"{list(strides)}")
+    return _pack_heads(t.data_ptr(), strides[0], strides[1], heads)
 
 
 def _rope_args(q, k, v, out, kv, batch, inv_freq, interleaved, factor, positions):
@@ -552,11 +561,11 @@ def _rope_args(q, k, v, out, kv, batch, inv_freq, interleaved, factor, positions
                          f"{list(inv_freq.shape)}")
     if positions is not None:
         _int32("positions", positions, (batch.tokens,))
-    byref = ctypes.byref
-    return (byref(_heads("q", q, kv, batch)), byref(_heads("k", k, kv, batch, kv.kv_heads)),
-            byref(_heads("v", v, kv, batch, kv.kv_heads)),
-            byref(_heads("out", out, kv, batch, q.shape[1])), kv._ref, batch._ref,
-            inv_freq.data_ptr(), inv_freq.shape[0], interleaved, factor, _ptr(positions))
+    heads, kv_heads = q.shape[1], kv.kv_heads
+    return (_heads("q", q, kv, batch, heads), _heads("k", k, kv, batch, kv_heads),
+            _heads("v", v, kv, batch, kv_heads), _heads("out", out, kv, batch, heads), kv._ref,
+            batch._ref, inv_freq.data_ptr(), inv_freq.shape[0], interleaved, factor,
+            None if positions is None else positions.data_ptr())
 
 
 def qmm_rope_append(q, k, v, out, kv, batch, inv_freq, interleaved=False, factor=1.0,
@@ -565,7 +574,7 @@ def qmm_rope_append(q, k, v, out, kv, batch, inv_freq, interleaved=False, factor
     v [tokens, kv_heads, head_dim] to the cache ``kv``; ``inv_freq`` [half] is
     float64, ``positions`` [tokens] int32 or None (a token's key number)."""
     _check(lib.qmm_rope_append(*_rope_args(q, k, v, out, kv, batch, inv_freq, interleaved, factor,
-                                           positions), _stream(stream)))
+                                           positions), _stream_at(q, stream)))
 
 
 def qmm_paged_attention_workspace_size(batch, q_heads, kv_heads, head_dim) -> int:
@@ -580,10 +589,10 @@ def _attention_args(q, kv, batch, out, workspace, scale, causal, window, softcap
                          f"{list(lse.shape)}")
     if scale is None:
         scale = kv.head_dim ** -0.5
-    byref = ctypes.byref
-    return (byref(_heads("q", q, kv, batch)), kv._ref, batch._ref,
-            byref(_heads("out", out, kv, batch, q.shape[1])), _ptr(lse), scale, causal, window,
-            softcap, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    heads = q.shape[1]
+    return (_heads("q", q, kv, batch, heads), kv._ref, batch._ref,
+            _heads("out", out, kv, batch, heads), None if lse is None else lse.data_ptr(), scale,
+            causal, window, softcap, workspace.data_ptr(), workspace.nbytes)
 
 
 def qmm_paged_attention(q, kv, batch, out, workspace, scale=None, causal=True, window=0,
@@ -592,7 +601,7 @@ def qmm_paged_attention(q, kv, batch, out, workspace, scale=None, causal=True, w
     where given, ``lse`` [tokens, heads] float32; ``scale`` defaults to
     head_dim ** -0.5."""
     _check(lib.qmm_paged_attention(*_attention_args(q, kv, batch, out, workspace, scale, causal,
-                                                    window, softcap, lse), _stream(stream)))
+                                                    window, softcap, lse), _stream_at(q, stream)))
 
 
 def qmm_pages_workspace_size(pool, count=0) -> int:
@@ -600,52 +609,50 @@ def qmm_pages_workspace_size(pool, count=0) -> int:
     return int(lib.qmm_pages_workspace_size(pool._ref, count))
 
 
-def _lists(pool, **lists):
-    """int32 lists of one length, but for the status word pair."""
-    n = None
-    for name, t in lists.items():
-        if name == "status":
-            _int32(name, t, (2,))
-            continue
-        _int32(name, t)
-        if n is not None and t.numel() != n:
-            raise ValueError(f"{', '.join(k for k in lists if k != 'status')} must have one length")
-        n = t.numel()
+def _lists(a_name, a, b_name=None, b=None, status=None):
+    """Checks int32 lists of one length and the pair of status words; the length."""
+    _int32(a_name, a)
+    n = a.numel()
+    if b is not None:
+        _int32(b_name, b)
+        if b.numel() != n:
+            raise ValueError(f"{a_name} and {b_name} must have one length, got {n} and {b.numel()}")
+    if status is not None:
+        _int32("status", status, (2,))
+    return n
 
 
 def qmm_pages_free(pool, seqs, stream=None):
-    _lists(pool, seqs=seqs)
-    _check(lib.qmm_pages_free(pool._ref, seqs.data_ptr(), seqs.numel(), _stream(stream)))
+    n = _lists("seqs", seqs)
+    _check(lib.qmm_pages_free(pool._ref, seqs.data_ptr(), n, _stream_at(seqs, stream)))
 
 
 def qmm_pages_fork(pool, parents, children, status, workspace, stream=None):
     """``status`` [2] int32, zeroed by the caller, tells on the device whether
     the list was served (qmm_pages_status)."""
-    _lists(pool, parents=parents, children=children, status=status)
-    _check(lib.qmm_pages_fork(pool._ref, parents.data_ptr(), children.data_ptr(), parents.numel(),
-                              status.data_ptr(), workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size(), _stream(stream)))
+    n = _lists("parents", parents, "children", children, status)
+    _check(lib.qmm_pages_fork(pool._ref, parents.data_ptr(), children.data_ptr(), n,
+                              status.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                              _stream_at(parents, stream)))
 
 
 def qmm_pages_reserve(pool, seqs, grow, status, workspace, stream=None):
-    _lists(pool, seqs=seqs, grow=grow, status=status)
-    _check(lib.qmm_pages_reserve(pool._ref, seqs.data_ptr(), grow.data_ptr(), seqs.numel(),
-                                 status.data_ptr(), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream(stream)))
+    n = _lists("seqs", seqs, "grow", grow, status)
+    _check(lib.qmm_pages_reserve(pool._ref, seqs.data_ptr(), grow.data_ptr(), n, status.data_ptr(),
+                                 workspace.data_ptr(), workspace.nbytes, _stream_at(seqs, stream)))
 
 
 def qmm_pages_copy(pool, src, dst, stream=None):
-    _lists(pool, src=src, dst=dst)
-    _check(lib.qmm_pages_copy(pool._ref, src.data_ptr(), dst.data_ptr(), src.numel(),
-                              _stream(stream)))
+    n = _lists("src", src, "dst", dst)
+    _check(lib.qmm_pages_copy(pool._ref, src.data_ptr(), dst.data_ptr(), n, _stream_at(src, stream)))
 
 
 def qmm_pages_compact(pool, refs_out, table_out, live, workspace, stream=None):
     """``refs_out`` and ``table_out`` take the new counts and table, ``live`` [1]
     the number of used pages, now the first ones."""
-    _int32("refs_out", refs_out, tuple(pool.refs.shape))
-    _int32("table_out", table_out, tuple(pool.table.shape))
+    _int32("refs_out", refs_out, pool.refs.shape)
+    _int32("table_out", table_out, pool.table.shape)
     _int32("live", live)
     _check(lib.qmm_pages_compact(pool._ref, refs_out.data_ptr(), table_out.data_ptr(),
-                                 live.data_ptr(), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream(stream)))
+                                 live.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                 _stream_at(refs_out, stream)))

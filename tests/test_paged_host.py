@@ -66,6 +66,11 @@ def test_pool_worked_values():
 
 # -- refusals at the C boundary ----------------------------------------------
 
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("heads", ctypes.c_int)]
+
+
 def structs(qmm, **kw):
     a = dict(k=FAKE, v=FAKE, ks=(65536, 2048, 128), vs=(65536, 2048, 128), pages=64, dtype=2, kv=8,
              page=16, dim=128, starts=FAKE, lens=FAKE, table=FAKE, tstride=32, seqs=4, tokens=4,
@@ -75,9 +80,9 @@ def structs(qmm, **kw):
     kv = qmm._PagedKV(a["k"], a["v"], *a["ks"], *a["vs"], a["pages"], a["dtype"], a["kv"], a["page"], a["dim"])
     batch = qmm._PagedBatch(a["starts"], a["lens"], a["table"], a["tstride"], a["seqs"], a["tokens"],
                             a["width"], a["max_new"], a["max_len"])
-    q = qmm._Heads(a["q"], a["qt"], a["qh"], a["heads"])
-    out = qmm._Heads(a["out"], 4096, 128, a["oheads"])
-    k = qmm._Heads(FAKE, 6144, 128, a["kheads"])
+    q = Heads(a["q"], a["qt"], a["qh"], a["heads"])
+    out = Heads(a["out"], 4096, 128, a["oheads"])
+    k = Heads(FAKE, 6144, 128, a["kheads"])
     return kv, batch, q, out, k
 
 
@@ -206,6 +211,11 @@ def test_attention_workspace_size(qmm, seqs, max_new, max_len, H, KV, D):
     n = qmm.lib.qmm_paged_attention_workspace_size(ctypes.byref(batch), H, KV, D)
     assert n >= 256 and n % 256 == 0 and n < 1 << 30
     assert qmm.lib.qmm_paged_attention_workspace_size(ctypes.byref(batch), H, H + 1, D) == 0
+
+
+def test_the_binding_packs_the_struct(qmm):
+    raw = qmm._pack_heads(FAKE, 6144, 128, 32)
+    assert raw == bytes(Heads(FAKE, 6144, 128, 32))
 
 
 # -- refusals of the binding -------------------------------------------------
