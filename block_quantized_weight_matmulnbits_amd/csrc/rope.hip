@@ -76,6 +76,10 @@ __global__ __launch_bounds__(ROPE_THREADS) void rope_append_kernel(
   // Each wave finds its token's sequence (the number of sequences that end at
   // or before it: their ends do not decrease) and, with the other waves of
   // the same token, its angles.
+  // Thousands of tokens pass the caches by (16384 of 48 heads of 128: 86 us with
+  // plain accesses, 82 without, 4.9 TB/s, what a large copy reaches here); a
+  // few are about to be read again.
+  constexpr bool STREAM = TB >= 4;
   constexpr int SHARE = TB >= 4 ? 1 : 4 / TB;   // waves of one token
   const int mine = wave / SHARE, t = t0 + mine;
   if (t < c.tokens) {
@@ -152,8 +156,13 @@ __global__ __launch_bounds__(ROPE_THREADS) void rope_append_kernel(
         o0 = n * 2 * VEC;
         o1 = o0 + VEC;
       }
-      x[u][0] = *(const V*)(from + o0);
-      x[u][1] = *(const V*)(from + o1);
+      if constexpr (STREAM) {
+        x[u][0] = __builtin_nontemporal_load((const V*)(from + o0));
+        x[u][1] = __builtin_nontemporal_load((const V*)(from + o1));
+      } else {
+        x[u][0] = *(const V*)(from + o0);
+        x[u][1] = *(const V*)(from + o1);
+      }
       to[u] += o0;
     }
 #pragma unroll
@@ -178,8 +187,13 @@ __global__ __launch_bounds__(ROPE_THREADS) void rope_append_kernel(
         __builtin_memcpy(&x[u][1], e + VEC, sizeof(V));
         if (!INTER) second = a.half;
       }
-      *(V*)to[u] = x[u][0];
-      *(V*)(to[u] + second) = x[u][1];
+      if constexpr (STREAM) {
+        __builtin_nontemporal_store(x[u][0], (V*)to[u]);
+        __builtin_nontemporal_store(x[u][1], (V*)(to[u] + second));
+      } else {
+        *(V*)to[u] = x[u][0];
+        *(V*)(to[u] + second) = x[u][1];
+      }
     }
   }
 }
