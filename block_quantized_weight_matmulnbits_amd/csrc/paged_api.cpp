@@ -361,6 +361,8 @@ int qmm_pages_fork(const qmm_page_pool* pool, const int32_t* parents, const int3
   CHECK(check_list(fn, "parents", parents, count));
   CHECK(check_list(fn, "children", children, count));
   CHECK(check_list(fn, "status", status, 1));
+  if (pool->planes * count > UINT32_MAX || count * pool->width > UINT32_MAX)
+    return fail(QMM_ERR_UNSUPPORTED, "%s: planes x count and count x width must be below 2^32.", fn);
   if (count == 0) return QMM_OK;
   CHECK(check_workspace(fn, workspace, workspace_bytes, qmm_pages_workspace_size(pool, count)));
   return hip_status(qmm::launch_pages_fork(pool_args(pool, workspace, stream), parents, children,

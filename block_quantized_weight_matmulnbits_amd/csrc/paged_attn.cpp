@@ -4,6 +4,15 @@
 
 #include <algorithm>
 
+#ifndef V_F1
+#define V_F1 0
+#endif
+#ifndef V_FW
+#define V_FW 256
+#endif
+#ifndef V_WIDE
+#define V_WIDE 256
+#endif
 namespace qmm {
 
 namespace {
@@ -17,7 +26,7 @@ constexpr int DT_F32 = 0, DT_F16 = 1;
 // more, shorter ones until the chip is filled, down to a block of 32 for each of
 // the four waves.  Filled it is by three workgroups a compute unit, two times
 // and a half over (as many tiles of rows are not split), or by one where a lane's registers leave room for no more.
-constexpr int64_t ROWS_FILL = 2048, ROWS_FILL_WIDE = 256, ROWS_MIN_CHUNK = 128, ROWS_MAX_CHUNK = 1024;
+constexpr int64_t ROWS_FILL = 2048, ROWS_FILL_WIDE = V_FW, ROWS_MIN_CHUNK = 128, ROWS_MAX_CHUNK = 1024;
 // Tiles kernel: whole tiles from TILE_WHOLE on are enough (one a compute unit,
 // twice); fewer are split to about as many parts, of TILE_MIN_CHUNK keys or
 // more.  Sequences with up to TILE_ROWS rows are left to the rows kernel.
@@ -124,10 +133,10 @@ hipError_t launch_paged_attention(AttnArgs a, char* workspace) {
   }
   if (few > 0) {
     // Next to many-row sequences most of the others have one token.
-    blocks = tiles || (int64_t)few * a.group <= 16 ? 1 : 2;
+    blocks = tiles || (V_F1 && a.dtype == DT_F32) || (int64_t)few * a.group <= 16 ? 1 : 2;
     const int64_t keys = seen(16 * blocks);
     r.row_tiles = (int)ceil_div((int64_t)few * a.group, 16 * blocks);
-    const bool wide = padded(c.dim) * (a.dtype == DT_F32 ? 4 : 2) * blocks > 256;
+    const bool wide = padded(c.dim) * (a.dtype == DT_F32 ? 4 : 2) * blocks > V_WIDE;
     cut(keys, rows_parts(c.seqs, few, keys, a.group, c.kv_heads, blocks, wide), ROWS_MIN_CHUNK,
         &r.chunk, &r.splits);
   }

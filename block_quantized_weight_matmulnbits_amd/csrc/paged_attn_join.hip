@@ -75,8 +75,9 @@ __global__ __launch_bounds__(SHARED ? JOIN_SHARED_THREADS : JOIN_THREADS) void j
 template <int DT, int LANES>
 hipError_t launch(const AttnArgs& a, int padded, int splits) {
   const int64_t rows = (int64_t)a.c.tokens * a.q_heads;
-  // Few rows: a workgroup each, which reads its parts side by side.
-  if (rows <= 2048)
+  // Few rows: a workgroup each, which reads its parts side by side (64 rows of
+  // up to 128 parts: 17 us without, 10 with; 980 rows of 5: 4.6 and 6.8).
+  if (rows <= 512)
     join_kernel<DT, LANES, true><<<dim3((uint32_t)rows), JOIN_SHARED_THREADS, 0, a.stream>>>(a, padded, splits);
   else
     join_kernel<DT, LANES, false><<<dim3((uint32_t)((rows + JOIN_THREADS / LANES - 1) / (JOIN_THREADS / LANES))),

@@ -22,7 +22,7 @@ namespace qmm {
 namespace {
 
 constexpr int PLAN_THREADS = 1024, PLAN_LDS = 1024;
-constexpr int COPY_THREADS = 256;
+constexpr int COPY_THREADS = 256, COPY_FLIGHT = 2;
 
 // Workspace: the number of pages to copy, then the lists.
 struct Plan {
@@ -86,6 +86,42 @@ __global__ __launch_bounds__(256) void free_kernel(PoolArgs p, const int32_t* se
   if (threadIdx.x == 0) p.lens[s] = 0;
 }
 
+// Pages src[i] -> dst[i] in every plane.  Work is cut into runs of two
+// vectors a thread over (move, plane, vector), all in flight; a workgroup
+// divides once for its run and by a launch constant from there.  A page is
+// read and written once, so both pass the caches by (1 GB moved: 209 us with
+// plain accesses, 197 without, 5.2 TB/s; four in flight: 208).
+template <typename V>
+__device__ __forceinline__ void copy_pages(const PoolArgs& p, const int32_t* src,
+                                           const int32_t* dst, int64_t moves, uint32_t per_page,
+                                           const FastDiv& by_vectors, const FastDiv& by_planes) {
+  constexpr int RUN = COPY_FLIGHT * COPY_THREADS;
+  const int64_t total = moves * p.planes * per_page;
+  for (int64_t base = (int64_t)blockIdx.x * RUN; base < total; base += (int64_t)gridDim.x * RUN) {
+    const int64_t pair0 = base / per_page;
+    const uint32_t off0 = (uint32_t)(base - pair0 * per_page);
+    V x[COPY_FLIGHT];
+    V* to[COPY_FLIGHT];
+#pragma unroll
+    for (int u = 0; u < COPY_FLIGHT; ++u) {
+      const uint32_t k = u * COPY_THREADS + threadIdx.x;
+      to[u] = nullptr;
+      if (base + k >= total) continue;
+      const uint32_t more = div_by(off0 + k, by_vectors), off = off0 + k - more * per_page;
+      const uint32_t pair = (uint32_t)(pair0 + more), m = div_by(pair, by_planes);
+      const uint32_t plane = pair - m * (uint32_t)p.planes;
+      const int a = src[m], b = dst[m];
+      if (a < 0 || a >= p.pages || b < 0 || b >= p.pages || a == b) continue;
+      char* at = p.data + plane * p.plane_stride;
+      x[u] = __builtin_nontemporal_load((const V*)(at + a * p.page_stride) + off);
+      to[u] = (V*)(at + b * p.page_stride) + off;
+    }
+#pragma unroll
+    for (int u = 0; u < COPY_FLIGHT; ++u)
+      if (to[u] != nullptr) __builtin_nontemporal_store(x[u], to[u]);
+  }
+}
+
 // Four reference counts from `page` on (a multiple of 4), free past the pool's
 // end as little as a used one.
 __device__ __forceinline__ i32x4 refs_at(const PoolArgs& p, int page) {
@@ -108,15 +144,17 @@ template <bool FORK>
 __global__ __launch_bounds__(PLAN_THREADS) void take_kernel(PoolArgs p, const int32_t* parents,
                                                             const int32_t* seqs,
                                                             const int32_t* grow, int count,
-                                                            int32_t* status) {
+                                                            int32_t* status, FastDiv by_width) {
   __shared__ uint32_t seen[POOL_MAX_SLOTS / 32];
-  __shared__ int32_t near_first[PLAN_LDS], near_length[PLAN_LDS], near_fresh[PLAN_LDS];
+  __shared__ int32_t near_first[PLAN_LDS], near_length[PLAN_LDS], near_have[PLAN_LDS],
+      near_fresh[PLAN_LDS];
   __shared__ int part[PLAN_THREADS / 64];
   __shared__ int bad;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x;
   const Plan w = plan_of(p.workspace, p.pages, count);
   int32_t* first_of = count <= PLAN_LDS ? near_first : w.first;
   int32_t* length_of = count <= PLAN_LDS ? near_length : w.length;
+  int32_t* have_of = count <= PLAN_LDS ? near_have : w.src;   // reserve has no copies
   const i32x4 front = refs_at(p, 4 * tid);
   const int before_status = status[0];
   int s = 0, arg = 0;
@@ -162,6 +200,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void take_kernel(PoolArgs p, const in
             const int to = pages_for(length, p);
             if (to > p.width) code = QMM_PAGES_TOO_LONG;
             need = to - pages_for(have, p);
+            have_of[i] = pages_for(have, p);
           }
         }
       }
@@ -177,13 +216,12 @@ __global__ __launch_bounds__(PLAN_THREADS) void take_kernel(PoolArgs p, const in
     needed += sum;
   }
   __syncthreads();
-  if (FORK && !bad) {
-    for (int i = wave; i < count; i += PLAN_THREADS / 64) {
-      const int32_t* row = p.table + (int64_t)parents[i] * p.table_stride;
-      const int held = pages_for(length_of[i], p);
-      for (int c = lane; c < held; c += 64)
-        if (row[c] < 0 || row[c] >= p.pages) bad = QMM_PAGES_BAD_ENTRY;
-    }
+  const int64_t entries = FORK && !bad ? (int64_t)count * p.width : 0;
+  for (int64_t e = tid; e < entries; e += PLAN_THREADS) {
+    const int i = (int)div_by((uint32_t)e, by_width), c = (int)(e - (int64_t)i * p.width);
+    if (c >= pages_for(length_of[i], p)) continue;
+    const int page = p.table[(int64_t)parents[i] * p.table_stride + c];
+    if (page < 0 || page >= p.pages) bad = QMM_PAGES_BAD_ENTRY;
   }
 
   // The lowest free pages, as many as are needed.
@@ -216,35 +254,41 @@ __global__ __launch_bounds__(PLAN_THREADS) void take_kernel(PoolArgs p, const in
     return;
   }
 
-  for (int i = tid; i < (int)needed; i += PLAN_THREADS) p.refs[fresh[i]] = 1;
-  // A wave an entry.  The lengths are those that were counted above: a slot
-  // that another entry fills here was empty then, and none of its row is read.
-  for (int i = wave; i < count; i += PLAN_THREADS / 64) {
-    const int slot = seqs[i], length = length_of[i], first = first_of[i];
-    int32_t* row = p.table + (int64_t)slot * p.table_stride;
-    const int held = pages_for(length, p);
-    if (FORK) {
-      // Full pages are shared, a part-filled last one is copied into a new one.
-      const int full = (int)div_by((uint32_t)length, p.by_page);
-      const int32_t* from = p.table + (int64_t)parents[i] * p.table_stride;
-      for (int c = lane; c < p.width; c += 64) {
-        int page = -1;
-        if (c < full) {
-          page = from[c];
-          atomicAdd(p.refs + page, 1);
-        } else if (c < held) {
-          page = fresh[first];
-          w.src[first] = from[c];
-          w.dst[first] = page;
-        }
-        row[c] = page;
+  // The lengths are those that were counted above: a slot that another entry
+  // fills here was empty then, and none of its row is read.
+  for (int k = tid; k < (int)needed; k += PLAN_THREADS) {
+    const int page = fresh[k];
+    p.refs[page] = 1;
+    if (!FORK) {
+      // The last entry whose pages begin at or before the k-th has it.
+      int lo = 0, hi = count - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (first_of[mid] <= k) lo = mid;
+        else hi = mid - 1;
       }
-    } else {
-      const int have = pages_for(p.lens[slot], p);
-      for (int c = have + lane; c < held; c += 64) row[c] = fresh[first + c - have];
+      p.table[(int64_t)seqs[lo] * p.table_stride + have_of[lo] + k - first_of[lo]] = page;
     }
-    if (lane == 0) p.lens[slot] = length;
   }
+  // Full pages are shared, a part-filled last one is copied into a new one.
+  for (int64_t e = tid; e < entries; e += PLAN_THREADS) {
+    const int i = (int)div_by((uint32_t)e, by_width), c = (int)(e - (int64_t)i * p.width);
+    const int length = length_of[i], full = (int)div_by((uint32_t)length, p.by_page);
+    int page = -1;
+    if (c < pages_for(length, p)) {
+      page = p.table[(int64_t)parents[i] * p.table_stride + c];
+      if (c < full) {
+        atomicAdd(p.refs + page, 1);
+      } else {
+        const int first = first_of[i];
+        w.src[first] = page;
+        page = fresh[first];
+        w.dst[first] = page;
+      }
+    }
+    p.table[(int64_t)seqs[i] * p.table_stride + c] = page;
+  }
+  for (int i = tid; i < count; i += PLAN_THREADS) p.lens[seqs[i]] = length_of[i];
   if (FORK && tid == 0) *w.moves = (int)needed;
 }
 
@@ -290,42 +334,6 @@ __global__ __launch_bounds__(PLAN_THREADS) void compact_kernel(PoolArgs p, int32
   if (tid == 0) {
     *w.moves = moves;
     *live_out = live;
-  }
-}
-
-// Pages src[i] -> dst[i] in every plane.  Work is cut into runs of 1024
-// vectors over (move, plane, vector), four a thread in flight; a workgroup
-// divides once for its run and by a launch constant from there.  A page is
-// read and written once, so both pass the caches by (1 GB moved: 218 us with
-// plain accesses, 208 without, 4.9 TB/s, what a large copy reaches here).
-template <typename V>
-__device__ __forceinline__ void copy_pages(const PoolArgs& p, const int32_t* src,
-                                           const int32_t* dst, int64_t moves, uint32_t per_page,
-                                           const FastDiv& by_vectors, const FastDiv& by_planes) {
-  constexpr int RUN = 4 * COPY_THREADS;
-  const int64_t total = moves * p.planes * per_page;
-  for (int64_t base = (int64_t)blockIdx.x * RUN; base < total; base += (int64_t)gridDim.x * RUN) {
-    const int64_t pair0 = base / per_page;
-    const uint32_t off0 = (uint32_t)(base - pair0 * per_page);
-    V x[4];
-    V* to[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t k = u * COPY_THREADS + threadIdx.x;
-      to[u] = nullptr;
-      if (base + k >= total) continue;
-      const uint32_t more = div_by(off0 + k, by_vectors), off = off0 + k - more * per_page;
-      const uint32_t pair = (uint32_t)(pair0 + more), m = div_by(pair, by_planes);
-      const uint32_t plane = pair - m * (uint32_t)p.planes;
-      const int a = src[m], b = dst[m];
-      if (a < 0 || a >= p.pages || b < 0 || b >= p.pages || a == b) continue;
-      char* at = p.data + plane * p.plane_stride;
-      x[u] = __builtin_nontemporal_load((const V*)(at + a * p.page_stride) + off);
-      to[u] = (V*)(at + b * p.page_stride) + off;
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (to[u] != nullptr) __builtin_nontemporal_store(x[u], to[u]);
   }
 }
 
@@ -375,7 +383,7 @@ hipError_t by_vector(const PoolArgs& p, F f) {
 }
 
 int copy_grid(const PoolArgs& p, int64_t moves, int64_t per_page) {
-  const int64_t runs = (moves * p.planes * per_page + 4 * COPY_THREADS - 1) / (4 * COPY_THREADS);
+  const int64_t runs = (moves * p.planes * per_page + COPY_FLIGHT * COPY_THREADS - 1) / (COPY_FLIGHT * COPY_THREADS);
   return (int)(runs < 1 ? 1 : runs > 8192 ? 8192 : runs);
 }
 
@@ -404,16 +412,18 @@ hipError_t launch_pages_free(const PoolArgs& p, const int32_t* seqs, int count) 
 
 hipError_t launch_pages_fork(const PoolArgs& p, const int32_t* parents, const int32_t* children,
                              int count, int32_t* status) {
-  take_kernel<true><<<1, PLAN_THREADS, 0, p.stream>>>(p, parents, children, nullptr, count, status);
+  take_kernel<true><<<1, PLAN_THREADS, 0, p.stream>>>(p, parents, children, nullptr, count, status,
+                                                      fast_div((uint32_t)p.width));
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || p.planes == 0 || p.page_bytes == 0) return e;
   const Plan w = plan_of(p.workspace, p.pages, count);
   return launch_copy(p, w.src, w.dst, w.moves, count);
 }
 
 hipError_t launch_pages_reserve(const PoolArgs& p, const int32_t* seqs, const int32_t* grow,
                                 int count, int32_t* status) {
-  take_kernel<false><<<1, PLAN_THREADS, 0, p.stream>>>(p, nullptr, seqs, grow, count, status);
+  take_kernel<false><<<1, PLAN_THREADS, 0, p.stream>>>(p, nullptr, seqs, grow, count, status,
+                                                       fast_div((uint32_t)p.width));
   return hipGetLastError();
 }
 
