@@ -4,15 +4,6 @@
 
 #include <algorithm>
 
-#ifndef V_F1
-#define V_F1 0
-#endif
-#ifndef V_FW
-#define V_FW 256
-#endif
-#ifndef V_WIDE
-#define V_WIDE 256
-#endif
 namespace qmm {
 
 namespace {
@@ -26,11 +17,14 @@ constexpr int DT_F32 = 0, DT_F16 = 1;
 // more, shorter ones until the chip is filled, down to a block of 32 for each of
 // the four waves.  Filled it is by three workgroups a compute unit, two times
 // and a half over (as many tiles of rows are not split), or by one where a lane's registers leave room for no more.
-constexpr int64_t ROWS_FILL = 2048, ROWS_FILL_WIDE = V_FW, ROWS_MIN_CHUNK = 128, ROWS_MAX_CHUNK = 1024;
-// Tiles kernel: whole tiles from TILE_WHOLE on are enough (one a compute unit,
-// twice); fewer are split to about as many parts, of TILE_MIN_CHUNK keys or
-// more.  Sequences with up to TILE_ROWS rows are left to the rows kernel.
-constexpr int64_t TILE_WHOLE = 512, TILE_MIN_CHUNK = 512, TILE_ROWS = 32;
+constexpr int64_t ROWS_FILL = 2048, ROWS_FILL_WIDE = 256, ROWS_MIN_CHUNK = 128, ROWS_MAX_CHUNK = 1024;
+// Tiles kernel: workgroups of 128 rows are resident twice on a compute unit
+// (once for heads over 128), those of 256 once.  The former are split to what
+// is resident at once (10 sequences of 48 rows, 8 heads, to 4000 keys: 61 us in
+// 560 parts, 72 in 240, 79 in 1200), the latter, whose sequences are long and uneven, to
+// twice that (three chunks of 509 tokens: 288 us, 327 in four times).
+// Sequences with up to TILE_ROWS rows are left to the rows kernel.
+constexpr int64_t UNITS = 256, TILE_MIN_CHUNK = 128, TILE_ROWS = 32;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -63,15 +57,19 @@ TilePlan plan_tile(int seqs, int tokens, int max_new, int group, int dim) {
   TilePlan p{};
   p.blocks = dim <= 128 && (int64_t)max_new * group > 128 ? 2 : 1;
   p.tiles = (int)(ceil_div((int64_t)tokens * group, 128 * p.blocks) + seqs);
-  // A single sequence is taken whatever it has.
-  p.skip_upto = seqs == 1 ? 0 : (int)(TILE_ROWS / group);
+  // Where every sequence has as many tokens, none has fewer.
+  p.skip_upto = (int64_t)seqs * max_new == tokens ? 0 : (int)(TILE_ROWS / group);
   return p;
 }
 
-int64_t tile_parts(int tokens, int64_t keys, int group, int kv_heads, int blocks) {
-  const int64_t whole = ceil_div((int64_t)tokens * group, 128 * blocks) * kv_heads;
-  if (whole >= TILE_WHOLE) return 1;
-  return std::max<int64_t>(1, std::min(ceil_div(TILE_WHOLE, whole), keys / TILE_MIN_CHUNK));
+int64_t tile_parts(int seqs, int tokens, int max_new, int64_t keys, int group, int kv_heads,
+                   int blocks, int dim) {
+  // Tiles: of equal sequences, or else whole ones of the batch's rows.
+  const int64_t height = 128 * blocks, resident = UNITS * (blocks == 1 && dim > 128 ? 1 : 2);
+  const int64_t tiles = kv_heads * ((int64_t)seqs * max_new == tokens
+                                        ? seqs * ceil_div((int64_t)max_new * group, height)
+                                        : ceil_div((int64_t)tokens * group, height));
+  return std::max<int64_t>(1, tiles >= resident ? 1 : std::min(ceil_div(resident, tiles), keys / (TILE_MIN_CHUNK * blocks * blocks)));
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -101,7 +99,7 @@ size_t attn_workspace_bytes(int seqs, int tokens, int max_new, int max_len, int 
     parts = std::max(parts, rows_parts(seqs, max_new, max_len, group, kv_heads, blocks, false));
   if ((int64_t)max_new * group > TILE_ROWS) {
     const TilePlan t = plan_tile(seqs, tokens, max_new, group, dim);
-    parts = std::max(parts, tile_parts(tokens, max_len, group, kv_heads, t.blocks));
+    parts = std::max(parts, tile_parts(seqs, tokens, max_new, max_len, group, kv_heads, t.blocks, dim));
     if (t.skip_upto > 0)
       for (int blocks = 1; blocks <= 2; ++blocks)
         parts = std::max(parts, rows_parts(seqs, t.skip_upto, max_len, group, kv_heads, blocks, false));
@@ -128,15 +126,18 @@ hipError_t launch_paged_attention(AttnArgs a, char* workspace) {
   if (tiles) {
     t = plan_tile(c.seqs, c.tokens, c.max_new, a.group, c.dim);
     const int64_t keys = seen(128 * t.blocks);
-    cut(keys, tile_parts(c.tokens, keys, a.group, c.kv_heads, t.blocks), 64, &t.chunk, &t.splits);
+    cut(keys, tile_parts(c.seqs, c.tokens, c.max_new, keys, a.group, c.kv_heads, t.blocks, c.dim), 64, &t.chunk, &t.splits);
     few = t.skip_upto;
   }
   if (few > 0) {
-    // Next to many-row sequences most of the others have one token.
-    blocks = tiles || (V_F1 && a.dtype == DT_F32) || (int64_t)few * a.group <= 16 ? 1 : 2;
+    // 16-bit rows go 16 to a workgroup: two blocks keep a wave alone on its SIMD,
+    // and what they save is read from L2 (20 sequences of 8 tokens, 4 heads a
+    // group: 126 us in 32 rows, 91 in 16).  In 32 bits the matrix cores bound
+    // them (300 tokens of 3 sequences: 365 us in 32 rows, 476 in 16).
+    blocks = a.dtype != DT_F32 || (int64_t)few * a.group <= 16 ? 1 : 2;
     const int64_t keys = seen(16 * blocks);
     r.row_tiles = (int)ceil_div((int64_t)few * a.group, 16 * blocks);
-    const bool wide = padded(c.dim) * (a.dtype == DT_F32 ? 4 : 2) * blocks > V_WIDE;
+    const bool wide = padded(c.dim) * (a.dtype == DT_F32 ? 4 : 2) * blocks > 768;
     cut(keys, rows_parts(c.seqs, few, keys, a.group, c.kv_heads, blocks, wide), ROWS_MIN_CHUNK,
         &r.chunk, &r.splits);
   }

@@ -27,7 +27,7 @@ constexpr size_t rows_lds_bytes(int row_bytes, int dp) {
 // Waves a SIMD that the registers are cut for.
 template <int DT, int DP, int NB> struct RowsWaves {
   static constexpr int RB = DP * (DT == DT_F32 ? 4 : 2);
-  static constexpr int N = RB * NB <= 256 ? 2 : 1;
+  static constexpr int N = RB * NB <= 768 ? 2 : 1;
 };
 
 template <int DT, int DP, int NB, bool CAP>
@@ -411,9 +411,10 @@ hipError_t launch_rows(const AttnArgs& a, const RowsPlan& plan, int skip_above) 
 template <int DT>
 hipError_t launch_rows_type(const AttnArgs& a, const RowsPlan& plan, int blocks, int skip_above) {
   const int d = a.c.dim;
-#define QMM_ROWS(DP)                                                             \
-  if (d <= DP) return blocks == 1 ? launch_rows<DT, DP, 1>(a, plan, skip_above)  \
-                                  : launch_rows<DT, DP, 2>(a, plan, skip_above);
+#define QMM_ROWS(DP)                                                                    \
+  if (d <= DP) return DT != DT_F32 || blocks == 1                                       \
+                          ? launch_rows<DT, DP, 1>(a, plan, skip_above)                 \
+                          : launch_rows<DT, DP, DT == DT_F32 ? 2 : 1>(a, plan, skip_above);
   QMM_ROWS(64) QMM_ROWS(96) QMM_ROWS(128) QMM_ROWS(192) QMM_ROWS(256)
 #undef QMM_ROWS
   return hipErrorInvalidValue;

@@ -72,7 +72,7 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   constexpr int SR = 64 / WAVES, IT = (SR * CH + 63) / 64;   // rows of a group that a wave loads
   constexpr int THREADS = 64 * WAVES, ROWS = 32 * NQ * WAVES;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  __shared__ int found[4];
+  __shared__ int found[5];
   __shared__ int odd;
 
   const CacheArgs& c = a.c;
@@ -88,10 +88,12 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   const int want = id / plan.splits, split = (id % plan.splits + want) % plan.splits;
   if (wave == 0) {
     int base = 0, seq = -1, tile = 0;
+    Seq of{};
     for (int s0 = 0; s0 < c.seqs && seq < 0; s0 += 64) {
       int mine = 0;
+      Seq q{};
       if (s0 + lane < c.seqs) {
-        const Seq q = seq_of(c, s0 + lane);
+        q = seq_of(c, s0 + lane);
         if (q.n > plan.skip_upto) mine = (q.n * a.group + ROWS - 1) / ROWS;
       }
       int sum = mine;
@@ -106,12 +108,18 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
         const int w = __builtin_ctzll(who);
         seq = s0 + w;
         tile = want - base - (__shfl(sum, w) - __shfl(mine, w));
+        of.t0 = __shfl(q.t0, w);
+        of.n = __shfl(q.n, w);
+        of.len = __shfl(q.len, w);
       }
       base += __shfl(sum, 63);
     }
     if (lane == 0) {
       found[0] = seq;
       found[1] = tile;
+      found[2] = of.t0;
+      found[3] = of.n;
+      found[4] = of.len;
       odd = 0;
     }
   }
@@ -119,7 +127,8 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   const int seq = __builtin_amdgcn_readfirstlane(found[0]);
   const int tile = __builtin_amdgcn_readfirstlane(found[1]);
   if (seq < 0) return;
-  const Seq sq = seq_of(c, seq);
+  const Seq sq{__builtin_amdgcn_readfirstlane(found[2]), __builtin_amdgcn_readfirstlane(found[3]),
+               __builtin_amdgcn_readfirstlane(found[4])};
   const int rows = sq.n * a.group, row0 = tile * ROWS;
   const int row1 = rows < row0 + ROWS ? rows : row0 + ROWS;
   const int pos0 = sq.len - sq.n;
@@ -428,9 +437,10 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
         for (int b = 0; b < NQ; ++b) o[b][v % DB] = Mfma32<DT>::run(vf[v], p[b][v / DB], o[b][v % DB]);
       }
       if (j + LEAD < VS) vf[j + LEAD] = value(vb, row, (j + LEAD) / DB, (j + LEAD) % DB);
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-        if (j == KS + (k + LEAD < VS ? k + LEAD : k + LEAD - VS)) kf[k] = key(kb, row, k);
+      if (j >= KS) {
+        const int x = j - KS, k = x >= LEAD ? x - LEAD : x + VS - LEAD;
+        if (k < KS && (x < LEAD || k + LEAD < VS)) kf[k] = key(kb, row, k);
+      }
 #pragma unroll
       for (int i = 16 * j / SLOTS; i < 16 * (j + 1) / SLOTS; ++i) prob(s, q, i);
       if (stage) {
@@ -469,22 +479,35 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   for (int x = threadIdx.x; x < 128 * (CH - chunks); x += THREADS)
     *(u32x4*)(lds + x % 128 / 64 * L::KBUF + x % 64 * L::KROW + (chunks + x / 128) * 16) =
         u32x4{0, 0, 0, 0};
-  // K groups -2 and -1 hold steps 0, 1 and 2; V group 0 belongs to the first
-  // look-up of its own.
+  // K groups -2 and -1 hold steps 0, 1 and 2.  The first five groups' places
+  // are looked up together, and then loaded together: each wait is a latency.
+  Stage k2, k1;
   if (sq.len > 0) {
-    look_up(-2);
-    load(row_address(), 0, gk);
-    store_k(-2, gk);
-    look_up(-1);
-    load(row_address(), 0, gk);
-    store_k(-1, gk);
-    look_up(0);
-    const uint64_t rows = row_address();
-    load(rows, 0, gk);
-    load(rows, 1, gv);
+    uint64_t rows[4];
+    int pages[4], ats[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      look_up(i - 2);
+      pages[i] = page;
+      ats[i] = at;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      page = pages[i];
+      at = ats[i];
+      rows[i] = row_address();
+    }
+    look_up(2);
+    load(rows[0], 0, k2);
+    load(rows[1], 0, k1);
+    load(rows[2], 1, gv);
+    load(rows[2], 0, gk);
+    store_k(-2, k2);
+    store_k(-1, k1);
     store_v(0, gv);
     mend_v(0);
-    look_up(1);
+    load(rows[3], 0, k1);
+    load(rows[3], 1, gv);
   }
   __syncthreads();
   scores(kbuf(-2), 32, s0);
@@ -506,12 +529,7 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   for (int k = 0; k < KS; ++k) kf[k] = key(kbuf(-1), 32, k);
   __syncthreads();
   store_k(0, gk);
-  if (sq.len > 0) {
-    const uint64_t rows = row_address();
-    look_up(2);
-    load(rows, 0, gk);
-    load(rows, 1, gv);
-  }
+  gk = k1;
   const int iters = (steps + 1) / 2;
   for (int t = 0; t < iters; ++t) {
     __syncthreads();
