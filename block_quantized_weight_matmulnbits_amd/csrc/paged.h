@@ -100,9 +100,10 @@ hipError_t launch_rows_bf16(const AttnArgs& a, const RowsPlan& plan, int blocks,
 // more than skip_upto new tokens.
 struct TilePlan {
   int splits, chunk, tiles, blocks, skip_upto, note;
+  int few_groups;   // workgroups after them that take the other sequences (`few`)
 };
-hipError_t launch_tile_f16(const AttnArgs& a, const TilePlan& plan);
-hipError_t launch_tile_bf16(const AttnArgs& a, const TilePlan& plan);
+hipError_t launch_tile_f16(const AttnArgs& a, const TilePlan& plan, const RowsPlan& few);
+hipError_t launch_tile_bf16(const AttnArgs& a, const TilePlan& plan, const RowsPlan& few);
 
 // The bookkeeping of the pages (strides and sizes of `data` in bytes).
 struct PoolArgs {

@@ -19,10 +19,10 @@ constexpr int DT_F32 = 0, DT_F16 = 1;
 // and a half over (as many tiles of rows are not split), or by one where a lane's registers leave room for no more.
 constexpr int64_t ROWS_FILL = 2048, ROWS_FILL_WIDE = 256, ROWS_MIN_CHUNK = 128, ROWS_MAX_CHUNK = 1024;
 // Tiles kernel: workgroups of 128 rows are resident twice on a compute unit
-// (once for heads over 128), those of 256 once.  The former are split to what
-// is resident at once (10 sequences of 48 rows, 8 heads, to 4000 keys: 61 us in
-// 560 parts, 72 in 240, 79 in 1200), the latter, whose sequences are long and uneven, to
-// twice that (three chunks of 509 tokens: 288 us, 327 in four times).
+// (once for heads over 128), those of 256 once; they are split to what is
+// resident at once.  10 sequences of 48 rows, 8 heads and 1500 to 4000 keys take
+// 61 us in 560 parts, 72 in 240, 79 in 1200; 192 tiles of 256 rows and 4096 keys
+// 115 us whole, 158 in three parts, which run in three rounds and are joined.
 // Sequences with up to TILE_ROWS rows are left to the rows kernel.
 constexpr int64_t UNITS = 256, TILE_MIN_CHUNK = 128, TILE_ROWS = 32;
 
@@ -65,11 +65,12 @@ TilePlan plan_tile(int seqs, int tokens, int max_new, int group, int dim) {
 int64_t tile_parts(int seqs, int tokens, int max_new, int64_t keys, int group, int kv_heads,
                    int blocks, int dim) {
   // Tiles: of equal sequences, or else whole ones of the batch's rows.
-  const int64_t height = 128 * blocks, resident = UNITS * (blocks == 1 && dim > 128 ? 1 : 2);
+  const int64_t height = 128 * blocks, resident = UNITS * (blocks == 2 || dim > 128 ? 1 : 2);
   const int64_t tiles = kv_heads * ((int64_t)seqs * max_new == tokens
                                         ? seqs * ceil_div((int64_t)max_new * group, height)
                                         : ceil_div((int64_t)tokens * group, height));
-  return std::max<int64_t>(1, tiles >= resident ? 1 : std::min(ceil_div(resident, tiles), keys / (TILE_MIN_CHUNK * blocks * blocks)));
+  const int64_t parts = blocks == 2 ? resident / tiles : ceil_div(resident, tiles);
+  return std::max<int64_t>(1, std::min(tiles >= resident ? 1 : parts, keys / TILE_MIN_CHUNK));
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -100,9 +101,7 @@ size_t attn_workspace_bytes(int seqs, int tokens, int max_new, int max_len, int 
   if ((int64_t)max_new * group > TILE_ROWS) {
     const TilePlan t = plan_tile(seqs, tokens, max_new, group, dim);
     parts = std::max(parts, tile_parts(seqs, tokens, max_new, max_len, group, kv_heads, t.blocks, dim));
-    if (t.skip_upto > 0)
-      for (int blocks = 1; blocks <= 2; ++blocks)
-        parts = std::max(parts, rows_parts(seqs, t.skip_upto, max_len, group, kv_heads, blocks, false));
+    if (t.skip_upto > 0) parts = std::max(parts, ceil_div(max_len, ROWS_MAX_CHUNK));
   }
   return 256 + (parts > 1 ? align256(parts_bytes(rows, parts, dim)) : 0);
 }
@@ -137,9 +136,11 @@ hipError_t launch_paged_attention(AttnArgs a, char* workspace) {
     blocks = a.dtype != DT_F32 || (int64_t)few * a.group <= 16 ? 1 : 2;
     const int64_t keys = seen(16 * blocks);
     r.row_tiles = (int)ceil_div((int64_t)few * a.group, 16 * blocks);
+    // Beside tiles parts only keep the longest of them from being the last.
+    int64_t parts = ceil_div(keys, ROWS_MAX_CHUNK);
     const bool wide = padded(c.dim) * (a.dtype == DT_F32 ? 4 : 2) * blocks > 768;
-    cut(keys, rows_parts(c.seqs, few, keys, a.group, c.kv_heads, blocks, wide), ROWS_MIN_CHUNK,
-        &r.chunk, &r.splits);
+    if (!tiles) parts = rows_parts(c.seqs, few, keys, a.group, c.kv_heads, blocks, wide);
+    cut(keys, parts, ROWS_MIN_CHUNK, &r.chunk, &r.splits);
   }
   const int splits = std::max(t.splits, r.splits);
   if (splits > 1) attn_parts(&a, workspace, splits);
@@ -152,14 +153,15 @@ hipError_t launch_paged_attention(AttnArgs a, char* workspace) {
     t.note = t.splits > 1;
     r.note = r.splits > 1;
   }
-  hipError_t e = hipSuccess;
-  if (few > 0) {
-    const int skip_above = tiles ? few : INT32_MAX;
-    e = a.dtype == DT_F32 ? launch_rows_f32(a, r, blocks, skip_above)
-        : a.dtype == DT_F16 ? launch_rows_f16(a, r, blocks, skip_above)
-                            : launch_rows_bf16(a, r, blocks, skip_above);
+  hipError_t e;
+  if (tiles) {
+    if (few > 0) t.few_groups = c.seqs * r.row_tiles * c.kv_heads * r.splits;
+    e = a.dtype == DT_F16 ? launch_tile_f16(a, t, r) : launch_tile_bf16(a, t, r);
+  } else {
+    e = a.dtype == DT_F32 ? launch_rows_f32(a, r, blocks, INT32_MAX)
+        : a.dtype == DT_F16 ? launch_rows_f16(a, r, blocks, INT32_MAX)
+                            : launch_rows_bf16(a, r, blocks, INT32_MAX);
   }
-  if (e == hipSuccess && tiles) e = a.dtype == DT_F16 ? launch_tile_f16(a, t) : launch_tile_bf16(a, t);
   if (e == hipSuccess && join) e = launch_join(a, padded(c.dim), splits);
   return e;
 }

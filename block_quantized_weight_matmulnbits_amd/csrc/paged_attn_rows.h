@@ -18,10 +18,11 @@
 namespace qmm {
 
 constexpr int ROWS_WAVES = 4, ROWS_THREADS = 64 * ROWS_WAVES, ROWS_BLOCK = 32;
+#define QMM_INLINE __attribute__((always_inline))
 
-constexpr size_t rows_lds_bytes(int row_bytes, int dp) {
+constexpr size_t rows_lds_bytes(int row_bytes, int dp, int waves) {
   const size_t v = (size_t)ROWS_BLOCK * row_bytes, o = (size_t)16 * (dp + 4) * 4;
-  return ROWS_WAVES * (v > o ? v : o);
+  return waves * (v > o ? v : o);
 }
 
 // Waves a SIMD that the registers are cut for.
@@ -30,9 +31,11 @@ template <int DT, int DP, int NB> struct RowsWaves {
   static constexpr int N = RB * NB <= 768 ? 2 : 1;
 };
 
-template <int DT, int DP, int NB, bool CAP>
-__global__ __launch_bounds__(ROWS_THREADS, (RowsWaves<DT, DP, NB>::N)) void attn_rows_kernel(AttnArgs a, RowsPlan plan,
-                                                                 ScoreScale scale, int skip_above) {
+// One workgroup of WAVES waves, number `id` of the plan's.
+template <int DT, int DP, int NB, int WAVES, bool CAP>
+__device__ __forceinline__ void attn_rows(const AttnArgs& a, const RowsPlan& plan,
+                                          const ScoreScale& scale, int skip_above, uint32_t id,
+                                          char* lds) {
   constexpr bool F32 = DT == DT_F32;
   using T = typename dt<DT>::T;
   constexpr int ES = (int)sizeof(T), RB = DP * ES;   // bytes of a padded row
@@ -44,8 +47,7 @@ __global__ __launch_bounds__(ROWS_THREADS, (RowsWaves<DT, DP, NB>::N)) void attn
   constexpr bool AHEAD = RB <= 512;
   constexpr int VBYTES = ROWS_BLOCK * RB;
   constexpr int OSTRIDE = DP + 4;
-  extern __shared__ __attribute__((aligned(1024))) char lds[];
-  __shared__ float2 wave_ml[ROWS_WAVES][16];
+  __shared__ float2 wave_ml[WAVES][16];
 
   const CacheArgs& c = a.c;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l15 = lane & 15, g = lane >> 4;
@@ -53,13 +55,13 @@ __global__ __launch_bounds__(ROWS_THREADS, (RowsWaves<DT, DP, NB>::N)) void attn
   // and the last parts of short sequences have no work: turned by the rest of
   // the number, every XCD gets first parts and last ones alike (64 sequences
   // of 17 to 8191 keys, in parts of 1024: 296 us without, 235 with).
-  uint32_t id = blockIdx.x;
   const int split = (id % plan.splits + id / plan.splits) % plan.splits;
   id /= plan.splits;
   const int kvh = id % c.kv_heads;
   id /= c.kv_heads;
   const int tile = id % plan.row_tiles, seq = id / plan.row_tiles;
 
+  if (seq >= c.seqs) return;
   const Seq sq = seq_of(c, seq);
   const int rows = sq.n * a.group, row0 = tile * 16 * NB;
   if (row0 >= rows || sq.n > skip_above) return;
@@ -167,7 +169,7 @@ __global__ __launch_bounds__(ROWS_THREADS, (RowsWaves<DT, DP, NB>::N)) void attn
     rw = rows_at(kb);
     load_k(rw, kf);
   }
-  for (; kb < end; kb += ROWS_BLOCK * ROWS_WAVES) {
+  for (; kb < end; kb += ROWS_BLOCK * WAVES) {
     if constexpr (!AHEAD) {
       rw = rows_at(kb);
       load_k(rw, kf);
@@ -178,7 +180,7 @@ __global__ __launch_bounds__(ROWS_THREADS, (RowsWaves<DT, DP, NB>::N)) void attn
 #pragma unroll
       for (int t = 0; t < 2; ++t) load_to_lds(piece(rw.v[t], s), vl + (s * 2 + t) * 1024);
     u32x4 kn[AHEAD ? 2 : 1][AHEAD ? KS : 1];
-    const int next = kb + ROWS_BLOCK * ROWS_WAVES;
+    const int next = kb + ROWS_BLOCK * WAVES;
     if constexpr (AHEAD) {
       if (next < end) {
         rw = rows_at(next);
@@ -360,16 +362,16 @@ __global__ __launch_bounds__(ROWS_THREADS, (RowsWaves<DT, DP, NB>::N)) void attn
     for (int d = 0; d < DB; ++d)
       *(f32x4*)(ol + (wave * 16 + l15) * OSTRIDE + 16 * d + 4 * g) = o[b][d];
     __syncthreads();
-    for (int e = threadIdx.x; e < 16 * (DP / 4); e += ROWS_THREADS) {
+    for (int e = threadIdx.x; e < 16 * (DP / 4); e += 64 * WAVES) {
       const int q = e / (DP / 4), d = e % (DP / 4) * 4, r = row0 + 16 * b + q;
       if (r >= row1 || d >= c.dim) continue;
       float top = -INFINITY, total = 0.f;
 #pragma unroll
-      for (int w = 0; w < ROWS_WAVES; ++w) top = fmaxf(top, wave_ml[w][q].x);
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, wave_ml[w][q].x);
       const float ref = top == -INFINITY ? 0.f : top;
       f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < ROWS_WAVES; ++w) {
+      for (int w = 0; w < WAVES; ++w) {
         const float f = exp2_fast(wave_ml[w][q].x - ref);
         total += f * wave_ml[w][q].y;
         x += f * *(const f32x4*)(ol + (w * 16 + q) * OSTRIDE + d);
@@ -391,10 +393,17 @@ __global__ __launch_bounds__(ROWS_THREADS, (RowsWaves<DT, DP, NB>::N)) void attn
   }
 }
 
+template <int DT, int DP, int NB, bool CAP>
+__global__ __launch_bounds__(ROWS_THREADS, (RowsWaves<DT, DP, NB>::N)) void attn_rows_kernel(
+    AttnArgs a, RowsPlan plan, ScoreScale scale, int skip_above) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  attn_rows<DT, DP, NB, ROWS_WAVES, CAP>(a, plan, scale, skip_above, blockIdx.x, lds);
+}
+
 template <int DT, int DP, int NB>
 hipError_t launch_rows(const AttnArgs& a, const RowsPlan& plan, int skip_above) {
   constexpr int ES = (int)sizeof(typename dt<DT>::T);
-  constexpr size_t bytes = rows_lds_bytes(DP * ES, DP);
+  constexpr size_t bytes = rows_lds_bytes(DP * ES, DP, ROWS_WAVES);
   const bool cap = a.softcap > 0.f;
   const ScoreScale k = cap ? ScoreScale{a.scale / a.softcap, a.softcap * LOG2E}
                            : ScoreScale{a.scale * LOG2E, 0.f};

@@ -9,6 +9,11 @@
 // step (matrix cores), the exponentials of this one (vector units) and the
 // product of the last one's probabilities with V (matrix cores).
 //
+// The last workgroups of a launch take the sequences with few rows, as the rows
+// kernel does: they fill the compute units that the tiles leave (three chunks
+// of 509 tokens and six single ones: 258 us in two launches, 246 in one, 270
+// with the few rows first).
+//
 // K and V pass through LDS in groups of two steps, two groups of each: the
 // global loads of a group are in flight for a whole group's work before they
 // are written to LDS.  Rows are padded there (K by 16 bytes, V to an odd
@@ -18,6 +23,7 @@
 #pragma once
 
 #include "paged_attn.h"
+#include "paged_attn_rows.h"
 #include "qmm_internal.h"
 
 namespace qmm {
@@ -48,8 +54,6 @@ __device__ __forceinline__ float pair_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-#define QMM_INLINE __attribute__((always_inline))
-
 // DK: the head's width in scores (16s), DV: in outputs (32s).
 template <int DK, int DV> struct TileLds {
   static constexpr int KROW = DK * 2 + 16, VROW = DV * 2 + (DV % 64 == 32 ? 0 : 64);
@@ -62,8 +66,8 @@ template <int DK, int DV> struct TileLds {
 constexpr float TILE_SLACK = 8.f;
 
 template <int DT, int DK, int DV, int WAVES, bool CAP>
-__global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kernel(AttnArgs a, TilePlan plan,
-                                                                    ScoreScale scale) {
+__global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kernel(
+    AttnArgs a, TilePlan plan, RowsPlan few, ScoreScale scale) {
   using T = typename dt<DT>::T;
   using L = TileLds<DK, DV>;
   using Op = MfmaOp<DT>;
@@ -71,11 +75,17 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   constexpr int NQ = 1;
   constexpr int SR = 64 / WAVES, IT = (SR * CH + 63) / 64;   // rows of a group that a wave loads
   constexpr int THREADS = 64 * WAVES, ROWS = 32 * NQ * WAVES;
+  constexpr int FEW = DV;   // the width that the few-row workgroups pad to
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   __shared__ int found[5];
   __shared__ int odd;
 
   const CacheArgs& c = a.c;
+  const uint32_t groups = (uint32_t)plan.tiles * plan.splits * c.kv_heads;
+  if (blockIdx.x >= groups) {
+    attn_rows<DT, FEW, 1, WAVES, CAP>(a, few, scale, plan.skip_upto, blockIdx.x - groups, lds);
+    return;
+  }
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l31 = lane & 31, half = lane >> 5, l15 = lane & 15;
 
@@ -611,32 +621,33 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
 }
 
 template <int DT, int DK, int DV, int WAVES>
-hipError_t launch_tile(const AttnArgs& a, const TilePlan& plan) {
+hipError_t launch_tile(const AttnArgs& a, const TilePlan& plan, const RowsPlan& few) {
   constexpr int THREADS = 64 * WAVES;
   const bool cap = a.softcap > 0.f;
   const ScoreScale k = cap ? ScoreScale{a.scale / a.softcap, a.softcap * LOG2E}
                            : ScoreScale{a.scale * LOG2E, 0.f};
-  constexpr int bytes = TileLds<DK, DV>::BYTES;
+  constexpr int need = (int)rows_lds_bytes(DV * 2, DV, WAVES);
+  constexpr int bytes = TileLds<DK, DV>::BYTES > need ? TileLds<DK, DV>::BYTES : need;
   const void* fn = cap ? (const void*)attn_tile_kernel<DT, DK, DV, WAVES, true>
                        : (const void*)attn_tile_kernel<DT, DK, DV, WAVES, false>;
   const hipError_t e = ensure_dynamic_lds(fn, bytes);
   if (e != hipSuccess) return e;
-  const dim3 grid((uint32_t)plan.tiles * plan.splits * a.c.kv_heads);
-  if (cap) attn_tile_kernel<DT, DK, DV, WAVES, true><<<grid, THREADS, bytes, a.stream>>>(a, plan, k);
-  else attn_tile_kernel<DT, DK, DV, WAVES, false><<<grid, THREADS, bytes, a.stream>>>(a, plan, k);
+  const dim3 grid((uint32_t)plan.few_groups + (uint32_t)plan.tiles * plan.splits * a.c.kv_heads);
+  if (cap) attn_tile_kernel<DT, DK, DV, WAVES, true><<<grid, THREADS, bytes, a.stream>>>(a, plan, few, k);
+  else attn_tile_kernel<DT, DK, DV, WAVES, false><<<grid, THREADS, bytes, a.stream>>>(a, plan, few, k);
   return hipGetLastError();
 }
 
 template <int DT>
-hipError_t launch_tile_type(const AttnArgs& a, const TilePlan& plan) {
+hipError_t launch_tile_type(const AttnArgs& a, const TilePlan& plan, const RowsPlan& few) {
   const int d = a.c.dim;
 #define QMM_TILE(DK, DV)                                                     \
-  if (d <= DK) return plan.blocks == 2 ? launch_tile<DT, DK, DV, 8>(a, plan) \
-                                       : launch_tile<DT, DK, DV, 4>(a, plan);
+  if (d <= DK) return plan.blocks == 2 ? launch_tile<DT, DK, DV, 8>(a, plan, few) \
+                                       : launch_tile<DT, DK, DV, 4>(a, plan, few);
   QMM_TILE(64, 64) QMM_TILE(80, 96) QMM_TILE(96, 96) QMM_TILE(128, 128)
 #undef QMM_TILE
-  if (d <= 192) return launch_tile<DT, 192, 192, 4>(a, plan);
-  return launch_tile<DT, 256, 256, 4>(a, plan);
+  if (d <= 192) return launch_tile<DT, 192, 192, 4>(a, plan, few);
+  return launch_tile<DT, 256, 256, 4>(a, plan, few);
 }
 
 }  // namespace qmm

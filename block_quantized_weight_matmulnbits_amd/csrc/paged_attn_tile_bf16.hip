@@ -3,8 +3,8 @@
 
 namespace qmm {
 
-hipError_t launch_tile_bf16(const AttnArgs& a, const TilePlan& plan) {
-  return launch_tile_type<DT_BF16>(a, plan);
+hipError_t launch_tile_bf16(const AttnArgs& a, const TilePlan& plan, const RowsPlan& few) {
+  return launch_tile_type<DT_BF16>(a, plan, few);
 }
 
 }  // namespace qmm
