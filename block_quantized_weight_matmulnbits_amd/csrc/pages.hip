@@ -372,6 +372,9 @@ __global__ __launch_bounds__(COPY_THREADS) void move_kernel(PoolArgs p, int32_t*
   copy_pages<V>(p, w.src, w.dst, *w.moves, per_page, by_vectors, by_planes);
 }
 
+// Division by n, which may be 0 where there is nothing to divide.
+FastDiv div_of(int64_t n) { return fast_div((uint32_t)(n > 0 ? n : 1)); }
+
 // Calls f with a value of the widest vector that the pages' bytes allow.
 template <typename F>
 hipError_t by_vector(const PoolArgs& p, F f) {
@@ -392,8 +395,7 @@ hipError_t launch_copy(const PoolArgs& p, const int32_t* src, const int32_t* dst
   return by_vector(p, [&](auto v) {
     const int64_t per = p.page_bytes / (int64_t)sizeof(v);
     copy_kernel<decltype(v)><<<copy_grid(p, count, per), COPY_THREADS, 0, p.stream>>>(
-        p, src, dst, moves, count, (uint32_t)per, fast_div((uint32_t)per),
-        fast_div((uint32_t)p.planes));
+        p, src, dst, moves, count, (uint32_t)per, div_of(per), div_of(p.planes));
     return hipGetLastError();
   });
 }
@@ -440,8 +442,7 @@ hipError_t launch_pages_compact(const PoolArgs& p, int32_t* refs_out, int32_t* t
     const int64_t per = p.page_bytes / (int64_t)sizeof(v);
     int grid = copy_grid(p, p.pages / 2 + 1, per);
     move_kernel<decltype(v)><<<grid, COPY_THREADS, 0, p.stream>>>(
-        p, refs_out, table_out, table_out_stride, live, (uint32_t)per, fast_div((uint32_t)per),
-        fast_div((uint32_t)p.planes), fast_div((uint32_t)(p.width > 0 ? p.width : 1)));
+        p, refs_out, table_out, table_out_stride, live, (uint32_t)per, div_of(per), div_of(p.planes), fast_div((uint32_t)(p.width > 0 ? p.width : 1)));
     return hipGetLastError();
   });
 }

@@ -151,13 +151,13 @@ def test_what_masked_keys_hold_does_not_matter(dtype, bad):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("n", [7, 150])
-def test_a_bad_value_reaches_only_the_tokens_that_see_it(dtype, n):
+@pytest.mark.parametrize("n,D", [(7, 64), (150, 64), (150, 128), (40, 256)])
+def test_a_bad_value_reaches_only_the_tokens_that_see_it(dtype, n, D):
     def spoil(kp, vp, table, lens):
         j = int(lens[0]) - 3   # seen by the last three tokens alone
         vp[table[0, j // 16], 0, j % 16, 5] = float("inf")
         vp[table[0, j // 16], 1, j % 16, 9] = float("nan")
-    run(dtype, [n], [210], 4, 2, 64, spoil=spoil)
+    run(dtype, [n], [210], 4, 2, D, spoil=spoil)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -248,3 +248,40 @@ def test_another_stream_and_replays_in_a_step():
         torch.cuda.synchronize()
         assert torch.equal(out, direct)
     step.close()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [1, 50])
+@pytest.mark.parametrize("far", [1 << 29, 1 << 30])
+def test_caches_past_32_bits_of_bytes(dtype, n, far):
+    """Pages `far` elements apart: the last one starts past 2^32 bytes."""
+    q = qmm()
+    page, KV, D, total, length = 16, 1, 64, 6, 90
+    size = torch.finfo(dtype).bits // 8
+    pages = min(total, (9 << 30) // (far * size) + 1)
+    length = min(length, pages * page)
+    whole = torch.empty(far * (pages - 1) + page * D * 2, dtype=dtype, device=DEV)
+    g = torch.Generator().manual_seed(n)
+    k, v = (torch.randn(pages, KV, page, D, generator=g).to(dtype) for _ in range(2))
+    views = [whole[i * page * D:].as_strided(k.shape, (far, page * D, D, 1)) for i in range(2)]
+    views[0].copy_(k)
+    views[1].copy_(v)
+    table = np.arange(pages)[::-1].copy()[None].astype(np.int32)
+    starts, lens = np.array([0, n], np.int32), np.array([length], np.int32)
+    x = torch.randn(n, 4, D, generator=g).to(dtype)
+    kv = q.PagedKV(*views)
+    batch = q.PagedBatch(dev(starts), dev(lens), dev(table), n, n, length)
+    out = torch.empty(n, 4, D, dtype=dtype, device=DEV)
+    ws = torch.empty(q.qmm_paged_attention_workspace_size(batch, 4, KV, D), dtype=torch.uint8, device=DEV)
+    q.qmm_paged_attention(x.to(DEV), kv, batch, out, ws)
+    want = ref.attention(x, k, v, starts, lens, table, ref.default_scale(D))
+    torch.cuda.synchronize()
+    ref.assert_close(out, want[0], ref.rounded(want[0], want[2], dtype), "out")
+    # The append, to the same places.
+    new = torch.randn(n, KV, D, generator=g).to(dtype)
+    f = ref.frequencies(D // 2)
+    wout = ref.rope(x, new, new, k, v, starts, lens, table, f)
+    q.qmm_rope_append(x.to(DEV), new.to(DEV), new.to(DEV), out, kv, batch, dev(f))
+    torch.cuda.synchronize()
+    ref.assert_close(views[0], wout[1], np.where(wout[4] > 0, ref.rounded(wout[1], wout[4], dtype), 0.0), "k")
+    ref.assert_close(views[1], wout[2], 0.0, "v")

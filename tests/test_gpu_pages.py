@@ -196,3 +196,32 @@ def test_reserve_replays_in_a_step():
         b.plain.reserve([0, 1, 2], [1, 1, 1])
         b.same("step")
     step.close()
+
+
+@pytest.mark.parametrize("shape", [(0, 20, 8), (3, 20, 0)])
+def test_a_pool_without_contents_keeps_its_tables(shape):
+    q = qmm()
+    b = Both(20, 4, 6, 5, {0: 9, 1: 4, 3: 16}, shape=(8,))
+    b.pool = q.PagePool(torch.empty(shape, dtype=torch.int16, device=DEV), b.refs, b.table, b.lens, 4)
+    b.fork([0], [2])
+    b.plain.data = b.data.cpu().numpy()
+    b.same("fork")
+    refs, table = torch.empty_like(b.refs), torch.empty_like(b.table)
+    live = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q.qmm_pages_compact(b.pool, refs, table, live, b.ws)
+    torch.cuda.synchronize()
+    assert live.item() == b.plain.compact()
+    np.testing.assert_array_equal(refs.cpu().numpy(), b.plain.refs)
+    np.testing.assert_array_equal(table.cpu().numpy(), b.plain.table)
+
+
+def test_pages_past_32_bits_of_bytes():
+    q = qmm()
+    stride = (1 << 30) + 64                      # bytes between pages
+    whole = torch.empty(6 * stride, dtype=torch.uint8, device=DEV)
+    data = whole.as_strided((1, 6, 256), (6 * stride, stride, 1))
+    data[0, 1] = 7
+    data[0, 5] = 9
+    q.qmm_pages_copy(q.PagePool(data), dev([5, 1]), dev([0, 4]))
+    torch.cuda.synchronize()
+    assert data[0, 0].eq(9).all() and data[0, 4].eq(7).all()
