@@ -48,6 +48,23 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
 }
 
+// The value of lane n of each 16 (n is a constant once loops are unrolled).
+template <int N> __device__ __forceinline__ uint32_t row_lane(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x150 + N, 0xF, 0xF, true);
+}
+__device__ __forceinline__ uint32_t row_broadcast(uint32_t v, int n) {
+  switch (n) {
+    case 0: return row_lane<0>(v);
+    case 1: return row_lane<1>(v);
+    case 2: return row_lane<2>(v);
+    case 3: return row_lane<3>(v);
+    case 4: return row_lane<4>(v);
+    case 5: return row_lane<5>(v);
+    case 6: return row_lane<6>(v);
+    default: return row_lane<7>(v);
+  }
+}
+
 // Maximum and sum over the four lanes that share a column (lane mod 16).
 __device__ __forceinline__ float col_max(float v) {
   v = fmaxf(v, __shfl_xor(v, 16));

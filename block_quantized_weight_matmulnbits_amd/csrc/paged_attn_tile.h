@@ -1,13 +1,19 @@
 // paged_attn_tile.h -- attention of many new tokens over a paged cache, for
 // 16-bit types: the bound is the matrix cores.
 //
-// A workgroup of four waves takes 128 or 256 query rows (new tokens times the
-// heads of a group, packed) of one key/value head; every wave owns 32 NQ of
-// them from the first key to the last and keeps their queries, running
+// A workgroup of four or eight waves takes 128 or 256 query rows (new tokens
+// times the heads of a group, packed) of one key/value head; every wave owns 32
+// of them from the first key to the last and keeps their queries, running
 // statistics and outputs in registers.  Keys come in steps of 32.  A step's
 // three parts have nothing to wait for in one another: the scores of the next
 // step (matrix cores), the exponentials of this one (vector units) and the
 // product of the last one's probabilities with V (matrix cores).
+//
+// 4096 new tokens after 12288 cached ones (32 heads of 128 over 8): 925 us, 1040
+// TFLOP/s, where a large matrix product reaches 1290 on this chip.  The matrix
+// cores are busy half of the time at 1.85 GHz: the chip lowers its clock under
+// the load (128 workgroups instead of 256 run at 2.15 GHz), so what is left is
+// energy, most of it in LDS reads and exponentials.
 //
 // The last workgroups of a launch take the sequences with few rows, as the rows
 // kernel does: they fill the compute units that the tiles leave (three chunks
@@ -72,6 +78,8 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   using L = TileLds<DK, DV>;
   using Op = MfmaOp<DT>;
   constexpr int KS = DK / 16, DB = DV / 32, CH = DK / 8;   // score steps, output blocks, chunks
+  // Blocks of 32 rows a wave.  Two halve the LDS reads, but their registers
+  // leave a SIMD one wave, and nothing to run while it waits (1007 us, not 930).
   constexpr int NQ = 1;
   constexpr int SR = 64 / WAVES, IT = (SR * CH + 63) / 64;   // rows of a group that a wave loads
   constexpr int THREADS = 64 * WAVES, ROWS = 32 * NQ * WAVES;
@@ -200,7 +208,6 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   // K those three steps on, 2 n + 3 and 2 n + 4; this wave loads SR rows of
   // each, from SR wave on.
   const int32_t* table = c.table + (int64_t)seq * c.table_stride;
-  //
   // A lane moves 16 bytes of IT rows of each.  Lanes past the rows, or past the
   // head's own width, repeat the first row or piece, so that nothing in the
   // loop is conditional.
@@ -242,16 +249,8 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   auto bring = [&](uint64_t rows, int i, int v) QMM_INLINE {   // the address of load i of K or V
     uint32_t x, y;
     if constexpr (BY16) {
-      constexpr int BCAST = 0x150;   // row_newbcast
-      const int lo32 = (int)(uint32_t)rows, hi32 = (int)(uint32_t)(rows >> 32);
-      if (v * IT + i == 0) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 0, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 0, 0xF, 0xF, true); }
-      else if (v * IT + i == 1) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 1, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 1, 0xF, 0xF, true); }
-      else if (v * IT + i == 2) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 2, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 2, 0xF, 0xF, true); }
-      else if (v * IT + i == 3) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 3, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 3, 0xF, 0xF, true); }
-      else if (v * IT + i == 4) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 4, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 4, 0xF, 0xF, true); }
-      else if (v * IT + i == 5) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 5, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 5, 0xF, 0xF, true); }
-      else if (v * IT + i == 6) { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 6, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 6, 0xF, 0xF, true); }
-      else { x = __builtin_amdgcn_update_dpp(0, lo32, BCAST + 7, 0xF, 0xF, true); y = __builtin_amdgcn_update_dpp(0, hi32, BCAST + 7, 0xF, 0xF, true); }
+      x = row_broadcast((uint32_t)rows, v * IT + i);
+      y = row_broadcast((uint32_t)(rows >> 32), v * IT + i);
     } else {
       const int who = (16 * v + srow[i]) * 4;
       x = __builtin_amdgcn_ds_bpermute(who, (int)(uint32_t)rows);
