@@ -23,6 +23,8 @@ namespace {
 
 constexpr int PLAN_THREADS = 1024, PLAN_LDS = 1024;
 constexpr int COPY_THREADS = 256, COPY_FLIGHT = 2;
+// A compaction of at most so many pages and copying workgroups is one launch.
+constexpr int NEAR_PAGES = 1024, NEAR_GRID = 4096;
 
 // Workspace: the number of pages to copy, then the lists.
 struct Plan {
@@ -292,48 +294,60 @@ __global__ __launch_bounds__(PLAN_THREADS) void take_kernel(PoolArgs p, const in
   if (FORK && tid == 0) *w.moves = (int)needed;
 }
 
-// The used pages at or past `live` (the number of used pages) move to the
-// holes before it, the k-th to the k-th.  Leaves the moves and the map of
-// every page in the workspace.
-__global__ __launch_bounds__(PLAN_THREADS) void compact_kernel(PoolArgs p, int32_t* live_out) {
-  __shared__ int part[PLAN_THREADS / 64];
-  const int tid = threadIdx.x;
-  const Plan w = plan_of(p.workspace, p.pages, 0);
-  int mine = 0, live;
-  for (int page = 4 * tid; page < p.pages; page += 4 * PLAN_THREADS) {
-    const i32x4 refs = refs_at(p, page);
+// Compaction: the used pages at or past `live` (the number of used pages) move
+// to the holes before it, the k-th to the k-th.  Fills the moves and the map of
+// every page to its new place; every thread of the workgroup calls it.
+struct Moves {
+  int live, count;
+};
+__device__ __forceinline__ Moves plan_moves(const PoolArgs& p, int* part, int32_t* src, int32_t* dst,
+                                            int32_t* map) {
+  const int tid = threadIdx.x, stride = 4 * blockDim.x;
+  const i32x4 front = refs_at(p, 4 * tid);
+  int mine = 0;
+  Moves m;
+  for (int page = 4 * tid; page < p.pages; page += stride) {
+    const i32x4 refs = page < stride ? front : refs_at(p, page);
 #pragma unroll
     for (int k = 0; k < 4; ++k) mine += page + k < p.pages && refs[k] > 0;
   }
-  block_scan(mine, part, live);
-  int holes = 0, moves = 0;
-  for (int base = 0; base < p.pages; base += 4 * PLAN_THREADS) {
+  block_scan(mine, part, m.live);
+  int holes = 0;
+  m.count = 0;
+  for (int base = 0; base < p.pages; base += stride) {
     const int page = base + 4 * tid;
-    const i32x4 refs = refs_at(p, page);
+    const i32x4 refs = base == 0 ? front : refs_at(p, page);
     int mark = 0, sum;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const bool in = page + k < p.pages, used = in && refs[k] > 0;
-      mark += (in && !used && page + k < live) + ((used && page + k >= live) << 16);
+      mark += (in && !used && page + k < m.live) + ((used && page + k >= m.live) << 16);
     }
     // At most 4096 of each, so both counts travel in one scan.
     const int before = block_scan(mark, part, sum);
-    int hole = holes + (before & 0xFFFF), move = moves + (before >> 16);
+    int hole = holes + (before & 0xFFFF), move = m.count + (before >> 16);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const bool in = page + k < p.pages, used = in && refs[k] > 0;
-      if (in && !used && page + k < live) w.dst[hole++] = page + k;
-      if (used && page + k >= live) w.src[move++] = page + k;
-      else if (in) w.fresh[page + k] = page + k;
+      if (in && !used && page + k < m.live) dst[hole++] = page + k;
+      if (used && page + k >= m.live) src[move++] = page + k;
+      else if (in) map[page + k] = page + k;
     }
     holes += sum & 0xFFFF;
-    moves += sum >> 16;
+    m.count += sum >> 16;
   }
   __syncthreads();
-  for (int k = tid; k < moves; k += PLAN_THREADS) w.fresh[w.src[k]] = w.dst[k];
-  if (tid == 0) {
-    *w.moves = moves;
-    *live_out = live;
+  for (int k = tid; k < m.count; k += blockDim.x) map[src[k]] = dst[k];
+  return m;
+}
+
+__global__ __launch_bounds__(PLAN_THREADS) void compact_kernel(PoolArgs p, int32_t* live_out) {
+  __shared__ int part[PLAN_THREADS / 64];
+  const Plan w = plan_of(p.workspace, p.pages, 0);
+  const Moves m = plan_moves(p, part, w.src, w.dst, w.fresh);
+  if (threadIdx.x == 0) {
+    *w.moves = m.count;
+    *live_out = m.live;
   }
 }
 
@@ -347,29 +361,48 @@ __global__ __launch_bounds__(COPY_THREADS) void copy_kernel(PoolArgs p, const in
 }
 
 // The copies of a compaction, with its counts and table written out anew.
-template <typename V>
+// NEAR: a small pool, which every workgroup plans for itself, in LDS, instead of
+// waiting for a launch that does (257 pages of 4 planes: 9.4 us in two launches,
+// 8.3 in one; with 8 planes of 1000 pages the plans of 8192 workgroups cost more
+// than the launch, 26 us against 21).
+template <typename V, bool NEAR>
 __global__ __launch_bounds__(COPY_THREADS) void move_kernel(PoolArgs p, int32_t* refs_out,
                                                             int32_t* table_out,
                                                             int64_t table_out_stride,
-                                                            const int32_t* live,
-                                                            uint32_t per_page, FastDiv by_vectors,
-                                                            FastDiv by_planes, FastDiv by_width) {
+                                                            int32_t* live, uint32_t per_page,
+                                                            FastDiv by_vectors, FastDiv by_planes,
+                                                            FastDiv by_width) {
+  __shared__ int part[COPY_THREADS / 64];
+  __shared__ int32_t near_src[NEAR ? NEAR_PAGES : 1], near_dst[NEAR ? NEAR_PAGES : 1],
+      near_map[NEAR ? NEAR_PAGES : 1];
   const Plan w = plan_of(p.workspace, p.pages, 0);
+  const int32_t *src = NEAR ? near_src : w.src, *dst = NEAR ? near_dst : w.dst;
+  const int32_t* map = NEAR ? near_map : w.fresh;
+  int n, moves;
+  if constexpr (NEAR) {
+    const Moves m = plan_moves(p, part, near_src, near_dst, near_map);
+    __syncthreads();
+    n = m.live;
+    moves = m.count;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *live = n;
+  } else {
+    n = *live;
+    moves = *w.moves;
+  }
   const int64_t threads = (int64_t)gridDim.x * COPY_THREADS;
   const int64_t id = (int64_t)blockIdx.x * COPY_THREADS + threadIdx.x;
-  const int n = *live;
   for (int64_t page = id; page < p.pages; page += threads) {
     const int refs = p.refs[page];
-    if (refs > 0) refs_out[w.fresh[page]] = refs;
+    if (refs > 0) refs_out[map[page]] = refs;
     if (page >= n) refs_out[page] = 0;
   }
   const int64_t entries = (int64_t)p.slots * p.width;
   for (int64_t e = id; e < entries; e += threads) {
     const int64_t s = div_by((uint32_t)e, by_width), c = e - s * p.width;
     const int page = p.table[s * p.table_stride + c];
-    table_out[s * table_out_stride + c] = page >= 0 && page < p.pages ? w.fresh[page] : page;
+    table_out[s * table_out_stride + c] = page >= 0 && page < p.pages ? map[page] : page;
   }
-  copy_pages<V>(p, w.src, w.dst, *w.moves, per_page, by_vectors, by_planes);
+  copy_pages<V>(p, src, dst, moves, per_page, by_vectors, by_planes);
 }
 
 // Division by n, which may be 0 where there is nothing to divide.
@@ -435,14 +468,22 @@ hipError_t launch_pages_copy(const PoolArgs& p, const int32_t* src, const int32_
 
 hipError_t launch_pages_compact(const PoolArgs& p, int32_t* refs_out, int32_t* table_out,
                                 int64_t table_out_stride, int32_t* live) {
-  compact_kernel<<<1, PLAN_THREADS, 0, p.stream>>>(p, live);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
   return by_vector(p, [&](auto v) {
+    using V = decltype(v);
     const int64_t per = p.page_bytes / (int64_t)sizeof(v);
-    int grid = copy_grid(p, p.pages / 2 + 1, per);
-    move_kernel<decltype(v)><<<grid, COPY_THREADS, 0, p.stream>>>(
-        p, refs_out, table_out, table_out_stride, live, (uint32_t)per, div_of(per), div_of(p.planes), fast_div((uint32_t)(p.width > 0 ? p.width : 1)));
+    const int grid = copy_grid(p, p.pages / 2 + 1, per);
+    if (p.pages <= NEAR_PAGES && grid <= NEAR_GRID) {
+      move_kernel<V, true><<<grid, COPY_THREADS, 0, p.stream>>>(
+          p, refs_out, table_out, table_out_stride, live, (uint32_t)per, div_of(per),
+          div_of(p.planes), div_of(p.width));
+      return hipGetLastError();
+    }
+    compact_kernel<<<1, PLAN_THREADS, 0, p.stream>>>(p, live);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    move_kernel<V, false><<<grid, COPY_THREADS, 0, p.stream>>>(
+        p, refs_out, table_out, table_out_stride, live, (uint32_t)per, div_of(per),
+        div_of(p.planes), div_of(p.width));
     return hipGetLastError();
   });
 }
