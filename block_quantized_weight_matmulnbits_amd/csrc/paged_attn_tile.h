@@ -371,11 +371,13 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
       }
     tops(x);
   };
-  // A new reference maximum where a row passed the old one by the slack.  It is
-  // a whole number, so that the factor that sums, outputs and probabilities
-  // not yet multiplied are taken down by is a power of two and rounds none of
-  // them.  The output follows (mo) only where `all` is set, at one place of
-  // the loop: until then it meets probabilities of its own reference alone.
+  // A new reference maximum where a row passed the old one by the slack.  A
+  // row's first is the maximum itself, so that a key which is seen alone has
+  // the probability 1 and its value comes out as it is; from there it rises by
+  // a whole number, so that the factor that the sum and the probabilities not
+  // yet multiplied are taken down by is a power of two and rounds neither.
+  // The output follows (mo) only where `all` is set, at one place of the loop:
+  // until then it meets probabilities of its own reference alone.
   auto renew = [&](bool all, u32x4 (&p)[NQ][2]) QMM_INLINE {
     bool past = false;
 #pragma unroll
@@ -386,10 +388,10 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
     if (__builtin_expect(!__any(past), 1)) return;
 #pragma unroll
     for (int b = 0; b < NQ; ++b) {
-      const float was = m[b];
-      m[b] = ceilf(fmaxf(was, top[b]));
+      const float was = m[b], up = ceilf(fmaxf(top[b] - was, 0.f));   // a NaN raises nothing
+      m[b] = was == -INFINITY ? fmaxf(top[b], was) : was + up;
       sub[b] = m[b] == -INFINITY ? 0.f : m[b];
-      const float back = exp2_fast(was - sub[b]);
+      const float back = was == -INFINITY ? 1.f : exp2_fast(-up);
       l[b] *= back;
       if (!all) continue;
 #pragma unroll
@@ -525,7 +527,7 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
 #pragma unroll
   for (int b = 0; b < NQ; ++b) {
     // A NaN is left to the sum.
-    m[b] = ceilf(fmaxf(top[b] * mul, -INFINITY));
+    m[b] = fmaxf(top[b] * mul, -INFINITY);
     mo[b] = m[b];
     sub[b] = m[b] == -INFINITY ? 0.f : m[b];
   }

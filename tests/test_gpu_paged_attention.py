@@ -124,6 +124,21 @@ def test_chunks_of_long_sequences_in_parts(dtype, window, counts, lens):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128, 192])
+@pytest.mark.parametrize("counts,lens", [([1, 1], [1, 77]), ([40, 1, 200], [75, 300, 200]),
+                                         ([60], [1900])])
+def test_a_key_that_is_seen_alone(dtype, D, counts, lens):
+    """Its probability is 1: the value comes out bit for bit."""
+    held = []
+    out = run(dtype, counts, lens, 4, 2, D, window=1, seed=D,
+              spoil=lambda k, v, table, lens: held.extend((v.clone(), table, lens)))
+    v, table, lens = held
+    rows = [v[table[b][j // 16], :, j % 16] for b, n in enumerate(counts)
+            for j in range(int(lens[b]) - n, int(lens[b]))]
+    assert torch.equal(out.cpu(), torch.stack(rows).repeat_interleave(2, dim=1))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_what_masked_keys_hold_does_not_matter(dtype, bad):
     """Places past a sequence's end, pages it does not hold, keys later than a
