@@ -95,11 +95,18 @@ hipError_t launch_rows_f32(const AttnArgs& a, const RowsPlan& plan, int blocks, 
 hipError_t launch_rows_f16(const AttnArgs& a, const RowsPlan& plan, int blocks, int skip_above);
 hipError_t launch_rows_bf16(const AttnArgs& a, const RowsPlan& plan, int blocks, int skip_above);
 
+// What a workgroup of the tiles kernel takes beside its keys, in keys (of 30
+// ns): to begin and end; to have its part joined; to park it, where every
+// resident workgroup does.
+constexpr int PART_OWN = 500, PART_JOIN = 200, PART_PARK = 300;
+
 // Many rows of queries a workgroup (paged_attn_tile.h), 16-bit types: 128 or
 // 256 rows (blocks 1 or 2), at most `tiles` tiles over all sequences with
 // more than skip_upto new tokens.
 struct TilePlan {
-  int splits, chunk, tiles, blocks, skip_upto, note;
+  int splits;   // parts of a tile's keys: no more than these; the kernel counts them
+  int room;     // workgroups a key/value head that are resident at once
+  int tiles, blocks, skip_upto, note;
   int few_groups;   // workgroups after them that take the other sequences (`few`)
 };
 hipError_t launch_tile_f16(const AttnArgs& a, const TilePlan& plan, const RowsPlan& few);

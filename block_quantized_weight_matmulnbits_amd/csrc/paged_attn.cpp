@@ -16,15 +16,19 @@ constexpr int DT_F32 = 0, DT_F16 = 1;
 // 205 of 512), so none is longer than ROWS_MAX_CHUNK; few rows are spread over
 // more, shorter ones until the chip is filled, down to a block of 32 for each of
 // the four waves.  Filled it is by three workgroups a compute unit, two times
-// and a half over (as many tiles of rows are not split), or by one where a lane's registers leave room for no more.
+// and a half over (as many tiles of rows are not split), or by one where a
+// lane's registers leave room for no more.
 constexpr int64_t ROWS_FILL = 2048, ROWS_FILL_WIDE = 256, ROWS_MIN_CHUNK = 128, ROWS_MAX_CHUNK = 1024;
 // Tiles kernel: workgroups of 128 rows are resident twice on a compute unit
-// (once for heads over 128), those of 256 once; they are split to what is
-// resident at once.  10 sequences of 48 rows, 8 heads and 1500 to 4000 keys take
-// 61 us in 560 parts, 72 in 240, 79 in 1200; 192 tiles of 256 rows and 4096 keys
-// 115 us whole, 158 in three parts, which run in three rounds and are joined.
+// (once for heads over 128), those of 256 once.  The kernel cuts long
+// sequences into parts by the lengths that it finds (the price is in
+// paged_attn_tile.h), where sequences may be uneven; the host only bounds them.
+// Three chunks of 509 tokens over 5777 to 9001 keys take 248 us whole, 217 so;
+// two of 700 over 10227 and 16000 391 and 330.  Even ones pay for the join that
+// finds nothing (three of 512 over 4096 keys: 118 whole, 122), so that short
+// ones, where less can be gained, are left whole (TILE_UNEVEN).
 // Sequences with up to TILE_ROWS rows are left to the rows kernel.
-constexpr int64_t UNITS = 256, TILE_MIN_CHUNK = 128, TILE_ROWS = 32;
+constexpr int64_t UNITS = 256, TILE_UNEVEN = 2048, TILE_ROWS = 32;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -50,6 +54,8 @@ int64_t rows_parts(int seqs, int max_new, int64_t keys, int group, int kv_heads,
                   std::max<int64_t>(1, std::min(fill, ceil_div(keys, ROWS_MIN_CHUNK))));
 }
 
+int64_t resident(int blocks, int dim) { return UNITS * (blocks == 2 || dim > 128 ? 1 : 2); }
+
 // Rows are counted over the whole batch where the host knows them: tokens.
 // Two blocks of 128 rows a workgroup halve what is read from L2; one where
 // registers end (wide heads) or rows would be left over.
@@ -62,15 +68,36 @@ TilePlan plan_tile(int seqs, int tokens, int max_new, int group, int dim) {
   return p;
 }
 
+// How many parts the keys of a tile may be cut into; the kernel, which knows
+// the sequences' lengths, decides (to the most that is resident at once).  A
+// long sequence among short ones takes more than its equal share of parts.
+// bound: no fewer than for any number of keys up to `keys`.
 int64_t tile_parts(int seqs, int tokens, int max_new, int64_t keys, int group, int kv_heads,
-                   int blocks, int dim) {
+                   int blocks, int dim, bool bound = false) {
   // Tiles: of equal sequences, or else whole ones of the batch's rows.
-  const int64_t height = 128 * blocks, resident = UNITS * (blocks == 2 || dim > 128 ? 1 : 2);
+  const int64_t height = 128 * blocks;
   const int64_t tiles = kv_heads * ((int64_t)seqs * max_new == tokens
                                         ? seqs * ceil_div((int64_t)max_new * group, height)
                                         : ceil_div((int64_t)tokens * group, height));
-  const int64_t parts = blocks == 2 ? resident / tiles : ceil_div(resident, tiles);
-  return std::max<int64_t>(1, std::min(tiles >= resident ? 1 : parts, keys / TILE_MIN_CHUNK));
+  const int64_t room = resident(blocks, dim);
+  // Tiles of one sequence are as long as one another, and more than half of
+  // what is resident gain nothing by parts; nor do short ones.
+  const bool uneven = seqs > 1 && keys >= TILE_UNEVEN;
+  if (tiles >= (uneven ? 2 * room : room / 2 + 1) ||
+      keys < 2 * (PART_JOIN + PART_PARK * std::min(2 * tiles, room) / room))
+    return 1;
+  if (seqs > 1) return std::min<int64_t>(2 * room / tiles + 1, 64);
+  if (bound) return std::min<int64_t>(room / tiles, 64);
+  // One sequence: the same price as the kernel's, of equal parts.
+  int64_t best = 1, least = keys;
+  for (int64_t p = 2; p <= std::min<int64_t>(room / tiles, 64); ++p) {
+    const int64_t price = ceil_div(keys, p) + PART_JOIN + PART_PARK * p * tiles / room;
+    if (price < least) {
+      best = p;
+      least = price;
+    }
+  }
+  return best;
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -100,7 +127,7 @@ size_t attn_workspace_bytes(int seqs, int tokens, int max_new, int max_len, int 
     parts = std::max(parts, rows_parts(seqs, max_new, max_len, group, kv_heads, blocks, false));
   if ((int64_t)max_new * group > TILE_ROWS) {
     const TilePlan t = plan_tile(seqs, tokens, max_new, group, dim);
-    parts = std::max(parts, tile_parts(seqs, tokens, max_new, max_len, group, kv_heads, t.blocks, dim));
+    parts = std::max(parts, tile_parts(seqs, tokens, max_new, max_len, group, kv_heads, t.blocks, dim, true));
     if (t.skip_upto > 0) parts = std::max(parts, ceil_div(max_len, ROWS_MAX_CHUNK));
   }
   return 256 + (parts > 1 ? align256(parts_bytes(rows, parts, dim)) : 0);
@@ -125,7 +152,10 @@ hipError_t launch_paged_attention(AttnArgs a, char* workspace) {
   if (tiles) {
     t = plan_tile(c.seqs, c.tokens, c.max_new, a.group, c.dim);
     const int64_t keys = seen(128 * t.blocks);
-    cut(keys, tile_parts(c.seqs, c.tokens, c.max_new, keys, a.group, c.kv_heads, t.blocks, c.dim), 64, &t.chunk, &t.splits);
+    t.splits = (int)tile_parts(c.seqs, c.tokens, c.max_new, keys, a.group, c.kv_heads, t.blocks,
+                               c.dim);
+    t.room = (int)(resident(t.blocks, c.dim) / c.kv_heads);
+    if (t.splits > 1) t.tiles = std::max(t.tiles, (c.seqs > 1 && 2 * t.tiles > t.room ? 2 : 1) * t.room);
     few = t.skip_upto;
   }
   if (few > 0) {

@@ -9,16 +9,17 @@
 // step (matrix cores), the exponentials of this one (vector units) and the
 // product of the last one's probabilities with V (matrix cores).
 //
-// 4096 new tokens after 12288 cached ones (32 heads of 128 over 8): 925 us, 1040
-// TFLOP/s, where a large matrix product reaches 1290 on this chip.  The matrix
+// 4096 new tokens after 12288 cached ones (32 heads of 128 over 8): 890 us, 1080
+// TFLOP/s (925 with a sequence's first tiles first: the last ones, which see the
+// most keys, are then the end of the launch), where a large matrix product reaches 1290 on this chip.  The matrix
 // cores are busy half of the time at 1.85 GHz: the chip lowers its clock under
 // the load (128 workgroups instead of 256 run at 2.15 GHz), so what is left is
 // energy, most of it in LDS reads and exponentials.
 //
 // The last workgroups of a launch take the sequences with few rows, as the rows
 // kernel does: they fill the compute units that the tiles leave (three chunks
-// of 509 tokens and six single ones: 258 us in two launches, 246 in one, 270
-// with the few rows first).
+// of 509 tokens and six single ones, tiles whole: 258 us in two launches, 246
+// in one, 270 with the few rows first).
 //
 // K and V pass through LDS in groups of two steps, two groups of each: the
 // global loads of a group are in flight for a whole group's work before they
@@ -60,6 +61,18 @@ __device__ __forceinline__ float pair_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// Minimum over the wave: turns among 16 lanes, then rows of 16 exchanged.
+__device__ __forceinline__ float wave_min(float v) {
+#define QMM_TURN(N)                                                                              \
+  v = fminf(v, __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), 0x120 + (N), \
+                                                           0xF, 0xF, true)));
+  QMM_TURN(1) QMM_TURN(2) QMM_TURN(4) QMM_TURN(8)
+#undef QMM_TURN
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fminf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  return -pair_max(-v);
+}
+
 // DK: the head's width in scores (16s), DV: in outputs (32s).
 template <int DK, int DV> struct TileLds {
   static constexpr int KROW = DK * 2 + 16, VROW = DV * 2 + (DV % 64 == 32 ? 0 : 64);
@@ -85,11 +98,11 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   constexpr int THREADS = 64 * WAVES, ROWS = 32 * NQ * WAVES;
   constexpr int FEW = DV;   // the width that the few-row workgroups pad to
   extern __shared__ __attribute__((aligned(1024))) char lds[];
-  __shared__ int found[5];
+  __shared__ int found[8];
   __shared__ int odd;
 
   const CacheArgs& c = a.c;
-  const uint32_t groups = (uint32_t)plan.tiles * plan.splits * c.kv_heads;
+  const uint32_t groups = (uint32_t)plan.tiles * c.kv_heads;
   if (blockIdx.x >= groups) {
     attn_rows<DT, FEW, 1, WAVES, CAP>(a, few, scale, plan.skip_upto, blockIdx.x - groups, lds);
     return;
@@ -97,56 +110,111 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l31 = lane & 31, half = lane >> 5, l15 = lane & 15;
 
-  // Heads fastest, so that one head's tiles meet in one L2; then parts, turned
-  // by the tile's number as in the rows kernel; the tiles of the sequences
-  // follow one another without gaps.
-  uint32_t id = blockIdx.x;
-  const int kvh = id % c.kv_heads;
-  id /= c.kv_heads;
-  const int want = id / plan.splits, split = (id % plan.splits + want) % plan.splits;
+  // Heads fastest, so that one head's tiles meet in one L2; then the parts of
+  // the sequences' tiles, which follow one another without gaps.  A sequence's
+  // last tiles see the most keys and come first.
+  const int kvh = blockIdx.x % c.kv_heads, want = blockIdx.x / c.kv_heads;
   if (wave == 0) {
-    int base = 0, seq = -1, tile = 0;
-    Seq of{};
-    for (int s0 = 0; s0 < c.seqs && seq < 0; s0 += 64) {
-      int mine = 0;
-      Seq q{};
-      if (s0 + lane < c.seqs) {
-        q = seq_of(c, s0 + lane);
-        if (q.n > plan.skip_upto) mine = (q.n * a.group + ROWS - 1) / ROWS;
+    struct Job {
+      Seq q;
+      int tiles;
+      uint32_t keys;   // that a tile sees at most
+    };
+    auto job_of = [&](int s) QMM_INLINE {
+      Job j{};
+      if (s >= c.seqs) return j;
+      j.q = seq_of(c, s);
+      if (j.q.n <= plan.skip_upto) return j;
+      j.tiles = (j.q.n * a.group + ROWS - 1) / ROWS;
+      j.keys = j.q.len < 1 ? 1 : j.q.len;
+      const uint32_t most = (uint32_t)a.window + ROWS / a.group + 1;
+      if (a.window && a.causal && j.keys > most) j.keys = most;
+      return j;
+    };
+    const Job job = job_of(lane);
+    auto jobs_at = [&](int s0) QMM_INLINE { return s0 == 0 ? job : job_of(s0 + lane); };
+    auto parts_in = [](uint32_t keys, uint32_t n) { return (keys - 1) / n + 1; };
+    // Parts of about 1 / rate keys: the same number wherever it is asked for.
+    auto parts_at = [](uint32_t keys, float rate) {
+      return max(1u, (uint32_t)ceilf((float)keys * rate));
+    };
+    // Every lane prices one length of parts, 7 % below its neighbour's, in keys
+    // of one workgroup's time: the longest part where all are resident at
+    // once, or else an equal share of all and half a part of waste at the end.
+    // (One sequence alone: as many as the host found.)
+    float rate = 0.f;
+    if (plan.splits > 1 && c.seqs > 1) {
+      uint32_t most = 1;
+      for (int s0 = 0; s0 < c.seqs; s0 += 64) {
+        const Job j = jobs_at(s0);
+        for (uint64_t rest = __ballot(j.tiles > 0); rest; rest &= rest - 1)
+          most = max(most, (uint32_t)__builtin_amdgcn_readlane(j.keys, __builtin_ctzll(rest)));
       }
+      const float mine = exp2_fast(0.1f * lane) / (float)most;
+      uint32_t units = 0;
+      float keys = 0.f, part = 0.f;
+      for (int s0 = 0; s0 < c.seqs; s0 += 64) {
+        const Job j = jobs_at(s0);
+        for (uint64_t rest = __ballot(j.tiles > 0); rest; rest &= rest - 1) {
+          const int w = __builtin_ctzll(rest);
+          const uint32_t t = __builtin_amdgcn_readlane(j.tiles, w);
+          const uint32_t k = __builtin_amdgcn_readlane(j.keys, w), n = parts_at(k, mine);
+          units += t * n;
+          part = fmaxf(part, (float)k * __builtin_amdgcn_rcpf((float)n));
+          keys += (float)t * (float)k;
+        }
+      }
+      const uint32_t longest = parts_at(most, mine);
+      const float full = (float)units / plan.room;
+      const float cost = PART_OWN + (longest == 1 ? 0.f : PART_JOIN + PART_PARK * fminf(full, 1.f));
+      float price = full <= 1.f ? part + cost : keys / plan.room + full * cost + 0.5f * part;
+      if (longest > (uint32_t)plan.splits || units > (uint32_t)plan.tiles) price = INFINITY;
+      const float best = wave_min(price);
+      const uint64_t who = __ballot(price == best && price < INFINITY);
+      if (who) rate = __shfl(mine, __builtin_ctzll(who));
+    }
+    int base = 0, seq = -1;
+    for (int s0 = 0; s0 < c.seqs && seq < 0; s0 += 64) {
+      const Job j = jobs_at(s0);
+      const int parts = c.seqs == 1 ? plan.splits : parts_at(j.keys, rate), mine = j.tiles * parts;
       int sum = mine;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
         const int y = __shfl_up(sum, d);
         if (lane >= d) sum += y;
       }
-      const bool here = want >= base + sum - mine && want < base + sum;
-      const uint64_t who = __ballot(here);
+      const int first = base + sum - mine;
+      const uint64_t who = __ballot(want >= first && want < first + mine);
       if (who) {
-        const int w = __builtin_ctzll(who);
-        seq = s0 + w;
-        tile = want - base - (__shfl(sum, w) - __shfl(mine, w));
-        of.t0 = __shfl(q.t0, w);
-        of.n = __shfl(q.n, w);
-        of.len = __shfl(q.len, w);
+        seq = s0 + __builtin_ctzll(who);
+        if (lane == __builtin_ctzll(who)) {
+          // Parts are turned by the tile's number, as in the rows kernel.
+          const int turn = (want - first) / parts;
+          found[1] = j.tiles - 1 - turn;
+          found[2] = j.q.t0;
+          found[3] = j.q.n;
+          found[4] = j.q.len;
+          found[5] = (want - first + turn) % parts;
+          found[6] = parts;
+          found[7] = parts_in(parts_in(j.keys, parts), 64) * 64;
+        }
       }
       base += __shfl(sum, 63);
     }
     if (lane == 0) {
       found[0] = seq;
-      found[1] = tile;
-      found[2] = of.t0;
-      found[3] = of.n;
-      found[4] = of.len;
       odd = 0;
     }
   }
   __syncthreads();
   const int seq = __builtin_amdgcn_readfirstlane(found[0]);
-  const int tile = __builtin_amdgcn_readfirstlane(found[1]);
   if (seq < 0) return;
+  const int tile = __builtin_amdgcn_readfirstlane(found[1]);
   const Seq sq{__builtin_amdgcn_readfirstlane(found[2]), __builtin_amdgcn_readfirstlane(found[3]),
                __builtin_amdgcn_readfirstlane(found[4])};
+  const int split = __builtin_amdgcn_readfirstlane(found[5]);
+  const int parts = __builtin_amdgcn_readfirstlane(found[6]);
+  const uint32_t chunk = __builtin_amdgcn_readfirstlane(found[7]);
   const int rows = sq.n * a.group, row0 = tile * ROWS;
   const int row1 = rows < row0 + ROWS ? rows : row0 + ROWS;
   const int pos0 = sq.len - sq.n;
@@ -154,11 +222,11 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   auto pos_of = [&](int r) { return pos0 + (int)div_by(r, a.by_group); };
   const int kmin = a.window ? clip(pos_of(row0) - a.window + 1) : 0;
   const int kmax = a.causal ? clip(pos_of(row1 - 1) + 1) : sq.len;
-  int active = kmax > kmin ? (kmax - kmin + plan.chunk - 1) / plan.chunk : 1;
-  active = active > plan.splits ? plan.splits : active;
+  int active = kmax > kmin ? (int)(((uint32_t)(kmax - kmin) - 1) / chunk + 1) : 1;
+  active = active > parts ? parts : active;
   if (split >= active) return;
-  const int begin = kmin + split * plan.chunk;
-  const int end = split == active - 1 ? kmax : begin + plan.chunk;
+  const int begin = kmin + split * chunk;
+  const int end = split == active - 1 ? kmax : begin + chunk;
   const int steps = end > begin ? (end - begin + 31) / 32 : 0;
 
   // The wave's rows: what all of them see, and each lane's own limits.
@@ -633,7 +701,7 @@ hipError_t launch_tile(const AttnArgs& a, const TilePlan& plan, const RowsPlan& 
                        : (const void*)attn_tile_kernel<DT, DK, DV, WAVES, false>;
   const hipError_t e = ensure_dynamic_lds(fn, bytes);
   if (e != hipSuccess) return e;
-  const dim3 grid((uint32_t)plan.few_groups + (uint32_t)plan.tiles * plan.splits * a.c.kv_heads);
+  const dim3 grid((uint32_t)plan.few_groups + (uint32_t)plan.tiles * a.c.kv_heads);
   if (cap) attn_tile_kernel<DT, DK, DV, WAVES, true><<<grid, THREADS, bytes, a.stream>>>(a, plan, few, k);
   else attn_tile_kernel<DT, DK, DV, WAVES, false><<<grid, THREADS, bytes, a.stream>>>(a, plan, few, k);
   return hipGetLastError();

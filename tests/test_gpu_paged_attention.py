@@ -123,6 +123,17 @@ def test_chunks_of_long_sequences_in_parts(dtype, window, counts, lens):
     run(dtype, counts, lens, 4, 1, 128, window=window, page=12, seed=3)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("window", [0, 2500])
+@pytest.mark.parametrize("counts,lens", [([300, 40, 3, 200], [5000, 900, 2500, 2300]),
+                                         ([130, 130], [2049, 130]), ([70] * 3, [6000, 64, 0]),
+                                         ([9] * 70, [40 * i for i in range(70)])])
+def test_chunks_of_uneven_sequences(dtype, window, counts, lens):
+    # Where parts are counted by the lengths, over more sequences than a wave has lanes too.
+    run(dtype, counts, lens, 8, 2, 64, window=window, seed=4)
+    run(dtype, counts, lens, 4, 1, 128, window=window, causal=window == 0, seed=5)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("D", [64, 128, 192])
 @pytest.mark.parametrize("counts,lens", [([1, 1], [1, 77]), ([40, 1, 200], [75, 300, 200]),
