@@ -225,7 +225,7 @@ __device__ __forceinline__ void attn_rows(const AttnArgs& a, const RowsPlan& pla
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float x = score<CAP, F32>(sc[b][t][i], scale);
+          float x = score<CAP>(sc[b][t][i], scale);
           if (!full) {
             const int j = kb + 16 * t + 4 * g + i;
             x = j >= lo[b] && j < hi[b] && j < end ? x : -INFINITY;

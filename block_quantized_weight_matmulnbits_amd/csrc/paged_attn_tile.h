@@ -429,14 +429,35 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
     if (!CAP && !part) return;
     int base = j0 + 4 * half;
     asm volatile("" : "+v"(base));   // a branch, not selects in every step
+    // Scores far below the cap, the usual ones, take the polynomial alone
+    // (2048 new tokens over 8192 keys: 351 us, 502 with both in every step).
+    bool far = false;
+    if constexpr (CAP) {
 #pragma unroll
-    for (int b = 0; b < NQ; ++b)
+      for (int b = 0; b < NQ; ++b) {
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(x[b][i]));
+        far |= !(most * fabsf(scale.mul) < TANH_NEAR);
+      }
+      far = __any(far);
+    }
+#pragma unroll
+    for (int b = 0; b < NQ; ++b) {
+      if (CAP && far) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[b][i] = score<true>(x[b][i], ScoreScale{fabsf(scale.mul), scale.cap});
+      } else if (CAP) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[b][i] = scale.cap * tanh_near(x[b][i] * fabsf(scale.mul));
+      }
+      if (!part) continue;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        if constexpr (CAP) x[b][i] = score<true, false>(x[b][i], ScoreScale{fabsf(scale.mul), scale.cap});
         const int j = base + 8 * (i / 4) + i % 4;
-        if (part && !(j >= lo[b] && j < hi[b])) x[b][i] = -INFINITY;
+        if (!(j >= lo[b] && j < hi[b])) x[b][i] = -INFINITY;
       }
+    }
     tops(x);
   };
   // A new reference maximum where a row passed the old one by the slack.  A

@@ -194,6 +194,26 @@ def test_large_negative_and_equal_scores(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [1, 40])
+def test_small_scores_under_a_cap(dtype, n):
+    """Products that are exact, far below the cap: what is left of the error of
+    lse is a dozen roundings of 32 bits."""
+    q, g = qmm(), torch.Generator().manual_seed(n)
+    H, KV, D, B = 8, 2, 64, 6
+    starts, lens, table, total = ref.make_batch([n] * B, [n + 9] * B, 16, n)
+    signs = lambda *shape: (2.0 * torch.randint(0, 2, shape, generator=g) - 1).to(dtype)  # noqa: E731
+    kp, vp, x = signs(total, KV, 16, D), signs(total, KV, 16, D), signs(n * B, H, D) / 4
+    want = ref.attention(x, kp, vp, starts, lens, table, 0.125, True, 3, 50.0)[1]
+    batch = q.PagedBatch(dev(starts), dev(lens), dev(table), n * B, n, n + 9)
+    out, lse = torch.empty(n * B, H, D, dtype=dtype, device=DEV), torch.empty(n * B, H, device=DEV)
+    ws = torch.zeros(q.qmm_paged_attention_workspace_size(batch, H, KV, D), dtype=torch.uint8, device=DEV)
+    q.qmm_paged_attention(x.to(DEV), q.PagedKV(kp.to(DEV), vp.to(DEV)), batch, out, ws, scale=0.125,
+                          window=3, softcap=50.0, lse=lse)
+    err = np.abs(lse.cpu().double().numpy() - np.asarray(want, dtype=np.float64))
+    assert np.all(err <= 12 * 2.0 ** -24 * (1 + np.abs(np.asarray(want, dtype=np.float64)))), err.max()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_seen_scores_of_minus_infinity(dtype):
     """Keys that a token sees but whose score is minus infinity; then all of them."""
     def some(kp, vp, table, lens):
