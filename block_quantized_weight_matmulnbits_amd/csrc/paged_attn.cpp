@@ -18,7 +18,8 @@ constexpr int DT_F32 = 0, DT_F16 = 1;
 // the four waves.  Filled it is by three workgroups a compute unit, two times
 // and a half over (as many tiles of rows are not split), or by one where a
 // lane's registers leave room for no more.
-constexpr int64_t ROWS_FILL = 2048, ROWS_FILL_WIDE = 256, ROWS_MIN_CHUNK = 128, ROWS_MAX_CHUNK = 1024;
+constexpr int64_t ROWS_FILL = 2048, ROWS_FILL_WIDE = 256, ROWS_MIN_CHUNK = 128, ROWS_MAX_CHUNK = 1024,
+                  ROWS_LONG_CHUNK = 4096;
 // Tiles kernel: workgroups of 128 rows are resident twice on a compute unit
 // (once for heads over 128), those of 256 once.  The kernel cuts long
 // sequences into parts by the lengths that it finds (the price is in
@@ -48,6 +49,11 @@ void cut(int64_t keys, int64_t parts, int64_t step, int* chunk, int* splits) {
 int64_t rows_parts(int seqs, int max_new, int64_t keys, int group, int kv_heads, int blocks,
                    bool wide) {
   const int64_t tiles = seqs * kv_heads * ceil_div((int64_t)max_new * group, 16 * blocks);
+  // Wide rows leave a compute unit one workgroup at a time: with many of them
+  // their beginnings and ends count (3 sequences of 300 f32 tokens over 900 to
+  // 2000 keys: 474 us in parts of 1024, 323 of ROWS_LONG_CHUNK; 6 of 150 over
+  // 300 to 5000: 867 and 946).
+  if (wide && tiles >= 2 * ROWS_FILL_WIDE) return ceil_div(keys, ROWS_LONG_CHUNK);
   if (tiles >= ROWS_FILL) return 1;
   const int64_t fill = ceil_div(wide ? ROWS_FILL_WIDE : ROWS_FILL, std::max<int64_t>(tiles, 1));
   return std::max(ceil_div(keys, ROWS_MAX_CHUNK),
@@ -162,7 +168,7 @@ hipError_t launch_paged_attention(AttnArgs a, char* workspace) {
     // 16-bit rows go 16 to a workgroup: two blocks keep a wave alone on its SIMD,
     // and what they save is read from L2 (20 sequences of 8 tokens, 4 heads a
     // group: 126 us in 32 rows, 91 in 16).  In 32 bits the matrix cores bound
-    // them (300 tokens of 3 sequences: 365 us in 32 rows, 476 in 16).
+    // them (300 tokens of 3 sequences each: 323 us in 32 rows, 453 in 16).
     blocks = a.dtype != DT_F32 || (int64_t)few * a.group <= 16 ? 1 : 2;
     const int64_t keys = seen(16 * blocks);
     r.row_tiles = (int)ceil_div((int64_t)few * a.group, 16 * blocks);

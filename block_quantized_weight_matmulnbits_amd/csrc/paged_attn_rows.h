@@ -14,7 +14,7 @@
 // 64 sequences of 17 to 8191 keys, a token each (32 heads of 128 over 8, bf16):
 // 230 us with the join, 4.98 TB/s of keys and values, where a large copy moves
 // 4.95.  Two sequences of 90001 and 131071 keys: 186 us, 4.9 TB/s.  Five guessed f32
-// tokens for each of 7 sequences: 23 us, of which latencies in a row are most.
+// tokens for each of 7 sequences: 22 us, of which latencies in a row are most.
 #pragma once
 
 #include "paged_attn.h"
@@ -64,7 +64,8 @@ __device__ __forceinline__ void attn_rows(const AttnArgs& a, const RowsPlan& pla
   id /= plan.splits;
   const int kvh = id % c.kv_heads;
   id /= c.kv_heads;
-  const int tile = id % plan.row_tiles, seq = id / plan.row_tiles;
+  // A sequence's last rows see the most keys and come first.
+  const int tile = plan.row_tiles - 1 - (int)(id % plan.row_tiles), seq = id / plan.row_tiles;
 
   if (seq >= c.seqs) return;
   const Seq sq = seq_of(c, seq);
@@ -270,9 +271,32 @@ __device__ __forceinline__ void attn_rows(const AttnArgs& a, const RowsPlan& pla
       }
       odd = __any(odd);
     }
+    auto value_f32 = [&](int d, int t, int i) QMM_INLINE {
+      return *(const float*)(vl + (d * 2 + t) * 1024 + (l15 / 4) * 256 + (4 * g + i) * 16 + (l15 % 4) * 4);
+    };
+    // 32 bits, where products bound many rows: nothing but products, of two
+    // blocks of columns in turn, so that none waits for the one before it (900
+    // tokens of 3 sequences, 32 heads of 128: 551 us as below, 474 so, both in parts of
+    // 1024 keys).
+    if (F32 && __builtin_expect(!odd, 1)) {
+#pragma unroll
+      for (int d = 0; d < DB; d += 2)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = d; e < d + 2; ++e) {
+              const float x = value_f32(e, t, i);
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                o[b][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, p[b][t][i], o[b][e], 0, 0, 0);
+            }
+    }
     // A block with such values is taken key by key: the product of that key
-    // alone, kept in the columns that see it.
-    const int rounds = odd ? ROWS_BLOCK : 1;
+    // alone, kept in the columns that see it.  In 16 bits the others pass
+    // through the same code (a copy without the choices gained nothing).
+    const int rounds = odd ? ROWS_BLOCK : F32 ? 0 : 1;
 #pragma unroll 1
     for (int key = 0; key < rounds; ++key) {
       const int only = odd ? (key % 16) / 4 == g ? key / 16 * 4 + key % 4 : -1 : -2;
@@ -290,9 +314,7 @@ __device__ __forceinline__ void attn_rows(const AttnArgs& a, const RowsPlan& pla
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float x = *(const float*)(vl + (d * 2 + t) * 1024 + (l15 / 4) * 256 +
-                                        (4 * g + i) * 16 + (l15 % 4) * 4);
-              if (odd && only != 4 * t + i) x = 0.f;
+              const float x = only == 4 * t + i ? value_f32(d, t, i) : 0.f;
 #pragma unroll
               for (int b = 0; b < NB; ++b)
                 n[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, p[b][t][i], n[b], 0, 0, 0);
