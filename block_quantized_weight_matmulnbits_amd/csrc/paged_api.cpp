@@ -337,7 +337,7 @@ int qmm_paged_attention(const qmm_heads* q, const qmm_paged_kv* kv, const qmm_pa
   a.q_wide = aligned(q->data, 16) && q->token_stride % v == 0 && q->head_stride % v == 0;
   a.out_wide = aligned(out->data, 4 * es) && out->token_stride % 4 == 0 && out->head_stride % 4 == 0;
   a.stream = (hipStream_t)stream;
-  return hip_status(qmm::launch_paged_attention(a, (char*)workspace), fn);
+  return hip_status(qmm::launch_paged_attention(a, (char*)workspace, workspace_bytes), fn);
 }
 
 size_t qmm_pages_workspace_size(const qmm_page_pool* pool, int64_t count) {

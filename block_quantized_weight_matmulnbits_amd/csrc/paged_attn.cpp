@@ -49,12 +49,16 @@ void cut(int64_t keys, int64_t parts, int64_t step, int* chunk, int* splits) {
 int64_t rows_parts(int seqs, int max_new, int64_t keys, int group, int kv_heads, int blocks,
                    bool wide) {
   const int64_t tiles = seqs * kv_heads * ceil_div((int64_t)max_new * group, 16 * blocks);
-  // Wide rows leave a compute unit one workgroup at a time: with many of them
-  // their beginnings and ends count (3 sequences of 300 f32 tokens over 900 to
-  // 2000 keys: 474 us in parts of 1024, 323 of ROWS_LONG_CHUNK; 6 of 150 over
-  // 300 to 5000: 867 and 946).
-  if (wide && tiles >= 2 * ROWS_FILL_WIDE) return ceil_div(keys, ROWS_LONG_CHUNK);
+  // As many tiles are not split, wide ones neither (f32, heads of 128: 2048 tokens
+  // over 8192 keys 3.3 ms whole, 3.9 in parts of 4096; four of 1024 over 2000 to
+  // 16384 8.5 and 13.3; 256 single tokens, 8 heads of 256: 4.8 and 5.9).
   if (tiles >= ROWS_FILL) return 1;
+  // Wide rows leave a compute unit one workgroup at a time: with many of them
+  // their beginnings and ends count.  f32, in parts of 1024 and of
+  // ROWS_LONG_CHUNK: 3 sequences of 300 tokens over 900 to 2000 keys 474 and 324
+  // us; 4 of 500 over 600 to 3000, a head a group, 281 and 255; one of 1024 over
+  // 6000 1589 and 1514; but 6 of 150 over 300 to 5000 856 and 945.
+  if (wide && tiles >= 2 * ROWS_FILL_WIDE) return ceil_div(keys, ROWS_LONG_CHUNK);
   const int64_t fill = ceil_div(wide ? ROWS_FILL_WIDE : ROWS_FILL, std::max<int64_t>(tiles, 1));
   return std::max(ceil_div(keys, ROWS_MAX_CHUNK),
                   std::max<int64_t>(1, std::min(fill, ceil_div(keys, ROWS_MIN_CHUNK))));
@@ -108,8 +112,9 @@ int64_t tile_parts(int seqs, int tokens, int max_new, int64_t keys, int group, i
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// The workspace for `parts` parts of every row.
+// The workspace for `parts` parts of every row; 0 where no row has several.
 size_t parts_bytes(int64_t rows, int64_t parts, int dim) {
+  if (parts <= 1) return 0;
   return align256(rows * 4) + align256(rows * parts * 8) + (size_t)(rows * parts) * padded(dim) * 4;
 }
 
@@ -120,28 +125,64 @@ void attn_parts(AttnArgs* a, char* ws, int64_t parts) {
   a->part_out = (float*)(ws + align256(rows * 4) + align256(rows * parts * 8));
 }
 
+// What a call is cut by, beside the keys that its rows see.
+struct Shape {
+  int seqs, tokens, max_new, group, kv_heads, dim;
+  bool f32, tiles;   // the queries' type; whether many rows may go to the tiles kernel
+};
+// Both kernels' shares of a call and the most parts that either cuts keys into.
+struct Cut {
+  bool tiles;
+  TilePlan t{};
+  int few, blocks;   // new tokens a sequence that the rows kernel takes, blocks of 16 rows
+  int64_t few_keys, tile_parts, rows_parts;
+  int64_t parts() const { return std::max(tile_parts, rows_parts); }
+};
+// The one place where parts are counted: for a launch, whose tiles of `height`
+// rows see at most seen(height) keys, and (bound) for any launch of this shape
+// whose tiles see no more.
+template <typename Seen> Cut cut_of(const Shape& s, Seen seen, bool bound) {
+  Cut p{};
+  p.few = s.max_new;
+  p.tile_parts = p.rows_parts = 1;
+  p.tiles = s.tiles && !s.f32 && (int64_t)s.max_new * s.group > TILE_ROWS;
+  if (p.tiles) {
+    p.t = plan_tile(s.seqs, s.tokens, s.max_new, s.group, s.dim);
+    p.tile_parts = tile_parts(s.seqs, s.tokens, s.max_new, seen(128 * p.t.blocks), s.group, s.kv_heads,
+                              p.t.blocks, s.dim, bound);
+    p.few = p.t.skip_upto;
+  }
+  if (p.few > 0) {
+    // 16-bit rows go 16 to a workgroup: two blocks keep a wave alone on its SIMD,
+    // and what they save is read from L2 (20 sequences of 8 tokens, 4 heads a
+    // group: 126 us in 32 rows, 91 in 16).  In 32 bits the matrix cores bound
+    // them (300 tokens of 3 sequences each: 323 us in 32 rows, 453 in 16).
+    p.blocks = !s.f32 || (int64_t)p.few * s.group <= 16 ? 1 : 2;
+    p.few_keys = seen(16 * p.blocks);
+    const bool wide = padded(s.dim) * (s.f32 ? 4 : 2) * p.blocks > 768;
+    // Beside tiles parts only keep the longest of them from being the last.
+    p.rows_parts = p.tiles ? ceil_div(p.few_keys, ROWS_MAX_CHUNK)
+                           : rows_parts(s.seqs, p.few, p.few_keys, s.group, s.kv_heads, p.blocks, wide);
+  }
+  return p;
+}
+
 }  // namespace
 
 size_t attn_workspace_bytes(int seqs, int tokens, int max_new, int max_len, int q_heads,
                             int kv_heads, int dim) {
-  // The most that any call may take: every type, with a window or without (a
-  // window makes parts shorter, never more than are asked for here).
-  const int group = q_heads / kv_heads;
-  const int64_t rows = (int64_t)tokens * q_heads;
+  // The most that any call may take: every type, by either kernel, with a
+  // window (which leaves fewer keys to see) or without.
   int64_t parts = 1;
-  for (int blocks = 1; blocks <= 2; ++blocks)
-    parts = std::max(parts, rows_parts(seqs, max_new, max_len, group, kv_heads, blocks, false));
-  if ((int64_t)max_new * group > TILE_ROWS) {
-    const TilePlan t = plan_tile(seqs, tokens, max_new, group, dim);
-    parts = std::max(parts, tile_parts(seqs, tokens, max_new, max_len, group, kv_heads, t.blocks, dim, true));
-    if (t.skip_upto > 0) parts = std::max(parts, ceil_div(max_len, ROWS_MAX_CHUNK));
+  for (int kind = 0; kind < 3; ++kind) {
+    const Shape s{seqs, tokens, max_new, q_heads / kv_heads, kv_heads, dim, kind == 0, kind == 2};
+    parts = std::max(parts, cut_of(s, [&](int64_t) { return (int64_t)max_len; }, true).parts());
   }
-  return 256 + (parts > 1 ? align256(parts_bytes(rows, parts, dim)) : 0);
+  return 256 + align256(parts_bytes((int64_t)tokens * q_heads, parts, dim));
 }
 
-hipError_t launch_paged_attention(AttnArgs a, char* workspace) {
+hipError_t launch_paged_attention(AttnArgs a, char* workspace, size_t workspace_bytes) {
   const CacheArgs& c = a.c;
-  const int64_t rows = (int64_t)c.max_new * a.group;
   // A tile of rows sees at most the window of its first row and its own tokens.
   auto seen = [&](int64_t height) {
     const int64_t most = (int64_t)a.window + height / a.group + 1;
@@ -151,38 +192,26 @@ hipError_t launch_paged_attention(AttnArgs a, char* workspace) {
   // a scale of 0 (which it takes out of the maximum) and strides past 32 bits
   // run on the rows kernel.
   const int64_t wide = std::max({c.k_page, c.v_page, c.k_token, c.v_token});
-  const bool tiles = a.dtype != DT_F32 && a.scale != 0.f && wide < INT32_MAX / 2 && rows > TILE_ROWS;
-  TilePlan t{};
+  const Cut p = cut_of(Shape{c.seqs, c.tokens, c.max_new, a.group, c.kv_heads, c.dim, a.dtype == DT_F32,
+                             a.scale != 0.f && wide < INT32_MAX / 2}, seen, false);
+  TilePlan t = p.t;
   RowsPlan r{};
-  int few = c.max_new, blocks = 1;
-  if (tiles) {
-    t = plan_tile(c.seqs, c.tokens, c.max_new, a.group, c.dim);
-    const int64_t keys = seen(128 * t.blocks);
-    t.splits = (int)tile_parts(c.seqs, c.tokens, c.max_new, keys, a.group, c.kv_heads, t.blocks,
-                               c.dim);
+  if (p.tiles) {
+    t.splits = (int)p.tile_parts;
     t.room = (int)(resident(t.blocks, c.dim) / c.kv_heads);
     if (t.splits > 1) t.tiles = std::max(t.tiles, (c.seqs > 1 && 2 * t.tiles > t.room ? 2 : 1) * t.room);
-    few = t.skip_upto;
   }
-  if (few > 0) {
-    // 16-bit rows go 16 to a workgroup: two blocks keep a wave alone on its SIMD,
-    // and what they save is read from L2 (20 sequences of 8 tokens, 4 heads a
-    // group: 126 us in 32 rows, 91 in 16).  In 32 bits the matrix cores bound
-    // them (300 tokens of 3 sequences each: 323 us in 32 rows, 453 in 16).
-    blocks = a.dtype != DT_F32 || (int64_t)few * a.group <= 16 ? 1 : 2;
-    const int64_t keys = seen(16 * blocks);
-    r.row_tiles = (int)ceil_div((int64_t)few * a.group, 16 * blocks);
-    // Beside tiles parts only keep the longest of them from being the last.
-    int64_t parts = ceil_div(keys, ROWS_MAX_CHUNK);
-    const bool wide = padded(c.dim) * (a.dtype == DT_F32 ? 4 : 2) * blocks > 768;
-    if (!tiles) parts = rows_parts(c.seqs, few, keys, a.group, c.kv_heads, blocks, wide);
-    cut(keys, parts, ROWS_MIN_CHUNK, &r.chunk, &r.splits);
+  if (p.few > 0) {
+    r.row_tiles = (int)ceil_div((int64_t)p.few * a.group, 16 * p.blocks);
+    cut(p.few_keys, p.rows_parts, ROWS_MIN_CHUNK, &r.chunk, &r.splits);
   }
   const int splits = std::max(t.splits, r.splits);
+  if (parts_bytes((int64_t)c.tokens * a.q_heads, splits, c.dim) > workspace_bytes)
+    return hipErrorInvalidValue;   // not a byte is written past what was given
   if (splits > 1) attn_parts(&a, workspace, splits);
   // Both kernels note how many parts each of their rows has.
   const bool join = splits > 1;
-  if (tiles && few > 0 && join) {
+  if (p.tiles && p.few > 0 && join) {
     t.note = 1;
     r.note = 1;
   } else {
@@ -190,13 +219,13 @@ hipError_t launch_paged_attention(AttnArgs a, char* workspace) {
     r.note = r.splits > 1;
   }
   hipError_t e;
-  if (tiles) {
-    if (few > 0) t.few_groups = c.seqs * r.row_tiles * c.kv_heads * r.splits;
+  if (p.tiles) {
+    if (p.few > 0) t.few_groups = c.seqs * r.row_tiles * c.kv_heads * r.splits;
     e = a.dtype == DT_F16 ? launch_tile_f16(a, t, r) : launch_tile_bf16(a, t, r);
   } else {
-    e = a.dtype == DT_F32 ? launch_rows_f32(a, r, blocks, INT32_MAX)
-        : a.dtype == DT_F16 ? launch_rows_f16(a, r, blocks, INT32_MAX)
-                            : launch_rows_bf16(a, r, blocks, INT32_MAX);
+    e = a.dtype == DT_F32 ? launch_rows_f32(a, r, p.blocks, INT32_MAX)
+        : a.dtype == DT_F16 ? launch_rows_f16(a, r, p.blocks, INT32_MAX)
+                            : launch_rows_bf16(a, r, p.blocks, INT32_MAX);
   }
   if (e == hipSuccess && join) e = launch_join(a, padded(c.dim), splits);
   return e;
