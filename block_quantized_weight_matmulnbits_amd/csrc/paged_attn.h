@@ -104,6 +104,15 @@ __device__ __forceinline__ int page_of(const CacheArgs& c, const int32_t* row, i
   return page < 0 ? 0 : page >= c.pages ? c.pages - 1 : page;
 }
 
+// Probabilities enter the second product in the values' type.  f16 has no more
+// than 24 bits below 1, and many keys that each hold less may be all of a row's
+// output where a key that holds nearly everything has a small value (an
+// attention sink): they are taken 2^(15 - slack) larger, 2^15 at most, where
+// `slack` is how far (log2) a score may pass its reference.  bf16 and f32 have
+// the range.
+template <int DT> constexpr int prob_shift(int slack) { return DT == DT_F16 ? 15 - slack : 0; }
+constexpr float exp2_of(int n) { return n < 0 ? 0.5f * exp2_of(n + 1) : n > 0 ? 2.f * exp2_of(n - 1) : 1.f; }
+
 // The score of a raw product in units of log2: capped or only scaled.
 struct ScoreScale {
   float mul, cap;   // plain: scale * log2(e); capped: scale / cap, cap * log2(e)

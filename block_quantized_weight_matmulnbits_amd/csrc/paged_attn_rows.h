@@ -52,6 +52,7 @@ __device__ __forceinline__ void attn_rows(const AttnArgs& a, const RowsPlan& pla
   constexpr bool AHEAD = RB <= 512;
   constexpr int VBYTES = ROWS_BLOCK * RB;
   constexpr int OSTRIDE = DP + 4;
+  constexpr float UP = exp2_of(prob_shift<DT>(0));   // of the outputs until they leave
   __shared__ float2 wave_ml[WAVES][16];
 
   const CacheArgs& c = a.c;
@@ -324,14 +325,15 @@ __device__ __forceinline__ void attn_rows(const AttnArgs& a, const RowsPlan& pla
             if (sees[b]) o[b][d] = n[b];
         }
       } else {
-        // Probabilities enter the product rounded to the values' type: the
+        // Probabilities enter the product rounded to the values' type, for the
         // matrix cores take no other pair; the sum l keeps them in 32 bits.
         using Op = MfmaOp<F32 ? DT_BF16 : DT>;
         u32x4 pb[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-          pb[b] = u32x4{Op::pack(p[b][0][0], p[b][0][1]), Op::pack(p[b][0][2], p[b][0][3]),
-                        Op::pack(p[b][1][0], p[b][1][1]), Op::pack(p[b][1][2], p[b][1][3])};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            pb[b][e] = Op::pack(p[b][e / 2][e % 2 * 2] * UP, p[b][e / 2][e % 2 * 2 + 1] * UP);
 #pragma unroll
         for (int d = 0; d < DB; ++d) {
           const char* at = vl + (d / 2) * 2048 + (2 * (d % 2) + (l15 % 4) / 2) * 256 +
@@ -403,6 +405,7 @@ __device__ __forceinline__ void attn_rows(const AttnArgs& a, const RowsPlan& pla
         total += f * wave_ml[w][q].y;
         x += f * *(const f32x4*)(ol + (w * 16 + q) * OSTRIDE + d);
       }
+      x *= 1.f / UP;
       if (plan.note) {
         const int i = (int)div_by(r, a.by_group);
         const int64_t row = (int64_t)(sq.t0 + i) * a.q_heads + kvh * a.group + r - i * a.group;

@@ -81,8 +81,11 @@ template <int DK, int DV> struct TileLds {
 };
 
 // The statistics rise above the reference maximum by at most this (log2)
-// before outputs are rescaled to a new one: probabilities stay below 2^8.
-constexpr float TILE_SLACK = 8.f;
+// before outputs are rescaled to a new one: probabilities stay below 2^slack.
+// What f16 has left of its range keeps the small ones (prob_shift): with 4 those
+// of 2^-25 and more keep all their bits (4096 new tokens over 16384 keys: 1012 us
+// without a shift, 1019 with a slack of 8, 1023 of 4, 1033 of 2).
+template <int DT> constexpr int tile_slack() { return DT == DT_F16 ? 4 : 8; }
 
 template <int DT, int DK, int DV, int WAVES, bool CAP>
 __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kernel(
@@ -96,6 +99,8 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   constexpr int NQ = 1;
   constexpr int SR = 64 / WAVES, IT = (SR * CH + 63) / 64;   // rows of a group that a wave loads
   constexpr int THREADS = 64 * WAVES, ROWS = 32 * NQ * WAVES;
+  constexpr int SLACK = tile_slack<DT>(), SHIFT = prob_shift<DT>(SLACK);   // of sums and outputs
+  constexpr float DOWN = exp2_of(-SHIFT);
   constexpr int FEW = DV;   // the width that the few-row workgroups pad to
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   __shared__ int found[8];
@@ -472,14 +477,14 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
 #pragma unroll
     for (int b = 0; b < NQ; ++b) {
       top[b] *= mul;
-      past |= top[b] > m[b] + TILE_SLACK || (all && mo[b] != m[b]);
+      past |= top[b] > m[b] + SLACK || (all && mo[b] != m[b]);
     }
     if (__builtin_expect(!__any(past), 1)) return;
 #pragma unroll
     for (int b = 0; b < NQ; ++b) {
       const float was = m[b], up = ceilf(fmaxf(top[b] - was, 0.f));   // a NaN raises nothing
       m[b] = was == -INFINITY ? fmaxf(top[b], was) : was + up;
-      sub[b] = m[b] == -INFINITY ? 0.f : m[b];
+      sub[b] = m[b] == -INFINITY ? 0.f : m[b] - SHIFT;
       const float back = was == -INFINITY ? 1.f : exp2_fast(-up);
       l[b] *= back;
       if (!all) continue;
@@ -489,7 +494,7 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
         for (int e = 0; e < 4; ++e)
           p[b][u][e] = Op::pack(bits16_to_f32<DT>((uint16_t)p[b][u][e]) * back,
                                 bits16_to_f32<DT>((uint16_t)(p[b][u][e] >> 16)) * back);
-      const float down = exp2_fast(mo[b] - sub[b]);
+      const float down = m[b] == -INFINITY ? 0.f : exp2_fast(mo[b] - m[b]);
 #pragma unroll
       for (int d = 0; d < DB; ++d) o[b][d] *= down;
       mo[b] = m[b];
@@ -618,7 +623,7 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
     // A NaN is left to the sum.
     m[b] = fmaxf(top[b] * mul, -INFINITY);
     mo[b] = m[b];
-    sub[b] = m[b] == -INFINITY ? 0.f : m[b];
+    sub[b] = m[b] == -INFINITY ? 0.f : m[b] - SHIFT;
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) prob(s0, p0, i);
@@ -645,7 +650,7 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
   // The output may still be a reference behind the sum.
 #pragma unroll
   for (int b = 0; b < NQ; ++b) {
-    const float down = exp2_fast(mo[b] - sub[b]);
+    const float down = m[b] == -INFINITY ? 0.f : exp2_fast(mo[b] - m[b]);
 #pragma unroll
     for (int d = 0; d < DB; ++d) o[b][d] *= down;
   }
@@ -696,16 +701,16 @@ __global__ __launch_bounds__(64 * WAVES, DV <= 128 ? 2 : 1) void attn_tile_kerne
         }
       if (a.lse != nullptr && half == 0)
         a.lse[tok * a.lse_token + (int64_t)h * a.lse_head] =
-            sum == 0.f ? -INFINITY : (m[b] + log2f(sum)) * LN2;
+            sum == 0.f ? -INFINITY : (m[b] + log2f(sum * DOWN)) * LN2;
     } else {
       const int64_t at = (int64_t)split * c.tokens * a.q_heads + tok * a.q_heads + h;
-      if (half == 0) ((float2*)a.part_stats)[at] = make_float2(m[b], sum);
+      if (half == 0) ((float2*)a.part_stats)[at] = make_float2(m[b], sum * DOWN);
 #pragma unroll
       for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           *(f32x4*)(a.part_out + at * DV + 32 * d + 8 * e + 4 * half) =
-              f32x4{o[b][d][4 * e], o[b][d][4 * e + 1], o[b][d][4 * e + 2], o[b][d][4 * e + 3]};
+              f32x4{o[b][d][4 * e], o[b][d][4 * e + 1], o[b][d][4 * e + 2], o[b][d][4 * e + 3]} * DOWN;
     }
   }
 }
