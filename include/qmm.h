@@ -370,7 +370,11 @@ int qmm_rope_append(const qmm_heads *q, const qmm_heads *k, const qmm_heads *v,
  * non-zero, j > slot - window where window > 0.  Query head h reads
  * key/value head h / (heads / kv_heads).  A token that sees no key gets 0 and
  * an lse of minus infinity; a key that is not seen has no influence, whatever
- * it holds.  Sums and the softmax are kept in fp32.
+ * it holds.  Scores, statistics and sums are kept in fp32.  The probabilities'
+ * product with 16-bit values takes them in two parts of that type (16 bits of
+ * bf16, 22 of f16); where a sequence has many rows (new tokens times the heads
+ * of a group: more than 32) in one, so that each may be off by half a step of
+ * the type.
  *   q, out    rows of heads of kv's dtype; head_dim <= 256, a multiple of
  *             8 (4 for f32); k_pages, v_pages and their strides 16-byte aligned
  *   lse       [tokens, heads] float32 (dense), or NULL
