@@ -80,7 +80,8 @@ struct AttnArgs {
 };
 size_t attn_workspace_bytes(int seqs, int tokens, int max_new, int max_len, int q_heads,
                             int kv_heads, int dim);
-// An error, and nothing enqueued, where the parts would pass workspace_bytes.
+// Errors, with nothing enqueued: hipErrorInvalidValue where the parts would pass
+// workspace_bytes, hipErrorInvalidConfiguration where a launch would be too large.
 hipError_t launch_paged_attention(AttnArgs a, char* workspace, size_t workspace_bytes);
 // Joins the parts of every row that has several (paged_attn_join.hip).
 hipError_t launch_join(const AttnArgs& a, int padded_dim, int splits);

@@ -164,8 +164,8 @@ int check_pool(const char* fn, const qmm_page_pool* p, bool tables, bool data) {
 }
 
 int check_list(const char* fn, const char* name, const int32_t* list, int64_t count) {
-  if (count < 0 || count > (1 << 24))
-    return fail(QMM_ERR_INVALID_ARG, "%s: count must be in 0 .. 2^24, got %lld.", fn,
+  if (count < 0 || count >= (1 << 24))
+    return fail(QMM_ERR_INVALID_ARG, "%s: count must be in 0 .. 2^24 - 1, got %lld.", fn,
                 (long long)count);
   if (count > 0 && (list == nullptr || !aligned(list, 4)))
     return fail(QMM_ERR_INVALID_ARG, "%s: %s must be a non-null, 4-byte aligned int32 device "
@@ -239,6 +239,9 @@ int qmm_rope_append(const qmm_heads* q, const qmm_heads* k, const qmm_heads* v,
     return fail(QMM_ERR_INVALID_ARG, "%s: positions must be a 4-byte aligned int32 array.", fn);
   if ((int64_t)(q->heads + 2 * (int64_t)kv->kv_heads) * kv->head_dim > (1 << 24))
     return fail(QMM_ERR_UNSUPPORTED, "%s: a token's heads pass 2^24 elements.", fn);
+  if (batch->tokens >= 1 << 26)
+    return fail(QMM_ERR_UNSUPPORTED, "%s: tokens must be below 2^26, got %lld. Why: a launch has fewer "
+                "than 2^32 threads. How to fix: split the batch.", fn, (long long)batch->tokens);
   if (batch->tokens == 0) return QMM_OK;
   qmm::RopeArgs a;
   a.c = cache_args(kv, batch);
@@ -306,10 +309,14 @@ int qmm_paged_attention(const qmm_heads* q, const qmm_paged_kv* kv, const qmm_pa
   if (!aligned(lse, 4))
     return fail(QMM_ERR_INVALID_ARG, "%s: lse must be a 4-byte aligned float32 array.", fn);
   const int64_t group = q->heads / kv->kv_heads;
+  auto too_large = [&] {
+    return fail(QMM_ERR_UNSUPPORTED, "%s: seqs x max_new x heads, or with them max_len, is too large "
+                "for one launch. How to fix: pass max_new and max_len as the largest counts of new "
+                "tokens and of keys, or split the batch.", fn);
+  };
   if (batch->max_new * group > (1 << 28) ||
       batch->seqs * kv->kv_heads * (batch->max_new * group / 16 + 1) > (1 << 28))
-    return fail(QMM_ERR_UNSUPPORTED, "%s: seqs x max_new x heads is too large for one launch. How "
-                "to fix: pass max_new as the largest count of new tokens, or split the batch.", fn);
+    return too_large();
   if (batch->tokens == 0 || batch->seqs == 0 || batch->max_new == 0) return QMM_OK;
   CHECK(check_workspace(fn, workspace, workspace_bytes,
                         qmm_paged_attention_workspace_size(batch, q->heads, kv->kv_heads,
@@ -337,7 +344,8 @@ int qmm_paged_attention(const qmm_heads* q, const qmm_paged_kv* kv, const qmm_pa
   a.q_wide = aligned(q->data, 16) && q->token_stride % v == 0 && q->head_stride % v == 0;
   a.out_wide = aligned(out->data, 4 * es) && out->token_stride % 4 == 0 && out->head_stride % 4 == 0;
   a.stream = (hipStream_t)stream;
-  return hip_status(qmm::launch_paged_attention(a, (char*)workspace, workspace_bytes), fn);
+  const hipError_t e = qmm::launch_paged_attention(a, (char*)workspace, workspace_bytes);
+  return e == hipErrorInvalidConfiguration ? too_large() : hip_status(e, fn);
 }
 
 size_t qmm_pages_workspace_size(const qmm_page_pool* pool, int64_t count) {

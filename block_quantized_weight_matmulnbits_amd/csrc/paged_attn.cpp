@@ -206,7 +206,16 @@ hipError_t launch_paged_attention(AttnArgs a, char* workspace, size_t workspace_
     cut(p.few_keys, p.rows_parts, ROWS_MIN_CHUNK, &r.chunk, &r.splits);
   }
   const int splits = std::max(t.splits, r.splits);
-  if (parts_bytes((int64_t)c.tokens * a.q_heads, splits, c.dim) > workspace_bytes)
+  // A launch has fewer than 2^32 threads: attention's, and the join's, which
+  // for many rows are a group of lanes each (paged_attn_join.hip).
+  const int64_t rows = (int64_t)c.tokens * a.q_heads;
+  const int64_t tiles = p.tiles ? std::max<int64_t>(t.tiles, ceil_div((int64_t)c.tokens * a.group, 128 * t.blocks) + c.seqs) : 0;
+  const int64_t few_groups = p.few > 0 ? (int64_t)c.seqs * r.row_tiles * c.kv_heads * r.splits : 0;
+  const int64_t threads = (tiles * c.kv_heads + few_groups) * 256 * (p.tiles ? t.blocks : 1);
+  const int64_t lanes = c.dim <= 64 ? 16 : c.dim <= 128 ? 32 : 64;
+  if (threads > UINT32_MAX || (splits > 1 && rows * lanes + 255 > UINT32_MAX))
+    return hipErrorInvalidConfiguration;
+  if (parts_bytes(rows, splits, c.dim) > workspace_bytes)
     return hipErrorInvalidValue;   // not a byte is written past what was given
   if (splits > 1) attn_parts(&a, workspace, splits);
   // Both kernels note how many parts each of their rows has.
@@ -220,7 +229,7 @@ hipError_t launch_paged_attention(AttnArgs a, char* workspace, size_t workspace_
   }
   hipError_t e;
   if (p.tiles) {
-    if (p.few > 0) t.few_groups = c.seqs * r.row_tiles * c.kv_heads * r.splits;
+    t.few_groups = (int)few_groups;
     e = a.dtype == DT_F16 ? launch_tile_f16(a, t, r) : launch_tile_bf16(a, t, r);
   } else {
     e = a.dtype == DT_F32 ? launch_rows_f32(a, r, p.blocks, INT32_MAX)

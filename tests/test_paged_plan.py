@@ -55,7 +55,13 @@ hipError_t launch_rows_f16(const AttnArgs& a, const RowsPlan& p, int, int) { ret
 hipError_t launch_rows_bf16(const AttnArgs& a, const RowsPlan& p, int, int) { return rows(a, p); }
 hipError_t launch_tile_f16(const AttnArgs& a, const TilePlan& p, const RowsPlan& f) { return tile(a, p, f); }
 hipError_t launch_tile_bf16(const AttnArgs& a, const TilePlan& p, const RowsPlan& f) { return tile(a, p, f); }
-hipError_t launch_join(const AttnArgs& a, int, int splits) { parts(a, splits); note[4] = splits; return hipSuccess; }
+hipError_t launch_join(const AttnArgs& a, int, int splits) {
+  const int64_t rows = (int64_t)a.c.tokens * a.q_heads, lanes = a.c.dim <= 64 ? 16 : a.c.dim <= 128 ? 32 : 64;
+  parts(a, splits);
+  most(note[2], rows <= 512 ? rows * 1024 : rows <= 4096 ? rows * 256 : (rows * lanes + 255) / 256 * 256);
+  note[4] = splits;
+  return hipSuccess;
+}
 size_t pages_workspace_bytes(int64_t, int64_t) { return 0; }
 hipError_t launch_pages_free(const PoolArgs&, const int32_t*, int) { return hipSuccess; }
 hipError_t launch_pages_fork(const PoolArgs&, const int32_t*, const int32_t*, int, int32_t*) { return hipSuccess; }
@@ -161,6 +167,8 @@ def test_random_plans_keep_to_their_workspace(plan):
         kv, group = rng.choice([1, 2, 3, 4, 8, 16, 32]), rng.choice([1, 2, 3, 4, 5, 7, 8, 16, 40])
         seqs, new = spread(1, 600), spread(1, 3000)
         tokens = seqs * new if rng.random() < 0.5 else rng.randint(1, seqs * new)
+        if tokens * kv * group > 1 << 25:   # past that the join may be too large for a launch
+            continue
         fits(plan, dtype=rng.randint(0, 2), heads=kv * group, kv=kv, dim=8 * rng.randint(1, 32), seqs=seqs,
              max_new=new, tokens=tokens, max_len=spread(1, 300000), causal=rng.randint(0, 1),
              window=rng.choice([0, 0, spread(1, 20000)]), scale=rng.choice([0.1, 0.1, 0.0, -0.1]),
@@ -178,3 +186,52 @@ def test_a_smaller_workspace_is_refused(plan):
         status = plan.so.qmm_paged_attention(rows, r(kv), r(batch), rows, None, 0.1, 1, 0, 0.0, FAKE, need - 1, None)
         assert status == plan.qmm.QMM_ERR_WORKSPACE
         assert plan.so.noted((ctypes.c_int64 * 6)()).decode().find(str(need)) > 0
+
+
+LAUNCH = 1 << 32   # a launch has fewer threads
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dtype=2, seqs=1 << 20, heads=16, kv=16),                                    # single tokens
+    dict(dtype=2, seqs=1 << 23, tokens=(1 << 23) + 63, max_new=64, heads=4, kv=1, max_len=131072),
+    dict(dtype=0, seqs=1 << 16, tokens=1 << 20, max_new=1200, heads=8, kv=8),         # bounds above the batch
+    dict(dtype=2, seqs=40, tokens=1 << 22, max_new=1 << 21, heads=64, kv=64, dim=256, max_len=1 << 21),
+])
+def test_a_call_that_is_too_large_for_a_launch_says_so(plan, kw):
+    status, _, did = plan.attend(**kw)
+    assert status == plan.qmm.QMM_ERR_UNSUPPORTED and "too large for one launch" in did["message"], (status, did)
+    assert did["threads"] == 0   # nothing was launched
+
+
+def test_launches_have_fewer_than_2_to_the_32_threads(plan):
+    rng = random.Random(5)
+    served = refused = 0
+    for _ in range(4000):
+        kv, group = rng.choice([1, 8, 32]), rng.choice([1, 4, 16])
+        seqs, new = int(2 ** rng.uniform(8, 24)), int(2 ** rng.uniform(0, 9))
+        tokens = seqs * new if rng.random() < 0.3 else seqs + rng.randint(0, new)
+        if tokens >= 1 << 30:
+            continue
+        status, _, did = plan.attend(dtype=rng.randint(0, 2), heads=kv * group, kv=kv, dim=rng.choice([64, 128, 256]),
+                                     seqs=seqs, tokens=tokens, max_new=new, max_len=int(2 ** rng.uniform(4, 18)))
+        assert did["threads"] < LAUNCH and did["groups"] >= 0
+        assert status in (0, plan.qmm.QMM_ERR_UNSUPPORTED)
+        served, refused = served + (status == 0), refused + (status != 0)
+    assert served > 500 and refused > 500
+
+
+def test_rows_and_lists_that_are_too_long_for_a_launch(plan):
+    so, r = plan.so, ctypes.byref
+    c = dict(dtype=2, heads=8, kv=8, dim=64, seqs=4, tokens=1 << 26, max_new=1 << 25, max_len=1 << 25)
+    kv, batch = plan.structs(c)
+    rows = plan.qmm._pack_heads(FAKE, 512, 64, 8)
+    out = (ctypes.c_int64 * 6)()
+    turn = lambda: so.qmm_rope_append(rows, rows, rows, rows, r(kv), r(batch), FAKE, 32, 0, 1.0, None, None)  # noqa: E731
+    assert turn() == plan.qmm.QMM_ERR_UNSUPPORTED
+    assert "2^26" in so.noted(out).decode()
+    batch.tokens -= 1
+    assert turn() == 0
+    pool = plan.qmm._PagePool(FAKE, 2, 64, 256, 1 << 14, 256, FAKE, FAKE, FAKE, 8, 16, 8, 16)
+    assert so.qmm_pages_free(r(pool), FAKE, 1 << 24, None) == plan.qmm.QMM_ERR_INVALID_ARG
+    assert "count must be" in so.noted(out).decode()
+    assert so.qmm_pages_free(r(pool), FAKE, (1 << 24) - 1, None) == 0
