@@ -125,11 +125,19 @@ def _stream(stream):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream_at(t, stream):
-    """``stream``, or the current one of t's device."""
-    if stream is None and _raw_stream is not None and t.is_cuda:
-        return _raw_stream(t.get_device())
+def _stream_at(gpu, stream):
+    """``stream``, or the current one of GPU number ``gpu``."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(gpu)
     return _stream(stream)
+
+
+def _elsewhere(name, t, gpu):
+    """The error for a tensor that is not on the GPU of the handle it came with
+    (whose number is -1 on the host)."""
+    if gpu < 0:
+        return ValueError(f"the cache and {name} must be on a GPU: the kernels read device memory")
+    return ValueError(f"{name} is on {t.device}, the cache on GPU {gpu}: pass tensors of one GPU")
 
 
 def qmm_last_error() -> str:
@@ -344,7 +352,7 @@ class Step:
         self._add(lib.qmm_step_add_paged_attention, (q, kv, batch, out, workspace, lse), *args)
 
     def add_pages_reserve(self, pool, seqs, grow, status, workspace):
-        n = _lists("seqs", seqs, "grow", grow, status)
+        n = _lists(pool, "seqs", seqs, "grow", grow, status, workspace)
         self._add(lib.qmm_step_add_pages_reserve, (pool, seqs, grow, status, workspace), pool._ref,
                   _ptr(seqs), _ptr(grow), n, _ptr(status), _ptr(workspace), workspace.nbytes)
 
@@ -464,6 +472,11 @@ def _int32(name, t, shape=None):
                          f"{list(t.shape)}")
 
 
+def _on(name, t, gpu):
+    if gpu < 0 or t.get_device() != gpu:
+        raise _elsewhere(name, t, gpu)
+
+
 def _rows(name, t):
     if t.dtype != torch.int32 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be an int32 tensor [rows, width] with dense rows, got "
@@ -489,6 +502,7 @@ class PagedKV:
         if self.head_dim > 1 and (k_pages.stride(3) != 1 or v_pages.stride(3) != 1):
             raise ValueError("head_dim must be the dense dimension of k_pages and v_pages")
         self.k_pages, self.v_pages, self.dtype = k_pages, v_pages, k_pages.dtype
+        self.gpu = k_pages.get_device()
         self._c = _PagedKV(_ptr(k_pages), _ptr(v_pages), *k_pages.stride()[:3],
                            *v_pages.stride()[:3], pages, _dt(k_pages), self.kv_heads,
                            self.page_size, self.head_dim)
@@ -509,6 +523,7 @@ class PagedBatch:
         if not starts.device == lens.device == table.device:
             raise ValueError("starts, lens and table must be on one device")
         self.starts, self.lens, self.table, self.tokens = starts, lens, table, int(tokens)
+        self.gpu = table.get_device()
         self._c = _PagedBatch(_ptr(starts), _ptr(lens), _ptr(table), table.stride(0), seqs,
                               self.tokens, table.shape[1], int(max_new), int(max_len))
         self._ref = ctypes.byref(self._c)
@@ -536,7 +551,7 @@ class PagePool:
         for n in data.shape[2:]:
             elems *= n
         self.data, self.refs, self.table, self.lens = data, refs, table, lens
-        self.page_size = int(page_size)
+        self.page_size, self.gpu = int(page_size), data.get_device()
         self._c = _PagePool(_ptr(data), data.shape[0], data.shape[1], elems * size,
                             data.stride(0) * size, data.stride(1) * size, _ptr(refs), _ptr(table),
                             _ptr(lens), stride, slots, width, self.page_size)
@@ -552,6 +567,8 @@ def _heads(name, t, kv, batch, heads):
         raise ValueError(f"{name} must be {kv.dtype} [{batch.tokens}, {heads}, {kv.head_dim}] with "
                          f"dense rows of head_dim, got {t.dtype} {list(shape)} with strides "
                          f"{list(strides)}")
+    if t.get_device() != kv.gpu:
+        raise _elsewhere(name, t, kv.gpu)
     return _pack_heads(t.data_ptr(), strides[0], strides[1], heads)
 
 
@@ -559,12 +576,17 @@ def _rope_args(q, k, v, out, kv, batch, inv_freq, interleaved, factor, positions
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise ValueError(f"inv_freq must be a dense float64 vector, got {inv_freq.dtype} "
                          f"{list(inv_freq.shape)}")
+    heads, kv_heads = q.shape[1], kv.kv_heads
+    rows = (_heads("q", q, kv, batch, heads), _heads("k", k, kv, batch, kv_heads),
+            _heads("v", v, kv, batch, kv_heads), _heads("out", out, kv, batch, heads))
+    if batch.gpu != kv.gpu:
+        raise _elsewhere("the batch", batch.table, kv.gpu)
     if positions is not None:
         _int32("positions", positions, (batch.tokens,))
-    heads, kv_heads = q.shape[1], kv.kv_heads
-    return (_heads("q", q, kv, batch, heads), _heads("k", k, kv, batch, kv_heads),
-            _heads("v", v, kv, batch, kv_heads), _heads("out", out, kv, batch, heads), kv._ref,
-            batch._ref, inv_freq.data_ptr(), inv_freq.shape[0], interleaved, factor,
+        _on("positions", positions, kv.gpu)
+    _on("inv_freq", inv_freq, kv.gpu)
+    return (*rows, kv._ref, batch._ref,
+            inv_freq.data_ptr(), inv_freq.shape[0], interleaved, factor,
             None if positions is None else positions.data_ptr())
 
 
@@ -574,7 +596,7 @@ def qmm_rope_append(q, k, v, out, kv, batch, inv_freq, interleaved=False, factor
     v [tokens, kv_heads, head_dim] to the cache ``kv``; ``inv_freq`` [half] is
     float64, ``positions`` [tokens] int32 or None (a token's key number)."""
     _check(lib.qmm_rope_append(*_rope_args(q, k, v, out, kv, batch, inv_freq, interleaved, factor,
-                                           positions), _stream_at(q, stream)))
+                                           positions), _stream_at(kv.gpu, stream)))
 
 
 def qmm_paged_attention_workspace_size(batch, q_heads, kv_heads, head_dim) -> int:
@@ -590,8 +612,13 @@ def _attention_args(q, kv, batch, out, workspace, scale, causal, window, softcap
     if scale is None:
         scale = kv.head_dim ** -0.5
     heads = q.shape[1]
-    return (_heads("q", q, kv, batch, heads), kv._ref, batch._ref,
-            _heads("out", out, kv, batch, heads), None if lse is None else lse.data_ptr(), scale,
+    q_rows, out_rows = _heads("q", q, kv, batch, heads), _heads("out", out, kv, batch, heads)
+    if batch.gpu != kv.gpu:
+        raise _elsewhere("the batch", batch.table, kv.gpu)
+    _on("workspace", workspace, kv.gpu)
+    if lse is not None:
+        _on("lse", lse, kv.gpu)
+    return (q_rows, kv._ref, batch._ref, out_rows, None if lse is None else lse.data_ptr(), scale,
             causal, window, softcap, workspace.data_ptr(), workspace.nbytes)
 
 
@@ -601,7 +628,8 @@ def qmm_paged_attention(q, kv, batch, out, workspace, scale=None, causal=True, w
     where given, ``lse`` [tokens, heads] float32; ``scale`` defaults to
     head_dim ** -0.5."""
     _check(lib.qmm_paged_attention(*_attention_args(q, kv, batch, out, workspace, scale, causal,
-                                                    window, softcap, lse), _stream_at(q, stream)))
+                                                    window, softcap, lse),
+                                   _stream_at(kv.gpu, stream)))
 
 
 def qmm_pages_workspace_size(pool, count=0) -> int:
@@ -609,50 +637,58 @@ def qmm_pages_workspace_size(pool, count=0) -> int:
     return int(lib.qmm_pages_workspace_size(pool._ref, count))
 
 
-def _lists(a_name, a, b_name=None, b=None, status=None):
-    """Checks int32 lists of one length and the pair of status words; the length."""
+def _lists(pool, a_name, a, b_name=None, b=None, status=None, workspace=None):
+    """Checks int32 lists of one length, the pair of status words and the
+    workspace, all on the pool's GPU; the length."""
     _int32(a_name, a)
     n = a.numel()
     if b is not None:
         _int32(b_name, b)
         if b.numel() != n:
             raise ValueError(f"{a_name} and {b_name} must have one length, got {n} and {b.numel()}")
+        _on(b_name, b, pool.gpu)
     if status is not None:
         _int32("status", status, (2,))
+        _on("status", status, pool.gpu)
+        _on("workspace", workspace, pool.gpu)
+    _on(a_name, a, pool.gpu)
     return n
 
 
 def qmm_pages_free(pool, seqs, stream=None):
-    n = _lists("seqs", seqs)
-    _check(lib.qmm_pages_free(pool._ref, seqs.data_ptr(), n, _stream_at(seqs, stream)))
+    n = _lists(pool, "seqs", seqs)
+    _check(lib.qmm_pages_free(pool._ref, seqs.data_ptr(), n, _stream_at(pool.gpu, stream)))
 
 
 def qmm_pages_fork(pool, parents, children, status, workspace, stream=None):
     """``status`` [2] int32, zeroed by the caller, tells on the device whether
     the list was served (qmm_pages_status)."""
-    n = _lists("parents", parents, "children", children, status)
+    n = _lists(pool, "parents", parents, "children", children, status, workspace)
     _check(lib.qmm_pages_fork(pool._ref, parents.data_ptr(), children.data_ptr(), n,
                               status.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-                              _stream_at(parents, stream)))
+                              _stream_at(pool.gpu, stream)))
 
 
 def qmm_pages_reserve(pool, seqs, grow, status, workspace, stream=None):
-    n = _lists("seqs", seqs, "grow", grow, status)
+    n = _lists(pool, "seqs", seqs, "grow", grow, status, workspace)
     _check(lib.qmm_pages_reserve(pool._ref, seqs.data_ptr(), grow.data_ptr(), n, status.data_ptr(),
-                                 workspace.data_ptr(), workspace.nbytes, _stream_at(seqs, stream)))
+                                 workspace.data_ptr(), workspace.nbytes, _stream_at(pool.gpu, stream)))
 
 
 def qmm_pages_copy(pool, src, dst, stream=None):
-    n = _lists("src", src, "dst", dst)
-    _check(lib.qmm_pages_copy(pool._ref, src.data_ptr(), dst.data_ptr(), n, _stream_at(src, stream)))
+    n = _lists(pool, "src", src, "dst", dst)
+    _check(lib.qmm_pages_copy(pool._ref, src.data_ptr(), dst.data_ptr(), n, _stream_at(pool.gpu, stream)))
 
 
 def qmm_pages_compact(pool, refs_out, table_out, live, workspace, stream=None):
     """``refs_out`` and ``table_out`` take the new counts and table, ``live`` [1]
     the number of used pages, now the first ones."""
-    _int32("refs_out", refs_out, pool.refs.shape)
-    _int32("table_out", table_out, pool.table.shape)
-    _int32("live", live)
+    if pool.refs is not None:   # without tables the call itself refuses the pool
+        _int32("refs_out", refs_out, pool.refs.shape)
+        _int32("table_out", table_out, pool.table.shape)
+        _int32("live", live)
+    for name, t in (("refs_out", refs_out), ("table_out", table_out), ("live", live), ("workspace", workspace)):
+        _on(name, t, pool.gpu)
     _check(lib.qmm_pages_compact(pool._ref, refs_out.data_ptr(), table_out.data_ptr(),
                                  live.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-                                 _stream_at(refs_out, stream)))
+                                 _stream_at(pool.gpu, stream)))
