@@ -33,9 +33,10 @@ int dtype_size(int dt) { return dt == QMM_F32 ? 4 : dt == QMM_F16 || dt == QMM_B
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-// Strides and element counts are kept below 2^40 elements, so that no product
-// of one with a 32-bit index passes 64 bits after scaling to bytes.
-constexpr int64_t MAX_STRIDE = (int64_t)1 << 40 >> 1;
+// The largest stride in elements (or bytes), past any allocation.  Kernels
+// multiply it in 64 bits by indices that the tensor has, so that a product is an
+// offset inside the tensor.
+constexpr int64_t MAX_STRIDE = (int64_t)1 << 39;
 bool stride_ok(int64_t s) { return s >= 0 && s <= MAX_STRIDE; }
 
 int check_kv(const char* fn, const qmm_paged_kv* kv) {

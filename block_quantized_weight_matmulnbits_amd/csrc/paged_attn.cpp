@@ -49,9 +49,15 @@ void cut(int64_t keys, int64_t parts, int64_t step, int* chunk, int* splits) {
 int64_t rows_parts(int seqs, int max_new, int64_t keys, int group, int kv_heads, int blocks,
                    bool wide) {
   const int64_t tiles = seqs * kv_heads * ceil_div((int64_t)max_new * group, 16 * blocks);
-  // As many tiles are not split, wide ones neither (f32, heads of 128: 2048 tokens
-  // over 8192 keys 3.3 ms whole, 3.9 in parts of 4096; four of 1024 over 2000 to
-  // 16384 8.5 and 13.3; 256 single tokens, 8 heads of 256: 4.8 and 5.9).
+  // As many tiles are not split.  In 16 bits that hardly matters where lengths
+  // are spread evenly (from 17 to 8191 keys, 64 sequences over 32 key/value heads
+  // 844 us whole and 834 in parts of 1024, 256 over 8 heads 846 and 861, both at
+  // the copy's rate), but one of 131072 keys among 255 of 500 takes 3849 us whole
+  // and 531 in parts, of a workspace of 545 MB: parts counted by the lengths on
+  // the device, as the tiles kernel has them, are what is missing.  Wide ones lose
+  // by parts (f32, heads of 128: 2048 tokens over 8192 keys 3.3 ms whole, 3.9 in
+  // parts of 4096; four of 1024 over 2000 to 16384 8.5 and 13.3; 256 single
+  // tokens, 8 heads of 256: 4.8 and 5.9).
   if (tiles >= ROWS_FILL) return 1;
   // Wide rows leave a compute unit one workgroup at a time: with many of them
   // their beginnings and ends count.  f32, in parts of 1024 and of

@@ -119,7 +119,8 @@ struct ScoreScale {
   float mul, cap;   // plain: scale * log2(e); capped: scale / cap, cap * log2(e)
 };
 // tanh x for |x| < TANH_NEAR: the odd polynomial of five terms past x that fits
-// it best there (by reweighted least squares), to 3e-9 of its value.
+// it best there (by reweighted least squares), to 4.6e-9 of its value; its
+// roundings in 32 bits come to more.
 constexpr float TANH_NEAR = 0.6f;
 __device__ __forceinline__ float tanh_near(float x) {
   const float u = x * x;

@@ -13,7 +13,7 @@
 //
 // 64 sequences of 17 to 8191 keys, a token each (32 heads of 128 over 8, bf16):
 // 230 us with the join, 4.98 TB/s of keys and values, where a large copy moves
-// 4.95.  Two sequences of 90001 and 131071 keys: 186 us, 4.9 TB/s.  Five guessed f32
+// 4.95.  Two sequences of 90001 and 131071 keys: 190 us, 4.8 TB/s.  Five guessed f32
 // tokens for each of 7 sequences: 22 us, of which latencies in a row are most.
 #pragma once
 

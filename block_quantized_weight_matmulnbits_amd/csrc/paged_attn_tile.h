@@ -9,12 +9,13 @@
 // step (matrix cores), the exponentials of this one (vector units) and the
 // product of the last one's probabilities with V (matrix cores).
 //
-// 4096 new tokens after 12288 cached ones (32 heads of 128 over 8): 890 us, 1080
-// TFLOP/s (925 with a sequence's first tiles first: the last ones, which see the
-// most keys, are then the end of the launch), where a large matrix product reaches 1290 on this chip.  The matrix
-// cores are busy half of the time at 1.85 GHz: the chip lowers its clock under
-// the load (128 workgroups instead of 256 run at 2.15 GHz), so what is left is
-// energy, most of it in LDS reads and exponentials.
+// 4096 new tokens after 12288 cached ones (32 heads of 128 over 8, bf16): 887 to
+// 940 us by the card, 1020 to 1085 TFLOP/s, where a large matrix product reaches
+// 1290 (with a sequence's first tiles first 4 % more: the last ones, which see the
+// most keys, are then the end of the launch).  At 940 us the matrix cores are
+// busy 0.54 of the time at 1.81 GHz: the chip lowers its clock under the load
+// (128 workgroups instead of 256 run at 2.15 GHz), so what is left is energy,
+// most of it in LDS reads and exponentials.
 //
 // The last workgroups of a launch take the sequences with few rows, as the rows
 // kernel does: they fill the compute units that the tiles leave (three chunks

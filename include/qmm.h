@@ -310,10 +310,11 @@ int qmm_lowp_quantize(const void *x, int x_dtype, int64_t rows, int64_t cols, in
  *   slot = lens[s] - starts[s + 1] + t,
  * and key j lies in page table[s * table_stride + j / page_size] at position
  * j % page_size.  starts [seqs + 1] does not decrease.  max_new and max_len
- * bound the tokens and keys of every sequence: they size the launches (and a
- * recorded step), and counts past them are cut to them.  A table entry outside
- * 0 .. pages - 1 gives wrong results, never an access out of bounds: nothing
- * is appended to it, and attention reads the first or last page for it.
+ * bound the tokens and keys of every sequence: they size attention's launches
+ * (and a recorded step), and attention cuts counts past them to them; the
+ * append does not use them.  A table entry outside 0 .. pages - 1 gives wrong
+ * results, never an access out of bounds: nothing is appended to it, and
+ * attention reads the first or last page for it.
  */
 typedef struct qmm_paged_kv {
     void *k_pages;               /* [pages, kv_heads, page_size, head_dim] */
