@@ -9,8 +9,8 @@
 // step (matrix cores), the exponentials of this one (vector units) and the
 // product of the last one's probabilities with V (matrix cores).
 //
-// 4096 new tokens after 12288 cached ones (32 heads of 128 over 8, bf16): 887 to
-// 940 us by the card, 1020 to 1085 TFLOP/s, where a large matrix product reaches
+// 4096 new tokens after 12288 cached ones (32 heads of 128 over 8, bf16): 884 to
+// 940 us by the card, 1020 to 1090 TFLOP/s, where a large matrix product reaches
 // 1290 (with a sequence's first tiles first 4 % more: the last ones, which see the
 // most keys, are then the end of the launch).  At 940 us the matrix cores are
 // busy 0.54 of the time at 1.81 GHz: the chip lowers its clock under the load
