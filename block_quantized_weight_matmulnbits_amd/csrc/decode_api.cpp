@@ -1,0 +1,129 @@
+// decode_api.cpp -- the extern "C" entry points around a decode step's
+// projections declared in include/qmm.h (norm, experts, sampling): arguments are
+// validated on the host (errors say what, why and how to fix), then the
+// launchers of rms_norm.hip, moe.hip and sample.hip enqueue the work.  Nothing
+// here allocates device memory or synchronizes.
+#include <math.h>
+#include <stdarg.h>
+#include <stdio.h>
+
+#include "../../include/qmm.h"
+#include "decode.h"
+#include "qmm_internal.h"
+
+namespace {
+
+int fail(int code, const char* fmt, ...) {
+  char buf[1024];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return qmm::set_error(code, buf);
+}
+
+int hip_status(hipError_t e, const char* fn) {
+  if (e == hipSuccess) return QMM_OK;
+  return fail(QMM_ERR_HIP, "%s: the HIP runtime reported '%s' while enqueueing the kernel. "
+              "Why: the launch or an earlier asynchronous operation on this device failed. "
+              "How to fix: check the device state and earlier errors on the stream.",
+              fn, hipGetErrorString(e));
+}
+
+int dtype_size(int dt) { return dt == QMM_F32 ? 4 : dt == QMM_F16 || dt == QMM_BF16 ? 2 : 0; }
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// Past any allocation; kernels multiply it in 64 bits by a row that the tensor has.
+constexpr int64_t MAX_STRIDE = (int64_t)1 << 39;
+
+int check_rows(const char* fn, const char* name, const qmm_rows* r, int64_t rows, int64_t cols,
+               int es) {
+  if (r->data == nullptr || !aligned(r->data, es))
+    return fail(QMM_ERR_INVALID_ARG, "%s: %s.data must be a non-null device pointer aligned to its "
+                "element size.", fn, name);
+  if (r->stride < 0 || r->stride > MAX_STRIDE || (rows > 1 && r->stride < cols))
+    return fail(QMM_ERR_INVALID_ARG, "%s: %s.stride=%lld does not hold a row of %lld elements. How "
+                "to fix: pass rows that do not overlap, with a dense last dimension.", fn, name,
+                (long long)r->stride, (long long)cols);
+  return QMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qmm_rms_norm(const qmm_rows* x, const qmm_rows* residual, const qmm_rows* h,
+                 const void* weight, int weight_dtype, float offset, double eps, const qmm_rows* y,
+                 const qmm_quant* quant, int dtype, int64_t rows, int64_t cols, void* stream) {
+  const char* fn = "qmm_rms_norm";
+  const int es = dtype_size(dtype);
+  if (es == 0 || (weight != nullptr && dtype_size(weight_dtype) == 0))
+    return fail(QMM_ERR_INVALID_ARG, "%s: dtype=%d / weight_dtype=%d is not a qmm_dtype. How to fix: "
+                "pass QMM_F32, QMM_F16 or QMM_BF16.", fn, dtype, weight_dtype);
+  if (rows < 0 || cols <= 0)
+    return fail(QMM_ERR_INVALID_ARG, "%s: rows must be >= 0 and cols positive, got rows=%lld "
+                "cols=%lld.", fn, (long long)rows, (long long)cols);
+  if (rows >= (int64_t)1 << 40 || cols > qmm::NORM_MAX_COLS)
+    return fail(QMM_ERR_UNSUPPORTED, "%s: rows must be below 2^40 and cols at most 2^20 (got rows=%lld "
+                "cols=%lld). Why: a row is one workgroup's.", fn, (long long)rows, (long long)cols);
+  if (!(eps >= 0.0) || isinf(eps) || !isfinite(offset))
+    return fail(QMM_ERR_INVALID_ARG, "%s: eps must be finite and not negative, offset finite (got %g, "
+                "%g).", fn, eps, (double)offset);
+  if (h == nullptr && y == nullptr && quant == nullptr)
+    return fail(QMM_ERR_INVALID_ARG, "%s: h, y and quant are all NULL. How to fix: pass an output.", fn);
+  if (x == nullptr) return fail(QMM_ERR_INVALID_ARG, "%s: x is NULL.", fn);
+  qmm::NormArgs a;
+  if (quant != nullptr) {
+    if (quant->kind != QMM_QUANT_INT8 && quant->kind != QMM_QUANT_MX && quant->kind != QMM_QUANT_TENSOR)
+      return fail(QMM_ERR_INVALID_ARG, "%s: quant.kind=%d is not a qmm_quant_kind.", fn, quant->kind);
+    const bool ints = quant->kind == QMM_QUANT_INT8;
+    if (ints && (quant->block_size < 16 || quant->block_size > qmm::NORM_MAX_COLS ||
+                 (quant->block_size & (quant->block_size - 1))))
+      return fail(QMM_ERR_INVALID_ARG, "%s: quant.block_size must be a power of two from 16 to 2^20, "
+                  "got %d. How to fix: pass the block_size of the weight that reads the codes.", fn,
+                  quant->block_size);
+    if (!ints && quant->format != QMM_LOWP_E4M3 && quant->format != QMM_LOWP_E5M2)
+      return fail(QMM_ERR_INVALID_ARG, "%s: quant.format=%d must be QMM_LOWP_E4M3 or QMM_LOWP_E5M2. "
+                  "Why: the output holds 8 bits an element.", fn, quant->format);
+    if (rows > 0 && (quant->codes == nullptr || quant->scales == nullptr ||
+                     (quant->kind != QMM_QUANT_MX && !aligned(quant->scales, 4))))
+      return fail(QMM_ERR_INVALID_ARG, "%s: quant.codes and quant.scales must be non-null device "
+                  "pointers (float32 scales 4-byte aligned).", fn);
+    a.kind = quant->kind;
+    a.format = quant->format;
+    a.block = ints ? quant->block_size : 32;
+    a.blocks = (int)((cols + a.block - 1) / a.block);
+    a.code_cols = ints ? a.blocks * a.block : (int)cols;
+    a.codes = (uint8_t*)quant->codes;
+    a.scales = quant->scales;
+  }
+  if (rows == 0) return QMM_OK;
+  const struct { const char* name; const qmm_rows* r; } each[] = {
+      {"x", x}, {"residual", residual}, {"h", h}, {"y", y}};
+  for (const auto& e : each) {
+    if (e.r == nullptr) continue;
+    const int st = check_rows(fn, e.name, e.r, rows, cols, es);
+    if (st != QMM_OK) return st;
+  }
+  if (!aligned(weight, weight == nullptr ? 1 : dtype_size(weight_dtype)))
+    return fail(QMM_ERR_INVALID_ARG, "%s: weight must be aligned to its element size.", fn);
+  if (h != nullptr && y != nullptr && h->data == y->data)
+    return fail(QMM_ERR_INVALID_ARG, "%s: h and y are two outputs and cannot be the same rows.", fn);
+  a.x = (const char*)x->data;
+  a.x_stride = x->stride;
+  if (residual) a.residual = (const char*)residual->data, a.residual_stride = residual->stride;
+  if (h) a.h = (char*)h->data, a.h_stride = h->stride;
+  if (y) a.y = (char*)y->data, a.y_stride = y->stride;
+  a.weight = (const char*)weight;
+  a.weight_dtype = weight_dtype;
+  a.offset = offset;
+  a.eps = eps;
+  a.dtype = dtype;
+  a.rows = rows;
+  a.cols = (int)cols;
+  a.stream = (hipStream_t)stream;
+  return hip_status(qmm::launch_rms_norm(a), fn);
+}
+
+}  // extern "C"

@@ -233,6 +233,15 @@ hipError_t ensure_dynamic_lds(const void* kernel, int bytes) {
   return e;
 }
 
+// The product of quantized activations: on the int8 matrix cores where they
+// are faster (compint8_tiled_preferred); else 3-bit weights on the generic
+// kernel, the rest on compint8_kernel.
+static hipError_t launch_compint8_product(const MatArgs& a, const int8_t* qa, const float* sa) {
+  if (a.tiled || compint8_tiled_preferred(a)) return launch_compint8_tiled(a, qa, sa);
+  if (a.bits == 3) return launch_generic_int(a, qa, 1, sa, nullptr);
+  return launch_compint8(a, qa, sa);
+}
+
 int gemm_compint8_impl(const char* fn, const void* A, int a_dtype, const uint8_t* B,
                        int b_layout, const void* scales, int s_dtype, const uint8_t* zero_points,
                        const int32_t* g_idx, int64_t g_idx_len, const void* bias, void* Y,
@@ -276,13 +285,7 @@ int gemm_compint8_impl(const char* fn, const void* A, int a_dtype, const uint8_t
   int8_t* qa = (int8_t*)workspace;
   float* sa = (float*)((char*)workspace + ws_qa_bytes(a.M, a.kb, a.block_size));
   hipError_t e = launch_quantize_a(a, qa, sa);
-  if (e == hipSuccess) {
-    // The int8 matrix cores where they are faster (compint8_tiled_preferred);
-    // else 3-bit weights on the generic kernel, the rest on compint8_kernel.
-    if (a.tiled || compint8_tiled_preferred(a)) e = launch_compint8_tiled(a, qa, sa);
-    else if (a.bits == 3) e = launch_generic_int(a, qa, 1, sa, nullptr);
-    else e = launch_compint8(a, qa, sa);
-  }
+  if (e == hipSuccess) e = launch_compint8_product(a, qa, sa);
   return hip_status(e, fn);
 }
 
@@ -337,6 +340,30 @@ int qmm_gemm_compint8(const void* A, int a_dtype, const uint8_t* B, int b_layout
   return qmm::gemm_compint8_impl("qmm_gemm_compint8", A, a_dtype, B, b_layout, scales, s_dtype,
                                  zero_points, g_idx, g_idx_len, bias, Y, M, K, N, block_size, bits,
                                  accuracy_level, workspace, workspace_bytes, nullptr, stream);
+}
+
+int qmm_gemm_compint8_quantized(const int8_t* qa, const float* sa, const uint8_t* B, int b_layout,
+                                const void* scales, int s_dtype, const uint8_t* zero_points,
+                                const void* bias, void* Y, int y_dtype, int64_t M, int64_t K,
+                                int64_t N, int block_size, int bits, void* stream) {
+  const char* fn = "qmm_gemm_compint8_quantized";
+  MatArgs a;
+  const int st = validate_matmul(fn, Route::CompInt8, qa, y_dtype, B, b_layout, scales, s_dtype,
+                                 zero_points, bias, Y, M, K, N, block_size, bits, 4, &a);
+  if (st != QMM_OK) return st;
+  if (M > 0 && (sa == nullptr || !aligned(qa, 16) || !aligned(sa, 4)))
+    return fail(QMM_ERR_INVALID_ARG, "%s: qa must be 16-byte aligned and sa a non-null, 4-byte "
+                "aligned device array. Why: they are the quantized activations [M, kb * "
+                "block_size] and their scales [M, kb]. How to fix: pass what qmm_rms_norm wrote.",
+                fn);
+  if (a.tiled && !qmm::compint8_tiled_supported(a))
+    return fail(QMM_ERR_UNSUPPORTED, "%s: on the tiled layout this needs block_size >= 32 and at "
+                "most 896 blocks per row (got block_size=%d, %lld blocks). How to fix: pass the "
+                "operator's layout (QMM_LAYOUT_ORT) for this weight.", fn, block_size,
+                (long long)a.kb);
+  if (M == 0) return QMM_OK;
+  a.stream = (hipStream_t)stream;
+  return hip_status(qmm::launch_compint8_product(a, qa, sa), fn);
 }
 
 int qmm_check_g_idx(const int32_t* g_idx, int64_t g_idx_len, int64_t K, int block_size) {

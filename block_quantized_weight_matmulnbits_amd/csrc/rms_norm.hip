@@ -1,0 +1,290 @@
+// rms_norm.hip -- root-mean-square norm with the residual's addition, and its
+// output in 8 bits with scales, for the projection that comes next:
+//   h = x + residual,  y = (h * i) * (weight + offset),
+//   i = 1 / sqrt(mean(h^2) + eps),
+// h in 32 bits, the mean and i in 64 bits (i then rounded to 32), each product
+// rounded to 32 bits.  The statistic has bits to spare because codes hang on its
+// last one: with it codes and scales are those of the definition bit for bit,
+// whatever the order of the sum.  h and y leave rounded once; the codes are
+// made of the unrounded y.  A scale is the block's maximum times the rounded
+// reciprocal of the format's largest value: half a step of 32 bits beside the
+// quotient.
+//
+// Bound by HBM: x and the residual in, h and the codes out.  A row is read
+// once and stays in registers, eight elements of a thread side by side, so that
+// the blocks that share a scale are groups of neighbouring lanes and their
+// maxima a few cross-lane steps.
+#include <algorithm>
+
+#include "decode.h"
+#include "qmm_device.h"
+
+namespace qmm {
+namespace {
+
+constexpr int CHUNK = 8;            // elements a thread holds side by side
+constexpr int WIDEST_SHUFFLE = 64;  // lanes of a block whose maximum is shuffled
+
+template <int DT>
+__device__ __forceinline__ float element(const char* p, int64_t i) {
+  return dt<DT>::to_f32(((const typename dt<DT>::T*)p)[i]);
+}
+
+// Elements [c, c + 8) of a row as fp32; zero past its end.  The vectors need no
+// alignment but the element's (gfx950 reads and writes them at any address).
+template <int DT>
+__device__ __forceinline__ void load8(const char* row, int c, int cols, float (&v)[CHUNK]) {
+  using T = typename dt<DT>::T;
+  if (c + CHUNK <= cols) {
+    T e[CHUNK];
+    __builtin_memcpy(e, (const T*)row + c, sizeof(e));
+#pragma unroll
+    for (int j = 0; j < CHUNK; ++j) v[j] = dt<DT>::to_f32(e[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < CHUNK; ++j) v[j] = c + j < cols ? element<DT>(row, c + j) : 0.f;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(char* row, int c, int cols, const float (&v)[CHUNK]) {
+  using T = typename dt<DT>::T;
+  T e[CHUNK];
+#pragma unroll
+  for (int j = 0; j < CHUNK; ++j) e[j] = dt<DT>::from_f32(v[j]);
+  if (c + CHUNK <= cols) {
+    __builtin_memcpy((T*)row + c, e, sizeof(e));
+  } else {
+#pragma unroll
+    for (int j = 0; j < CHUNK; ++j)
+      if (c + j < cols) ((T*)row)[c + j] = e[j];
+  }
+}
+
+__device__ __forceinline__ void load_weight(const NormArgs& a, int c, float (&w)[CHUNK]) {
+  if (a.weight == nullptr) {
+#pragma unroll
+    for (int j = 0; j < CHUNK; ++j) w[j] = 1.f;
+  } else if (a.weight_dtype == DT_F32) {
+    load8<DT_F32>(a.weight, c, a.cols, w);
+  } else if (a.weight_dtype == DT_F16) {
+    load8<DT_F16>(a.weight, c, a.cols, w);
+  } else {
+    load8<DT_BF16>(a.weight, c, a.cols, w);
+  }
+#pragma unroll
+  for (int j = 0; j < CHUNK; ++j) w[j] += a.offset;
+}
+
+// Two FP8 codes (OCP E4M3 or E5M2): nearest, ties to even, saturating; a NaN is
+// 0x7F.
+__device__ __forceinline__ uint32_t fp8_pair(float x, float y, int format) {
+  const float most = format == 0 ? 448.f : 57344.f;
+  const float a = __builtin_amdgcn_fmed3f(x, -most, most), b = __builtin_amdgcn_fmed3f(y, -most, most);
+  uint32_t c = format == 0 ? __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false)
+                           : __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
+  c &= 0xFFFFu;
+  if (x != x) c = (c & 0xFF00u) | 0x7Fu;
+  if (y != y) c = (c & 0xFFu) | 0x7F00u;
+  return c;
+}
+
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// body(p) for each of a thread's pieces, unrolled where they are registers.
+template <int NP, typename Body>
+__device__ __forceinline__ void each_piece(int pieces, Body body) {
+  if constexpr (NP > 0) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) body(p);
+  } else {
+    for (int p = 0; p < pieces; ++p) body(p);
+  }
+}
+
+// RT threads a row, NP chunks a thread in registers (0: rows too long for
+// them are read again where needed).
+template <int DT, int RT, int NP>
+__global__ __launch_bounds__(RT < 256 ? 256 : RT) void rms_norm_kernel(NormArgs a) {
+  constexpr int ES = (int)sizeof(typename dt<DT>::T);
+  constexpr int ROWS = RT < 256 ? 256 / RT : 1;
+  constexpr int WAVES = RT / 64;
+  __shared__ double sums[WAVES];
+  __shared__ uint32_t tops[NP == 0 ? NORM_MAX_COLS / 1024 : RT * NP * CHUNK / 1024 + 1];
+  const int t = threadIdx.x % RT, lane = threadIdx.x & 63, wave = t >> 6;
+  // Chunks of the codes' row, which may be padded to whole blocks.
+  const int chunks = ((a.kind == QUANT_INT8 ? a.code_cols : a.cols) + CHUNK - 1) / CHUNK;
+  const int pieces = NP > 0 ? NP : (chunks + RT - 1) / RT;
+  const int log_block = 31 - __builtin_clz(a.block | 1);
+  const bool wide = a.kind == QUANT_INT8 && a.block > CHUNK * WIDEST_SHUFFLE;
+
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / RT; row < a.rows;
+       row += (int64_t)gridDim.x * ROWS) {
+    const char* x = a.x + row * a.x_stride * ES;
+    const char* r = a.residual ? a.residual + row * a.residual_stride * ES : nullptr;
+    float v[NP > 0 ? NP : 1][CHUNK];
+    auto sum8 = [&](int c, float (&out)[CHUNK]) {
+      load8<DT>(x, c, a.cols, out);
+      if (r) {
+        float e[CHUNK];
+        load8<DT>(r, c, a.cols, e);
+#pragma unroll
+        for (int j = 0; j < CHUNK; ++j) out[j] += e[j];
+      }
+    };
+    double ss = 0.0;
+    if constexpr (NP > 0) each_piece<NP>(pieces, [&](int p) { sum8((p * RT + t) * CHUNK, v[p]); });
+    each_piece<NP>(pieces, [&](int p) {
+      float(&e)[CHUNK] = v[NP > 0 ? p : 0];
+      if constexpr (NP == 0) sum8((p * RT + t) * CHUNK, e);
+#pragma unroll
+      for (int j = 0; j < CHUNK; ++j) ss = __builtin_fma((double)e[j], (double)e[j], ss);
+    });
+    ss = wave_sum_f64(ss);
+    if constexpr (WAVES > 1) {
+      __syncthreads();               // the row before has been read
+      if (lane == 0) sums[wave] = ss;
+      if (wide)
+        for (int b = t; b < a.blocks; b += RT) tops[b] = 0u;
+      __syncthreads();
+      ss = 0.0;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) ss += sums[w];
+    }
+    const float inv = (float)(1.0 / sqrt(ss / (double)a.cols + a.eps));
+
+    // y of a piece; zero past the row's end.
+    auto normed = [&](int p, float (&y)[CHUNK]) {
+      const int c = (p * RT + t) * CHUNK;
+      float w[CHUNK];
+      load_weight(a, c, w);
+      float e[CHUNK];
+      if constexpr (NP == 0) sum8(c, e);
+#pragma unroll
+      for (int j = 0; j < CHUNK; ++j) {
+        const float h = NP > 0 ? v[NP > 0 ? p : 0][j] : e[j];
+        y[j] = c + j < a.cols ? h * inv * w[j] : 0.f;
+      }
+    };
+    auto chunk_top = [&](const float (&y)[CHUNK]) {
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < CHUNK; ++j) m = fmaxf(m, fabsf(y[j]));
+      return m;
+    };
+    if constexpr (WAVES > 1) {
+      // Blocks that several waves share: their maxima meet in LDS (the bits of
+      // floats that are not negative order as they do).
+      if (wide) {
+        each_piece<NP>(pieces, [&](int p) {
+          const int c = (p * RT + t) * CHUNK;
+          float y[CHUNK];
+          normed(p, y);
+          if (c < a.code_cols) atomicMax(&tops[c >> log_block], __float_as_uint(chunk_top(y)));
+        });
+        __syncthreads();
+      }
+    }
+
+    each_piece<NP>(pieces, [&](int p) {
+      const int c = (p * RT + t) * CHUNK;
+      float y[CHUNK];
+      normed(p, y);
+      if (a.h) {
+        float h[CHUNK];
+        if constexpr (NP == 0) sum8(c, h);
+#pragma unroll
+        for (int j = 0; j < CHUNK; ++j) h[j] = NP > 0 ? v[NP > 0 ? p : 0][j] : h[j];
+        store8<DT>(a.h + row * a.h_stride * ES, c, a.cols, h);
+      }
+      if (a.y) store8<DT>(a.y + row * a.y_stride * ES, c, a.cols, y);
+      if (a.kind == QUANT_NONE) return;
+      uint32_t word[2] = {0u, 0u};
+      if (a.kind == QUANT_INT8) {
+        float top = chunk_top(y);
+        if (wide) {
+          top = __uint_as_float(c < a.code_cols ? tops[c >> log_block] : 0u);
+        } else {
+          for (int o = 1; o < a.block / CHUNK; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+        }
+        const float s = top * (1.f / 127.f);
+        if (c < a.code_cols && (c & (a.block - 1)) == 0)
+          ((float*)a.scales)[row * a.blocks + (c >> log_block)] = s;
+#pragma unroll
+        for (int j = 0; j < CHUNK; ++j) {
+          const float q = fminf(fmaxf(rintf(y[j] / s), -127.f), 127.f);
+          word[j / 4] |= (s != 0.f ? (uint32_t)(int)q & 0xFFu : 0u) << (8 * (j % 4));
+        }
+      } else {
+        float q[CHUNK];
+        if (a.kind == QUANT_MX) {
+          float top = chunk_top(y);
+          top = fmaxf(top, __shfl_xor(top, 1));
+          top = fmaxf(top, __shfl_xor(top, 2));
+          // The exponent of the scale that would put the maximum on the
+          // format's; dividing by a power of two is exact.
+          const float raw = top > 0.f ? top * (a.format == 0 ? 1.f / 448.f : 1.f / 57344.f) : 1.f;
+          const uint32_t e = (__float_as_uint(raw) >> 23) & 0xFFu;
+          if (c < a.cols && c % 32 == 0)
+            ((uint8_t*)a.scales)[row * a.blocks + c / 32] = (uint8_t)e;
+          // e = 255 (an infinite maximum) is a NaN; e = 254 cannot be.
+          const float back = __uint_as_float(e == 255u ? 0x7FC00000u : (254u - e) << 23);
+#pragma unroll
+          for (int j = 0; j < CHUNK; ++j) q[j] = y[j] * back;
+        } else {
+          const float s = *(const float*)a.scales;
+#pragma unroll
+          for (int j = 0; j < CHUNK; ++j) q[j] = s != 0.f ? y[j] / s : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < CHUNK; j += 2)
+          word[j / 4] |= fp8_pair(q[j], q[j + 1], a.format) << (8 * (j % 4));
+      }
+      uint8_t* to = a.codes + row * a.code_cols + c;
+      if (c + CHUNK <= a.code_cols) {
+        __builtin_memcpy(to, word, CHUNK);
+      } else {
+#pragma unroll
+        for (int j = 0; j < CHUNK; ++j)
+          if (c + j < a.code_cols) to[j] = (uint8_t)(word[j / 4] >> (8 * (j % 4)));
+      }
+    });
+  }
+}
+
+template <int DT, int RT, int NP>
+hipError_t launch(const NormArgs& a) {
+  constexpr int ROWS = RT < 256 ? 256 / RT : 1, THREADS = RT < 256 ? 256 : RT;
+  // A workgroup a row, fewer and a loop where that would pass a launch's size.
+  const int64_t groups = std::min<int64_t>((a.rows + ROWS - 1) / ROWS, 1 << 20);
+  rms_norm_kernel<DT, RT, NP><<<dim3((uint32_t)groups), THREADS, 0, a.stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_size(const NormArgs& a) {
+  const int chunks = ((a.kind == QUANT_INT8 ? a.code_cols : a.cols) + CHUNK - 1) / CHUNK;
+  if (chunks <= 64) return launch<DT, 64, 1>(a);
+  if (chunks <= 256) return launch<DT, 256, 1>(a);
+  if (chunks <= 512) return launch<DT, 256, 2>(a);
+  if (chunks <= 1024) return launch<DT, 512, 2>(a);
+  if (chunks <= 2048) return launch<DT, 1024, 2>(a);
+  if (chunks <= 4096) return launch<DT, 1024, 4>(a);
+  return launch<DT, 1024, 0>(a);
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs& a) {
+  switch (a.dtype) {
+    case DT_F32: return launch_size<DT_F32>(a);
+    case DT_F16: return launch_size<DT_F16>(a);
+    default: return launch_size<DT_BF16>(a);
+  }
+}
+
+}  // namespace qmm

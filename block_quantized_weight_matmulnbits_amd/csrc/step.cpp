@@ -49,6 +49,14 @@ int add_call(qmm_step* step, std::function<int(void*)> call) {
   return QMM_OK;
 }
 
+// A struct that a caller may leave out, kept with the recorded call.
+template <typename T> struct Copied {
+  bool given = false;
+  T value{};
+  const T* get() const { return given ? &value : nullptr; }
+};
+template <typename T> Copied<T> copied(const T* p) { return p ? Copied<T>{true, *p} : Copied<T>{}; }
+
 }  // namespace
 
 extern "C" {
@@ -134,6 +142,29 @@ int qmm_step_add_pages_reserve(qmm_step* step, const qmm_page_pool* pool, const 
   const qmm_page_pool p = *pool;
   return add_call(step, [=](void* s) {
     return qmm_pages_reserve(&p, seqs, grow, count, status, workspace, workspace_bytes, s);
+  });
+}
+
+int qmm_step_add_rms_norm(qmm_step* step, const qmm_rows* x, const qmm_rows* residual,
+                          const qmm_rows* h, const void* weight, int weight_dtype, float offset,
+                          double eps, const qmm_rows* y, const qmm_quant* quant, int dtype,
+                          int64_t rows, int64_t cols) {
+  const auto rx = copied(x), rr = copied(residual), rh = copied(h), ry = copied(y);
+  const auto q = copied(quant);
+  return add_call(step, [=](void* s) {
+    return qmm_rms_norm(rx.get(), rr.get(), rh.get(), weight, weight_dtype, offset, eps, ry.get(),
+                        q.get(), dtype, rows, cols, s);
+  });
+}
+
+int qmm_step_add_gemm_compint8_quantized(qmm_step* step, const int8_t* qa, const float* sa,
+                                         const uint8_t* B, int b_layout, const void* scales,
+                                         int s_dtype, const uint8_t* zero_points, const void* bias,
+                                         void* Y, int y_dtype, int64_t M, int64_t K, int64_t N,
+                                         int block_size, int bits) {
+  return add_call(step, [=](void* s) {
+    return qmm_gemm_compint8_quantized(qa, sa, B, b_layout, scales, s_dtype, zero_points, bias, Y,
+                                       y_dtype, M, K, N, block_size, bits, s);
   });
 }
 

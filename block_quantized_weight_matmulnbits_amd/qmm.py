@@ -73,6 +73,12 @@ _SIGS = {
     "qmm_step_add_paged_attention": ([_vp, _vp, _vp, _vp, _vp, _vp, _f32, _i32, _i64, _f32, _vp, _sz],
                                      _i32),
     "qmm_step_add_pages_reserve": ([_vp, _vp, _vp, _vp, _i64, _vp, _vp, _sz], _i32),
+    "qmm_rms_norm": ([_vp, _vp, _vp, _vp, _i32, _f32, _f64, _vp, _vp, _i32, _i64, _i64, _vp], _i32),
+    "qmm_gemm_compint8_quantized": ([_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _i64, _i64, _i64,
+                                     _i32, _i32, _vp], _i32),
+    "qmm_step_add_rms_norm": ([_vp] * 5 + [_i32, _f32, _f64, _vp, _vp, _i32, _i64, _i64], _i32),
+    "qmm_step_add_gemm_compint8_quantized": ([_vp] * 4 + [_i32, _vp, _i32, _vp, _vp, _vp, _i32, _i64, _i64,
+                                                          _i64, _i32, _i32], _i32),
     "qmm_step_finalize": ([_vp], _i32),
     "qmm_step_launch": ([_vp, _vp], _i32),
     "qmm_step_size": ([_vp], _i32),
@@ -301,7 +307,8 @@ def qmm_gemm_fp4(A, W, scales, fmt, global_scale, bias, Y, M, K, N, stream=None)
 class Step:
     """A recorded sequence of calls replayed as one HIP graph (qmm_step_* in
     include/qmm.h).  add_gemv / add_gemm / add_gemm_compint8 /
-    add_rope_append / add_paged_attention / add_pages_reserve take the arguments of the functions of the same name (without a stream);
+    add_rope_append / add_paged_attention / add_pages_reserve / add_rms_norm /
+    add_gemm_compint8_quantized take the arguments of the functions of the same name (without a stream);
     finalize() validates and captures; launch(stream) replays.  The tensors
     passed are kept referenced for the step's life, since the graph holds
     their device addresses."""
@@ -357,6 +364,15 @@ class Step:
         n = _lists(pool, "seqs", seqs, "grow", grow, status, workspace)
         self._add(lib.qmm_step_add_pages_reserve, (pool, seqs, grow, status, workspace), pool._ref,
                   _ptr(seqs), _ptr(grow), n, _ptr(status), _ptr(workspace), workspace.nbytes)
+
+    def add_rms_norm(self, x, weight, residual=None, h=None, y=None, eps=1e-5, offset=0.0, codes=None,
+                     scales=None, fmt="int8", layout="block", block_size=0):
+        _, args = _norm_args(x, weight, residual, h, y, eps, offset, codes, scales, fmt, layout, block_size)
+        self._add(lib.qmm_step_add_rms_norm, (x, weight, residual, h, y, codes, scales), *args)
+
+    def add_gemm_compint8_quantized(self, qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size, bits):
+        _, args = _quantized_args(qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size, bits)
+        self._add(lib.qmm_step_add_gemm_compint8_quantized, (qa, sa, B, scales, zero_points, bias, Y), *args)
 
     def finalize(self):
         _check(lib.qmm_step_finalize(self._h))
@@ -684,3 +700,117 @@ def qmm_pages_compact(pool, refs_out, table_out, live, workspace, stream=None):
     _check(lib.qmm_pages_compact(pool._ref, refs_out.data_ptr(), table_out.data_ptr(),
                                  live.data_ptr(), workspace.data_ptr(), workspace.nbytes,
                                  _stream_at(pool.gpu, stream)))
+
+
+# struct qmm_rows, as bytes: data, stride; struct qmm_quant: kind, format,
+# block_size, codes, scales.
+_pack_rows = struct.Struct("@Pq").pack
+_pack_quant = struct.Struct("@iii4xPP").pack
+
+QMM_QUANT_INT8, QMM_QUANT_MX, QMM_QUANT_TENSOR = 0, 1, 2
+QUANT_LAYOUTS = {"block": QMM_QUANT_INT8, "mx": QMM_QUANT_MX, "tensor": QMM_QUANT_TENSOR}
+_BYTES = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
+
+
+def _apart(**tensors):
+    """The error for the first of ``tensors`` that is not on the first one's GPU."""
+    (first, x), *rest = tensors.items()
+    if x.get_device() < 0:
+        return ValueError(f"{first} must be on a GPU: the kernels read device memory")
+    name, t = next((n, t) for n, t in rest if t is not None and t.get_device() != x.get_device())
+    return ValueError(f"{name} is on {t.device}, {first} on {x.device}: pass tensors of one GPU")
+
+
+def _matrix(name, t, shape, dtype):
+    """The struct of rows of ``shape`` [rows, cols]."""
+    strides = t.stride()
+    if t.shape != shape or t.dtype is not dtype or (strides[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be {dtype} {list(shape)} with a dense last dimension, got {t.dtype} "
+                         f"{list(t.shape)} with strides {list(strides)}")
+    return _pack_rows(t.data_ptr(), strides[0])
+
+
+def _dense(name, t, shape, dtype):
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a dense {dtype} tensor of shape {list(shape)}, got {t.dtype} "
+                         f"{list(t.shape)}")
+    return t.data_ptr()
+
+
+def _quant_struct(codes, scales, rows, cols, fmt, layout, block_size):
+    if scales is None:
+        raise ValueError("codes are written with their scales: pass scales")
+    kind = QUANT_LAYOUTS[layout]
+    if kind == QMM_QUANT_INT8:
+        if fmt != "int8" or block_size < 1:
+            raise ValueError(f'layout "block" writes "int8" codes in blocks of block_size, got fmt={fmt!r} '
+                             f"block_size={block_size}")
+        kb = -(-cols // block_size)
+        return _pack_quant(kind, 0, block_size, _dense("codes", codes, (rows, kb * block_size), torch.int8),
+                           _dense("scales", scales, (rows, kb), torch.float32))
+    if fmt not in LOWP_FORMATS:
+        raise ValueError(f'fmt must be "e4m3" or "e5m2" with layout {layout!r}, got {fmt!r}')
+    if codes.dtype not in _BYTES:
+        raise ValueError(f"codes must be uint8 or an 8-bit float, got {codes.dtype}")
+    if kind == QMM_QUANT_MX:
+        if scales.dtype not in (torch.uint8, torch.float8_e8m0fnu):
+            raise ValueError(f"scales must be E8M0 bytes (uint8 or float8_e8m0fnu), got {scales.dtype}")
+        s = _dense("scales", scales, (rows, -(-cols // 32)), scales.dtype)
+    else:
+        s = _dense("scales", scales, (1,), torch.float32)
+    return _pack_quant(kind, LOWP_FORMATS[fmt], 0, _dense("codes", codes, (rows, cols), codes.dtype), s)
+
+
+def _norm_args(x, weight, residual, h, y, eps, offset, codes, scales, fmt, layout, block_size):
+    if x.dim() != 2 or x.dtype not in _TORCH_TO_QMM:
+        raise ValueError(f"x must be [rows, cols] of float32, float16 or bfloat16, got {x.dtype} "
+                         f"{list(x.shape)}")
+    shape, dtype, gpu = x.shape, x.dtype, x.get_device()
+    rows, cols = shape
+    quant = None if codes is None else _quant_struct(codes, scales, rows, cols, fmt, layout, block_size)
+    w = None
+    if weight is not None:
+        if weight.dtype not in _TORCH_TO_QMM:
+            raise ValueError(f"weight must be float32, float16 or bfloat16, got {weight.dtype}")
+        w = _dense("weight", weight, (cols,), weight.dtype)
+    for t in (weight, residual, h, y, codes, scales):
+        if t is not None and t.get_device() != gpu or gpu < 0:
+            raise _apart(x=x, weight=weight, residual=residual, h=h, y=y, codes=codes, scales=scales)
+    return gpu, (_matrix("x", x, shape, dtype),
+                 None if residual is None else _matrix("residual", residual, shape, dtype),
+                 None if h is None else _matrix("h", h, shape, dtype), w,
+                 0 if weight is None else _TORCH_TO_QMM[weight.dtype], offset, eps,
+                 None if y is None else _matrix("y", y, shape, dtype), quant, _TORCH_TO_QMM[dtype],
+                 rows, cols)
+
+
+def qmm_rms_norm(x, weight, residual=None, h=None, y=None, eps=1e-5, offset=0.0, codes=None, scales=None,
+                 fmt="int8", layout="block", block_size=0, stream=None):
+    """h = x + residual and y = h / rms(h) * (weight + offset) for x [rows, cols],
+    each where its tensor is given, and y in 8 bits: ``codes`` and ``scales`` with
+    layout "block" ("int8" codes [rows, kb * block_size], float32 scales [rows, kb],
+    for qmm_gemm_compint8_quantized), "mx" ("e4m3" / "e5m2" codes [rows, cols], E8M0
+    scales [rows, ceil(cols / 32)], for qmm_lowp_matmul) or "tensor" (FP8 codes by
+    the float32 scale [1] given)."""
+    gpu, args = _norm_args(x, weight, residual, h, y, eps, offset, codes, scales, fmt, layout, block_size)
+    _check(lib.qmm_rms_norm(*args, _stream_at(gpu, stream)))
+
+
+def _quantized_args(qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size, bits):
+    b, layout, s, sdt = _weights(B, scales, K, N, block_size, bits)
+    gpu = qa.get_device()
+    for t in (sa, B.buf if isinstance(B, Repacked) else B, scales, zero_points, bias, Y):
+        if t is not None and t.get_device() != gpu or gpu < 0:
+            raise _apart(qa=qa, sa=sa, B=B.buf if isinstance(B, Repacked) else B, scales=scales,
+                         zero_points=zero_points, bias=bias, Y=Y)
+    kb = -(-K // block_size)
+    return gpu, (_dense("qa", qa, (M, kb * block_size), torch.int8), _dense("sa", sa, (M, kb), torch.float32),
+                 b, layout, s, sdt, _ptr(zero_points), _ptr(bias), _ptr(Y), _dt(Y), M, K, N, block_size, bits)
+
+
+def qmm_gemm_compint8_quantized(qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size, bits,
+                                stream=None):
+    """qmm_gemm_compint8 on int8 activations ``qa`` [M, kb * block_size] and their
+    scales ``sa`` [M, kb] float32, as qmm_rms_norm writes them."""
+    gpu, args = _quantized_args(qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size, bits)
+    _check(lib.qmm_gemm_compint8_quantized(*args, _stream_at(gpu, stream)))

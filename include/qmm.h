@@ -455,6 +455,76 @@ int qmm_pages_compact(const qmm_page_pool *pool, int32_t *refs_out, int32_t *tab
                       int32_t *live, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Around a decode step's projections: the norm that feeds them, a layer of
+ * experts for a few tokens, and the choice of the next token.
+ *
+ * Rows [rows, cols] of a float dtype with a stride (in elements) of their own.
+ */
+typedef struct qmm_rows {
+    void *data;
+    int64_t stride;
+} qmm_rows;
+
+/* An output in 8 bits with scales, as the library's products read it. */
+typedef enum qmm_quant_kind {
+    /* int8 codes [rows, kb * block_size] and f32 scales [rows, kb], kb =
+     * ceil(cols / block_size), block_size a power of two from 16 to 2^20, as
+     * qmm_gemm_compint8_quantized reads them: scale = amax * (1 / 127), code =
+     * y / scale rounded half to even (0 where the scale is 0, and past cols). */
+    QMM_QUANT_INT8 = 0,
+    /* FP8 codes [rows, cols] and E8M0 scales [rows, ceil(cols / 32)], as
+     * qmm_lowp_matmul reads them with QMM_LOWP_MX: the scale is the exponent field
+     * of amax * (1 / max_finite) (of 1 where amax is 0), the codes as in
+     * qmm_lowp_quantize. */
+    QMM_QUANT_MX = 1,
+    /* FP8 codes [rows, cols] with one scale for all, which is given: scales[0],
+     * an f32 that is read (codes of y / scale; 0 where the scale is 0). */
+    QMM_QUANT_TENSOR = 2
+} qmm_quant_kind;
+
+typedef struct qmm_quant {
+    int kind;                    /* qmm_quant_kind */
+    int format;                  /* QMM_LOWP_E4M3 or QMM_LOWP_E5M2; INT8: not read */
+    int block_size;              /* INT8; else not read */
+    void *codes;
+    void *scales;
+} qmm_quant;
+
+/*
+ * Root-mean-square norm of x [rows, cols], with the residual's addition:
+ *   h = x + residual,   y = (h * i) * (weight + offset),
+ *   i = 1 / sqrt(sum(h^2) / cols + eps).
+ * h is formed in fp32, the sum and i in 64 bits; i is rounded to fp32 and each
+ * product to fp32.  The outputs h and y are rounded once to dtype; quant's codes
+ * are made of the unrounded fp32 y (reciprocals and products of scales in fp32,
+ * maxima skip nan), so that they and their scales are the definition's bit for
+ * bit.
+ *   residual   or NULL: h = x
+ *   h, y, quant  outputs, each or NULL (one at least is wanted); h and y may be
+ *              x's or residual's own rows (same address and stride)
+ *   weight     [cols] of weight_dtype, or NULL: ones; offset is added to it
+ *   cols       1 .. 2^20;  rows = 0 is a no-op
+ */
+int qmm_rms_norm(const qmm_rows *x, const qmm_rows *residual, const qmm_rows *h,
+                 const void *weight, int weight_dtype, float offset, double eps,
+                 const qmm_rows *y, const qmm_quant *quant, int dtype, int64_t rows,
+                 int64_t cols, void *stream);
+
+/*
+ * qmm_gemm_compint8 on activations that are quantized already: qa [M, kb *
+ * block_size] int8 (16-byte aligned) and sa [M, kb] float32, as QMM_QUANT_INT8
+ * writes them with the weight's block_size; y_dtype is the dtype of bias and Y.
+ * The other arguments, the kernels and the result are qmm_gemm_compint8's on the
+ * same codes and scales; no workspace, no group indices, and on the tiled layout
+ * block_size >= 32 for every M.
+ */
+int qmm_gemm_compint8_quantized(const int8_t *qa, const float *sa, const uint8_t *B,
+                                int b_layout, const void *scales, int s_dtype,
+                                const uint8_t *zero_points, const void *bias, void *Y,
+                                int y_dtype, int64_t M, int64_t K, int64_t N, int block_size,
+                                int bits, void *stream);
+
+/*
  * A step: a fixed sequence of calls (say the projections and the attention of
  * one decode step) recorded once and replayed as one HIP graph.  The pages find
  * the decode step's cost outside the kernels -- per-operator dispatch and
@@ -528,6 +598,18 @@ int qmm_step_add_paged_attention(qmm_step *step, const qmm_heads *q,
 int qmm_step_add_pages_reserve(qmm_step *step, const qmm_page_pool *pool,
                                const int32_t *seqs, const int32_t *grow, int64_t count,
                                int32_t *status, void *workspace, size_t workspace_bytes);
+
+/* So do those around the projections. */
+int qmm_step_add_rms_norm(qmm_step *step, const qmm_rows *x, const qmm_rows *residual,
+                          const qmm_rows *h, const void *weight, int weight_dtype, float offset,
+                          double eps, const qmm_rows *y, const qmm_quant *quant, int dtype,
+                          int64_t rows, int64_t cols);
+
+int qmm_step_add_gemm_compint8_quantized(qmm_step *step, const int8_t *qa, const float *sa,
+                                         const uint8_t *B, int b_layout, const void *scales,
+                                         int s_dtype, const uint8_t *zero_points,
+                                         const void *bias, void *Y, int y_dtype, int64_t M,
+                                         int64_t K, int64_t N, int block_size, int bits);
 
 int qmm_step_finalize(qmm_step *step);
 
