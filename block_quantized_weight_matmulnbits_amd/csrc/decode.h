@@ -30,4 +30,22 @@ struct NormArgs {
 constexpr int64_t NORM_MAX_COLS = 1 << 20;
 hipError_t launch_rms_norm(const NormArgs& a);
 
+struct SampleArgs {
+  const char* logits = nullptr;       // [rows, vocab]
+  int64_t stride = 0;                 // in elements
+  int64_t rows = 0;
+  int vocab = 0, dtype = 0;
+  const float* temperature = nullptr; // [rows] each, or null
+  const int32_t* top_k = nullptr;
+  const float* top_p = nullptr;
+  const float* min_p = nullptr;
+  const float* uniform = nullptr;     // [rows]
+  int32_t* tokens = nullptr;          // [rows]
+  float* logprobs = nullptr;          // [rows] or null
+  hipStream_t stream = nullptr;
+};
+constexpr int64_t SAMPLE_MAX_VOCAB = 1 << 22;
+size_t sample_workspace_bytes(int64_t rows, int64_t vocab);
+hipError_t launch_sample(const SampleArgs& a, char* workspace);
+
 }  // namespace qmm

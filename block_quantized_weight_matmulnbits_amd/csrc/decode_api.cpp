@@ -49,6 +49,18 @@ int check_rows(const char* fn, const char* name, const qmm_rows* r, int64_t rows
   return QMM_OK;
 }
 
+int check_workspace(const char* fn, const void* ws, size_t bytes, size_t need) {
+  if (ws == nullptr || bytes < need)
+    return fail(QMM_ERR_WORKSPACE, "%s: the workspace holds %zu bytes at %p, %zu are needed. How to "
+                "fix: pass %s_workspace_size bytes of device memory.", fn, bytes, ws, need, fn);
+  if (!aligned(ws, 256))
+    return fail(QMM_ERR_WORKSPACE, "%s: the workspace must be 256-byte aligned. How to fix: pass "
+                "the start of a fresh allocation.", fn);
+  return QMM_OK;
+}
+
+constexpr int64_t SAMPLE_MAX_ROWS = ((int64_t)1 << 21) - 1;
+
 }  // namespace
 
 extern "C" {
@@ -124,6 +136,56 @@ int qmm_rms_norm(const qmm_rows* x, const qmm_rows* residual, const qmm_rows* h,
   a.cols = (int)cols;
   a.stream = (hipStream_t)stream;
   return hip_status(qmm::launch_rms_norm(a), fn);
+}
+
+size_t qmm_sample_workspace_size(int64_t rows, int64_t vocab) {
+  if (rows < 0 || rows > SAMPLE_MAX_ROWS || vocab <= 0 || vocab > qmm::SAMPLE_MAX_VOCAB) return 0;
+  return qmm::sample_workspace_bytes(rows, vocab);
+}
+
+int qmm_sample(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride,
+               const float* temperature, const int32_t* top_k, const float* top_p,
+               const float* min_p, const float* uniform, int32_t* tokens, float* logprobs,
+               void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "qmm_sample";
+  const int es = dtype_size(dtype);
+  if (es == 0)
+    return fail(QMM_ERR_INVALID_ARG, "%s: dtype=%d is not a qmm_dtype. How to fix: pass QMM_F32, "
+                "QMM_F16 or QMM_BF16.", fn, dtype);
+  if (rows < 0 || vocab <= 0)
+    return fail(QMM_ERR_INVALID_ARG, "%s: rows must be >= 0 and vocab positive, got rows=%lld "
+                "vocab=%lld.", fn, (long long)rows, (long long)vocab);
+  if (rows > SAMPLE_MAX_ROWS || vocab > qmm::SAMPLE_MAX_VOCAB)
+    return fail(QMM_ERR_UNSUPPORTED, "%s: rows must be below 2^21 and vocab at most 2^22 (got "
+                "rows=%lld vocab=%lld). How to fix: split the rows.", fn, (long long)rows,
+                (long long)vocab);
+  if (rows == 0) return QMM_OK;
+  if (logits == nullptr || uniform == nullptr || tokens == nullptr)
+    return fail(QMM_ERR_INVALID_ARG, "%s: logits, uniform and tokens must be non-null device "
+                "pointers.", fn);
+  if (!aligned(logits, es) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
+      !aligned(min_p, 4) || !aligned(uniform, 4) || !aligned(tokens, 4) || !aligned(logprobs, 4))
+    return fail(QMM_ERR_INVALID_ARG, "%s: every array must be aligned to its element size.", fn);
+  if (row_stride < 0 || row_stride > MAX_STRIDE || (rows > 1 && row_stride < vocab))
+    return fail(QMM_ERR_INVALID_ARG, "%s: row_stride=%lld does not hold a row of %lld logits.", fn,
+                (long long)row_stride, (long long)vocab);
+  const int st = check_workspace(fn, workspace, workspace_bytes, qmm::sample_workspace_bytes(rows, vocab));
+  if (st != QMM_OK) return st;
+  qmm::SampleArgs a;
+  a.logits = (const char*)logits;
+  a.stride = row_stride;
+  a.rows = rows;
+  a.vocab = (int)vocab;
+  a.dtype = dtype;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.uniform = uniform;
+  a.tokens = tokens;
+  a.logprobs = logprobs;
+  a.stream = (hipStream_t)stream;
+  return hip_status(qmm::launch_sample(a, (char*)workspace), fn);
 }
 
 }  // extern "C"

@@ -168,6 +168,17 @@ int qmm_step_add_gemm_compint8_quantized(qmm_step* step, const int8_t* qa, const
   });
 }
 
+int qmm_step_add_sample(qmm_step* step, const void* logits, int dtype, int64_t rows, int64_t vocab,
+                        int64_t row_stride, const float* temperature, const int32_t* top_k,
+                        const float* top_p, const float* min_p, const float* uniform,
+                        int32_t* tokens, float* logprobs, void* workspace,
+                        size_t workspace_bytes) {
+  return add_call(step, [=](void* s) {
+    return qmm_sample(logits, dtype, rows, vocab, row_stride, temperature, top_k, top_p, min_p,
+                      uniform, tokens, logprobs, workspace, workspace_bytes, s);
+  });
+}
+
 int qmm_step_finalize(qmm_step* step) {
   if (step == nullptr) return qmm::set_error(QMM_ERR_INVALID_ARG, "qmm_step_finalize: step is NULL.");
   if (step->exec != nullptr) return QMM_OK;

@@ -79,6 +79,9 @@ _SIGS = {
     "qmm_step_add_rms_norm": ([_vp] * 5 + [_i32, _f32, _f64, _vp, _vp, _i32, _i64, _i64], _i32),
     "qmm_step_add_gemm_compint8_quantized": ([_vp] * 4 + [_i32, _vp, _i32, _vp, _vp, _vp, _i32, _i64, _i64,
                                                           _i64, _i32, _i32], _i32),
+    "qmm_sample_workspace_size": ([_i64, _i64], _sz),
+    "qmm_sample": ([_vp, _i32, _i64, _i64, _i64] + [_vp] * 8 + [_sz, _vp], _i32),
+    "qmm_step_add_sample": ([_vp, _vp, _i32, _i64, _i64, _i64] + [_vp] * 8 + [_sz], _i32),
     "qmm_step_finalize": ([_vp], _i32),
     "qmm_step_launch": ([_vp, _vp], _i32),
     "qmm_step_size": ([_vp], _i32),
@@ -308,7 +311,7 @@ class Step:
     """A recorded sequence of calls replayed as one HIP graph (qmm_step_* in
     include/qmm.h).  add_gemv / add_gemm / add_gemm_compint8 /
     add_rope_append / add_paged_attention / add_pages_reserve / add_rms_norm /
-    add_gemm_compint8_quantized take the arguments of the functions of the same name (without a stream);
+    add_gemm_compint8_quantized / add_sample take the arguments of the functions of the same name (without a stream);
     finalize() validates and captures; launch(stream) replays.  The tensors
     passed are kept referenced for the step's life, since the graph holds
     their device addresses."""
@@ -373,6 +376,12 @@ class Step:
     def add_gemm_compint8_quantized(self, qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size, bits):
         _, args = _quantized_args(qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size, bits)
         self._add(lib.qmm_step_add_gemm_compint8_quantized, (qa, sa, B, scales, zero_points, bias, Y), *args)
+
+    def add_sample(self, logits, uniform, tokens, workspace, temperature=None, top_k=None, top_p=None,
+                   min_p=None, logprobs=None):
+        _, args = _sample_args(logits, uniform, tokens, workspace, temperature, top_k, top_p, min_p, logprobs)
+        self._add(lib.qmm_step_add_sample, (logits, uniform, tokens, workspace, temperature, top_k, top_p,
+                                            min_p, logprobs), *args)
 
     def finalize(self):
         _check(lib.qmm_step_finalize(self._h))
@@ -814,3 +823,37 @@ def qmm_gemm_compint8_quantized(qa, sa, B, scales, zero_points, bias, Y, M, K, N
     scales ``sa`` [M, kb] float32, as qmm_rms_norm writes them."""
     gpu, args = _quantized_args(qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size, bits)
     _check(lib.qmm_gemm_compint8_quantized(*args, _stream_at(gpu, stream)))
+
+
+def qmm_sample_workspace_size(rows, vocab) -> int:
+    """Bytes of the workspace; calls on one stream may share it."""
+    return int(lib.qmm_sample_workspace_size(rows, vocab))
+
+
+def _sample_args(logits, uniform, tokens, workspace, temperature, top_k, top_p, min_p, logprobs):
+    if logits.dim() != 2 or logits.dtype not in _TORCH_TO_QMM or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError(f"logits must be [rows, vocab] of float32, float16 or bfloat16 with dense rows, got "
+                         f"{logits.dtype} {list(logits.shape)}")
+    rows, vocab = logits.shape
+    shape, gpu, f32 = (rows,), logits.get_device(), torch.float32
+    given = [None if t is None else _dense(name, t, shape, dtype) for name, t, dtype in (
+        ("temperature", temperature, f32), ("top_k", top_k, _INT32), ("top_p", top_p, f32),
+        ("min_p", min_p, f32), ("uniform", uniform, f32), ("tokens", tokens, _INT32),
+        ("logprobs", logprobs, f32))]
+    for t in (uniform, tokens, workspace, temperature, top_k, top_p, min_p, logprobs):
+        if t is not None and t.get_device() != gpu or gpu < 0:
+            raise _apart(logits=logits, uniform=uniform, tokens=tokens, workspace=workspace,
+                         temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, logprobs=logprobs)
+    return gpu, (logits.data_ptr(), _TORCH_TO_QMM[logits.dtype], rows, vocab, logits.stride(0), *given,
+                 workspace.data_ptr(), workspace.nbytes)
+
+
+def qmm_sample(logits, uniform, tokens, workspace, temperature=None, top_k=None, top_p=None, min_p=None,
+               logprobs=None, stream=None):
+    """The next token of each row of logits [rows, vocab] into ``tokens`` [rows]
+    int32 (-1 where a row leaves nothing), by ``uniform`` [rows] in [0, 1);
+    ``temperature``, ``top_p``, ``min_p`` [rows] float32 and ``top_k`` [rows]
+    int32, each or None; ``logprobs`` [rows] float32 takes the log of the token's
+    share of what the filters leave."""
+    gpu, args = _sample_args(logits, uniform, tokens, workspace, temperature, top_k, top_p, min_p, logprobs)
+    _check(lib.qmm_sample(*args, _stream_at(gpu, stream)))

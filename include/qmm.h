@@ -525,6 +525,40 @@ int qmm_gemm_compint8_quantized(const int8_t *qa, const float *sa, const uint8_t
                                 int bits, void *stream);
 
 /*
+ * The next token of each row of logits [rows, vocab] (dtype; rows row_stride
+ * elements apart), from a given number uniform[row] in [0, 1).  With
+ *   w_i = exp((l_i - max l) / temperature)
+ * and the tokens in the order of their logits (the largest first, ties: the
+ * lowest index), the ones that stay are
+ *   the first top_k; of those the shortest beginning whose sum of w reaches
+ *   top_p times the sum over the first top_k; of those the ones with w >= min_p,
+ * and the token is the lowest index at which the running sum of w over the
+ * staying tokens, in the order of their indices, passes uniform times their
+ * sum.  w is formed in 64 bits and added as whole multiples of 2^-(62 -
+ * ceil(log2 vocab)), so that the choice does not depend on the order of sums.
+ *   temperature, top_k, top_p, min_p   [rows] device arrays, each or NULL (1, 0,
+ *            1, 0).  A temperature that is not above 0 takes the largest logit.
+ *            top_k <= 0 or >= vocab, top_p >= 1 (or nan) and min_p <= 0 (or nan)
+ *            filter nothing; the first token always stays (min_p counts as 1
+ *            where it is larger, top_p as 0 where it is less).
+ *   tokens   [rows] int32;  logprobs [rows] float32 or NULL: the log of the
+ *            token's share of the staying tokens' sum
+ *   workspace  qmm_sample_workspace_size bytes, 256-byte aligned; calls on one
+ *            stream may share it
+ * A logit that is nan or minus infinity has w = 0 and is never chosen; where a
+ * row has no other, its token is -1 and its logprob minus infinity.  Where the
+ * largest is plus infinity, the tokens that have it share everything equally.
+ * vocab 1 .. 2^22, rows < 2^21 (rows = 0 is a no-op).
+ */
+size_t qmm_sample_workspace_size(int64_t rows, int64_t vocab);
+
+int qmm_sample(const void *logits, int dtype, int64_t rows, int64_t vocab,
+               int64_t row_stride, const float *temperature, const int32_t *top_k,
+               const float *top_p, const float *min_p, const float *uniform,
+               int32_t *tokens, float *logprobs, void *workspace,
+               size_t workspace_bytes, void *stream);
+
+/*
  * A step: a fixed sequence of calls (say the projections and the attention of
  * one decode step) recorded once and replayed as one HIP graph.  The pages find
  * the decode step's cost outside the kernels -- per-operator dispatch and
@@ -610,6 +644,12 @@ int qmm_step_add_gemm_compint8_quantized(qmm_step *step, const int8_t *qa, const
                                          int s_dtype, const uint8_t *zero_points,
                                          const void *bias, void *Y, int y_dtype, int64_t M,
                                          int64_t K, int64_t N, int block_size, int bits);
+
+int qmm_step_add_sample(qmm_step *step, const void *logits, int dtype, int64_t rows,
+                        int64_t vocab, int64_t row_stride, const float *temperature,
+                        const int32_t *top_k, const float *top_p, const float *min_p,
+                        const float *uniform, int32_t *tokens, float *logprobs,
+                        void *workspace, size_t workspace_bytes);
 
 int qmm_step_finalize(qmm_step *step);
 

@@ -45,3 +45,41 @@ def mx_of(y, fmt):
     e = torch.where(top > 0, top * torch.tensor(1.0 / FP8[fmt][1]), 1.0).view(torch.int32) >> 23
     s = torch.where(e == 255, float("nan"), torch.ldexp(torch.ones(e.shape, dtype=torch.float64), e - 127)).float()
     return fp8_of((p / s).view(rows, -1)[:, :cols], fmt), e[..., 0].to(torch.uint8)
+
+
+# -- sampling ----------------------------------------------------------------
+
+def sample_row(z, t, k, p, m, u):
+    """(token, logprob) of one row of 64-bit logits, by the definition."""
+    z = np.where(np.isnan(z), -np.inf, z)
+    n = len(z)
+    order = np.lexsort((np.arange(n), -z))
+    top = z[order[0]]
+    if top == -np.inf:
+        return -1, -np.inf
+    if not t > 0:
+        t, k = 1.0, 1
+    with np.errstate(invalid="ignore"):
+        w = np.where(z == top, 1.0, 0.0 if np.isinf(top) else np.exp((z - top) / t))
+    if k <= 0 or k > n:
+        k = n
+    best = order[:k]
+    if p < 1:
+        cum = np.cumsum(w[best])
+        best = best[:1 + np.searchsorted(cum, max(p, 0.0) * cum[-1], side="left")]
+    best = best[w[best] >= min(m, 1.0)] if m > 0 else best
+    at = np.sort(best)
+    cum = np.cumsum(w[at])
+    j = np.searchsorted(cum, u * cum[-1], side="right")
+    return int(at[j]), float(np.log(w[at[j]]) - np.log(cum[-1]))
+
+
+def sample_allowed(z, t, k, p, m, u, vocab):
+    """Every (token, logprob) that sums held to the definition's whole units may
+    lead to: a unit is 2^-(62 - ceil(log2 vocab)), each weight is off by half of
+    one, and the sums of 64 bits here by less than that; so next to a border of u
+    or top_p both sides are right."""
+    d = vocab * 2.0 ** -(62 - max(0, math.ceil(math.log2(vocab))))
+    us = {min(max(u + e, 0.0), 1 - 2.0 ** -53) for e in (-d, 0.0, d)}
+    ps = {p} if not p < 1 else {max(p - d, 0.0), p, min(p + d, 1 - 2.0 ** -53)}
+    return [sample_row(z, t, k, a, m, b) for a in ps for b in us]

@@ -1,0 +1,255 @@
+"""qmm_sample against the definition in 64 bits: the token itself, and the log of
+its share within 32 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import decode_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def qmm():
+    from block_quantized_weight_matmulnbits_amd import qmm as q
+    return q
+
+
+def draw(rows, vocab, dtype, seed=0, spread=3.0, peaks=4):
+    g = torch.Generator().manual_seed(seed)
+    z = torch.randn(rows, vocab, generator=g) * spread
+    if peaks:
+        at = torch.randint(0, vocab, (rows, peaks), generator=g)
+        z.scatter_(1, at, z.amax(1, keepdim=True) + 2 * torch.randn(rows, peaks, generator=g))
+    return z.to(dtype), torch.rand(rows, generator=g)
+
+
+def sample(qmm, z, u, temperature=None, top_k=None, top_p=None, min_p=None):
+    """tokens, logprobs; settings are numbers, lists or None."""
+    rows, vocab = z.shape
+    d = z if z.is_cuda else z.to(DEV)
+
+    def put(v, dtype):
+        return None if v is None else torch.as_tensor(v, dtype=dtype).expand(rows).contiguous().to(DEV)
+
+    tokens = torch.full((rows,), -7, dtype=torch.int32, device=DEV)
+    logprobs = torch.full((rows,), 7.0, device=DEV)
+    ws = torch.full((qmm.qmm_sample_workspace_size(rows, vocab),), 0xA5, dtype=torch.uint8, device=DEV)
+    qmm.qmm_sample(d, u.to(DEV), tokens, ws, put(temperature, torch.float32), put(top_k, torch.int32),
+                   put(top_p, torch.float32), put(min_p, torch.float32), logprobs)
+    return tokens.cpu(), logprobs.cpu()
+
+
+def check(qmm, z, u, temperature=None, top_k=None, top_p=None, min_p=None):
+    rows, vocab = z.shape
+    tokens, logprobs = sample(qmm, z, u, temperature, top_k, top_p, min_p)
+
+    def setting(v, otherwise, dtype):
+        v = torch.as_tensor(otherwise if v is None else v, dtype=dtype).expand(rows)
+        return v.double().numpy()
+
+    t, k, p, m = (setting(*v) for v in ((temperature, 1.0, torch.float32), (top_k, 0, torch.int32),
+                                        (top_p, 1.0, torch.float32), (min_p, 0.0, torch.float32)))
+    z64, u64 = z.double().cpu().numpy(), u.double().numpy()
+    for i in range(rows):
+        allowed = ref.sample_allowed(z64[i], t[i], int(k[i]), p[i], m[i], u64[i], vocab)
+        match = [lp for token, lp in allowed if token == int(tokens[i])]
+        assert match, f"row {i}: {int(tokens[i])}, not one of {sorted({a for a, _ in allowed})}"
+        # The sum is off by half a unit a weight (d in all), the weight by one; then
+        # a rounding to 32 bits; (l - top) / T and its exp by a few bits of 64.
+        d = vocab * 2.0 ** -(62 - math.ceil(math.log2(vocab)))
+        got = float(logprobs[i])
+        assert any(got == lp or abs(got - lp) <= 2.0 ** -24 * abs(lp) + 2 * d + 2.0 ** -44 for lp in match)
+    return tokens
+
+
+SETTINGS = [dict(), dict(temperature=0.7), dict(top_k=1), dict(top_k=40), dict(top_p=0.9), dict(min_p=0.05),
+            dict(temperature=0.0), dict(temperature=1.4, top_k=50, top_p=0.8, min_p=0.02),
+            dict(top_k=300, top_p=0.5), dict(temperature=0.3, top_p=0.95, min_p=0.1), dict(top_k=3, min_p=0.3)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("kw", SETTINGS, ids=str)
+@pytest.mark.parametrize("rows,vocab", [(1, 1), (3, 2), (2, 63), (5, 64), (4, 65), (3, 1000), (9, 4097), (2, 32000),
+                                        (1, 50021), (2, 131072)])
+def test_settings_and_sizes(qmm, rows, vocab, kw, dtype):
+    z, u = draw(rows, vocab, TYPES[dtype], seed=vocab + rows)
+    check(qmm, z, u, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kw", [dict(temperature=1.5), dict(top_p=0.7), dict(top_k=2000), dict(top_k=5000, top_p=0.9),
+                                dict(top_p=0.99, min_p=0.01)], ids=str)
+def test_flat_distributions(qmm, kw, dtype):
+    z, u = draw(6, 20011, TYPES[dtype], seed=3, spread=0.5, peaks=0)
+    check(qmm, z, u, **kw)
+
+
+def test_settings_by_row(qmm):
+    g = np.random.default_rng(5)
+    rows = 200
+    z, u = draw(rows, 8000, torch.bfloat16, seed=9)
+    check(qmm, z, u, temperature=g.choice([0.0, -1.0, 0.5, 1.0, 2.0], rows), top_k=g.choice([-3, 0, 1, 7, 100, 8000, 9999], rows),
+          top_p=g.choice([0.0, 0.3, 0.9, 1.0, 1.5], rows), min_p=g.choice([0.0, 0.05, 0.5, 1.0, 2.0], rows))
+
+
+def test_ties_go_to_the_lowest_index(qmm):
+    z = torch.zeros(4, 9000)
+    z[1, ::3] = 1.0
+    z[2, 100:5000] = 2.0
+    z[3, -5:] = 4.0
+    for dtype in TYPES.values():
+        for u in (0.0, 0.3, 0.999999):
+            for kw in (dict(top_k=1), dict(top_k=7), dict(top_k=3500), dict(top_p=0.1), dict(top_k=4, top_p=0.5),
+                       dict(temperature=0.0), dict(min_p=1.0), dict()):
+                check(qmm, z.to(dtype), torch.full((4,), u), **kw)
+    # Equal weights are exact: k tokens, u = j / k falls on the j-th.
+    tokens = [int(sample(qmm, z[:1], torch.tensor([j / 8]), top_k=8)[0]) for j in range(8)]
+    assert tokens == list(range(8))
+
+
+def test_many_equal_logits_in_one_place(qmm):
+    z = torch.full((2, 131072), -4.0)
+    z[:, 50000:70000] = 1.0
+    z[1, 7] = 1.25
+    for kw in (dict(top_k=15000), dict(top_p=0.6), dict(top_k=10000, top_p=0.9), dict(top_k=30000, top_p=0.999)):
+        for u in (0.0, 0.5, 0.99):
+            check(qmm, z.bfloat16(), torch.tensor([u, u]), **kw)
+            check(qmm, z, torch.tensor([u, u]), **kw)
+
+
+def test_masked_logits(qmm):
+    z, u = draw(8, 3000, torch.float32, seed=2)
+    z[0, :] = -math.inf                  # nothing is left
+    z[1, 1:] = -math.inf                 # one token
+    z[2, ::2] = -math.inf
+    z[3, ::2] = math.nan
+    z[4, 17] = math.inf                  # certain
+    z[5, [3, 900, 2999]] = math.inf      # three share
+    z[6, :] = math.nan
+    z[7, :] = torch.finfo(torch.float32).min
+    z[7, 5] = 0.0
+    for kw in SETTINGS:
+        tokens = check(qmm, z, u, **kw)
+        assert int(tokens[0]) == -1 and int(tokens[6]) == -1 and int(tokens[1]) == 0 and int(tokens[4]) == 17
+        assert int(tokens[2]) % 2 == 1 and int(tokens[3]) % 2 == 1 and int(tokens[5]) in (3, 900, 2999)
+        assert int(tokens[7]) == 5
+    low = torch.full((2, 700), torch.finfo(torch.bfloat16).min, dtype=torch.bfloat16)
+    check(qmm, low, torch.tensor([0.0, 0.99]), top_k=5)
+
+
+def test_numbers_at_the_ends(qmm):
+    z, _ = draw(6, 5000, torch.float32, seed=4)
+    u = torch.tensor([0.0, 2.0 ** -149, 1 - 2.0 ** -24, 0.5, 1.0, -1.0])
+    tokens, _ = sample(qmm, z, u, top_k=20)
+    clipped = u.clamp(0, 1 - 2.0 ** -24)
+    want = [ref.sample_row(z[i].double().numpy(), 1.0, 20, 1.0, 0.0, float(clipped[i].double()))[0] for i in range(6)]
+    assert tokens.tolist() == want
+
+
+def test_extreme_temperatures(qmm):
+    z, u = draw(5, 2000, torch.float32, seed=6)
+    for t in (1e-6, 1e-30, 1e6, 3e38, math.inf):
+        check(qmm, z, u, temperature=t)
+        check(qmm, z, u, temperature=t, top_p=0.5)
+    check(qmm, z * 1e36, u, temperature=1e36, top_k=10)
+
+
+def test_the_shares_are_the_distributions(qmm):
+    """Numbers spread evenly over [0, 1) choose each token as often as its share."""
+    z = torch.tensor([[1.0, 3.0, 2.0, 0.0, 2.5]])
+    n = 4096
+    u = (torch.arange(n) + 0.5) / n
+    tokens, _ = sample(qmm, z.expand(n, 5).contiguous(), u, temperature=0.9, top_k=4)
+    w = torch.exp(z[0].double() / 0.9)
+    w[3] = 0
+    share = torch.bincount(tokens.long(), minlength=5).double() / n
+    assert ((share - w / w.sum()).abs() <= 1.0 / n).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_strided_and_unaligned_rows(qmm, dtype):
+    z, u = draw(7, 1501, TYPES[dtype], seed=8)
+    big = torch.full((7, 1600), 50.0, dtype=TYPES[dtype], device=DEV)
+    v = big[:, 37:37 + 1501]
+    v.copy_(z)
+    for kw in (dict(top_k=30, top_p=0.9), dict()):
+        assert torch.equal(check(qmm, v, u, **kw), sample(qmm, z, u, **kw)[0])
+
+
+def test_many_rows(qmm):
+    z, u = draw(3000, 517, torch.float16, seed=10)
+    check(qmm, z, u, temperature=0.8, top_k=20, top_p=0.9)
+
+
+def test_rows_past_32_bits_of_offsets(qmm):
+    rows, vocab, stride = 3, 5000, 1 << 30
+    big = torch.empty(2 * stride + vocab, dtype=torch.float32, device=DEV)
+    v = big.as_strided((rows, vocab), (stride, 1))
+    z, u = draw(rows, vocab, torch.float32, seed=12)
+    v.copy_(z)
+    check(qmm, v, u, top_p=0.9)
+
+
+def test_the_workspace_may_hold_anything_and_serve_again(qmm):
+    a, ua = draw(4, 40000, torch.bfloat16, seed=13)
+    b, ub = draw(64, 900, torch.float32, seed=14)
+    n = max(qmm.qmm_sample_workspace_size(4, 40000), qmm.qmm_sample_workspace_size(64, 900))
+    ws = torch.randint(0, 256, (n,), dtype=torch.uint8, device=DEV)
+    da, db = a.to(DEV), b.to(DEV)
+    ka, kb = (torch.full((r,), 50, dtype=torch.int32, device=DEV) for r in (4, 64))
+    for _ in range(3):
+        ta, tb = (torch.empty(r, dtype=torch.int32, device=DEV) for r in (4, 64))
+        qmm.qmm_sample(da, ua.to(DEV), ta, ws, top_k=ka)
+        qmm.qmm_sample(db, ub.to(DEV), tb, ws, top_k=kb)
+        assert torch.equal(ta.cpu(), sample(qmm, a, ua, top_k=50)[0])
+        assert torch.equal(tb.cpu(), sample(qmm, b, ub, top_k=50)[0])
+
+
+def test_recorded_in_a_step(qmm):
+    z, u = draw(5, 30000, torch.bfloat16, seed=15)
+    d, ud = z.to(DEV), u.to(DEV)
+    tokens = torch.empty(5, dtype=torch.int32, device=DEV)
+    ws = torch.zeros(qmm.qmm_sample_workspace_size(5, 30000), dtype=torch.uint8, device=DEV)
+    k = torch.full((5,), 60, dtype=torch.int32, device=DEV)
+    p = torch.full((5,), 0.9, device=DEV)
+    step = qmm.Step()
+    step.add_sample(d, ud, tokens, ws, top_k=k, top_p=p)
+    step.finalize()
+    for seed in range(4):
+        z, u = draw(5, 30000, torch.bfloat16, seed=20 + seed)
+        d.copy_(z)
+        ud.copy_(u)
+        step.launch()
+        torch.cuda.synchronize()
+        assert torch.equal(tokens.cpu(), sample(qmm, z, u, top_k=60, top_p=0.9)[0])
+    step.close()
+
+
+def test_two_streams_at_once(qmm):
+    z, u = draw(16, 60000, torch.bfloat16, seed=30)
+    want = sample(qmm, z, u, top_k=100, top_p=0.95)[0]
+    d, ud = z.to(DEV), u.to(DEV)
+    k, p = torch.full((16,), 100, dtype=torch.int32, device=DEV), torch.full((16,), 0.95, device=DEV)
+    torch.cuda.synchronize()
+    out = []
+    for s in (torch.cuda.Stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(s):
+            ws = torch.empty(qmm.qmm_sample_workspace_size(16, 60000), dtype=torch.uint8, device=DEV)
+            for _ in range(4):
+                t = torch.empty(16, dtype=torch.int32, device=DEV)
+                qmm.qmm_sample(d, ud, t, ws, top_k=k, top_p=p)
+                out.append(t)
+    torch.cuda.synchronize()
+    assert all(torch.equal(t.cpu(), want) for t in out)
+
+
+def test_no_rows(qmm):
+    z = torch.empty(0, 50, device=DEV)
+    qmm.qmm_sample(z, torch.empty(0, device=DEV), torch.empty(0, dtype=torch.int32, device=DEV),
+                   torch.empty(256, dtype=torch.uint8, device=DEV))
