@@ -30,6 +30,31 @@ struct NormArgs {
 constexpr int64_t NORM_MAX_COLS = 1 << 20;
 hipError_t launch_rms_norm(const NormArgs& a);
 
+// One projection of every expert: [experts, rows] rows of `cols` codes.
+struct MoeProj {
+  const uint8_t* codes = nullptr;
+  const char* scales = nullptr;
+  const uint8_t* zp = nullptr;        // or null
+  int rows = 0, cols = 0, blocks = 0; // blocks of a row
+  int64_t row_bytes = 0, zp_row_bytes = 0;
+};
+struct MoeArgs {
+  const char* x = nullptr;            // [tokens, hidden], strides in elements
+  char* y = nullptr;
+  int64_t x_stride = 0, y_stride = 0;
+  MoeProj up, down;                   // up: gate rows, then up rows
+  const char* logits = nullptr;       // [tokens, experts], or null and
+  const int32_t* ids = nullptr;       // [tokens, top_k]
+  const float* weights = nullptr;
+  int64_t logits_stride = 0;
+  int tokens = 0, hidden = 0, inter = 0, experts = 0, top_k = 0, normalize = 0;
+  int dtype = 0, s_dtype = 0, logits_dtype = 0, bits = 0, block = 0;
+  hipStream_t stream = nullptr;
+};
+constexpr int MOE_MAX_TOKENS = 256, MOE_MAX_EXPERTS = 1024, MOE_MAX_TOP_K = 32;
+size_t moe_workspace_bytes(int tokens, int hidden, int inter, int experts, int top_k);
+hipError_t launch_moe(const MoeArgs& a, char* workspace);
+
 struct SampleArgs {
   const char* logits = nullptr;       // [rows, vocab]
   int64_t stride = 0;                 // in elements

@@ -59,6 +59,32 @@ int check_workspace(const char* fn, const void* ws, size_t bytes, size_t need) {
   return QMM_OK;
 }
 
+int check_moe_sizes(const char* fn, const qmm_moe_weights* w) {
+  if (w->bits != 4 && w->bits != 8)
+    return fail(w->bits == 2 || w->bits == 3 ? QMM_ERR_UNSUPPORTED : QMM_ERR_INVALID_ARG,
+                "%s: experts' weights have 4 or 8 bits, got bits=%d. How to fix: export them with "
+                "bits=4 or 8.", fn, w->bits);
+  if (w->block_size < 16 || (w->block_size & (w->block_size - 1)) || w->block_size > 1 << 20)
+    return fail(QMM_ERR_INVALID_ARG, "%s: block_size must be a power of two from 16 to 2^20, got %d.",
+                fn, w->block_size);
+  if (dtype_size(w->s_dtype) == 0)
+    return fail(QMM_ERR_INVALID_ARG, "%s: s_dtype=%d is not a qmm_dtype.", fn, w->s_dtype);
+  if (w->hidden <= 0 || w->inter <= 0 || w->experts <= 0)
+    return fail(QMM_ERR_INVALID_ARG, "%s: hidden, inter and experts must be positive, got %lld, %lld, "
+                "%d.", fn, (long long)w->hidden, (long long)w->inter, w->experts);
+  if (w->experts > qmm::MOE_MAX_EXPERTS || w->hidden > 1 << 18 || w->inter > 1 << 18)
+    return fail(QMM_ERR_UNSUPPORTED, "%s: at most %d experts, hidden and inter at most 2^18 (got %d, "
+                "%lld, %lld).", fn, qmm::MOE_MAX_EXPERTS, w->experts, (long long)w->hidden,
+                (long long)w->inter);
+  auto bytes = [&](int64_t rows, int64_t cols) {
+    return rows * ((cols + w->block_size - 1) / w->block_size) * w->block_size * w->bits / 8;
+  };
+  if (bytes(2 * w->inter, w->hidden) > INT32_MAX || bytes(w->hidden, w->inter) > INT32_MAX)
+    return fail(QMM_ERR_UNSUPPORTED, "%s: the codes of one expert's projection must be below 2^31 "
+                "bytes. Why: offsets in it are 32-bit.", fn);
+  return QMM_OK;
+}
+
 constexpr int64_t SAMPLE_MAX_ROWS = ((int64_t)1 << 21) - 1;
 
 }  // namespace
@@ -186,6 +212,102 @@ int qmm_sample(const void* logits, int dtype, int64_t rows, int64_t vocab, int64
   a.logprobs = logprobs;
   a.stream = (hipStream_t)stream;
   return hip_status(qmm::launch_sample(a, (char*)workspace), fn);
+}
+
+size_t qmm_moe_workspace_size(const qmm_moe_weights* w, int64_t tokens, int top_k) {
+  if (w == nullptr || tokens < 0 || tokens > qmm::MOE_MAX_TOKENS || top_k < 1 ||
+      top_k > qmm::MOE_MAX_TOP_K || check_moe_sizes("qmm_moe_workspace_size", w) != QMM_OK)
+    return 0;
+  return qmm::moe_workspace_bytes((int)tokens, (int)w->hidden, (int)w->inter, w->experts, top_k);
+}
+
+int qmm_moe(const qmm_rows* x, const qmm_moe_weights* w, const qmm_moe_route* route,
+            const qmm_rows* y, int dtype, int64_t tokens, void* workspace, size_t workspace_bytes,
+            void* stream) {
+  const char* fn = "qmm_moe";
+  const int es = dtype_size(dtype);
+  if (x == nullptr || w == nullptr || route == nullptr || y == nullptr)
+    return fail(QMM_ERR_INVALID_ARG, "%s: x, w, route and y must be non-null.", fn);
+  if (es == 0)
+    return fail(QMM_ERR_INVALID_ARG, "%s: dtype=%d is not a qmm_dtype. How to fix: pass QMM_F32, "
+                "QMM_F16 or QMM_BF16.", fn, dtype);
+  int st = check_moe_sizes(fn, w);
+  if (st != QMM_OK) return st;
+  if (tokens < 0)
+    return fail(QMM_ERR_INVALID_ARG, "%s: tokens must be >= 0, got %lld.", fn, (long long)tokens);
+  if (tokens > qmm::MOE_MAX_TOKENS)
+    return fail(QMM_ERR_UNSUPPORTED, "%s: at most %d tokens, got %lld. Why: every expert's tokens are "
+                "taken together, for a few of them. How to fix: split the batch, or group the tokens by "
+                "expert for qmm_gemm.", fn, qmm::MOE_MAX_TOKENS, (long long)tokens);
+  if (route->top_k < 1 || route->top_k > qmm::MOE_MAX_TOP_K ||
+      (route->logits != nullptr && route->top_k > w->experts))
+    return fail(QMM_ERR_INVALID_ARG, "%s: route.top_k must be from 1 to %d and no more than the "
+                "experts (%d), got %d.", fn, qmm::MOE_MAX_TOP_K, w->experts, route->top_k);
+  if (tokens == 0) return QMM_OK;
+  st = check_rows(fn, "x", x, tokens, w->hidden, es);
+  if (st == QMM_OK) st = check_rows(fn, "y", y, tokens, w->hidden, es);
+  if (st != QMM_OK) return st;
+  if (w->gate_up == nullptr || w->gate_up_scales == nullptr || w->down == nullptr ||
+      w->down_scales == nullptr || !aligned(w->gate_up, 16) || !aligned(w->down, 16))
+    return fail(QMM_ERR_INVALID_ARG, "%s: the codes must be non-null, 16-byte aligned and the scales "
+                "non-null device pointers.", fn);
+  const int ss = dtype_size(w->s_dtype);
+  if (!aligned(w->gate_up_scales, ss) || !aligned(w->down_scales, ss))
+    return fail(QMM_ERR_INVALID_ARG, "%s: scales must be aligned to their element size.", fn);
+  if (route->logits != nullptr) {
+    const int ls = dtype_size(route->logits_dtype);
+    if (ls == 0 || !aligned(route->logits, ls))
+      return fail(QMM_ERR_INVALID_ARG, "%s: route.logits must have a qmm_dtype (got %d) and be aligned "
+                  "to its element size.", fn, route->logits_dtype);
+    if (route->logits_stride < 0 || route->logits_stride > MAX_STRIDE ||
+        (tokens > 1 && route->logits_stride < w->experts))
+      return fail(QMM_ERR_INVALID_ARG, "%s: route.logits_stride=%lld does not hold a row of %d logits.",
+                  fn, (long long)route->logits_stride, w->experts);
+  } else if (route->ids == nullptr || route->weights == nullptr || !aligned(route->ids, 4) ||
+             !aligned(route->weights, 4)) {
+    return fail(QMM_ERR_INVALID_ARG, "%s: route needs logits, or ids and weights (4-byte aligned). How "
+                "to fix: pass one of the two.", fn);
+  }
+  st = check_workspace(fn, workspace, workspace_bytes,
+                       qmm::moe_workspace_bytes((int)tokens, (int)w->hidden, (int)w->inter, w->experts,
+                                                route->top_k));
+  if (st != QMM_OK) return st;
+  qmm::MoeArgs a;
+  a.x = (const char*)x->data;
+  a.y = (char*)y->data;
+  a.x_stride = x->stride;
+  a.y_stride = y->stride;
+  auto proj = [&](const uint8_t* codes, const void* scales, const uint8_t* zp, int64_t rows, int64_t cols) {
+    qmm::MoeProj p;
+    p.codes = codes;
+    p.scales = (const char*)scales;
+    p.zp = zp;
+    p.rows = (int)rows;
+    p.cols = (int)cols;
+    p.blocks = (int)((cols + w->block_size - 1) / w->block_size);
+    p.row_bytes = (int64_t)p.blocks * w->block_size * w->bits / 8;
+    p.zp_row_bytes = ((int64_t)p.blocks * w->bits + 7) / 8;
+    return p;
+  };
+  a.up = proj(w->gate_up, w->gate_up_scales, w->gate_up_zero_points, 2 * w->inter, w->hidden);
+  a.down = proj(w->down, w->down_scales, w->down_zero_points, w->hidden, w->inter);
+  a.logits = (const char*)route->logits;
+  a.ids = route->ids;
+  a.weights = route->weights;
+  a.logits_stride = route->logits_stride;
+  a.logits_dtype = route->logits_dtype;
+  a.normalize = route->normalize;
+  a.top_k = route->top_k;
+  a.tokens = (int)tokens;
+  a.hidden = (int)w->hidden;
+  a.inter = (int)w->inter;
+  a.experts = w->experts;
+  a.dtype = dtype;
+  a.s_dtype = w->s_dtype;
+  a.bits = w->bits;
+  a.block = w->block_size;
+  a.stream = (hipStream_t)stream;
+  return hip_status(qmm::launch_moe(a, (char*)workspace), fn);
 }
 
 }  // extern "C"

@@ -1,0 +1,341 @@
+// moe.hip -- a layer of experts on block-quantized weights for a few tokens:
+// the router's choice, the gate and up projections with SiLU, the down
+// projection, and the sum over a token's experts.
+#include <algorithm>
+
+#include "decode.h"
+#include "mfma_ops.h"
+#include "qmm_device.h"
+
+namespace qmm {
+namespace {
+
+constexpr int ROUTE_THREADS = 1024, ROUTE_WAVES = ROUTE_THREADS / 64;
+constexpr int MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP_K;
+
+struct Active {
+  int expert, start, count, unused;
+};
+
+// The workspace.  Pair p = token * top_k + j is a token's j-th expert.
+struct MoeWork {
+  int* ids;              // [pairs] experts, -1: none
+  float* weights;        // [pairs]
+  int* order;            // pairs by expert
+  Active* active;        // experts that have any, by number
+  int* n_active;
+  uint16_t* x;           // [parts][tokens][hidden, padded]: bf16 parts of x
+  uint16_t* h;           // [parts][pairs][inter, padded]: what enters the down projection
+  float* out;            // [pairs][hidden]: weighted outputs of the pairs
+  int x_cols, h_cols, x_parts, h_parts;
+};
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+int padded(int n) { return (n + 127) / 128 * 128; }
+
+// Lays the workspace out from `base` (null: only the size).
+size_t lay_out(int tokens, int hidden, int inter, int experts, int top_k, int dtype, char* base,
+               MoeWork* w) {
+  const size_t pairs = (size_t)tokens * top_k;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* p = base + at;
+    at += align256(bytes);
+    return p;
+  };
+  w->x_parts = dtype == DT_BF16 ? 1 : dtype == DT_F16 ? 2 : 3;
+  w->h_parts = dtype == DT_F32 ? 3 : 2;
+  w->x_cols = padded(hidden);
+  w->h_cols = padded(inter);
+  w->n_active = (int*)take(4);
+  w->ids = (int*)take(4 * pairs);
+  w->weights = (float*)take(4 * pairs);
+  w->order = (int*)take(4 * pairs);
+  w->active = (Active*)take(sizeof(Active) * std::min<size_t>(experts, pairs));
+  w->x = (uint16_t*)take(2 * (size_t)w->x_parts * tokens * w->x_cols);
+  w->h = (uint16_t*)take(2 * (size_t)w->h_parts * pairs * w->h_cols);
+  w->out = (float*)take(4 * pairs * (size_t)hidden);
+  return at;
+}
+
+__device__ __forceinline__ float load_logit(const MoeArgs& a, int64_t i) {
+  float v;
+  if (a.logits_dtype == DT_F32) v = ((const float*)a.logits)[i];
+  else if (a.logits_dtype == DT_F16) v = (float)((const _Float16*)a.logits)[i];
+  else v = __uint_as_float((uint32_t)((const uint16_t*)a.logits)[i] << 16);
+  return v != v ? -INFINITY : v;
+}
+
+// Orders as the values do (-0 as 0).
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    const uint64_t u = __shfl_xor(v, o);
+    v = u > v ? u : v;
+  }
+  return v;
+}
+__device__ __forceinline__ float wave_add(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// One wave: token t's experts and their weights in lanes 0 .. top_k - 1.
+__device__ void choose(const MoeArgs& a, int t, int lane, int* id, float* weight) {
+  *id = -1;
+  *weight = 0.f;
+  if (a.logits == nullptr) {
+    if (lane < a.top_k) {
+      *id = a.ids[t * a.top_k + lane];
+      *weight = a.weights[t * a.top_k + lane];
+    }
+  } else {
+    constexpr int PER = MOE_MAX_EXPERTS / 64;
+    float v[PER];
+    uint64_t best = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = lane + 64 * i;
+      v[i] = 64 * i < a.experts && e < a.experts ? load_logit(a, t * a.logits_stride + e) : -INFINITY;
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) top = fmaxf(top, v[i]);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    // Infinite logits share everything equally.
+    auto part = [&](float l) { return top == INFINITY ? (l == INFINITY ? 1.f : 0.f) : expf(l - top); };
+    float sum = 0.f;
+    if (top > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (64 * i < a.experts && v[i] > -INFINITY) sum += part(v[i]);
+      sum = wave_add(sum);
+      float chosen = 0.f, mine = 0.f;
+      uint32_t taken = 0;
+      for (int j = 0; j < a.top_k; ++j) {
+        best = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int e = lane + 64 * i;
+          if (64 * i >= a.experts || e >= a.experts || (taken >> i & 1)) continue;
+          const uint64_t at = (uint64_t)order_key(v[i]) << 32 | (uint32_t)~e;
+          best = at > best ? at : best;
+        }
+        best = wave_max_u64(best);
+        const int e = (int)~(uint32_t)best;
+        const uint32_t key = (uint32_t)(best >> 32);
+        const float l = __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+        if ((e & 63) == lane) taken |= 1u << (e >> 6);
+        const float p = l > -INFINITY ? part(l) : 0.f;
+        chosen += p;
+        if (lane == j) {
+          *id = e;
+          mine = p;
+        }
+      }
+      *weight = mine / (a.normalize ? chosen : sum);
+    }
+  }
+  if (*id < 0 || *id >= a.experts || *weight == 0.f || lane >= a.top_k) *id = -1;
+}
+
+// The order of eight codes' values in a matrix-core operand (see weights8 below).
+template <int BITS> __device__ __forceinline__ int code_at(int i) {
+  return BITS == 4 ? i / 2 + 4 * (i % 2) : (i & 4) + (i / 2 % 2) + 2 * (i % 2);
+}
+
+// v as a sum of bf16 values, of 8 bits each.
+template <int PARTS>
+__device__ __forceinline__ void split(float v, uint16_t (&part)[PARTS]) {
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) {
+    part[p] = MfmaOp<DT_BF16>::round(v);
+    v -= bits16_to_f32<DT_BF16>(part[p]);
+  }
+}
+
+// Workgroup 0 routes; the others lay x out for the matrix cores.
+template <int DT, int BITS>
+__global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork w) {
+  using T = typename dt<DT>::T;
+  constexpr int PARTS = DT == DT_BF16 ? 1 : DT == DT_F16 ? 2 : 3;
+  if (blockIdx.x > 0) {
+    const int chunks = w.x_cols / 8;
+    const int64_t all = (int64_t)a.tokens * chunks;
+    for (int64_t i = (int64_t)(blockIdx.x - 1) * ROUTE_THREADS + threadIdx.x; i < all;
+         i += (int64_t)(gridDim.x - 1) * ROUTE_THREADS) {
+      const int t = (int)(i / chunks), c = (int)(i % chunks) * 8;
+      const T* from = (const T*)a.x + t * a.x_stride;
+      uint16_t e[PARTS][8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = c + code_at<BITS>(j);
+        uint16_t part[PARTS];
+        split<PARTS>(k < a.hidden ? dt<DT>::to_f32(from[k]) : 0.f, part);
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) e[p][j] = part[p];
+      }
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p)
+        __builtin_memcpy(__builtin_assume_aligned(w.x + ((int64_t)p * a.tokens + t) * w.x_cols + c, 16),
+                         e[p], 16);
+    }
+    return;
+  }
+  __shared__ int ids[MAX_PAIRS];
+  __shared__ uint32_t upto[ROUTE_WAVES];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int pairs = a.tokens * a.top_k;
+  for (int t = wave; t < a.tokens; t += ROUTE_WAVES) {
+    int id;
+    float weight;
+    choose(a, t, lane, &id, &weight);
+    if (lane < a.top_k) {
+      ids[t * a.top_k + lane] = id;
+      w.ids[t * a.top_k + lane] = id;
+      w.weights[t * a.top_k + lane] = weight;
+    }
+  }
+  __syncthreads();
+  // Thread e counts expert e's pairs and lists them in order.
+  const int e = threadIdx.x;
+  uint32_t count = 0;
+  if (e < a.experts)
+    for (int p = 0; p < pairs; ++p) count += ids[p] == e;
+  // Pairs and active experts before this one, in one word.
+  uint32_t sum = count | (uint32_t)(count > 0) << 16;
+  const uint32_t own = sum;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t v = __shfl_up(sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 63) upto[wave] = sum;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+  for (int v = 0; v < ROUTE_WAVES; ++v) {
+    if (v < wave) before += upto[v];
+    all += upto[v];
+  }
+  before += sum - own;
+  if (threadIdx.x == 0) *w.n_active = (int)(all >> 16);
+  if (count == 0) return;
+  int start = (int)(before & 0xFFFFu);
+  w.active[before >> 16] = Active{e, start, (int)count, 0};
+  for (int p = 0; p < pairs; ++p)
+    if (ids[p] == e) w.order[start++] = p;
+}
+
+// Row `row` of an expert's projection times 1 or 2 columns of bf16 parts: one wave.
+template <int BITS>
+__device__ float row_dot(const MoeArgs& a, const MoeProj& m, int e, int row, const uint16_t* v,
+                         int64_t part_stride, int parts) {
+  const int lane = threadIdx.x & 63;
+  const int64_t at = (int64_t)e * m.rows + row;
+  const uint8_t* codes = m.codes + at * m.row_bytes;
+  float sum = 0.f;
+  for (int k = lane; k < m.cols; k += 64) {
+    const int b = k / a.block;
+    const int code = BITS == 8 ? codes[k] : codes[k / 2] >> (4 * (k % 2)) & 15;
+    int z = 1 << (BITS - 1);
+    if (m.zp) {
+      const uint8_t* zr = m.zp + at * m.zp_row_bytes;
+      z = BITS == 8 ? zr[b] : zr[b / 2] >> (4 * (b % 2)) & 15;
+    }
+    const int64_t s = at * m.blocks + b;
+    const float scale = a.s_dtype == DT_F32 ? ((const float*)m.scales)[s]
+                        : a.s_dtype == DT_F16 ? (float)((const _Float16*)m.scales)[s]
+                                              : bits16_to_f32<DT_BF16>(((const uint16_t*)m.scales)[s]);
+    int place = 0;
+    for (int i = 0; i < 8; ++i)
+      if (code_at<BITS>(i) == k % 8) place = i;
+    float x = 0.f;
+    for (int p = parts - 1; p >= 0; --p) x += bits16_to_f32<DT_BF16>(v[p * part_stride + (k & ~7) + place]);
+    sum += (float)(code - z) * scale * x;
+  }
+  return wave_add(sum);
+}
+
+template <int BITS, int PARTS>
+__global__ void up_kernel(MoeArgs a, MoeWork w) {
+  const int pair = blockIdx.y, j = blockIdx.x * 4 + threadIdx.x / 64;
+  const int e = w.ids[pair];
+  if (e < 0 || j >= w.h_cols) return;
+  const uint16_t* x = w.x + (int64_t)(pair / a.top_k) * w.x_cols;
+  float h = 0.f;
+  if (j < a.inter) {
+    const float g = row_dot<BITS>(a, a.up, e, j, x, (int64_t)a.tokens * w.x_cols, w.x_parts);
+    const float u = row_dot<BITS>(a, a.up, e, a.inter + j, x, (int64_t)a.tokens * w.x_cols, w.x_parts);
+    h = g / (1.f + expf(-g)) * u;
+  }
+  uint16_t part[PARTS];
+  split<PARTS>(h, part);
+  int place = 0;
+  for (int i = 0; i < 8; ++i)
+    if (code_at<BITS>(i) == j % 8) place = i;
+  if (threadIdx.x % 64 == 0)
+    for (int p = 0; p < PARTS; ++p)
+      w.h[((int64_t)p * a.tokens * a.top_k + pair) * w.h_cols + (j & ~7) + place] = part[p];
+}
+
+template <int BITS>
+__global__ void down_kernel(MoeArgs a, MoeWork w) {
+  const int pair = blockIdx.y, n = blockIdx.x * 4 + threadIdx.x / 64;
+  const int e = w.ids[pair];
+  if (e < 0 || n >= a.hidden) return;
+  const float o = row_dot<BITS>(a, a.down, e, n, w.h + (int64_t)pair * w.h_cols,
+                                (int64_t)a.tokens * a.top_k * w.h_cols, w.h_parts);
+  if (threadIdx.x % 64 == 0) w.out[(int64_t)pair * a.hidden + n] = o * w.weights[pair];
+}
+
+// y: the sum of a token's pairs, in their order.
+template <int DT>
+__global__ __launch_bounds__(256) void combine_kernel(MoeArgs a, MoeWork w) {
+  const int t = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
+  if (n >= a.hidden) return;
+  float sum = 0.f;
+  for (int j = 0; j < a.top_k; ++j) {
+    const int pair = t * a.top_k + j;
+    if (w.ids[pair] >= 0) sum += w.out[(int64_t)pair * a.hidden + n];
+  }
+  ((typename dt<DT>::T*)a.y)[t * a.y_stride + n] = dt<DT>::from_f32(sum);
+}
+
+template <int DT, int BITS>
+hipError_t launch(const MoeArgs& a, const MoeWork& w) {
+  const int64_t chunks = (int64_t)a.tokens * w.x_cols / 8;
+  const uint32_t stage = (uint32_t)std::min<int64_t>((chunks + ROUTE_THREADS - 1) / ROUTE_THREADS, 256);
+  route_kernel<DT, BITS><<<dim3(1 + stage), ROUTE_THREADS, 0, a.stream>>>(a, w);
+  const uint32_t pairs = a.tokens * a.top_k;
+  up_kernel<BITS, DT == DT_F32 ? 3 : 2><<<dim3((w.h_cols + 3) / 4, pairs), 256, 0, a.stream>>>(a, w);
+  down_kernel<BITS><<<dim3((a.hidden + 3) / 4, pairs), 256, 0, a.stream>>>(a, w);
+  combine_kernel<DT><<<dim3((a.hidden + 255) / 256, a.tokens), 256, 0, a.stream>>>(a, w);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t moe_workspace_bytes(int tokens, int hidden, int inter, int experts, int top_k) {
+  MoeWork w;
+  return lay_out(tokens, hidden, inter, experts, top_k, DT_F32, nullptr, &w);
+}
+
+hipError_t launch_moe(const MoeArgs& a, char* workspace) {
+  MoeWork w;
+  lay_out(a.tokens, a.hidden, a.inter, a.experts, a.top_k, a.dtype, workspace, &w);
+  const bool four = a.bits == 4;
+  switch (a.dtype) {
+    case DT_F32: return four ? launch<DT_F32, 4>(a, w) : launch<DT_F32, 8>(a, w);
+    case DT_F16: return four ? launch<DT_F16, 4>(a, w) : launch<DT_F16, 8>(a, w);
+    default: return four ? launch<DT_BF16, 4>(a, w) : launch<DT_BF16, 8>(a, w);
+  }
+}
+
+}  // namespace qmm

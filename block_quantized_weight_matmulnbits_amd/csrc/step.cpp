@@ -168,6 +168,18 @@ int qmm_step_add_gemm_compint8_quantized(qmm_step* step, const int8_t* qa, const
   });
 }
 
+int qmm_step_add_moe(qmm_step* step, const qmm_rows* x, const qmm_moe_weights* w,
+                     const qmm_moe_route* route, const qmm_rows* y, int dtype, int64_t tokens,
+                     void* workspace, size_t workspace_bytes) {
+  const auto rx = copied(x), ry = copied(y);
+  const auto cw = copied(w);
+  const auto cr = copied(route);
+  return add_call(step, [=](void* s) {
+    return qmm_moe(rx.get(), cw.get(), cr.get(), ry.get(), dtype, tokens, workspace,
+                   workspace_bytes, s);
+  });
+}
+
 int qmm_step_add_sample(qmm_step* step, const void* logits, int dtype, int64_t rows, int64_t vocab,
                         int64_t row_stride, const float* temperature, const int32_t* top_k,
                         const float* top_p, const float* min_p, const float* uniform,

@@ -79,6 +79,9 @@ _SIGS = {
     "qmm_step_add_rms_norm": ([_vp] * 5 + [_i32, _f32, _f64, _vp, _vp, _i32, _i64, _i64], _i32),
     "qmm_step_add_gemm_compint8_quantized": ([_vp] * 4 + [_i32, _vp, _i32, _vp, _vp, _vp, _i32, _i64, _i64,
                                                           _i64, _i32, _i32], _i32),
+    "qmm_moe_workspace_size": ([_vp, _i64, _i32], _sz),
+    "qmm_moe": ([_vp, _vp, _vp, _vp, _i32, _i64, _vp, _sz, _vp], _i32),
+    "qmm_step_add_moe": ([_vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _sz], _i32),
     "qmm_sample_workspace_size": ([_i64, _i64], _sz),
     "qmm_sample": ([_vp, _i32, _i64, _i64, _i64] + [_vp] * 8 + [_sz, _vp], _i32),
     "qmm_step_add_sample": ([_vp, _vp, _i32, _i64, _i64, _i64] + [_vp] * 8 + [_sz], _i32),
@@ -311,7 +314,7 @@ class Step:
     """A recorded sequence of calls replayed as one HIP graph (qmm_step_* in
     include/qmm.h).  add_gemv / add_gemm / add_gemm_compint8 /
     add_rope_append / add_paged_attention / add_pages_reserve / add_rms_norm /
-    add_gemm_compint8_quantized / add_sample take the arguments of the functions of the same name (without a stream);
+    add_gemm_compint8_quantized / add_moe / add_sample take the arguments of the functions of the same name (without a stream);
     finalize() validates and captures; launch(stream) replays.  The tensors
     passed are kept referenced for the step's life, since the graph holds
     their device addresses."""
@@ -376,6 +379,11 @@ class Step:
     def add_gemm_compint8_quantized(self, qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size, bits):
         _, args = _quantized_args(qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size, bits)
         self._add(lib.qmm_step_add_gemm_compint8_quantized, (qa, sa, B, scales, zero_points, bias, Y), *args)
+
+    def add_moe(self, x, weights, y, workspace, logits=None, top_k=0, normalize=True, ids=None,
+                expert_weights=None):
+        _, args = _moe_args(x, weights, y, workspace, logits, top_k, normalize, ids, expert_weights)
+        self._add(lib.qmm_step_add_moe, (x, weights, y, workspace, logits, ids, expert_weights), *args)
 
     def add_sample(self, logits, uniform, tokens, workspace, temperature=None, top_k=None, top_p=None,
                    min_p=None, logprobs=None):
@@ -823,6 +831,93 @@ def qmm_gemm_compint8_quantized(qa, sa, B, scales, zero_points, bias, Y, M, K, N
     scales ``sa`` [M, kb] float32, as qmm_rms_norm writes them."""
     gpu, args = _quantized_args(qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size, bits)
     _check(lib.qmm_gemm_compint8_quantized(*args, _stream_at(gpu, stream)))
+
+
+class _MoeWeights(ctypes.Structure):
+    _fields_ = ([(f"{p}{t}", _vp) for p in ("gate_up", "down") for t in ("", "_scales", "_zero_points")]
+                + [("hidden", _i64), ("inter", _i64)]
+                + [(n, _i32) for n in ("experts", "s_dtype", "block_size", "bits")])
+
+
+# struct qmm_moe_route, as bytes: logits, logits_stride, logits_dtype, normalize,
+# ids, weights, top_k.
+_pack_route = struct.Struct("@PqiiPPi4x").pack
+
+
+class MoeWeights:
+    """The experts of a layer, one after the other in the operator's layout:
+    ``gate_up`` [experts, 2 * inter, blocks of hidden, block_size * bits / 8] uint8
+    (the gate's rows first), its scales [experts, 2 * inter, blocks] and packed zero
+    points [experts, 2 * inter, bytes] (or None); ``down`` [experts, hidden, blocks
+    of inter, block_size * bits / 8] likewise."""
+
+    def __init__(self, gate_up, gate_up_scales, gate_up_zero_points, down, down_scales, down_zero_points,
+                 hidden, inter, block_size, bits):
+        experts = gate_up.shape[0]
+        if gate_up_scales.dtype is not down_scales.dtype or gate_up_scales.dtype not in _TORCH_TO_QMM:
+            raise ValueError(f"the scales must share one dtype of float32, float16 or bfloat16, got "
+                             f"{gate_up_scales.dtype} and {down_scales.dtype}")
+        for name, codes, scales, zp, rows, cols in (
+                ("gate_up", gate_up, gate_up_scales, gate_up_zero_points, 2 * inter, hidden),
+                ("down", down, down_scales, down_zero_points, hidden, inter)):
+            kb = -(-cols // block_size)
+            _dense(name, codes, (experts, rows, kb, block_size * bits // 8), torch.uint8)
+            _dense(name + "_scales", scales, (experts, rows, kb), scales.dtype)
+            if zp is not None:
+                _dense(name + "_zero_points", zp, (experts, rows, -(-kb * bits // 8)), torch.uint8)
+        self.tensors = dict(gate_up=gate_up, gate_up_scales=gate_up_scales, gate_up_zero_points=gate_up_zero_points,
+                            down=down, down_scales=down_scales, down_zero_points=down_zero_points)
+        self.gpu = gate_up.get_device()
+        if any(t is not None and t.get_device() != self.gpu for t in self.tensors.values()) or self.gpu < 0:
+            raise _apart(**self.tensors)
+        self.experts, self.hidden, self.inter = experts, int(hidden), int(inter)
+        self._c = _MoeWeights(*(_ptr(t) for t in self.tensors.values()), self.hidden, self.inter, experts,
+                              _dt(gate_up_scales), int(block_size), int(bits))
+        self._ref = ctypes.byref(self._c)
+
+
+def qmm_moe_workspace_size(weights, tokens, top_k) -> int:
+    """Bytes of the workspace; calls on one stream may share it."""
+    return int(lib.qmm_moe_workspace_size(weights._ref, tokens, top_k))
+
+
+def _moe_args(x, weights, y, workspace, logits, top_k, normalize, ids, expert_weights):
+    if x.dim() != 2 or x.dtype not in _TORCH_TO_QMM:
+        raise ValueError(f"x must be [tokens, hidden] of float32, float16 or bfloat16, got {x.dtype} "
+                         f"{list(x.shape)}")
+    tokens, gpu = x.shape[0], weights.gpu
+    shape = (tokens, weights.hidden)
+    if (logits is None) == (ids is None) or (ids is None) != (expert_weights is None):
+        raise ValueError("pass logits and top_k, or ids and expert_weights")
+    if ids is None:
+        if (logits.shape != (tokens, weights.experts) or logits.dtype not in _TORCH_TO_QMM
+                or (logits.stride(1) != 1 and weights.experts > 1)):
+            raise ValueError(f"logits must be [{tokens}, {weights.experts}] of float32, float16 or bfloat16 "
+                             f"with dense rows, got {logits.dtype} {list(logits.shape)}")
+        route = _pack_route(logits.data_ptr(), logits.stride(0), _TORCH_TO_QMM[logits.dtype], bool(normalize),
+                            0, 0, top_k)
+    else:
+        if ids.dim() != 2:
+            raise ValueError(f"ids must be [tokens, top_k], got {list(ids.shape)}")
+        route = _pack_route(0, 0, 0, 0, _dense("ids", ids, (tokens, ids.shape[1]), _INT32),
+                            _dense("expert_weights", expert_weights, ids.shape, torch.float32), ids.shape[1])
+    for t in (x, y, workspace, logits, ids, expert_weights):
+        if t is not None and t.get_device() != gpu:
+            raise _apart(weights=weights.tensors["gate_up"], x=x, y=y, workspace=workspace, logits=logits,
+                         ids=ids, expert_weights=expert_weights)
+    return gpu, (_matrix("x", x, shape, x.dtype), weights._ref, route, _matrix("y", y, shape, x.dtype),
+                 _TORCH_TO_QMM[x.dtype], tokens, workspace.data_ptr(), workspace.nbytes)
+
+
+def qmm_moe(x, weights, y, workspace, logits=None, top_k=0, normalize=True, ids=None, expert_weights=None,
+            stream=None):
+    """y [tokens, hidden] = the sum over each token's experts of weight * down(silu(gate
+    x) * up x).  The experts are the ``top_k`` of the router's ``logits`` [tokens,
+    experts] (weights: their softmax, over the chosen ones where ``normalize``), or
+    the given ``ids`` [tokens, top_k] int32 (out of range: none) with
+    ``expert_weights`` [tokens, top_k] float32."""
+    gpu, args = _moe_args(x, weights, y, workspace, logits, top_k, normalize, ids, expert_weights)
+    _check(lib.qmm_moe(*args, _stream_at(gpu, stream)))
 
 
 def qmm_sample_workspace_size(rows, vocab) -> int:

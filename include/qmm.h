@@ -525,6 +525,64 @@ int qmm_gemm_compint8_quantized(const int8_t *qa, const float *sa, const uint8_t
                                 int bits, void *stream);
 
 /*
+ * A layer of experts for a few tokens, on block-quantized weights.  Every expert
+ * has the operator's layout (qmm_gemv: QMM_LAYOUT_ORT), one after the other:
+ *   gate_up    [experts, 2 inter, ceil(hidden / bs), bs * bits / 8]: the rows of the
+ *              gate, then those of the up projection; gate_up_scales [experts,
+ *              2 inter, ceil(hidden / bs)] of s_dtype; gate_up_zero_points
+ *              [experts, 2 inter, ceil(ceil(hidden / bs) * bits / 8)] or NULL
+ *   down       the same for [experts, hidden] rows of inter elements
+ * bits 4 or 8, block_size a power of two from 16 up.  The codes are 16-byte
+ * aligned.  At most 1024 experts, hidden and inter up to 2^18, the codes of one
+ * expert's gate_up, and of its down, below 2^31 bytes.
+ */
+typedef struct qmm_moe_weights {
+    const uint8_t *gate_up;
+    const void *gate_up_scales;
+    const uint8_t *gate_up_zero_points;
+    const uint8_t *down;
+    const void *down_scales;
+    const uint8_t *down_zero_points;
+    int64_t hidden, inter;
+    int experts, s_dtype, block_size, bits;
+} qmm_moe_weights;
+
+/* Which experts a token goes to: the top_k largest of the router's logits
+ * [tokens, experts] (ties: the lowest index; nan counts as minus infinity) with
+ * their softmax over all experts as weights, divided by the chosen ones' sum
+ * where normalize is non-zero; or, where logits is NULL, the given ids [tokens,
+ * top_k] and weights [tokens, top_k].  An id out of 0 .. experts - 1 and a weight
+ * of 0 stand for no expert; an id may repeat.  A row without a logit above minus
+ * infinity has no experts.  1 <= top_k <= 32 (and <= experts with logits). */
+typedef struct qmm_moe_route {
+    const void *logits;
+    int64_t logits_stride;       /* in elements */
+    int logits_dtype, normalize;
+    const int32_t *ids;
+    const float *weights;
+    int top_k;
+} qmm_moe_route;
+
+/*
+ * y[t] = sum_j w_tj down_e(silu(gate_e x_t) * (up_e x_t)),   e = id_tj,
+ * silu(a) = a / (1 + exp(-a)), for x and y [tokens, hidden] of dtype (rows with
+ * strides; y may be x).  Only the chosen experts' weights are read, once for all
+ * of up to 64 tokens of an expert.  Products are of x and whole codes, summed in
+ * fp32, each block's sum then scaled; between the projections an f32 layer keeps
+ * 24 bits and a 16-bit one 16 bits of every value; y is rounded once.  A token
+ * without experts gets 0.  Values of x that are not finite make the token's own
+ * y nan.
+ * tokens 0 .. 256 (split larger batches, or group the tokens by expert for
+ * qmm_gemm); workspace: qmm_moe_workspace_size bytes, 256-byte aligned; calls on
+ * one stream may share it.
+ */
+size_t qmm_moe_workspace_size(const qmm_moe_weights *w, int64_t tokens, int top_k);
+
+int qmm_moe(const qmm_rows *x, const qmm_moe_weights *w, const qmm_moe_route *route,
+            const qmm_rows *y, int dtype, int64_t tokens, void *workspace,
+            size_t workspace_bytes, void *stream);
+
+/*
  * The next token of each row of logits [rows, vocab] (dtype; rows row_stride
  * elements apart), from a given number uniform[row] in [0, 1).  With
  *   w_i = exp((l_i - max l) / temperature)
@@ -644,6 +702,10 @@ int qmm_step_add_gemm_compint8_quantized(qmm_step *step, const int8_t *qa, const
                                          int s_dtype, const uint8_t *zero_points,
                                          const void *bias, void *Y, int y_dtype, int64_t M,
                                          int64_t K, int64_t N, int block_size, int bits);
+
+int qmm_step_add_moe(qmm_step *step, const qmm_rows *x, const qmm_moe_weights *w,
+                     const qmm_moe_route *route, const qmm_rows *y, int dtype,
+                     int64_t tokens, void *workspace, size_t workspace_bytes);
 
 int qmm_step_add_sample(qmm_step *step, const void *logits, int dtype, int64_t rows,
                         int64_t vocab, int64_t row_stride, const float *temperature,
