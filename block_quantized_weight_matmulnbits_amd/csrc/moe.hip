@@ -3,32 +3,13 @@
 // projection, and the sum over a token's experts.
 #include <algorithm>
 
-#include "decode.h"
-#include "mfma_ops.h"
-#include "qmm_device.h"
+#include "moe.h"
 
 namespace qmm {
 namespace {
 
 constexpr int ROUTE_THREADS = 1024, ROUTE_WAVES = ROUTE_THREADS / 64;
 constexpr int MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP_K;
-
-struct Active {
-  int expert, start, count, unused;
-};
-
-// The workspace.  Pair p = token * top_k + j is a token's j-th expert.
-struct MoeWork {
-  int* ids;              // [pairs] experts, -1: none
-  float* weights;        // [pairs]
-  int* order;            // pairs by expert
-  Active* active;        // experts that have any, by number
-  int* n_active;
-  uint16_t* x;           // [parts][tokens][hidden, padded]: bf16 parts of x
-  uint16_t* h;           // [parts][pairs][inter, padded]: what enters the down projection
-  float* out;            // [pairs][hidden]: weighted outputs of the pairs
-  int x_cols, h_cols, x_parts, h_parts;
-};
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 int padded(int n) { return (n + 127) / 128 * 128; }
@@ -43,17 +24,16 @@ size_t lay_out(int tokens, int hidden, int inter, int experts, int top_k, int dt
     at += align256(bytes);
     return p;
   };
-  w->x_parts = dtype == DT_BF16 ? 1 : dtype == DT_F16 ? 2 : 3;
-  w->h_parts = dtype == DT_F32 ? 3 : 2;
   w->x_cols = padded(hidden);
   w->h_cols = padded(inter);
+  w->max_active = (int)std::min<size_t>(experts, pairs);
   w->n_active = (int*)take(4);
   w->ids = (int*)take(4 * pairs);
   w->weights = (float*)take(4 * pairs);
   w->order = (int*)take(4 * pairs);
-  w->active = (Active*)take(sizeof(Active) * std::min<size_t>(experts, pairs));
-  w->x = (uint16_t*)take(2 * (size_t)w->x_parts * tokens * w->x_cols);
-  w->h = (uint16_t*)take(2 * (size_t)w->h_parts * pairs * w->h_cols);
+  w->active = (MoeActive*)take(sizeof(MoeActive) * w->max_active);
+  w->x = (uint16_t*)take(2 * (size_t)moe_x_parts(dtype) * tokens * w->x_cols);
+  w->h = (uint16_t*)take(2 * (size_t)moe_h_parts(dtype) * pairs * w->h_cols);
   w->out = (float*)take(4 * pairs * (size_t)hidden);
   return at;
 }
@@ -146,26 +126,11 @@ __device__ void choose(const MoeArgs& a, int t, int lane, int* id, float* weight
   if (*id < 0 || *id >= a.experts || *weight == 0.f || lane >= a.top_k) *id = -1;
 }
 
-// The order of eight codes' values in a matrix-core operand (see weights8 below).
-template <int BITS> __device__ __forceinline__ int code_at(int i) {
-  return BITS == 4 ? i / 2 + 4 * (i % 2) : (i & 4) + (i / 2 % 2) + 2 * (i % 2);
-}
-
-// v as a sum of bf16 values, of 8 bits each.
-template <int PARTS>
-__device__ __forceinline__ void split(float v, uint16_t (&part)[PARTS]) {
-#pragma unroll
-  for (int p = 0; p < PARTS; ++p) {
-    part[p] = MfmaOp<DT_BF16>::round(v);
-    v -= bits16_to_f32<DT_BF16>(part[p]);
-  }
-}
-
 // Workgroup 0 routes; the others lay x out for the matrix cores.
 template <int DT, int BITS>
 __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork w) {
   using T = typename dt<DT>::T;
-  constexpr int PARTS = DT == DT_BF16 ? 1 : DT == DT_F16 ? 2 : 3;
+  constexpr int PARTS = moe_x_parts(DT);
   if (blockIdx.x > 0) {
     const int chunks = w.x_cols / 8;
     const int64_t all = (int64_t)a.tokens * chunks;
@@ -178,7 +143,7 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
       for (int j = 0; j < 8; ++j) {
         const int k = c + code_at<BITS>(j);
         uint16_t part[PARTS];
-        split<PARTS>(k < a.hidden ? dt<DT>::to_f32(from[k]) : 0.f, part);
+        split_bf16<PARTS>(k < a.hidden ? dt<DT>::to_f32(from[k]) : 0.f, part);
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) e[p][j] = part[p];
       }
@@ -228,71 +193,9 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
   if (threadIdx.x == 0) *w.n_active = (int)(all >> 16);
   if (count == 0) return;
   int start = (int)(before & 0xFFFFu);
-  w.active[before >> 16] = Active{e, start, (int)count, 0};
+  w.active[before >> 16] = MoeActive{e, start, (int)count, 0};
   for (int p = 0; p < pairs; ++p)
     if (ids[p] == e) w.order[start++] = p;
-}
-
-// Row `row` of an expert's projection times 1 or 2 columns of bf16 parts: one wave.
-template <int BITS>
-__device__ float row_dot(const MoeArgs& a, const MoeProj& m, int e, int row, const uint16_t* v,
-                         int64_t part_stride, int parts) {
-  const int lane = threadIdx.x & 63;
-  const int64_t at = (int64_t)e * m.rows + row;
-  const uint8_t* codes = m.codes + at * m.row_bytes;
-  float sum = 0.f;
-  for (int k = lane; k < m.cols; k += 64) {
-    const int b = k / a.block;
-    const int code = BITS == 8 ? codes[k] : codes[k / 2] >> (4 * (k % 2)) & 15;
-    int z = 1 << (BITS - 1);
-    if (m.zp) {
-      const uint8_t* zr = m.zp + at * m.zp_row_bytes;
-      z = BITS == 8 ? zr[b] : zr[b / 2] >> (4 * (b % 2)) & 15;
-    }
-    const int64_t s = at * m.blocks + b;
-    const float scale = a.s_dtype == DT_F32 ? ((const float*)m.scales)[s]
-                        : a.s_dtype == DT_F16 ? (float)((const _Float16*)m.scales)[s]
-                                              : bits16_to_f32<DT_BF16>(((const uint16_t*)m.scales)[s]);
-    int place = 0;
-    for (int i = 0; i < 8; ++i)
-      if (code_at<BITS>(i) == k % 8) place = i;
-    float x = 0.f;
-    for (int p = parts - 1; p >= 0; --p) x += bits16_to_f32<DT_BF16>(v[p * part_stride + (k & ~7) + place]);
-    sum += (float)(code - z) * scale * x;
-  }
-  return wave_add(sum);
-}
-
-template <int BITS, int PARTS>
-__global__ void up_kernel(MoeArgs a, MoeWork w) {
-  const int pair = blockIdx.y, j = blockIdx.x * 4 + threadIdx.x / 64;
-  const int e = w.ids[pair];
-  if (e < 0 || j >= w.h_cols) return;
-  const uint16_t* x = w.x + (int64_t)(pair / a.top_k) * w.x_cols;
-  float h = 0.f;
-  if (j < a.inter) {
-    const float g = row_dot<BITS>(a, a.up, e, j, x, (int64_t)a.tokens * w.x_cols, w.x_parts);
-    const float u = row_dot<BITS>(a, a.up, e, a.inter + j, x, (int64_t)a.tokens * w.x_cols, w.x_parts);
-    h = g / (1.f + expf(-g)) * u;
-  }
-  uint16_t part[PARTS];
-  split<PARTS>(h, part);
-  int place = 0;
-  for (int i = 0; i < 8; ++i)
-    if (code_at<BITS>(i) == j % 8) place = i;
-  if (threadIdx.x % 64 == 0)
-    for (int p = 0; p < PARTS; ++p)
-      w.h[((int64_t)p * a.tokens * a.top_k + pair) * w.h_cols + (j & ~7) + place] = part[p];
-}
-
-template <int BITS>
-__global__ void down_kernel(MoeArgs a, MoeWork w) {
-  const int pair = blockIdx.y, n = blockIdx.x * 4 + threadIdx.x / 64;
-  const int e = w.ids[pair];
-  if (e < 0 || n >= a.hidden) return;
-  const float o = row_dot<BITS>(a, a.down, e, n, w.h + (int64_t)pair * w.h_cols,
-                                (int64_t)a.tokens * a.top_k * w.h_cols, w.h_parts);
-  if (threadIdx.x % 64 == 0) w.out[(int64_t)pair * a.hidden + n] = o * w.weights[pair];
 }
 
 // y: the sum of a token's pairs, in their order.
@@ -313,9 +216,11 @@ hipError_t launch(const MoeArgs& a, const MoeWork& w) {
   const int64_t chunks = (int64_t)a.tokens * w.x_cols / 8;
   const uint32_t stage = (uint32_t)std::min<int64_t>((chunks + ROUTE_THREADS - 1) / ROUTE_THREADS, 256);
   route_kernel<DT, BITS><<<dim3(1 + stage), ROUTE_THREADS, 0, a.stream>>>(a, w);
-  const uint32_t pairs = a.tokens * a.top_k;
-  up_kernel<BITS, DT == DT_F32 ? 3 : 2><<<dim3((w.h_cols + 3) / 4, pairs), 256, 0, a.stream>>>(a, w);
-  down_kernel<BITS><<<dim3((a.hidden + 3) / 4, pairs), 256, 0, a.stream>>>(a, w);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess)
+    e = DT == DT_BF16 ? launch_moe_up_1(a, w) : DT == DT_F16 ? launch_moe_up_2(a, w) : launch_moe_up_3(a, w);
+  if (e == hipSuccess) e = DT == DT_F32 ? launch_moe_down_3(a, w) : launch_moe_down_2(a, w);
+  if (e != hipSuccess) return e;
   combine_kernel<DT><<<dim3((a.hidden + 255) / 256, a.tokens), 256, 0, a.stream>>>(a, w);
   return hipGetLastError();
 }
