@@ -7,13 +7,15 @@
 // codes a row) and join through LDS.  Weights are read once, straight into
 // registers, 16 bytes a lane; HBM is the bound.
 //
-// The matrix cores multiply bf16 parts of x with whole codes, so that weights are
-// not rounded: a 4-bit code c is the bf16 value 16 + c (one shift and one
-// and-or for two codes), an 8-bit one two such fields.  What the 16 and the zero
-// point add to a block's sum is (16 + z) times the sum of x over the block,
-// which one more product, with ones, gives in the same registers; then the
-// block's sum is scaled, in fp32:
+// The matrix cores multiply x (an f32 one in three bf16 parts) with whole numbers,
+// so that weights are not rounded, and a block's sum is scaled in fp32.  A 4-bit
+// code c is the 16-bit value 16 + c (one shift and one and-or for two codes); what the 16 and the
+// zero point add to a block's sum is (16 + z) times the sum of x over the block,
+// which one more product, with ones, gives in the same registers:
 //   out += s * (sum (16 + c) x  -  (16 + z) sum x).
+// Those sums are up to some five times the result's size, which 16-bit types do
+// not see; f32 layers, and 8-bit codes, for which the offset would be 256, enter
+// as c - z.
 // A lane loads 16 consecutive bytes, one block of 32 codes for example, but a
 // matrix instruction takes 32 codes of one block from the four lanes that share
 // a row, so their 32-bit words are transposed first (4 swaps for 4 instructions).
@@ -40,31 +42,34 @@ struct MoeWork {
   int* order;            // pairs by expert
   MoeActive* active;     // by the expert's number
   int* n_active;
-  uint16_t* x;           // [parts][tokens][hidden, padded]: bf16 parts of x
+  uint16_t* x;           // [parts][tokens][hidden, padded]
   uint16_t* h;           // [parts][pairs][inter, padded]: what enters the down projection
   float* out;            // [pairs][hidden]: weighted outputs of the pairs
   int x_cols, h_cols;    // padded to 128 with zeros
   int max_active;        // active experts at most
 };
 
-// bf16 parts that hold x (exactly) and h (16 bits of it, 24 of an f32 layer's).
-constexpr int moe_x_parts(int dtype) { return dtype == DT_BF16 ? 1 : dtype == DT_F16 ? 2 : 3; }
+// Parts that hold x (exactly: x itself, or three of bf16) and h (16 bits of it,
+// or 24, in bf16, which has the range).
+constexpr int moe_x_parts(int dtype) { return dtype == DT_F32 ? 3 : 1; }
 constexpr int moe_h_parts(int dtype) { return dtype == DT_F32 ? 3 : 2; }
 
-// The projections' launchers, one instance file a number of parts.
-hipError_t launch_moe_up_1(const MoeArgs& a, const MoeWork& w);
-hipError_t launch_moe_up_2(const MoeArgs& a, const MoeWork& w);
-hipError_t launch_moe_up_3(const MoeArgs& a, const MoeWork& w);
-hipError_t launch_moe_down_2(const MoeArgs& a, const MoeWork& w);
-hipError_t launch_moe_down_3(const MoeArgs& a, const MoeWork& w);
+// The projections' launchers, one instance file a type.
+hipError_t launch_moe_up_bf16(const MoeArgs& a, const MoeWork& w);
+hipError_t launch_moe_up_f16(const MoeArgs& a, const MoeWork& w);
+hipError_t launch_moe_up_f32(const MoeArgs& a, const MoeWork& w);
+hipError_t launch_moe_down_16(const MoeArgs& a, const MoeWork& w);
+hipError_t launch_moe_down_f32(const MoeArgs& a, const MoeWork& w);
 
+// Whether weights enter the matrix cores as whole numbers c - z, or offset.
+constexpr bool moe_whole(int bits, int dtype) { return bits == 8 || dtype == DT_F32; }
 // Which of eight consecutive codes stands at place i of a matrix-core operand:
-// fields of a 32-bit word are taken from both of its halves at once.
-template <int BITS> __host__ __device__ constexpr int code_at(int i) {
-  return BITS == 4 ? i / 2 + 4 * (i % 2) : (i & 4) + (i / 2 % 2) + 2 * (i % 2);
+// offset ones are taken from both halves of a 32-bit word at once.
+template <bool WHOLE> __host__ __device__ constexpr int code_at(int i) {
+  return WHOLE ? i : i / 2 + 4 * (i % 2);
 }
-template <int BITS> __device__ __forceinline__ int place_of_code(int k) {
-  return BITS == 4 ? 2 * (k % 4) + k / 4 : (k & 4) + 2 * (k % 2) + (k / 2 % 2);
+template <bool WHOLE> __device__ __forceinline__ int place_of_code(int k) {
+  return WHOLE ? k : 2 * (k % 4) + k / 4;
 }
 
 // v as a sum of bf16 values, of 8 bits each.
@@ -92,52 +97,62 @@ __device__ __forceinline__ void swap_rows(uint32_t& a, uint32_t& b) {
   b = r[1];
 }
 
-// UP: gate and up rows, to h; else the down projection, to out.  PARTS bf16
-// parts of the input.  NS blocks a step of 64 bytes (1 also where a block is
+// UP: gate and up rows, to h; else the down projection, to out.  PARTS parts of
+// the input, of XDT (16-bit).  NS blocks a step of 64 bytes (1 also where a block is
 // longer).  RT tiles of 16 tokens at once.
-template <bool UP, int BITS, int PARTS, int H_PARTS, int SDT, int NS, int RT>
+template <bool UP, int XDT, int BITS, int PARTS, int H_PARTS, int SDT, bool ZP, int NS, int RT>
 __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kernel(MoeArgs a, MoeWork w,
                                                                                   int tiles) {
+  constexpr bool WHOLE = moe_whole(BITS, PARTS == 3 ? DT_F32 : DT_BF16);
   constexpr int CODES = 64 * 8 / BITS, UNITS = CODES / 32;   // a step's, 32 a unit
-  constexpr int HALVES = BITS == 4 && NS == 8 ? 2 : BITS == 8 && NS == 4 ? 2 : 1;  // blocks of 16: two a unit
-  constexpr int FIELDS = BITS / 4;
-  constexpr float FIELD0 = BITS == 4 ? 16.f : 272.f;
-  constexpr bool AHEAD = RT * PARTS <= 2;    // x is loaded a step ahead, too
+  constexpr int HALVES = NS == 2 * UNITS ? 2 : 1;            // blocks of 16: two a unit
+  constexpr int PER = HALVES == 2 ? 1 : UNITS / NS;          // units a block
+  constexpr bool EARLY = RT * PARTS <= 2;    // a step's inputs fit beside its weights
+  constexpr int S_WORDS = (NS * (SDT == DT_F32 ? 4 : 2) + 3) / 4;
+  constexpr int Z_BYTES = (NS * BITS + 7) / 8;
+  // 1 and 16 of XDT, twice, and the place of a code's lowest bit in 16 + code.
+  constexpr uint32_t ONE = XDT == DT_BF16 ? 0x3F803F80u : 0x3C003C00u;
+  constexpr uint32_t OFFSET = XDT == DT_BF16 ? 0x41804180u : 0x4C004C00u;
+  constexpr int PLACE = XDT == DT_BF16 ? 3 : 6;
   using ST = typename dt<SDT>::T;
-  using V8 = typename MfmaOp<DT_BF16>::V;
+  using Op = MfmaOp<XDT>;
+  using V8 = typename Op::V;
 
   const int tile = blockIdx.x % tiles, number = blockIdx.x / tiles;
   if (number >= *w.n_active) return;
   const MoeActive act = w.active[number];
   const MoeProj& m = UP ? a.up : a.down;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l15 = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int width = UP ? a.inter : a.hidden;   // outputs
   const int n0 = tile * (UP ? 16 : 32);
 
   __shared__ float part_sum[MOE_WAVES][8][64];
   __shared__ float total[8][64];
 
-  // Rows of the weights; those past the last one are read as it and dropped.
-  const uint8_t* codes[2];
-  const ST* scales[2];
-  const uint8_t* zps[2];
+  // The expert's weights (the host keeps their offsets below 2^31), and this
+  // lane's rows; those past the last one are read as it and dropped.
+  const int64_t first = (int64_t)act.expert * m.rows;
+  const char* const codes = (const char*)m.codes + first * m.row_bytes;
+  const char* const scales = m.scales + first * m.blocks * (int64_t)sizeof(ST);
+  const char* const zps = (const char*)m.zp + first * m.zp_row_bytes;
+  uint32_t row[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     int n = n0 + l15 + (UP ? 0 : 16 * t);
     n = n < width ? n : width - 1;
-    const int64_t row = (int64_t)act.expert * m.rows + (UP ? t * a.inter + n : n);
-    codes[t] = m.codes + row * m.row_bytes;
-    scales[t] = (const ST*)m.scales + row * m.blocks;
-    zps[t] = m.zp ? m.zp + row * m.zp_row_bytes : nullptr;
+    row[t] = UP ? t * a.inter + n : n;
   }
-  const int row_bytes = (int)m.row_bytes, blocks = m.blocks;
+  const uint32_t row_bytes = (uint32_t)m.row_bytes, zp_row_bytes = (uint32_t)m.zp_row_bytes;
+  const int blocks = m.blocks;
   const int log_block = 31 - __builtin_clz(a.block);
   const int steps = (m.cols + CODES - 1) / CODES;
+  const int whole_steps = min(row_bytes / 64u, (uint32_t)steps);
   const int x_cols = UP ? w.x_cols : w.h_cols;
   const int64_t x_part = (int64_t)(UP ? a.tokens : a.tokens * a.top_k) * x_cols;
   // Which eight of a unit's 32 codes a lane holds after the swaps.
   const int chunk = BITS == 4 ? g : (g >> 1) | (g & 1) << 1;
-  const V8 ones = __builtin_bit_cast(V8, u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+  const V8 ones = __builtin_bit_cast(V8, ONE * u32x4{1u, 1u, 1u, 1u});
 
   for (int r0 = 0; r0 < act.count; r0 += 16 * RT) {
     // Row r of a tile is token (r % 4) * 4 + r / 4, so that up to four tokens
@@ -151,61 +166,56 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
       x[rt] = (UP ? w.x + (int64_t)(pair / a.top_k) * x_cols : w.h + (int64_t)pair * x_cols) + 8 * chunk;
     }
 
-    auto load_x = [&](int step, int unit, int rt, int p) {
-      return *(const u32x4*)(x[rt] + p * x_part + step * CODES + 32 * unit);
-    };
+    // A step's weights: 16 bytes of each row, its scales and zero points.
     struct Raw {
       u32x4 c[2];
-      ST s[2][NS];
-      uint32_t z[2];
-      u32x4 x[AHEAD ? RT : 1][AHEAD ? PARTS : 1][AHEAD ? UNITS : 1];
+      uint32_t s[2][S_WORDS], z[2];
     };
-    auto load = [&](int step, Raw& d) {
+    // WHOLE_STEP: all of its blocks are the row's.  Nothing here goes by a branch,
+    // which would have a wave wait for loads ahead with the ones that it needs.
+    auto load = [&](int step, Raw& d, auto whole) {
+      constexpr bool WHOLE_STEP = decltype(whole)::value;
+      const int b0 = (step * CODES) >> log_block;
+      const uint32_t at = step * 64 + 16 * g, byte = b0 * BITS / 8;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         // Codes past a row's end meet zeros of x: any will do.
-        const int at = step * 64 + 16 * g;
-        if constexpr (BITS == 4 && NS == 8) {
+        const uint32_t from = row[t] * row_bytes;
+        if constexpr (WHOLE_STEP) {
+          __builtin_memcpy(&d.c[t], codes + (from + at), 16);
+        } else if constexpr (BITS == 4 && NS == 8) {
           u32x2 lo, hi;
-          __builtin_memcpy(&lo, codes[t] + (at < row_bytes - 8 ? at : row_bytes - 8), 8);
-          __builtin_memcpy(&hi, codes[t] + (at + 8 < row_bytes - 8 ? at + 8 : row_bytes - 8), 8);
+          __builtin_memcpy(&lo, codes + (from + min(at, row_bytes - 8)), 8);
+          __builtin_memcpy(&hi, codes + (from + min(at + 8, row_bytes - 8)), 8);
           d.c[t] = u32x4{lo[0], lo[1], hi[0], hi[1]};
         } else {
-          d.c[t] = *(const u32x4*)(codes[t] + (at < row_bytes - 16 ? at : row_bytes - 16));
+          d.c[t] = *(const u32x4*)(codes + (from + min(at, row_bytes - 16)));
         }
-        const int b0 = (step * CODES) >> log_block;
-        if (NS == 1 || b0 + NS <= blocks) {
-          __builtin_memcpy(d.s[t], scales[t] + b0, sizeof(d.s[t]));
+        const uint32_t s_from = row[t] * blocks;
+        if constexpr (WHOLE_STEP) {
+          d.s[t][0] = 0;
+          __builtin_memcpy(d.s[t], scales + (s_from + b0) * (uint32_t)sizeof(ST), NS * sizeof(ST));
         } else {
 #pragma unroll
-          for (int b = 0; b < NS; ++b) d.s[t][b] = scales[t][b0 + b < blocks ? b0 + b : blocks - 1];
-        }
-        if (m.zp) {
-          if constexpr (NS * BITS <= 8) {
-            const int byte = BITS == 4 ? b0 >> 1 : b0;
-            d.z[t] = zps[t][byte];
-            if (BITS == 4 && NS == 1) d.z[t] >>= 4 * (b0 & 1);
-          } else if (b0 + NS <= blocks) {
-            d.z[t] = 0;
-            __builtin_memcpy(&d.z[t], zps[t] + b0 * BITS / 8, NS * BITS / 8);
-          } else {
-            d.z[t] = 0;
-            const int last = (int)m.zp_row_bytes - 1;
+          for (int k = 0; k < S_WORDS; ++k) d.s[t][k] = 0;
 #pragma unroll
-            for (int b = 0; b < NS * BITS / 8; ++b) {
-              const int byte = b0 * BITS / 8 + b;
-              d.z[t] |= (uint32_t)zps[t][byte < last ? byte : last] << (8 * b);
-            }
+          for (int b = 0; b < NS; ++b) {
+            uint32_t v = 0;
+            __builtin_memcpy(&v, scales + (s_from + min(b0 + b, blocks - 1)) * (uint32_t)sizeof(ST), sizeof(ST));
+            d.s[t][b * sizeof(ST) / 4] |= v << (8 * (b * sizeof(ST) % 4));
           }
         }
-      }
-      if constexpr (AHEAD) {
+        if constexpr (ZP) {
+          const uint32_t z_from = row[t] * zp_row_bytes;
+          d.z[t] = 0;
+          if constexpr (WHOLE_STEP) {
+            __builtin_memcpy(&d.z[t], zps + (z_from + byte), Z_BYTES);
+          } else {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-            for (int u = 0; u < UNITS; ++u) d.x[rt][p][u] = load_x(step, u, rt, p);
+            for (int b = 0; b < Z_BYTES; ++b)
+              d.z[t] |= (uint32_t)(uint8_t)zps[z_from + min(byte + b, zp_row_bytes - 1)] << (8 * b);
+          }
+        }
       }
     };
 
@@ -215,79 +225,114 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) out[t][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+    auto x_at = [&](int step, int u, int rt, int p) {
+      return *(const u32x4*)(x[rt] + p * x_part + step * CODES + 32 * u);
+    };
+    struct Inputs {
+      u32x4 v[EARLY ? UNITS : 1][RT][PARTS];
+    };
+    auto load_x = [&](int step, Inputs& in) {
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) in.v[EARLY ? u : 0][rt][p] = x_at(step, u, rt, p);
+    };
+
     // RESULTS of a lane's four are wanted.
-    auto compute = [&](int step, Raw& d, auto results) {
+    auto compute = [&](int step, const Raw& d, const Inputs& in, auto results) {
       constexpr int RESULTS = decltype(results)::value;
+      constexpr f32x4 ZERO = {0.f, 0.f, 0.f, 0.f};
+      uint32_t c[2][4];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        uint32_t c[4] = {d.c[t][0], d.c[t][1], d.c[t][2], d.c[t][3]};
-        swap_halves(c[0], c[2]);
-        swap_halves(c[1], c[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[t][i] = d.c[t][i];
+        swap_halves(c[t][0], c[t][2]);
+        swap_halves(c[t][1], c[t][3]);
         if constexpr (BITS == 4) {
-          swap_rows(c[0], c[1]);
-          swap_rows(c[2], c[3]);
+          swap_rows(c[t][0], c[t][1]);
+          swap_rows(c[t][2], c[t][3]);
         }
-        d.c[t] = u32x4{c[0], c[1], c[2], c[3]};
       }
-      constexpr f32x4 ZERO = {0.f, 0.f, 0.f, 0.f};
-      constexpr int PER = HALVES == 2 ? 1 : UNITS / NS;    // units a block
-      f32x4 acc[HALVES][2][FIELDS][RT], xs[HALVES][RT];
+      auto zero = [&](int t, int b) {
+        const int odd = BITS == 4 && NS == 1 ? 4 * ((step * CODES) >> log_block & 1) : 0;
+        return ZP ? (float)(d.z[t] >> (BITS * b + odd) & ((1u << BITS) - 1u)) : (float)(1 << (BITS - 1));
+      };
+      // Eight of a unit's codes, as bf16.
+      auto weights = [&](int t, int u) {
+        u32x4 v;
+        if constexpr (WHOLE) {
+          float z = zero(t, HALVES == 2 ? 2 * u : u / PER);
+          if constexpr (HALVES == 2) z = chunk >> 1 ? zero(t, 2 * u + 1) : z;
+          const uint32_t word = c[t][BITS == 4 ? u : 2 * u];
+          const uint32_t lo = BITS == 4 ? word & 0x0F0F0F0Fu : 0u, hi = BITS == 4 ? word >> 4 & 0x0F0F0F0Fu : 0u;
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        V8 wt[2][FIELDS];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-          for (int f = 0; f < FIELDS; ++f) {
-            u32x4 v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // Codes at bits 3 .. 6 of each half: 16 + code in bf16.
-              const uint32_t word = BITS == 4 ? d.c[t][u] : d.c[t][2 * u + i / 2];
-              const int right = BITS == 4 ? 4 * i - 3 : 8 * (i % 2) + 4 * f - 3;
-              const uint32_t at = right < 0 ? word << -right : word >> right;
-              v[i] = (at & 0x00780078u) | 0x41804180u;
+          for (int i = 0; i < 4; ++i) {
+            float p, q;
+            if constexpr (BITS == 4) {
+              p = (float)(lo >> (8 * i) & 255u);
+              q = (float)(hi >> (8 * i) & 255u);
+            } else {
+              const uint32_t from = c[t][2 * u + i / 2] >> (16 * (i % 2));
+              p = (float)(from & 255u);
+              q = (float)(from >> 8 & 255u);
             }
-            wt[t][f] = __builtin_bit_cast(V8, v);
+            v[i] = Op::pack(p - z, q - z);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int left = PLACE - 4 * i;
+            const uint32_t at = left >= 0 ? c[t][u] << (left & 31) : c[t][u] >> (-left & 31);
+            v[i] = (at & 0x000F000Fu << PLACE) | OFFSET;
           }
         }
+        return __builtin_bit_cast(V8, v);
+      };
+      f32x4 acc[HALVES][2][RT], xs[HALVES][RT];
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        V8 wt[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) wt[t] = weights(t, u);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
           for (int p = 0; p < PARTS; ++p) {
-            u32x4 xv;
-            if constexpr (AHEAD) xv = d.x[rt][p][u];
-            else xv = load_x(step, u, rt, p);
+            const u32x4 xv = EARLY ? in.v[EARLY ? u : 0][rt][p] : x_at(step, u, rt, p);
 #pragma unroll
             for (int h = 0; h < HALVES; ++h) {
               const u32x4 mine = HALVES == 1 || (chunk >> 1) == h ? xv : u32x4{0u, 0u, 0u, 0u};
               const V8 v = __builtin_bit_cast(V8, mine);
-              const bool fresh = (HALVES == 2 || u % PER == 0) && p == 0;
-              xs[h][rt] = MfmaOp<DT_BF16>::run(v, ones, fresh ? ZERO : xs[h][rt]);
+              const bool fresh = u % PER == 0 && p == 0;
+              if constexpr (!WHOLE) xs[h][rt] = Op::run(v, ones, fresh ? ZERO : xs[h][rt]);
 #pragma unroll
               for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int f = 0; f < FIELDS; ++f)
-                  acc[h][t][f][rt] = MfmaOp<DT_BF16>::run(v, wt[t][f], fresh ? ZERO : acc[h][t][f][rt]);
+                acc[h][t][rt] = Op::run(v, wt[t], fresh ? ZERO : acc[h][t][rt]);
             }
           }
-        if (HALVES == 1 && (u + 1) % PER != 0) continue;
+        // Registers hold what one unit needs at a time.
+        __builtin_amdgcn_sched_barrier(0);
+        if ((u + 1) % PER != 0) continue;
         // The end of a block.
 #pragma unroll
         for (int h = 0; h < HALVES; ++h)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int b = HALVES == 2 ? 2 * u + h : u / PER;
-            const float s = dt<SDT>::to_f32(d.s[t][b]);
-            const float z = FIELD0 + (m.zp ? (float)(d.z[t] >> (BITS * b) & ((1u << BITS) - 1u))
-                                           : (float)(1 << (BITS - 1)));
+            const uint32_t raw = d.s[t][b * sizeof(ST) / 4] >> (8 * (b * sizeof(ST) % 4));
+            float s;
+            if constexpr (SDT == DT_F32) s = __uint_as_float(raw);
+            else s = bits16_to_f32<SDT>((uint16_t)raw);
+            const float z = 16.f + (WHOLE ? 0.f : zero(t, b));
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
               for (int i = 0; i < RESULTS; ++i) {
-                float v = acc[h][t][0][rt][i];
-                if constexpr (FIELDS == 2) v = __builtin_fmaf(16.f, acc[h][t][FIELDS - 1][rt][i], v);
-                v = __builtin_fmaf(-z, xs[h][rt][i], v);
+                float v = acc[h][t][rt][i];
+                if constexpr (!WHOLE) v = __builtin_fmaf(-z, xs[h][rt][i], v);
                 out[t][rt][i] = __builtin_fmaf(s, v, out[t][rt][i]);
               }
           }
@@ -296,12 +341,30 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
 
     auto walk = [&](auto results) {
       Raw d, next;
+      Inputs in;
       int step = wave;
-      if (step < steps) load(step, d);
-      for (; step < steps; step += MOE_WAVES) {
-        if (step + MOE_WAVES < steps) load(step + MOE_WAVES, next);
-        compute(step, d, results);
-        d = next;
+      // Opaque, or the first step's addresses would be kept in registers over
+      // all of the expert's tiles of tokens.
+      asm volatile("" : "+s"(step));
+      if (step < whole_steps) {
+        load(step, d, std::true_type{});
+        for (; step + MOE_WAVES < whole_steps; step += MOE_WAVES) {
+          // Loads are waited for in their order: inputs before weights ahead.
+          if constexpr (EARLY) load_x(step, in);
+          __builtin_amdgcn_sched_barrier(0);
+          load(step + MOE_WAVES, next, std::true_type{});
+          compute(step, d, in, results);
+          d = next;
+        }
+        if constexpr (EARLY) load_x(step, in);
+        compute(step, d, in, results);
+      }
+      if (whole_steps < steps && wave == whole_steps % MOE_WAVES) {
+        int last = whole_steps;
+        asm volatile("" : "+s"(last));
+        if constexpr (EARLY) load_x(last, in);
+        load(last, d, std::false_type{});
+        compute(last, d, in, results);
       }
     };
     if (UP && n0 >= width) {
@@ -338,7 +401,7 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
           const int64_t pair = w.order[act.start + j];
 #pragma unroll
           for (int p = 0; p < H_PARTS; ++p)
-            w.h[((int64_t)p * a.tokens * a.top_k + pair) * w.h_cols + (n & ~7) + place_of_code<BITS>(n & 7)] =
+            w.h[((int64_t)p * a.tokens * a.top_k + pair) * w.h_cols + (n & ~7) + place_of_code<WHOLE>(n & 7)] =
                 part[p];
         }
       } else if (j < act.count && n < a.hidden) {
@@ -349,35 +412,42 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
   }
 }
 
-template <bool UP, int BITS, int PARTS, int H_PARTS, int SDT, int NS>
+template <bool UP, int XDT, int BITS, int PARTS, int H_PARTS, int SDT, bool ZP, int NS>
 hipError_t launch_rows(const MoeArgs& a, const MoeWork& w) {
   const int tiles = UP ? w.h_cols / 16 : (a.hidden + 31) / 32;
   const dim3 grid((uint32_t)tiles * w.max_active);
-  if (a.tokens <= 16) moe_project_kernel<UP, BITS, PARTS, H_PARTS, SDT, NS, 1><<<grid, MOE_THREADS, 0, a.stream>>>(a, w, tiles);
-  else if (a.tokens <= 32) moe_project_kernel<UP, BITS, PARTS, H_PARTS, SDT, NS, 2><<<grid, MOE_THREADS, 0, a.stream>>>(a, w, tiles);
-  else moe_project_kernel<UP, BITS, PARTS, H_PARTS, SDT, NS, 4><<<grid, MOE_THREADS, 0, a.stream>>>(a, w, tiles);
+  if (a.tokens <= 16) moe_project_kernel<UP, XDT, BITS, PARTS, H_PARTS, SDT, ZP, NS, 1><<<grid, MOE_THREADS, 0, a.stream>>>(a, w, tiles);
+  else if (a.tokens <= 32) moe_project_kernel<UP, XDT, BITS, PARTS, H_PARTS, SDT, ZP, NS, 2><<<grid, MOE_THREADS, 0, a.stream>>>(a, w, tiles);
+  else moe_project_kernel<UP, XDT, BITS, PARTS, H_PARTS, SDT, ZP, NS, 4><<<grid, MOE_THREADS, 0, a.stream>>>(a, w, tiles);
   return hipGetLastError();
 }
 
-template <bool UP, int PARTS, int H_PARTS, int SDT>
+template <bool UP, int XDT, int PARTS, int H_PARTS, int SDT, bool ZP>
 hipError_t launch_blocks(const MoeArgs& a, const MoeWork& w) {
   if (a.bits == 4) {
-    if (a.block == 16) return launch_rows<UP, 4, PARTS, H_PARTS, SDT, 8>(a, w);
-    if (a.block == 32) return launch_rows<UP, 4, PARTS, H_PARTS, SDT, 4>(a, w);
-    if (a.block == 64) return launch_rows<UP, 4, PARTS, H_PARTS, SDT, 2>(a, w);
-    return launch_rows<UP, 4, PARTS, H_PARTS, SDT, 1>(a, w);
+    if (a.block == 16) return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 8>(a, w);
+    if (a.block == 32) return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 4>(a, w);
+    if (a.block == 64) return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 2>(a, w);
+    return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 1>(a, w);
   }
-  if (a.block == 16) return launch_rows<UP, 8, PARTS, H_PARTS, SDT, 4>(a, w);
-  if (a.block == 32) return launch_rows<UP, 8, PARTS, H_PARTS, SDT, 2>(a, w);
-  return launch_rows<UP, 8, PARTS, H_PARTS, SDT, 1>(a, w);
+  if (a.block == 16) return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 4>(a, w);
+  if (a.block == 32) return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 2>(a, w);
+  return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 1>(a, w);
 }
 
-template <bool UP, int PARTS, int H_PARTS>
+template <bool UP, int XDT, int PARTS, int H_PARTS>
 hipError_t launch_moe_project(const MoeArgs& a, const MoeWork& w) {
+  const bool zp = (UP ? a.up : a.down).zp != nullptr;
   switch (a.s_dtype) {
-    case DT_F32: return launch_blocks<UP, PARTS, H_PARTS, DT_F32>(a, w);
-    case DT_F16: return launch_blocks<UP, PARTS, H_PARTS, DT_F16>(a, w);
-    default: return launch_blocks<UP, PARTS, H_PARTS, DT_BF16>(a, w);
+    case DT_F32:
+      return zp ? launch_blocks<UP, XDT, PARTS, H_PARTS, DT_F32, true>(a, w)
+                : launch_blocks<UP, XDT, PARTS, H_PARTS, DT_F32, false>(a, w);
+    case DT_F16:
+      return zp ? launch_blocks<UP, XDT, PARTS, H_PARTS, DT_F16, true>(a, w)
+                : launch_blocks<UP, XDT, PARTS, H_PARTS, DT_F16, false>(a, w);
+    default:
+      return zp ? launch_blocks<UP, XDT, PARTS, H_PARTS, DT_BF16, true>(a, w)
+                : launch_blocks<UP, XDT, PARTS, H_PARTS, DT_BF16, false>(a, w);
   }
 }
 

@@ -141,9 +141,11 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
       uint16_t e[PARTS][8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int k = c + code_at<BITS>(j);
+        const int k = c + code_at<moe_whole(BITS, DT)>(j);
         uint16_t part[PARTS];
-        split_bf16<PARTS>(k < a.hidden ? dt<DT>::to_f32(from[k]) : 0.f, part);
+        const T v = k < a.hidden ? from[k] : T(0);
+        if constexpr (DT == DT_F32) split_bf16<PARTS>(v, part);
+        else part[0] = __builtin_bit_cast(uint16_t, v);
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) e[p][j] = part[p];
       }
@@ -218,8 +220,8 @@ hipError_t launch(const MoeArgs& a, const MoeWork& w) {
   route_kernel<DT, BITS><<<dim3(1 + stage), ROUTE_THREADS, 0, a.stream>>>(a, w);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess)
-    e = DT == DT_BF16 ? launch_moe_up_1(a, w) : DT == DT_F16 ? launch_moe_up_2(a, w) : launch_moe_up_3(a, w);
-  if (e == hipSuccess) e = DT == DT_F32 ? launch_moe_down_3(a, w) : launch_moe_down_2(a, w);
+    e = DT == DT_BF16 ? launch_moe_up_bf16(a, w) : DT == DT_F16 ? launch_moe_up_f16(a, w) : launch_moe_up_f32(a, w);
+  if (e == hipSuccess) e = DT == DT_F32 ? launch_moe_down_f32(a, w) : launch_moe_down_16(a, w);
   if (e != hipSuccess) return e;
   combine_kernel<DT><<<dim3((a.hidden + 255) / 256, a.tokens), 256, 0, a.stream>>>(a, w);
   return hipGetLastError();

@@ -146,14 +146,14 @@ def route(logits, top_k, normalize):
 
 def moe(x, experts, ids, weights, dtype):
     """(y, bound) [tokens, hidden] in 64 bits.  bound: how far a right layer may be,
-    products of x and whole codes (offset by 16 a 4-bit field) being summed in 32
+    products of x and whole numbers (4-bit codes offset by 16) being summed in 32
     bits: a block's sum and its zero point's part, scaled, then the blocks'."""
     T, H = x.shape
     x64 = x.double().numpy()
     y, bound = np.zeros((T, H)), np.zeros((T, H))
     u = 2.0 ** -23        # a step of 32 bits: sums in matrix cores may be cut, not rounded
     keep = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -16
-    field = 16 if experts.bits == 4 else 272
+    field = 16 if experts.bits == 4 and dtype != torch.float32 else 0
 
     def project(e, which, v, dv):
         c, z, s = experts.values(which, e)
