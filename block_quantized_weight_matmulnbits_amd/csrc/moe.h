@@ -3,8 +3,8 @@
 //
 // A workgroup takes 32 rows of one expert's weights (16 of the gate and the same
 // 16 of the up projection, or 32 of the down projection) for all of the expert's
-// tokens, 16 RT at a time; its eight waves split K step by step (64 bytes of
-// codes a row) and join through LDS.  Weights are read once, straight into
+// tokens, 16 RT at a time; its four waves split K step by step (128 bytes of
+// codes a row, a line of the caches) and join through LDS.  Weights are read once, straight into
 // registers, 16 bytes a lane; HBM is the bound.
 //
 // The matrix cores multiply x (an f32 one in three bf16 parts) with whole numbers,
@@ -22,6 +22,7 @@
 // x is laid out once in the order that the codes have then.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "decode.h"
@@ -30,7 +31,11 @@
 
 namespace qmm {
 
-// An expert with tokens: its pairs are order[start .. start + count).
+// Experts with more tokens are taken by the kernel of four tiles of 16.
+constexpr int MOE_FEW = 16;
+
+// An expert with tokens: its pairs are order[start .. start + count).  Experts
+// with more than MOE_FEW come first; entries without one have a count of 0.
 struct MoeActive {
   int expert, start, count, unused;
 };
@@ -40,12 +45,11 @@ struct MoeWork {
   int* ids;              // [pairs] experts, -1: none
   float* weights;        // [pairs]
   int* order;            // pairs by expert
-  MoeActive* active;     // by the expert's number
-  int* n_active;
+  MoeActive* active;     // [max_active]
   uint16_t* x;           // [parts][tokens][hidden, padded]
   uint16_t* h;           // [parts][pairs][inter, padded]: what enters the down projection
   float* out;            // [pairs][hidden]: weighted outputs of the pairs
-  int x_cols, h_cols;    // padded to 128 with zeros
+  int x_cols, h_cols;    // padded to 256 with zeros
   int max_active;        // active experts at most
 };
 
@@ -84,7 +88,7 @@ __device__ __forceinline__ void split_bf16(float v, uint16_t (&part)[PARTS]) {
 
 #ifdef __HIPCC__
 
-constexpr int MOE_WAVES = 8, MOE_THREADS = 64 * MOE_WAVES;
+constexpr int MOE_WAVES = 4, MOE_THREADS = 64 * MOE_WAVES;
 
 __device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
   const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
@@ -98,18 +102,19 @@ __device__ __forceinline__ void swap_rows(uint32_t& a, uint32_t& b) {
 }
 
 // UP: gate and up rows, to h; else the down projection, to out.  PARTS parts of
-// the input, of XDT (16-bit).  NS blocks a step of 64 bytes (1 also where a block is
+// the input, of XDT (16-bit).  NS blocks a step of 128 bytes (1 also where a block is
 // longer).  RT tiles of 16 tokens at once.
 template <bool UP, int XDT, int BITS, int PARTS, int H_PARTS, int SDT, bool ZP, int NS, int RT>
-__global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kernel(MoeArgs a, MoeWork w,
-                                                                                  int tiles) {
+__global__ __launch_bounds__(MOE_THREADS, RT == 1 && PARTS == 1 && NS <= 8 ? 3 : 2) void moe_project_kernel(MoeArgs a, MoeWork w,
+                                                                                  int tiles, int least, int most) {
   constexpr bool WHOLE = moe_whole(BITS, PARTS == 3 ? DT_F32 : DT_BF16);
-  constexpr int CODES = 64 * 8 / BITS, UNITS = CODES / 32;   // a step's, 32 a unit
+  constexpr int CODES = 128 * 8 / BITS, UNITS = CODES / 32;  // a step's, 32 a unit
+  constexpr int HALF = UNITS / 2;                            // units of 64 bytes
   constexpr int HALVES = NS == 2 * UNITS ? 2 : 1;            // blocks of 16: two a unit
   constexpr int PER = HALVES == 2 ? 1 : UNITS / NS;          // units a block
   constexpr bool EARLY = RT * PARTS <= 2;    // a step's inputs fit beside its weights
   constexpr int S_WORDS = (NS * (SDT == DT_F32 ? 4 : 2) + 3) / 4;
-  constexpr int Z_BYTES = (NS * BITS + 7) / 8;
+  constexpr int Z_BYTES = (NS * BITS + 7) / 8, Z_WORDS = (Z_BYTES + 3) / 4;
   // 1 and 16 of XDT, twice, and the place of a code's lowest bit in 16 + code.
   constexpr uint32_t ONE = XDT == DT_BF16 ? 0x3F803F80u : 0x3C003C00u;
   constexpr uint32_t OFFSET = XDT == DT_BF16 ? 0x41804180u : 0x4C004C00u;
@@ -119,8 +124,8 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
   using V8 = typename Op::V;
 
   const int tile = blockIdx.x % tiles, number = blockIdx.x / tiles;
-  if (number >= *w.n_active) return;
   const MoeActive act = w.active[number];
+  if (act.count < least || act.count > most) return;
   const MoeProj& m = UP ? a.up : a.down;
   const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -128,7 +133,6 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
   const int n0 = tile * (UP ? 16 : 32);
 
   __shared__ float part_sum[MOE_WAVES][8][64];
-  __shared__ float total[8][64];
 
   // The expert's weights (the host keeps their offsets below 2^31), and this
   // lane's rows; those past the last one are read as it and dropped.
@@ -147,7 +151,7 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
   const int blocks = m.blocks;
   const int log_block = 31 - __builtin_clz(a.block);
   const int steps = (m.cols + CODES - 1) / CODES;
-  const int whole_steps = min(row_bytes / 64u, (uint32_t)steps);
+  const int whole_steps = min(row_bytes / 128u, (uint32_t)steps);
   const int x_cols = UP ? w.x_cols : w.h_cols;
   const int64_t x_part = (int64_t)(UP ? a.tokens : a.tokens * a.top_k) * x_cols;
   // Which eight of a unit's 32 codes a lane holds after the swaps.
@@ -155,41 +159,34 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
   const V8 ones = __builtin_bit_cast(V8, ONE * u32x4{1u, 1u, 1u, 1u});
 
   for (int r0 = 0; r0 < act.count; r0 += 16 * RT) {
-    // Row r of a tile is token (r % 4) * 4 + r / 4, so that up to four tokens
-    // stand in the first of a lane's four results.
-    const uint16_t* x[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      int j = r0 + 16 * rt + (l15 % 4) * 4 + l15 / 4;
-      j = j < act.count ? j : r0;
-      const int pair = w.order[act.start + j];
-      x[rt] = (UP ? w.x + (int64_t)(pair / a.top_k) * x_cols : w.h + (int64_t)pair * x_cols) + 8 * chunk;
-    }
-
-    // A step's weights: 16 bytes of each row, its scales and zero points.
+    // A step's weights: two times 16 bytes of each row, its scales and zero points.
     struct Raw {
-      u32x4 c[2];
-      uint32_t s[2][S_WORDS], z[2];
+      u32x4 c[2][2];
+      uint32_t s[2][S_WORDS], z[2][Z_WORDS];
     };
     // WHOLE_STEP: all of its blocks are the row's.  Nothing here goes by a branch,
     // which would have a wave wait for loads ahead with the ones that it needs.
     auto load = [&](int step, Raw& d, auto whole) {
       constexpr bool WHOLE_STEP = decltype(whole)::value;
       const int b0 = (step * CODES) >> log_block;
-      const uint32_t at = step * 64 + 16 * g, byte = b0 * BITS / 8;
+      const uint32_t byte = b0 * BITS / 8;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         // Codes past a row's end meet zeros of x: any will do.
         const uint32_t from = row[t] * row_bytes;
-        if constexpr (WHOLE_STEP) {
-          __builtin_memcpy(&d.c[t], codes + (from + at), 16);
-        } else if constexpr (BITS == 4 && NS == 8) {
-          u32x2 lo, hi;
-          __builtin_memcpy(&lo, codes + (from + min(at, row_bytes - 8)), 8);
-          __builtin_memcpy(&hi, codes + (from + min(at + 8, row_bytes - 8)), 8);
-          d.c[t] = u32x4{lo[0], lo[1], hi[0], hi[1]};
-        } else {
-          d.c[t] = *(const u32x4*)(codes + (from + min(at, row_bytes - 16)));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t at = step * 128 + 64 * k + 16 * g;
+          if constexpr (WHOLE_STEP) {
+            __builtin_memcpy(&d.c[t][k], codes + (from + at), 16);
+          } else if constexpr (BITS == 4 && HALVES == 2) {
+            u32x2 lo, hi;
+            __builtin_memcpy(&lo, codes + (from + min(at, row_bytes - 8)), 8);
+            __builtin_memcpy(&hi, codes + (from + min(at + 8, row_bytes - 8)), 8);
+            d.c[t][k] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+          } else {
+            d.c[t][k] = *(const u32x4*)(codes + (from + min(at, row_bytes - 16)));
+          }
         }
         const uint32_t s_from = row[t] * blocks;
         if constexpr (WHOLE_STEP) {
@@ -207,17 +204,37 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
         }
         if constexpr (ZP) {
           const uint32_t z_from = row[t] * zp_row_bytes;
-          d.z[t] = 0;
+#pragma unroll
+          for (int k = 0; k < Z_WORDS; ++k) d.z[t][k] = 0;
           if constexpr (WHOLE_STEP) {
-            __builtin_memcpy(&d.z[t], zps + (z_from + byte), Z_BYTES);
+            __builtin_memcpy(d.z[t], zps + (z_from + byte), Z_BYTES);
           } else {
 #pragma unroll
             for (int b = 0; b < Z_BYTES; ++b)
-              d.z[t] |= (uint32_t)(uint8_t)zps[z_from + min(byte + b, zp_row_bytes - 1)] << (8 * b);
+              d.z[t][b / 4] |= (uint32_t)(uint8_t)zps[z_from + min(byte + b, zp_row_bytes - 1)] << (8 * (b % 4));
           }
         }
       }
     };
+
+    // The first step is on its way before anything else is looked up.
+    Raw d;
+    // Opaque, or its addresses would be kept in registers over all of the expert's
+    // tiles of tokens.
+    int own = wave;
+    asm volatile("" : "+s"(own));
+    if (own < whole_steps) load(own, d, std::true_type{});
+
+    // Row r of a tile is token (r % 4) * 4 + r / 4, so that up to four tokens
+    // stand in the first of a lane's four results.
+    const uint16_t* x[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      int j = r0 + 16 * rt + (l15 % 4) * 4 + l15 / 4;
+      j = j < act.count ? j : r0;
+      const int pair = w.order[act.start + j];
+      x[rt] = (UP ? w.x + (int64_t)(pair / a.top_k) * x_cols : w.h + (int64_t)pair * x_cols) + 8 * chunk;
+    }
 
     f32x4 out[2][RT];
 #pragma unroll
@@ -245,20 +262,9 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
       constexpr int RESULTS = decltype(results)::value;
       constexpr f32x4 ZERO = {0.f, 0.f, 0.f, 0.f};
       uint32_t c[2][4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c[t][i] = d.c[t][i];
-        swap_halves(c[t][0], c[t][2]);
-        swap_halves(c[t][1], c[t][3]);
-        if constexpr (BITS == 4) {
-          swap_rows(c[t][0], c[t][1]);
-          swap_rows(c[t][2], c[t][3]);
-        }
-      }
       auto zero = [&](int t, int b) {
         const int odd = BITS == 4 && NS == 1 ? 4 * ((step * CODES) >> log_block & 1) : 0;
-        return ZP ? (float)(d.z[t] >> (BITS * b + odd) & ((1u << BITS) - 1u)) : (float)(1 << (BITS - 1));
+        return ZP ? (float)(d.z[t][b * BITS / 32] >> (BITS * b % 32 + odd) & ((1u << BITS) - 1u)) : (float)(1 << (BITS - 1));
       };
       // Eight of a unit's codes, as bf16.
       auto weights = [&](int t, int u) {
@@ -266,7 +272,7 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
         if constexpr (WHOLE) {
           float z = zero(t, HALVES == 2 ? 2 * u : u / PER);
           if constexpr (HALVES == 2) z = chunk >> 1 ? zero(t, 2 * u + 1) : z;
-          const uint32_t word = c[t][BITS == 4 ? u : 2 * u];
+          const uint32_t word = c[t][BITS == 4 ? u % HALF : 2 * (u % HALF)];
           const uint32_t lo = BITS == 4 ? word & 0x0F0F0F0Fu : 0u, hi = BITS == 4 ? word >> 4 & 0x0F0F0F0Fu : 0u;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -275,7 +281,7 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
               p = (float)(lo >> (8 * i) & 255u);
               q = (float)(hi >> (8 * i) & 255u);
             } else {
-              const uint32_t from = c[t][2 * u + i / 2] >> (16 * (i % 2));
+              const uint32_t from = c[t][2 * (u % HALF) + i / 2] >> (16 * (i % 2));
               p = (float)(from & 255u);
               q = (float)(from >> 8 & 255u);
             }
@@ -285,7 +291,7 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int left = PLACE - 4 * i;
-            const uint32_t at = left >= 0 ? c[t][u] << (left & 31) : c[t][u] >> (-left & 31);
+            const uint32_t at = left >= 0 ? c[t][u % HALF] << (left & 31) : c[t][u % HALF] >> (-left & 31);
             v[i] = (at & 0x000F000Fu << PLACE) | OFFSET;
           }
         }
@@ -294,6 +300,19 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
       f32x4 acc[HALVES][2][RT], xs[HALVES][RT];
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
+        if (u % HALF == 0) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[t][i] = d.c[t][u / HALF][i];
+            swap_halves(c[t][0], c[t][2]);
+            swap_halves(c[t][1], c[t][3]);
+            if constexpr (BITS == 4) {
+              swap_rows(c[t][0], c[t][1]);
+              swap_rows(c[t][2], c[t][3]);
+            }
+          }
+        }
         V8 wt[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) wt[t] = weights(t, u);
@@ -340,18 +359,14 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
     };
 
     auto walk = [&](auto results) {
-      Raw d, next;
       Inputs in;
-      int step = wave;
-      // Opaque, or the first step's addresses would be kept in registers over
-      // all of the expert's tiles of tokens.
-      asm volatile("" : "+s"(step));
+      int step = own;
       if (step < whole_steps) {
-        load(step, d, std::true_type{});
         for (; step + MOE_WAVES < whole_steps; step += MOE_WAVES) {
           // Loads are waited for in their order: inputs before weights ahead.
           if constexpr (EARLY) load_x(step, in);
           __builtin_amdgcn_sched_barrier(0);
+          Raw next;
           load(step + MOE_WAVES, next, std::true_type{});
           compute(step, d, in, results);
           d = next;
@@ -384,29 +399,30 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
 #pragma unroll
         for (int i = 0; i < 4; ++i) part_sum[wave][4 * t + i][lane] = out[t][rt][i];
       __syncthreads();
-      float v = 0.f;
+      float v[2] = {0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < MOE_WAVES; ++k) v += part_sum[k][wave][lane];
-      // This thread's sum: tile wave / 4, result wave % 4.
-      const int j = r0 + 16 * rt + (wave % 4) * 4 + g;
-      const int n = n0 + l15 + (UP ? 0 : 16 * (wave / 4));
+      for (int k = 0; k < MOE_WAVES; ++k) {
+        v[0] += part_sum[k][wave][lane];
+        v[1] += part_sum[k][4 + wave][lane];
+      }
+      // This thread's sums: result `wave` of both tiles.
+      const int j = r0 + 16 * rt + wave * 4 + g, n = n0 + l15;
+      if (j >= act.count) continue;
+      const int pair = w.order[act.start + j];
       if constexpr (UP) {
-        total[wave][lane] = v;
-        __syncthreads();
-        if (wave < 4 && j < act.count && n < w.h_cols) {
-          const float up = total[4 + wave][lane];
-          const float h = n < a.inter ? v / (1.f + expf(-v)) * up : 0.f;
-          uint16_t part[H_PARTS];
-          split_bf16<H_PARTS>(h, part);
-          const int64_t pair = w.order[act.start + j];
+        if (n >= w.h_cols) continue;
+        const float h = n < a.inter ? v[0] / (1.f + expf(-v[0])) * v[1] : 0.f;
+        uint16_t part[H_PARTS];
+        split_bf16<H_PARTS>(h, part);
 #pragma unroll
-          for (int p = 0; p < H_PARTS; ++p)
-            w.h[((int64_t)p * a.tokens * a.top_k + pair) * w.h_cols + (n & ~7) + place_of_code<WHOLE>(n & 7)] =
-                part[p];
-        }
-      } else if (j < act.count && n < a.hidden) {
-        const int pair = w.order[act.start + j];
-        w.out[(int64_t)pair * a.hidden + n] = v * w.weights[pair];
+        for (int p = 0; p < H_PARTS; ++p)
+          w.h[((int64_t)p * a.tokens * a.top_k + pair) * w.h_cols + (n & ~7) + place_of_code<WHOLE>(n & 7)] =
+              part[p];
+      } else {
+        const float weight = w.weights[pair];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (n + 16 * t < a.hidden) w.out[(int64_t)pair * a.hidden + n + 16 * t] = v[t] * weight;
       }
     }
   }
@@ -415,24 +431,35 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 ? 4 : 2) void moe_project_kern
 template <bool UP, int XDT, int BITS, int PARTS, int H_PARTS, int SDT, bool ZP, int NS>
 hipError_t launch_rows(const MoeArgs& a, const MoeWork& w) {
   const int tiles = UP ? w.h_cols / 16 : (a.hidden + 31) / 32;
-  const dim3 grid((uint32_t)tiles * w.max_active);
-  if (a.tokens <= 16) moe_project_kernel<UP, XDT, BITS, PARTS, H_PARTS, SDT, ZP, NS, 1><<<grid, MOE_THREADS, 0, a.stream>>>(a, w, tiles);
-  else if (a.tokens <= 32) moe_project_kernel<UP, XDT, BITS, PARTS, H_PARTS, SDT, ZP, NS, 2><<<grid, MOE_THREADS, 0, a.stream>>>(a, w, tiles);
-  else moe_project_kernel<UP, XDT, BITS, PARTS, H_PARTS, SDT, ZP, NS, 4><<<grid, MOE_THREADS, 0, a.stream>>>(a, w, tiles);
+  // Experts with many tokens come first among the active ones, and can be no
+  // more than `many`.
+  const int many = a.tokens > MOE_FEW ? std::min(w.max_active, a.tokens * a.top_k / (MOE_FEW + 1)) : 0;
+  if (many > 0)
+    moe_project_kernel<UP, XDT, BITS, PARTS, H_PARTS, SDT, ZP, NS, 4>
+        <<<dim3((uint32_t)tiles * many), MOE_THREADS, 0, a.stream>>>(a, w, tiles, MOE_FEW + 1, INT32_MAX);
+  moe_project_kernel<UP, XDT, BITS, PARTS, H_PARTS, SDT, ZP, NS, 1>
+      <<<dim3((uint32_t)tiles * w.max_active), MOE_THREADS, 0, a.stream>>>(a, w, tiles, 1,
+                                                                          many > 0 ? MOE_FEW : INT32_MAX);
   return hipGetLastError();
 }
 
 template <bool UP, int XDT, int PARTS, int H_PARTS, int SDT, bool ZP>
 hipError_t launch_blocks(const MoeArgs& a, const MoeWork& w) {
   if (a.bits == 4) {
-    if (a.block == 16) return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 8>(a, w);
-    if (a.block == 32) return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 4>(a, w);
-    if (a.block == 64) return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 2>(a, w);
-    return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 1>(a, w);
+    switch (a.block) {
+      case 16: return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 16>(a, w);
+      case 32: return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 8>(a, w);
+      case 64: return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 4>(a, w);
+      case 128: return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 2>(a, w);
+      default: return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 1>(a, w);
+    }
   }
-  if (a.block == 16) return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 4>(a, w);
-  if (a.block == 32) return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 2>(a, w);
-  return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 1>(a, w);
+  switch (a.block) {
+    case 16: return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 8>(a, w);
+    case 32: return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 4>(a, w);
+    case 64: return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 2>(a, w);
+    default: return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 1>(a, w);
+  }
 }
 
 template <bool UP, int XDT, int PARTS, int H_PARTS>

@@ -12,7 +12,7 @@ constexpr int ROUTE_THREADS = 1024, ROUTE_WAVES = ROUTE_THREADS / 64;
 constexpr int MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP_K;
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
-int padded(int n) { return (n + 127) / 128 * 128; }
+int padded(int n) { return (n + 255) / 256 * 256; }
 
 // Lays the workspace out from `base` (null: only the size).
 size_t lay_out(int tokens, int hidden, int inter, int experts, int top_k, int dtype, char* base,
@@ -27,7 +27,6 @@ size_t lay_out(int tokens, int hidden, int inter, int experts, int top_k, int dt
   w->x_cols = padded(hidden);
   w->h_cols = padded(inter);
   w->max_active = (int)std::min<size_t>(experts, pairs);
-  w->n_active = (int*)take(4);
   w->ids = (int*)take(4 * pairs);
   w->weights = (float*)take(4 * pairs);
   w->order = (int*)take(4 * pairs);
@@ -66,7 +65,9 @@ __device__ __forceinline__ float wave_add(float v) {
   return v;
 }
 
-// One wave: token t's experts and their weights in lanes 0 .. top_k - 1.
+// One wave: token t's experts and their weights in lanes 0 .. top_k - 1; at most
+// 64 PER experts.
+template <int PER>
 __device__ void choose(const MoeArgs& a, int t, int lane, int* id, float* weight) {
   *id = -1;
   *weight = 0.f;
@@ -76,7 +77,6 @@ __device__ void choose(const MoeArgs& a, int t, int lane, int* id, float* weight
       *weight = a.weights[t * a.top_k + lane];
     }
   } else {
-    constexpr int PER = MOE_MAX_EXPERTS / 64;
     float v[PER];
     uint64_t best = 0;
 #pragma unroll
@@ -157,13 +157,15 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
     return;
   }
   __shared__ int ids[MAX_PAIRS];
-  __shared__ uint32_t upto[ROUTE_WAVES];
+  __shared__ uint64_t upto[ROUTE_WAVES];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int pairs = a.tokens * a.top_k;
   for (int t = wave; t < a.tokens; t += ROUTE_WAVES) {
     int id;
     float weight;
-    choose(a, t, lane, &id, &weight);
+    if (a.experts <= 64) choose<1>(a, t, lane, &id, &weight);
+    else if (a.experts <= 256) choose<4>(a, t, lane, &id, &weight);
+    else choose<MOE_MAX_EXPERTS / 64>(a, t, lane, &id, &weight);
     if (lane < a.top_k) {
       ids[t * a.top_k + lane] = id;
       w.ids[t * a.top_k + lane] = id;
@@ -173,29 +175,33 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
   __syncthreads();
   // Thread e counts expert e's pairs and lists them in order.
   const int e = threadIdx.x;
-  uint32_t count = 0;
+  int count = 0;
   if (e < a.experts)
     for (int p = 0; p < pairs; ++p) count += ids[p] == e;
-  // Pairs and active experts before this one, in one word.
-  uint32_t sum = count | (uint32_t)(count > 0) << 16;
-  const uint32_t own = sum;
+  // Pairs, active experts and those with many tokens before this one: a field
+  // of 20 bits each.
+  const uint64_t own = (uint64_t)count | (uint64_t)(count > 0) << 20 | (uint64_t)(count > MOE_FEW) << 40;
+  uint64_t sum = own;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const uint32_t v = __shfl_up(sum, o);
+    const uint64_t v = __shfl_up(sum, o);
     if (lane >= o) sum += v;
   }
   if (lane == 63) upto[wave] = sum;
   __syncthreads();
-  uint32_t before = 0, all = 0;
+  uint64_t before = 0, all = 0;
   for (int v = 0; v < ROUTE_WAVES; ++v) {
     if (v < wave) before += upto[v];
     all += upto[v];
   }
   before += sum - own;
-  if (threadIdx.x == 0) *w.n_active = (int)(all >> 16);
+  auto field = [](uint64_t v, int i) { return (int)(v >> (20 * i) & 0xFFFFFu); };
+  for (int i = field(all, 1) + threadIdx.x; i < w.max_active; i += ROUTE_THREADS)
+    w.active[i] = MoeActive{0, 0, 0, 0};
   if (count == 0) return;
-  int start = (int)(before & 0xFFFFu);
-  w.active[before >> 16] = MoeActive{e, start, (int)count, 0};
+  int start = field(before, 0);
+  const int many = field(before, 2), few = field(before, 1) - many;
+  w.active[count > MOE_FEW ? many : field(all, 2) + few] = MoeActive{e, start, count, 0};
   for (int p = 0; p < pairs; ++p)
     if (ids[p] == e) w.order[start++] = p;
 }
