@@ -3,11 +3,12 @@
 //
 // A workgroup takes 32 rows of one expert's weights (16 of the gate and the same
 // 16 of the up projection, or 32 of the down projection) for all of the expert's
-// tokens, 16 RT at a time; its four waves split K step by step (128 bytes of
+// tokens, up to 16 RT at a time; its four waves split K step by step (128 bytes of
 // codes a row, a line of the caches) and join through LDS.  Weights are read once, straight into
 // registers, 16 bytes a lane; HBM is the bound.
 //
-// The matrix cores multiply x (an f32 one in three bf16 parts) with whole numbers,
+// The matrix cores multiply x (an f32 one in three bf16 parts, h in two or three:
+// a row each, so that few tokens fill the instruction's 16) with whole numbers,
 // so that weights are not rounded, and a block's sum is scaled in fp32.  A 4-bit
 // code c is the 16-bit value 16 + c (one shift and one and-or for two codes); what the 16 and the
 // zero point add to a block's sum is (16 + z) times the sum of x over the block,
@@ -31,11 +32,8 @@
 
 namespace qmm {
 
-// Experts with more tokens are taken by the kernel of four tiles of 16.
-constexpr int MOE_FEW = 16;
-
-// An expert with tokens: its pairs are order[start .. start + count).  Experts
-// with more than MOE_FEW come first; entries without one have a count of 0.
+// An expert with tokens: its pairs are order[start .. start + count).  The ones
+// with the most come first; entries without any have a count of 0.
 struct MoeActive {
   int expert, start, count, unused;
 };
@@ -58,12 +56,21 @@ struct MoeWork {
 constexpr int moe_x_parts(int dtype) { return dtype == DT_F32 ? 3 : 1; }
 constexpr int moe_h_parts(int dtype) { return dtype == DT_F32 ? 3 : 2; }
 
-// The projections' launchers, one instance file a type.
-hipError_t launch_moe_up_bf16(const MoeArgs& a, const MoeWork& w);
-hipError_t launch_moe_up_f16(const MoeArgs& a, const MoeWork& w);
-hipError_t launch_moe_up_f32(const MoeArgs& a, const MoeWork& w);
-hipError_t launch_moe_down_16(const MoeArgs& a, const MoeWork& w);
-hipError_t launch_moe_down_f32(const MoeArgs& a, const MoeWork& w);
+// One of the layer's two projections.
+struct MoeSide {
+  bool up;               // gate and up rows, to h; else the down projection, to out
+  int tiles;             // workgroups an expert
+  int parts, h_parts;    // of an input; of what goes to h
+  const uint16_t* x;     // inputs: [parts][tokens or pairs][x_cols]
+  int64_t x_part, h_part;  // elements of a part
+  int x_cols;
+};
+// One instance file each: 16-bit inputs and 4-bit codes, offset; whole numbers.
+hipError_t launch_moe_bf16(const MoeArgs& a, const MoeWork& w, const MoeSide& side);
+hipError_t launch_moe_f16(const MoeArgs& a, const MoeWork& w, const MoeSide& side);
+hipError_t launch_moe_whole4_bf16(const MoeArgs& a, const MoeWork& w, const MoeSide& side);
+hipError_t launch_moe_whole8_bf16(const MoeArgs& a, const MoeWork& w, const MoeSide& side);
+hipError_t launch_moe_whole8_f16(const MoeArgs& a, const MoeWork& w, const MoeSide& side);
 
 // Whether weights enter the matrix cores as whole numbers c - z, or offset.
 constexpr bool moe_whole(int bits, int dtype) { return bits == 8 || dtype == DT_F32; }
@@ -101,18 +108,16 @@ __device__ __forceinline__ void swap_rows(uint32_t& a, uint32_t& b) {
   b = r[1];
 }
 
-// UP: gate and up rows, to h; else the down projection, to out.  PARTS parts of
-// the input, of XDT (16-bit).  NS blocks a step of 128 bytes (1 also where a block is
-// longer).  RT tiles of 16 tokens at once.
-template <bool UP, int XDT, int BITS, int PARTS, int H_PARTS, int SDT, bool ZP, int NS, int RT>
-__global__ __launch_bounds__(MOE_THREADS, RT == 1 && PARTS == 1 && NS <= 8 ? 3 : 2) void moe_project_kernel(MoeArgs a, MoeWork w,
-                                                                                  int tiles, int least, int most) {
-  constexpr bool WHOLE = moe_whole(BITS, PARTS == 3 ? DT_F32 : DT_BF16);
+// Inputs of XDT (16-bit).  WHOLE: weights enter as c - z.  NS blocks a step of 128
+// bytes (1 also where a block is longer).  RT tiles of 16 rows of inputs at once.
+template <int XDT, int BITS, bool WHOLE, int SDT, bool ZP, int NS, int RT>
+__global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_project_kernel(
+    MoeArgs a, MoeWork w, MoeSide side, int least, int most) {
   constexpr int CODES = 128 * 8 / BITS, UNITS = CODES / 32;  // a step's, 32 a unit
   constexpr int HALF = UNITS / 2;                            // units of 64 bytes
   constexpr int HALVES = NS == 2 * UNITS ? 2 : 1;            // blocks of 16: two a unit
   constexpr int PER = HALVES == 2 ? 1 : UNITS / NS;          // units a block
-  constexpr bool EARLY = RT * PARTS <= 2;    // a step's inputs fit beside its weights
+  constexpr bool EARLY = RT == 1;            // a step's inputs fit beside its weights
   constexpr int S_WORDS = (NS * (SDT == DT_F32 ? 4 : 2) + 3) / 4;
   constexpr int Z_BYTES = (NS * BITS + 7) / 8, Z_WORDS = (Z_BYTES + 3) / 4;
   // 1 and 16 of XDT, twice, and the place of a code's lowest bit in 16 + code.
@@ -123,14 +128,15 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && PARTS == 1 && NS <= 8 ? 3 :
   using Op = MfmaOp<XDT>;
   using V8 = typename Op::V;
 
-  const int tile = blockIdx.x % tiles, number = blockIdx.x / tiles;
+  const int tile = blockIdx.x % side.tiles, number = blockIdx.x / side.tiles;
   const MoeActive act = w.active[number];
   if (act.count < least || act.count > most) return;
-  const MoeProj& m = UP ? a.up : a.down;
+  const bool up = side.up;
+  const MoeProj& m = up ? a.up : a.down;
   const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int width = UP ? a.inter : a.hidden;   // outputs
-  const int n0 = tile * (UP ? 16 : 32);
+  const int width = up ? a.inter : a.hidden;   // outputs
+  const int n0 = tile * (up ? 16 : 32);
 
   __shared__ float part_sum[MOE_WAVES][8][64];
 
@@ -143,22 +149,26 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && PARTS == 1 && NS <= 8 ? 3 :
   uint32_t row[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    int n = n0 + l15 + (UP ? 0 : 16 * t);
+    int n = n0 + l15 + (up ? 0 : 16 * t);
     n = n < width ? n : width - 1;
-    row[t] = UP ? t * a.inter + n : n;
+    row[t] = up ? t * a.inter + n : n;
   }
   const uint32_t row_bytes = (uint32_t)m.row_bytes, zp_row_bytes = (uint32_t)m.zp_row_bytes;
   const int blocks = m.blocks;
   const int log_block = 31 - __builtin_clz(a.block);
   const int steps = (m.cols + CODES - 1) / CODES;
   const int whole_steps = min(row_bytes / 128u, (uint32_t)steps);
-  const int x_cols = UP ? w.x_cols : w.h_cols;
-  const int64_t x_part = (int64_t)(UP ? a.tokens : a.tokens * a.top_k) * x_cols;
+  const int parts = side.parts, fit = 16 / parts;   // tokens of a tile
   // Which eight of a unit's 32 codes a lane holds after the swaps.
   const int chunk = BITS == 4 ? g : (g >> 1) | (g & 1) << 1;
   const V8 ones = __builtin_bit_cast(V8, ONE * u32x4{1u, 1u, 1u, 1u});
 
-  for (int r0 = 0; r0 < act.count; r0 += 16 * RT) {
+  // An and-or takes one scalar operand at most.
+  uint32_t mask = 0x000F000Fu << PLACE, offset = OFFSET;
+  asm("" : "+s"(mask));
+  asm("" : "+v"(offset));
+
+  for (int r0 = 0; r0 < act.count; r0 += fit * RT) {
     // A step's weights: two times 16 bytes of each row, its scales and zero points.
     struct Raw {
       u32x4 c[2][2];
@@ -225,15 +235,19 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && PARTS == 1 && NS <= 8 ? 3 :
     asm volatile("" : "+s"(own));
     if (own < whole_steps) load(own, d, std::true_type{});
 
-    // Row r of a tile is token (r % 4) * 4 + r / 4, so that up to four tokens
-    // stand in the first of a lane's four results.
+    // A token takes a row for each of its parts.  Row r of a tile is place (r % 4) *
+    // 4 + r / 4, so that the first places stand in the first of a lane's four
+    // results; places beyond the last token repeat the first.
     const uint16_t* x[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      int j = r0 + 16 * rt + (l15 % 4) * 4 + l15 / 4;
-      j = j < act.count ? j : r0;
+      const int place = (l15 % 4) * 4 + l15 / 4;
+      int j = place / parts, p = place - j * parts;
+      const bool there = j < fit && r0 + rt * fit + j < act.count;
+      j = there ? r0 + rt * fit + j : r0;
+      p = there ? p : 0;
       const int pair = w.order[act.start + j];
-      x[rt] = (UP ? w.x + (int64_t)(pair / a.top_k) * x_cols : w.h + (int64_t)pair * x_cols) + 8 * chunk;
+      x[rt] = side.x + p * side.x_part + (int64_t)(up ? pair / a.top_k : pair) * side.x_cols + 8 * chunk;
     }
 
     f32x4 out[2][RT];
@@ -242,19 +256,15 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && PARTS == 1 && NS <= 8 ? 3 :
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) out[t][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    auto x_at = [&](int step, int u, int rt, int p) {
-      return *(const u32x4*)(x[rt] + p * x_part + step * CODES + 32 * u);
-    };
+    auto x_at = [&](int step, int u, int rt) { return *(const u32x4*)(x[rt] + step * CODES + 32 * u); };
     struct Inputs {
-      u32x4 v[EARLY ? UNITS : 1][RT][PARTS];
+      u32x4 v[EARLY ? UNITS : 1][RT];
     };
     auto load_x = [&](int step, Inputs& in) {
 #pragma unroll
       for (int u = 0; u < UNITS; ++u)
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p) in.v[EARLY ? u : 0][rt][p] = x_at(step, u, rt, p);
+        for (int rt = 0; rt < RT; ++rt) in.v[EARLY ? u : 0][rt] = x_at(step, u, rt);
     };
 
     // RESULTS of a lane's four are wanted.
@@ -262,9 +272,14 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && PARTS == 1 && NS <= 8 ? 3 :
       constexpr int RESULTS = decltype(results)::value;
       constexpr f32x4 ZERO = {0.f, 0.f, 0.f, 0.f};
       uint32_t c[2][4];
-      auto zero = [&](int t, int b) {
+      auto zero_bits = [&](int t, int b) {
         const int odd = BITS == 4 && NS == 1 ? 4 * ((step * CODES) >> log_block & 1) : 0;
-        return ZP ? (float)(d.z[t][b * BITS / 32] >> (BITS * b % 32 + odd) & ((1u << BITS) - 1u)) : (float)(1 << (BITS - 1));
+        return d.z[t][b * BITS / 32] >> (BITS * b % 32 + odd) & ((1u << BITS) - 1u);
+      };
+      auto zero = [&](int t, int b) { return ZP ? (float)zero_bits(t, b) : (float)(1 << (BITS - 1)); };
+      // 16 + z: a float of 16 whose last bit is 2^-19.
+      auto zero_offset = [&](int t, int b) {
+        return ZP ? __uint_as_float(zero_bits(t, b) << 19 | 0x41800000u) : 24.f;
       };
       // Eight of a unit's codes, as bf16.
       auto weights = [&](int t, int u) {
@@ -292,7 +307,7 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && PARTS == 1 && NS <= 8 ? 3 :
           for (int i = 0; i < 4; ++i) {
             const int left = PLACE - 4 * i;
             const uint32_t at = left >= 0 ? c[t][u % HALF] << (left & 31) : c[t][u % HALF] >> (-left & 31);
-            v[i] = (at & 0x000F000Fu << PLACE) | OFFSET;
+            v[i] = (at & mask) | offset;
           }
         }
         return __builtin_bit_cast(V8, v);
@@ -317,21 +332,18 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && PARTS == 1 && NS <= 8 ? 3 :
 #pragma unroll
         for (int t = 0; t < 2; ++t) wt[t] = weights(t, u);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int rt = 0; rt < RT; ++rt) {
+          const u32x4 xv = EARLY ? in.v[EARLY ? u : 0][rt] : x_at(step, u, rt);
 #pragma unroll
-          for (int p = 0; p < PARTS; ++p) {
-            const u32x4 xv = EARLY ? in.v[EARLY ? u : 0][rt][p] : x_at(step, u, rt, p);
+          for (int h = 0; h < HALVES; ++h) {
+            const u32x4 mine = HALVES == 1 || (chunk >> 1) == h ? xv : u32x4{0u, 0u, 0u, 0u};
+            const V8 v = __builtin_bit_cast(V8, mine);
+            const bool fresh = u % PER == 0;
+            if constexpr (!WHOLE) xs[h][rt] = Op::run(v, ones, fresh ? ZERO : xs[h][rt]);
 #pragma unroll
-            for (int h = 0; h < HALVES; ++h) {
-              const u32x4 mine = HALVES == 1 || (chunk >> 1) == h ? xv : u32x4{0u, 0u, 0u, 0u};
-              const V8 v = __builtin_bit_cast(V8, mine);
-              const bool fresh = u % PER == 0 && p == 0;
-              if constexpr (!WHOLE) xs[h][rt] = Op::run(v, ones, fresh ? ZERO : xs[h][rt]);
-#pragma unroll
-              for (int t = 0; t < 2; ++t)
-                acc[h][t][rt] = Op::run(v, wt[t], fresh ? ZERO : acc[h][t][rt]);
-            }
+            for (int t = 0; t < 2; ++t) acc[h][t][rt] = Op::run(v, wt[t], fresh ? ZERO : acc[h][t][rt]);
           }
+        }
         // Registers hold what one unit needs at a time.
         __builtin_amdgcn_sched_barrier(0);
         if ((u + 1) % PER != 0) continue;
@@ -345,7 +357,7 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && PARTS == 1 && NS <= 8 ? 3 :
             float s;
             if constexpr (SDT == DT_F32) s = __uint_as_float(raw);
             else s = bits16_to_f32<SDT>((uint16_t)raw);
-            const float z = 16.f + (WHOLE ? 0.f : zero(t, b));
+            const float z = WHOLE ? 0.f : zero_offset(t, b);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -368,6 +380,7 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && PARTS == 1 && NS <= 8 ? 3 :
           __builtin_amdgcn_sched_barrier(0);
           Raw next;
           load(step + MOE_WAVES, next, std::true_type{});
+          __builtin_amdgcn_sched_barrier(0);
           compute(step, d, in, results);
           d = next;
         }
@@ -382,42 +395,51 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && PARTS == 1 && NS <= 8 ? 3 :
         compute(last, d, in, results);
       }
     };
-    if (UP && n0 >= width) {
+    const int places = (act.count - r0) * parts;
+    if (n0 >= width) {
       // Beyond the last column: zeros, which pad h.
-    } else if (RT == 1 && act.count - r0 <= 4) {
+    } else if (RT == 1 && places <= 4) {
       walk(std::integral_constant<int, 1>{});
+    } else if (RT == 1 && places <= 8) {
+      walk(std::integral_constant<int, 2>{});
     } else {
       walk(std::integral_constant<int, 4>{});
     }
 
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      if (r0 + 16 * rt >= act.count) break;
+      const int first_token = r0 + rt * fit;
+      if (first_token >= act.count) break;
       __syncthreads();
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) part_sum[wave][4 * t + i][lane] = out[t][rt][i];
       __syncthreads();
+      // This thread's sums: column l15 of both tiles for one token.
+      const int j = threadIdx.x >> 4, n = n0 + l15;
+      if (j >= fit || first_token + j >= act.count) continue;
       float v[2] = {0.f, 0.f};
+      for (int p = parts - 1; p >= 0; --p) {
+        const int place = j * parts + p, at = place % 4 * 16 + l15;
+        float s[2] = {0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < MOE_WAVES; ++k) {
-        v[0] += part_sum[k][wave][lane];
-        v[1] += part_sum[k][4 + wave][lane];
+        for (int k = 0; k < MOE_WAVES; ++k) {
+          s[0] += part_sum[k][place / 4][at];
+          s[1] += part_sum[k][4 + place / 4][at];
+        }
+        v[0] += s[0];
+        v[1] += s[1];
       }
-      // This thread's sums: result `wave` of both tiles.
-      const int j = r0 + 16 * rt + wave * 4 + g, n = n0 + l15;
-      if (j >= act.count) continue;
-      const int pair = w.order[act.start + j];
-      if constexpr (UP) {
+      const int pair = w.order[act.start + first_token + j];
+      if (up) {
         if (n >= w.h_cols) continue;
-        const float h = n < a.inter ? v[0] / (1.f + expf(-v[0])) * v[1] : 0.f;
-        uint16_t part[H_PARTS];
-        split_bf16<H_PARTS>(h, part);
-#pragma unroll
-        for (int p = 0; p < H_PARTS; ++p)
-          w.h[((int64_t)p * a.tokens * a.top_k + pair) * w.h_cols + (n & ~7) + place_of_code<WHOLE>(n & 7)] =
-              part[p];
+        float h = n < a.inter ? v[0] / (1.f + expf(-v[0])) * v[1] : 0.f;
+        uint16_t* to = w.h + (int64_t)pair * w.h_cols + (n & ~7) + place_of_code<WHOLE>(n & 7);
+        for (int p = 0; p < side.h_parts; ++p, to += side.h_part) {
+          *to = MfmaOp<DT_BF16>::round(h);
+          h -= bits16_to_f32<DT_BF16>(*to);
+        }
       } else {
         const float weight = w.weights[pair];
 #pragma unroll
@@ -428,53 +450,48 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && PARTS == 1 && NS <= 8 ? 3 :
   }
 }
 
-template <bool UP, int XDT, int BITS, int PARTS, int H_PARTS, int SDT, bool ZP, int NS>
-hipError_t launch_rows(const MoeArgs& a, const MoeWork& w) {
-  const int tiles = UP ? w.h_cols / 16 : (a.hidden + 31) / 32;
-  // Experts with many tokens come first among the active ones, and can be no
-  // more than `many`.
-  const int many = a.tokens > MOE_FEW ? std::min(w.max_active, a.tokens * a.top_k / (MOE_FEW + 1)) : 0;
+template <int XDT, int BITS, bool WHOLE, int SDT, bool ZP, int NS>
+hipError_t launch_rows(const MoeArgs& a, const MoeWork& w, const MoeSide& side) {
+  // Where an expert has more tokens than fit a tile of 16 rows, on the average,
+  // the ones with so many are taken four tiles at a time; they come first among
+  // the active ones, and are no more than `many`.  (For a few of them a tile after
+  // another costs less than the launch.)
+  const int fit = 16 / side.parts, pairs = a.tokens * a.top_k;
+  const int many = pairs > fit * a.experts ? std::min(w.max_active, pairs / (fit + 1)) : 0;
   if (many > 0)
-    moe_project_kernel<UP, XDT, BITS, PARTS, H_PARTS, SDT, ZP, NS, 4>
-        <<<dim3((uint32_t)tiles * many), MOE_THREADS, 0, a.stream>>>(a, w, tiles, MOE_FEW + 1, INT32_MAX);
-  moe_project_kernel<UP, XDT, BITS, PARTS, H_PARTS, SDT, ZP, NS, 1>
-      <<<dim3((uint32_t)tiles * w.max_active), MOE_THREADS, 0, a.stream>>>(a, w, tiles, 1,
-                                                                          many > 0 ? MOE_FEW : INT32_MAX);
+    moe_project_kernel<XDT, BITS, WHOLE, SDT, ZP, NS, 4>
+        <<<dim3((uint32_t)side.tiles * many), MOE_THREADS, 0, a.stream>>>(a, w, side, fit + 1, INT32_MAX);
+  moe_project_kernel<XDT, BITS, WHOLE, SDT, ZP, NS, 1>
+      <<<dim3((uint32_t)side.tiles * w.max_active), MOE_THREADS, 0, a.stream>>>(a, w, side, 1, many > 0 ? fit : INT32_MAX);
   return hipGetLastError();
 }
 
-template <bool UP, int XDT, int PARTS, int H_PARTS, int SDT, bool ZP>
-hipError_t launch_blocks(const MoeArgs& a, const MoeWork& w) {
-  if (a.bits == 4) {
-    switch (a.block) {
-      case 16: return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 16>(a, w);
-      case 32: return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 8>(a, w);
-      case 64: return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 4>(a, w);
-      case 128: return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 2>(a, w);
-      default: return launch_rows<UP, XDT, 4, PARTS, H_PARTS, SDT, ZP, 1>(a, w);
-    }
-  }
+template <int XDT, int BITS, bool WHOLE, int SDT, bool ZP>
+hipError_t launch_blocks(const MoeArgs& a, const MoeWork& w, const MoeSide& side) {
+  // Blocks of a step of 128 bytes.
+  constexpr int CODES = 128 * 8 / BITS;
   switch (a.block) {
-    case 16: return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 8>(a, w);
-    case 32: return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 4>(a, w);
-    case 64: return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 2>(a, w);
-    default: return launch_rows<UP, XDT, 8, PARTS, H_PARTS, SDT, ZP, 1>(a, w);
+    case 16: return launch_rows<XDT, BITS, WHOLE, SDT, ZP, CODES / 16>(a, w, side);
+    case 32: return launch_rows<XDT, BITS, WHOLE, SDT, ZP, CODES / 32>(a, w, side);
+    case 64: return launch_rows<XDT, BITS, WHOLE, SDT, ZP, CODES / 64>(a, w, side);
+    case 128: return launch_rows<XDT, BITS, WHOLE, SDT, ZP, CODES / 128>(a, w, side);
+    default: return launch_rows<XDT, BITS, WHOLE, SDT, ZP, 1>(a, w, side);
   }
 }
 
-template <bool UP, int XDT, int PARTS, int H_PARTS>
-hipError_t launch_moe_project(const MoeArgs& a, const MoeWork& w) {
-  const bool zp = (UP ? a.up : a.down).zp != nullptr;
+template <int XDT, int BITS, bool WHOLE>
+hipError_t launch_moe_scales(const MoeArgs& a, const MoeWork& w, const MoeSide& side) {
+  const bool zp = (side.up ? a.up : a.down).zp != nullptr;
   switch (a.s_dtype) {
     case DT_F32:
-      return zp ? launch_blocks<UP, XDT, PARTS, H_PARTS, DT_F32, true>(a, w)
-                : launch_blocks<UP, XDT, PARTS, H_PARTS, DT_F32, false>(a, w);
+      return zp ? launch_blocks<XDT, BITS, WHOLE, DT_F32, true>(a, w, side)
+                : launch_blocks<XDT, BITS, WHOLE, DT_F32, false>(a, w, side);
     case DT_F16:
-      return zp ? launch_blocks<UP, XDT, PARTS, H_PARTS, DT_F16, true>(a, w)
-                : launch_blocks<UP, XDT, PARTS, H_PARTS, DT_F16, false>(a, w);
+      return zp ? launch_blocks<XDT, BITS, WHOLE, DT_F16, true>(a, w, side)
+                : launch_blocks<XDT, BITS, WHOLE, DT_F16, false>(a, w, side);
     default:
-      return zp ? launch_blocks<UP, XDT, PARTS, H_PARTS, DT_BF16, true>(a, w)
-                : launch_blocks<UP, XDT, PARTS, H_PARTS, DT_BF16, false>(a, w);
+      return zp ? launch_blocks<XDT, BITS, WHOLE, DT_BF16, true>(a, w, side)
+                : launch_blocks<XDT, BITS, WHOLE, DT_BF16, false>(a, w, side);
   }
 }
 

@@ -157,7 +157,7 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
     return;
   }
   __shared__ int ids[MAX_PAIRS];
-  __shared__ uint64_t upto[ROUTE_WAVES];
+  __shared__ int upto[ROUTE_WAVES], counts[ROUTE_THREADS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int pairs = a.tokens * a.top_k;
   for (int t = wave; t < a.tokens; t += ROUTE_WAVES) {
@@ -178,30 +178,23 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
   int count = 0;
   if (e < a.experts)
     for (int p = 0; p < pairs; ++p) count += ids[p] == e;
-  // Pairs, active experts and those with many tokens before this one: a field
-  // of 20 bits each.
-  const uint64_t own = (uint64_t)count | (uint64_t)(count > 0) << 20 | (uint64_t)(count > MOE_FEW) << 40;
-  uint64_t sum = own;
+  // Pairs before this expert's.
+  int sum = count;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const uint64_t v = __shfl_up(sum, o);
+    const int v = __shfl_up(sum, o);
     if (lane >= o) sum += v;
   }
   if (lane == 63) upto[wave] = sum;
+  counts[e] = count;
   __syncthreads();
-  uint64_t before = 0, all = 0;
-  for (int v = 0; v < ROUTE_WAVES; ++v) {
-    if (v < wave) before += upto[v];
-    all += upto[v];
-  }
-  before += sum - own;
-  auto field = [](uint64_t v, int i) { return (int)(v >> (20 * i) & 0xFFFFFu); };
-  for (int i = field(all, 1) + threadIdx.x; i < w.max_active; i += ROUTE_THREADS)
-    w.active[i] = MoeActive{0, 0, 0, 0};
+  int start = sum - count;
+  for (int v = 0; v < wave; ++v) start += upto[v];
+  // The place among the active ones: after those with more.
+  int place = 0;
+  for (int o = 0; o < a.experts; ++o) place += counts[o] > count || (counts[o] == count && o < e);
+  if (e < a.experts && place < w.max_active) w.active[place] = MoeActive{e, start, count, 0};
   if (count == 0) return;
-  int start = field(before, 0);
-  const int many = field(before, 2), few = field(before, 1) - many;
-  w.active[count > MOE_FEW ? many : field(all, 2) + few] = MoeActive{e, start, count, 0};
   for (int p = 0; p < pairs; ++p)
     if (ids[p] == e) w.order[start++] = p;
 }
@@ -225,9 +218,19 @@ hipError_t launch(const MoeArgs& a, const MoeWork& w) {
   const uint32_t stage = (uint32_t)std::min<int64_t>((chunks + ROUTE_THREADS - 1) / ROUTE_THREADS, 256);
   route_kernel<DT, BITS><<<dim3(1 + stage), ROUTE_THREADS, 0, a.stream>>>(a, w);
   hipError_t e = hipGetLastError();
+  const int64_t x_part = (int64_t)a.tokens * w.x_cols, h_part = (int64_t)a.tokens * a.top_k * w.h_cols;
+  const MoeSide up{true, w.h_cols / 16, moe_x_parts(DT), moe_h_parts(DT), w.x, x_part, h_part, w.x_cols};
+  const MoeSide down{false, (a.hidden + 31) / 32, moe_h_parts(DT), 0, w.h, h_part, 0, w.h_cols};
+  // h is bf16 in every layer.
   if (e == hipSuccess)
-    e = DT == DT_BF16 ? launch_moe_up_bf16(a, w) : DT == DT_F16 ? launch_moe_up_f16(a, w) : launch_moe_up_f32(a, w);
-  if (e == hipSuccess) e = DT == DT_F32 ? launch_moe_down_f32(a, w) : launch_moe_down_16(a, w);
+    e = BITS == 8 ? (DT == DT_F16 ? launch_moe_whole8_f16(a, w, up) : launch_moe_whole8_bf16(a, w, up))
+        : DT == DT_F32 ? launch_moe_whole4_bf16(a, w, up)
+        : DT == DT_F16 ? launch_moe_f16(a, w, up)
+                       : launch_moe_bf16(a, w, up);
+  if (e == hipSuccess)
+    e = BITS == 8 ? launch_moe_whole8_bf16(a, w, down)
+        : DT == DT_F32 ? launch_moe_whole4_bf16(a, w, down)
+                       : launch_moe_bf16(a, w, down);
   if (e != hipSuccess) return e;
   combine_kernel<DT><<<dim3((a.hidden + 255) / 256, a.tokens), 256, 0, a.stream>>>(a, w);
   return hipGetLastError();

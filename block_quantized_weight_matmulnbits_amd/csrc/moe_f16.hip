@@ -1,0 +1,10 @@
+// moe_f16.hip -- experts' projections of 4-bit codes, offset, and f16 inputs.
+#include "moe.h"
+
+namespace qmm {
+
+hipError_t launch_moe_f16(const MoeArgs& a, const MoeWork& w, const MoeSide& side) {
+  return launch_moe_scales<DT_F16, 4, false>(a, w, side);
+}
+
+}  // namespace qmm
