@@ -6,32 +6,71 @@
 // top_p of K's sum; of those, the ones with w_i >= min_p.  The token is the first
 // one in the order of the indices whose running sum passes u times the whole.
 //
-// Nothing is sorted.  A threshold (the last token that is kept, as a key and an
-// index) is found digit by digit, by counts for top-k and by sums for top-p, and
-// the running sum by two passes of a row.  Sums decide which token a number
-// falls on, so weights are formed in 64 bits and added as whole numbers, of
-// which no order of addition changes a bit: w is held to 2^-SHIFT, SHIFT = 62 -
-// log2(vocab) (45 bits for 131072 tokens).
+// Sums decide which token a number falls on, so weights are formed in 64 bits and
+// added as whole numbers, of which no order of addition changes a bit: w is held
+// to 2^-SHIFT, SHIFT = 62 - log2(vocab) (45 bits for 131072 tokens).
+//
+// Nothing is sorted.  A row is cut into chunks and read three times (from HBM
+// once: a batch's logits stay in the caches): for its maximum; for how many
+// tokens, and how much weight, lie in each of 1024 buckets of their distance from
+// it, which says in which bucket top-k and top-p end; and for the sum of each
+// chunk before those buckets and a list of what is in them.  One workgroup a row
+// then finds the last token that is kept, digit by digit of (logit, index) over
+// the list, and the chunk and the token that u falls on.  The list is long only
+// where thousands of logits are nearly equal; such a row is searched as a whole.
+// Rows that fit the list are done in one launch.
+#include <algorithm>
+
 #include "decode.h"
 #include "qmm_device.h"
 
 namespace qmm {
 namespace {
 
-constexpr int THREADS = 1024, WAVES = THREADS / 64;
+constexpr int BUCKETS = 1024, PER_UNIT = 32;   // buckets of 1 / 32 of a nat
+constexpr int LIST = 4096;                     // tokens of a list
+constexpr int STEP = 2048;                     // chunks are a multiple of this
+constexpr int MAX_CHUNKS = 64;
+constexpr int64_t BATCH = 2048;                // rows that the workspace holds at once
+constexpr int PASS_THREADS = 256, LAST_THREADS = 1024, LAST_WAVES = LAST_THREADS / 64;
 
-// Orders as the values do; a NaN below all, so that it is never chosen, -0 as 0.
+// What the passes leave of a row.
+struct RowWork {
+  uint64_t first[MAX_CHUNKS];    // the place of each chunk's first token
+  uint64_t sums[MAX_CHUNKS];     // weight of each chunk's tokens before the listed ones
+  uint64_t bucket_weight[BUCKETS];
+  uint32_t bucket_count[BUCKETS];
+  uint32_t listed;               // tokens in the list
+  uint32_t unused;
+  uint32_t list[LIST];           // indices
+};
+
+// Orders as the values do; a NaN below all, so that it is never chosen.
 template <int DT>
 __device__ __forceinline__ float logit(const char* row, int i) {
   const float v = dt<DT>::to_f32(((const typename dt<DT>::T*)row)[i]);
   return v != v ? -INFINITY : v;
 }
-__device__ __forceinline__ uint32_t key_of(float v) {
-  const uint32_t b = __float_as_uint(v + 0.f);
-  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+
+// The place of a token in the order, larger first: the logit's bits (-0 as 0) in
+// the order of the values, then the index.  16-bit logits need only their own.
+constexpr int INDEX_BITS = 24;
+template <int DT> constexpr int place_bits() { return INDEX_BITS + (DT == DT_F32 ? 32 : 16); }
+template <int DT>
+__device__ __forceinline__ uint64_t place_of(float v, int i) {
+  uint32_t b;
+  if constexpr (DT == DT_F16) {
+    const uint32_t h = __builtin_bit_cast(uint16_t, (_Float16)(v + 0.f));
+    b = h & 0x8000u ? ~h & 0xFFFFu : h | 0x8000u;
+  } else {
+    b = __float_as_uint(v + 0.f);
+    b ^= (uint32_t)((int32_t)b >> 31) | 0x80000000u;
+    if (DT == DT_BF16) b >>= 16;
+  }
+  return (uint64_t)b << INDEX_BITS | (uint32_t)((1 << INDEX_BITS) - 1 - i);
 }
-__device__ __forceinline__ float value_of(uint32_t key) {
-  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+__device__ __forceinline__ int index_of(uint64_t place) {
+  return (1 << INDEX_BITS) - 1 - (int)(place & ((1 << INDEX_BITS) - 1));
 }
 
 // exp(x) for x <= 0 in 64 bits: 2^n times a Taylor polynomial of 13 terms in
@@ -60,219 +99,591 @@ __device__ __forceinline__ double exp_f64(double x) {
   return ldexp(p, (int)n);
 }
 
-// A row's settings and the weight of its tokens.
+// A row's settings and the weights of its tokens.
 struct Row {
-  double top, over_t;    // the largest logit; the temperature
-  int shift, k;
+  float top;
+  double t;
+  float per_bucket;      // buckets a unit of the logit
+  int shift, k;          // k >= vocab: all
   double p, min_p, u;
-  bool greedy;
+  bool one;              // only the first token
 
-  __device__ double weight(float l) const {
+  __device__ __forceinline__ double weight(float l) const {
     // Infinite logits share everything equally.
     if (top == INFINITY) return l == INFINITY ? 1.0 : 0.0;
-    return exp_f64(((double)l - top) / over_t);
+    return exp_f64(((double)l - (double)top) / t);
   }
-  __device__ uint64_t units(double w) const { return (uint64_t)rint(ldexp(w, shift)); }
+  __device__ __forceinline__ uint64_t units(double w) const { return (uint64_t)rint(ldexp(w, shift)); }
+  // Does not fall as the logit does: a difference and a product, both rounded.
+  __device__ __forceinline__ int bucket(float l) const {
+    if (l == top) return 0;
+    const float d = (top - l) * per_bucket;
+    return d < (float)(BUCKETS - 1) ? (int)d : BUCKETS - 1;
+  }
+  __device__ __forceinline__ bool all(int vocab) const { return k >= vocab && p >= 1.0; }
 };
+
+__device__ Row row_of(const SampleArgs& a, int64_t row, float top, int shift) {
+  Row r;
+  r.top = top;
+  const float t = a.temperature ? a.temperature[row] : 1.f;
+  const bool greedy = !(t > 0.f);
+  r.t = greedy ? 1.0 : t;
+  r.per_bucket = (float)PER_UNIT / (float)r.t;
+  r.shift = shift;
+  r.k = a.top_k ? a.top_k[row] : 0;
+  if (r.k <= 0 || r.k > a.vocab) r.k = a.vocab;
+  if (greedy) r.k = 1;
+  const float p = a.top_p ? a.top_p[row] : 1.f, m = a.min_p ? a.min_p[row] : 0.f;
+  r.p = p < 1.f ? (p > 0.f ? p : 0.0) : 1.0;
+  r.min_p = m > 0.f ? (m < 1.f ? m : 1.0) : 0.0;
+  r.u = a.uniform[row];
+  r.one = r.k == 1;
+  return r;
+}
 
 __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
+__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    const uint64_t u = __shfl_xor(v, o);
+    v = u > v ? u : v;
+  }
+  return v;
+}
+// Sum over this lane and those before it.
+__device__ __forceinline__ uint64_t wave_upto_u64(uint64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint64_t u = __shfl_up(v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
 
-struct Shared {
-  uint64_t sums[256];
-  uint64_t waves[WAVES];
-  uint64_t found, left;
-  uint32_t digit;
-  float top;
+// body(i, logit) for the tokens [begin, end) of a row, eight side by side a thread.
+template <int DT, typename Body>
+__device__ __forceinline__ void each_token(const char* row, int begin, int end, Body body) {
+  using T = typename dt<DT>::T;
+  for (int i0 = begin + (int)threadIdx.x * 8; i0 < end; i0 += PASS_THREADS * 8) {
+    T e[8];
+    if (i0 + 8 <= end) {
+      __builtin_memcpy(e, (const T*)row + i0, sizeof(e));   // at any address
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = ((const T*)row)[i0 + j < end ? i0 + j : end - 1];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v = dt<DT>::to_f32(e[j]);
+      if (i0 + j < end) body(i0 + j, v != v ? -INFINITY : v);
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ const char* row_at(const SampleArgs& a, int64_t row) {
+  return a.logits + row * a.stride * (int64_t)sizeof(typename dt<DT>::T);
+}
+// The first token of a row, from the chunks' (every wave for itself).
+__device__ __forceinline__ uint64_t first_of(const RowWork& w, int chunks) {
+  const int lane = threadIdx.x & 63;
+  return wave_max_u64(lane < chunks ? w.first[lane] : 0);
+}
+
+// The first pass: the first token of each chunk, and a clean slate.
+template <int DT>
+__global__ __launch_bounds__(PASS_THREADS) void first_kernel(SampleArgs a, RowWork* work, int chunk, int chunks) {
+  const int64_t row = blockIdx.x / chunks;
+  const int c = blockIdx.x % chunks, begin = c * chunk, end = min(begin + chunk, a.vocab);
+  RowWork& w = work[row];
+  uint64_t best = 0;
+  each_token<DT>(row_at<DT>(a, row), begin, end, [&](int i, float l) {
+    const uint64_t at = place_of<DT>(l, i);
+    best = at > best ? at : best;
+  });
+  __shared__ uint64_t waves[PASS_THREADS / 64];
+  best = wave_max_u64(best);
+  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = best;
+  for (int b = c * PASS_THREADS + threadIdx.x; b < BUCKETS; b += chunks * PASS_THREADS) {
+    w.bucket_weight[b] = 0;
+    w.bucket_count[b] = 0;
+  }
+  if (c == 0 && threadIdx.x == 0) w.listed = 0;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int v = 1; v < PASS_THREADS / 64; ++v) best = waves[v] > best ? waves[v] : best;
+    w.first[c] = best;
+  }
+}
+
+// The second pass: the buckets, where a row is filtered.
+template <int DT>
+__global__ __launch_bounds__(PASS_THREADS) void bucket_kernel(SampleArgs a, RowWork* work, int chunk, int chunks,
+                                                             int shift) {
+  const int64_t row = blockIdx.x / chunks;
+  const int c = blockIdx.x % chunks, begin = c * chunk, end = min(begin + chunk, a.vocab);
+  RowWork& w = work[row];
+  const char* logits = row_at<DT>(a, row);
+  const Row r = row_of(a, row, logit<DT>(logits, index_of(first_of(w, chunks))), shift);
+  if (r.top == -INFINITY || r.one || r.all(a.vocab)) return;
+  __shared__ uint64_t weight[BUCKETS];
+  __shared__ uint32_t count[BUCKETS];
+  for (int b = threadIdx.x; b < BUCKETS; b += PASS_THREADS) {
+    weight[b] = 0;
+    count[b] = 0;
+  }
+  __syncthreads();
+  const bool weigh = r.p < 1.0;
+  each_token<DT>(logits, begin, end, [&](int, float l) {
+    const int b = r.bucket(l);
+    atomicAdd(&count[b], 1u);
+    if (weigh) {
+      const uint64_t n = r.units(r.weight(l));
+      if (n) atomicAdd((unsigned long long*)&weight[b], (unsigned long long)n);
+    }
+  });
+  __syncthreads();
+  for (int b = threadIdx.x; b < BUCKETS; b += PASS_THREADS) {
+    if (count[b]) atomicAdd(&w.bucket_count[b], count[b]);
+    if (weight[b]) atomicAdd((unsigned long long*)&w.bucket_weight[b], (unsigned long long)weight[b]);
+  }
+}
+
+// Where top-k and top-p end, as far as the buckets tell.
+struct Ends {
+  int k_bucket;                  // top-k's (BUCKETS: it keeps all)
+  int p_from, p_upto;            // top-p's is one of these (BUCKETS: it keeps all)
+  uint64_t k_count, k_weight;    // tokens and weight before k_bucket
+  uint64_t p_weight;             // weight before p_from
+  uint64_t weight;               // of all
+  uint32_t listed;               // tokens in these buckets
+  // Kept for certain; to be looked at.
+  __device__ __forceinline__ bool before(int b) const { return b < (p_from < k_bucket ? p_from : k_bucket); }
+  __device__ __forceinline__ bool at(int b) const { return b == k_bucket || (b >= p_from && b <= p_upto); }
 };
 
-// A sum over the workgroup, for everybody.
-__device__ uint64_t group_sum(Shared& s, uint64_t v) {
-  v = wave_sum_u64(v);
+// A workgroup of `threads`; BUCKETS / 256 buckets each of its first 256 threads.
+__device__ Ends ends_of(const RowWork& w, const Row& r, int vocab) {
+  constexpr int EACH = BUCKETS / 256;
+  __shared__ uint64_t wave_n[4], wave_w[4], say[8];
+  __shared__ int where[4];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  uint64_t n[EACH], v[EACH], sum_n = 0, sum_w = 0;
+  if (t < 256) {
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+      sum_n += n[j] = w.bucket_count[t * EACH + j];
+      sum_w += v[j] = w.bucket_weight[t * EACH + j];
+    }
+  }
+  uint64_t upto_n = wave_upto_u64(sum_n, lane), upto_w = wave_upto_u64(sum_w, lane);
+  if (t < 256 && lane == 63) {
+    wave_n[wave] = upto_n;
+    wave_w[wave] = upto_w;
+  }
+  if (t < 4) where[t] = BUCKETS;
+  if (t < 8) say[t] = 0;
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) s.waves[threadIdx.x >> 6] = v;
+  uint64_t all = 0;
+  for (int k = 0; k < 4; ++k) {
+    if (k < wave) {
+      upto_n += wave_n[k];
+      upto_w += wave_w[k];
+    }
+    all += wave_w[k];
+  }
+  const uint64_t from_n = upto_n - sum_n, from_w = upto_w - sum_w;
+  // The bucket in which a running sum (of counts or weights) reaches `want`.
+  auto reach = [&](const uint64_t (&x)[EACH], uint64_t from, uint64_t upto, uint64_t want, int slot) {
+    if (t >= 256 || !(from < want && upto >= want)) return;
+    uint64_t at_n = from_n, at_w = from_w;
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+      if (from < want && from + x[j] >= want) {
+        where[slot] = t * EACH + j;
+        say[2 * slot] = at_n;
+        say[2 * slot + 1] = at_w;
+      }
+      from += x[j];
+      at_n += n[j];
+      at_w += v[j];
+    }
+  };
+  if (r.k < vocab) reach(n, from_n, upto_n, r.k, 0);
   __syncthreads();
-  uint64_t t = 0;
-  for (int w = 0; w < WAVES; ++w) t += s.waves[w];
-  return t;
+  Ends e;
+  e.k_bucket = where[0];
+  e.k_count = say[0];
+  e.k_weight = e.k_bucket < BUCKETS ? say[1] : all;
+  e.weight = all;
+  e.p_from = e.p_upto = BUCKETS;
+  e.p_weight = 0;
+  if (r.p < 1.0) {
+    // top-k's own sum lies between the weight before its bucket and with it.
+    const uint64_t most = e.k_bucket < BUCKETS ? e.k_weight + w.bucket_weight[e.k_bucket] : all;
+    const double lo = ceil(r.p * (double)e.k_weight), hi = ceil(r.p * (double)most);
+    reach(v, from_w, upto_w, lo < 1.0 ? 1 : (uint64_t)lo, 1);
+    reach(v, from_w, upto_w, hi < 1.0 ? 1 : (uint64_t)hi, 2);
+    __syncthreads();
+    e.p_from = where[1];
+    e.p_upto = where[2];
+    e.p_weight = say[3];
+  }
+  uint64_t listed = 0;
+  if (t < 256) {
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) listed += e.at(t * EACH + j) ? n[j] : 0;
+  }
+  listed = wave_sum_u64(listed);
+  __syncthreads();
+  if (t < 256 && lane == 0) wave_n[wave] = listed;
+  __syncthreads();
+  e.listed = (uint32_t)(wave_n[0] + wave_n[1] + wave_n[2] + wave_n[3]);
+  __syncthreads();
+  return e;
 }
 
-// The place of a token in the order: larger first.
-__device__ __forceinline__ uint64_t place_of(uint32_t key, int i) {
-  return (uint64_t)key << 32 | (uint32_t)~i;
+// The third pass: the weight of each chunk before the ends, and the list.
+template <int DT>
+__global__ __launch_bounds__(PASS_THREADS) void list_kernel(SampleArgs a, RowWork* work, int chunk, int chunks,
+                                                           int shift) {
+  const int64_t row = blockIdx.x / chunks;
+  const int c = blockIdx.x % chunks, begin = c * chunk, end = min(begin + chunk, a.vocab);
+  RowWork& w = work[row];
+  const char* logits = row_at<DT>(a, row);
+  const Row r = row_of(a, row, logit<DT>(logits, index_of(first_of(w, chunks))), shift);
+  if (r.top == -INFINITY || r.one) return;
+  const bool all = r.all(a.vocab);
+  Ends e;
+  if (!all) {
+    e = ends_of(w, r, a.vocab);
+    if (e.listed > LIST) return;   // the row is searched as a whole
+  }
+  uint64_t sum = 0;
+  each_token<DT>(logits, begin, end, [&](int i, float l) {
+    const int b = all ? 0 : r.bucket(l);
+    if (all || e.before(b)) {
+      const double x = r.weight(l);
+      if (x >= r.min_p) sum += r.units(x);
+    } else if (e.at(b)) {
+      // In any order: the list is a set.
+      const uint32_t at = atomicAdd(&w.listed, 1u);
+      if (at < LIST) w.list[at] = i;
+    }
+  });
+  __shared__ uint64_t waves[PASS_THREADS / 64];
+  sum = wave_sum_u64(sum);
+  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int v = 1; v < PASS_THREADS / 64; ++v) sum += waves[v];
+    w.sums[c] = sum;
+  }
 }
+
+struct Search {
+  uint64_t amounts[256];
+  uint32_t counts[256];
+  uint64_t waves[LAST_WAVES];
+  uint64_t left, last;
+  uint32_t digit, single, found;
+};
 
 // The place of the last token of the shortest beginning of the order whose
-// amounts reach `want`, among the places that are not below `from`; 0 where all
-// of them together do not.  amount(i, place): 1, or the weight.
-template <int DT, typename Amount>
-__device__ uint64_t threshold(Shared& s, const char* row, int vocab, uint64_t from, uint64_t want,
-                              Amount amount) {
+// amounts reach `want`, among the places from `from` on; 0 where all of them
+// together do not.  each(body): body(place, amount) for every token to look at.
+template <int DT, typename Each>
+__device__ uint64_t threshold(Search& s, uint64_t from, uint64_t want, Each each) {
   uint64_t prefix = 0;
-  for (int bit = 56; bit >= 0; bit -= 8) {
+  for (int bit = place_bits<DT>() - 8; bit >= 0; bit -= 8) {
     __syncthreads();
-    if (threadIdx.x < 256) s.sums[threadIdx.x] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < vocab; i += THREADS) {
-      const float l = logit<DT>(row, i);
-      const uint64_t at = place_of(key_of(l), i);
-      if (at < from || (bit < 56 && at >> (bit + 8) != prefix)) continue;
-      const uint64_t n = amount(l);
-      if (n) atomicAdd((unsigned long long*)&s.sums[at >> bit & 255], (unsigned long long)n);
+    if (threadIdx.x < 256) {
+      s.amounts[threadIdx.x] = 0;
+      s.counts[threadIdx.x] = 0;
     }
+    __syncthreads();
+    each([&](uint64_t at, uint64_t amount) {
+      if (at < from || at >> (bit + 8) != prefix || amount == 0) return;
+      atomicAdd((unsigned long long*)&s.amounts[at >> bit & 255], (unsigned long long)amount);
+      atomicAdd(&s.counts[at >> bit & 255], 1u);
+    });
     __syncthreads();
     // The digit, from the largest down, at which the amounts reach `want`.
     if (threadIdx.x < 64) {
+      const int lane = threadIdx.x;
       uint64_t own = 0, four[4];
-      for (int j = 0; j < 4; ++j) {
-        four[j] = s.sums[255 - (threadIdx.x * 4 + j)];
-        own += four[j];
-      }
-      uint64_t before = own;
-      for (int o = 1; o < 64; o <<= 1) {
-        const uint64_t v = __shfl_up(before, o);
-        if ((int)threadIdx.x >= o) before += v;
-      }
-      const uint64_t all = __shfl(before, 63);
-      before -= own;
-      if (threadIdx.x == 0) {
-        s.found = all >= want;
-      }
-      if (before < want && before + own >= want) {
-        int j = 0;
-        while (before + four[j] < want) before += four[j++];
-        s.digit = 255 - (threadIdx.x * 4 + j);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) own += four[j] = s.amounts[255 - (lane * 4 + j)];
+      const uint64_t upto = wave_upto_u64(own, lane), all = __shfl(upto, 63);
+      if (lane == 0) s.found = all >= want;
+      uint64_t before = upto - own;
+      if (before < want && upto >= want) {
+        int found = -1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (found < 0 && before + four[j] >= want) found = j;
+          if (found < 0) before += four[j];
+        }
+        s.digit = 255 - (lane * 4 + found);
         s.left = want - before;
+        s.single = s.counts[s.digit] == 1;
       }
     }
     __syncthreads();
     if (!s.found) return 0;
     prefix = prefix << 8 | s.digit;
     want = s.left;
+    if (s.single && bit > 0) {
+      // One token is left: it is the last.
+      each([&](uint64_t at, uint64_t amount) {
+        if (at >= from && at >> bit == prefix && amount != 0) s.last = at;
+      });
+      __syncthreads();
+      return s.last;
+    }
   }
   return prefix;
 }
 
-// One workgroup a row, which it reads again for every digit.
-template <int DT>
-__global__ __launch_bounds__(THREADS) void sample_row_kernel(SampleArgs a, int shift) {
-  __shared__ Shared s;
+// The last launch, a workgroup a row.  WHOLE: the only one, for rows that fit the
+// list.
+template <int DT, bool WHOLE>
+__global__ __launch_bounds__(LAST_THREADS) void last_kernel(SampleArgs a, RowWork* work, int chunk, int chunks,
+                                                           int shift) {
+  __shared__ Search s;
+  __shared__ float list[LIST];       // the logits of the listed tokens,
+  __shared__ int index[WHOLE ? 1 : LIST];   // and their indices
+  __shared__ uint64_t sums[MAX_CHUNKS];
+  __shared__ uint64_t begin_sum;
+  __shared__ int begin_chunk;
   const int64_t row = blockIdx.x;
-  const char* logits = a.logits + row * a.stride * (int64_t)sizeof(typename dt<DT>::T);
-  const int vocab = a.vocab;
+  const char* logits = row_at<DT>(a, row);
+  const int vocab = a.vocab, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 
-  uint32_t best = 0;
-  for (int i = threadIdx.x; i < vocab; i += THREADS) {
-    const uint32_t k = key_of(logit<DT>(logits, i));
-    best = k > best ? k : best;
+  uint64_t first;
+  if constexpr (WHOLE) {
+    first = 0;
+    for (int i = threadIdx.x; i < vocab; i += LAST_THREADS) {
+      const float l = logit<DT>(logits, i);
+      list[i] = l;
+      const uint64_t at = place_of<DT>(l, i);
+      first = at > first ? at : first;
+    }
+    first = wave_max_u64(first);
+    if (lane == 0) s.waves[wave] = first;
+    __syncthreads();
+    for (int v = 0; v < LAST_WAVES; ++v) first = s.waves[v] > first ? s.waves[v] : first;
+    __syncthreads();
+  } else {
+    first = first_of(work[row], chunks);
   }
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    const uint32_t v = __shfl_xor(best, o);
-    best = v > best ? v : best;
-  }
-  if ((threadIdx.x & 63) == 0) s.waves[threadIdx.x >> 6] = best;
-  __syncthreads();
-  for (int w = 0; w < WAVES; ++w) best = s.waves[w] > best ? (uint32_t)s.waves[w] : best;
-  __syncthreads();
-
-  Row r;
-  r.top = value_of(best);
-  const float t = a.temperature ? a.temperature[row] : 1.f;
-  r.greedy = !(t > 0.f);
-  r.over_t = r.greedy ? 1.0 : t;
-  r.shift = shift;
-  r.k = a.top_k ? a.top_k[row] : 0;
-  if (r.k <= 0 || r.k > vocab) r.k = vocab;
-  if (r.greedy) r.k = 1;
-  const float p = a.top_p ? a.top_p[row] : 1.f, m = a.min_p ? a.min_p[row] : 0.f;
-  r.p = p < 1.f ? (p > 0.f ? p : 0.0) : 1.0;
-  r.min_p = m > 0.f ? (m < 1.f ? m : 1.0) : 0.0;
-  r.u = a.uniform[row];
-  if (r.top == -INFINITY) {
-    // Nothing is left to choose from.
+  const Row r = row_of(a, row, logit<DT>(logits, index_of(first)), shift);
+  auto answer = [&](int token, float logprob) {
+    a.tokens[row] = token;
+    if (a.logprobs) a.logprobs[row] = logprob;
+  };
+  if (r.top == -INFINITY || r.one) {
+    // Nothing is left to choose from, or no choice.
     if (threadIdx.x == 0) {
-      a.tokens[row] = -1;
-      if (a.logprobs) a.logprobs[row] = -INFINITY;
+      if (r.top == -INFINITY) answer(-1, -INFINITY);
+      else answer(index_of(first), 0.f);
     }
     return;
   }
 
+  // The place of the last token that is kept, and the chunks' sums.
   uint64_t from = 0;
-  if (r.k < vocab)
-    from = threshold<DT>(s, logits, vocab, 0, r.k, [](float) { return (uint64_t)1; });
-  auto units = [&](float l) { return r.units(r.weight(l)); };
-  if (r.p < 1.0) {
-    uint64_t sum = 0;
-    for (int i = threadIdx.x; i < vocab; i += THREADS) {
-      const float l = logit<DT>(logits, i);
-      if (place_of(key_of(l), i) >= from) sum += units(l);
-    }
-    // A token is kept while the sum before it is below p times the whole: the
-    // last one is where the sum reaches that.
-    const double want = ceil(r.p * (double)group_sum(s, sum));
-    const uint64_t at = threshold<DT>(s, logits, vocab, from, want < 1.0 ? 1 : (uint64_t)want, units);
-    from = at > from ? at : from;
-  }
-  // Tokens that are kept, a run of the row for each wave.
-  auto kept = [&](int i, double* w) {
-    const float l = logit<DT>(logits, i);
-    if (place_of(key_of(l), i) < from) return (uint64_t)0;
-    *w = r.weight(l);
-    return *w >= r.min_p ? r.units(*w) : 0;
+  auto sum_all = [&](uint64_t v) {
+    v = wave_sum_u64(v);
+    __syncthreads();
+    if (lane == 0) s.waves[wave] = v;
+    __syncthreads();
+    uint64_t t = 0;
+    for (int k = 0; k < LAST_WAVES; ++k) t += s.waves[k];
+    return t;
   };
-  const int run = (vocab + WAVES * 64 - 1) / (WAVES * 64) * 64, lane = threadIdx.x & 63,
-            wave = threadIdx.x >> 6;
-  const int begin = wave * run, end = begin + run < vocab ? begin + run : vocab;
+  // Both filters over some tokens: every(body) calls body(i, logit) for each, of
+  // which `in` says whether a filter's end may lie there.
+  auto filter = [&](auto every, auto in_k, auto in_p, uint64_t k_want, uint64_t k_weight, uint64_t p_weight) {
+    uint64_t k_from = 0;
+    if (r.k < vocab)
+      k_from = threshold<DT>(s, 0, k_want, [&](auto body) {
+        every([&](int i, float l) {
+          if (in_k(l)) body(place_of<DT>(l, i), (uint64_t)1);
+        });
+      });
+    from = k_from;
+    if (r.p < 1.0) {
+      uint64_t sum = 0;
+      every([&](int i, float l) {
+        if (in_k(l) && place_of<DT>(l, i) >= k_from) sum += r.units(r.weight(l));
+      });
+      // A token is kept while the sum before it is below p times the whole: the
+      // last one is where the sum reaches that.
+      const double want = ceil(r.p * (double)(k_weight + sum_all(sum)));
+      const uint64_t p_from = threshold<DT>(s, k_from, (want < 1.0 ? 1 : (uint64_t)want) - p_weight, [&](auto body) {
+        every([&](int i, float l) {
+          if (in_p(l)) body(place_of<DT>(l, i), r.units(r.weight(l)));
+        });
+      });
+      from = p_from > from ? p_from : from;
+    }
+  };
+  auto always = [](float) { return true; };
+  auto whole_row = [&](auto body) {
+    for (int i = threadIdx.x; i < vocab; i += LAST_THREADS) body(i, WHOLE ? list[WHOLE ? i : 0] : logit<DT>(logits, i));
+  };
+  auto kept = [&](float l, int i, double* x) {
+    if (place_of<DT>(l, i) < from) return (uint64_t)0;
+    *x = r.weight(l);
+    return *x >= r.min_p ? r.units(*x) : 0;
+  };
+  double x;
+  int at = 0, upto = vocab;          // where the token is looked for
+  uint64_t before = 0, total = 0;
+  bool searched = WHOLE;
+  if constexpr (WHOLE) {
+    if (!r.all(vocab)) filter(whole_row, always, always, r.k, 0, 0);
+  } else {
+    RowWork& w = work[row];
+    const bool all = r.all(vocab);
+    Ends e;
+    if (!all) e = ends_of(w, r, vocab);
+    if (!all && e.listed > LIST) {
+      filter(whole_row, always, always, r.k, 0, 0);
+      searched = true;
+    } else {
+      if ((int)threadIdx.x < chunks) sums[threadIdx.x] = w.sums[threadIdx.x];
+      if (!all) {
+        const int n = (int)e.listed;
+        for (int j = threadIdx.x; j < n; j += LAST_THREADS) {
+          index[j] = w.list[j];
+          list[j] = logit<DT>(logits, index[j]);
+        }
+        __syncthreads();
+        auto listed = [&](auto body) {
+          for (int j = threadIdx.x; j < n; j += LAST_THREADS) body(index[j], list[j]);
+        };
+        // The weight that the listed tokens of top-k's bucket add to is what lies
+        // before it.
+        filter(listed, [&](float l) { return r.bucket(l) == e.k_bucket; },
+               [&](float l) { const int b = r.bucket(l); return b >= e.p_from && b <= e.p_upto; },
+               r.k - e.k_count, e.k_weight, e.p_weight);
+        listed([&](int i, float l) {
+          const uint64_t n = kept(l, i, &x);
+          if (n) atomicAdd((unsigned long long*)&sums[i / chunk], (unsigned long long)n);
+        });
+      }
+      __syncthreads();
+      // The chunk that u falls on.
+      if (wave == 0) {
+        const uint64_t own = lane < chunks ? sums[lane] : 0, upto_here = wave_upto_u64(own, lane);
+        const uint64_t everything = __shfl(upto_here, 63);
+        const double target = fmin(fmax(r.u, 0.0), 1.0 - 0x1p-53) * (double)everything;
+        const uint64_t here = __ballot((double)upto_here > target);
+        if (lane == __builtin_ctzll(here)) {
+          begin_chunk = lane;
+          begin_sum = upto_here - own;
+        }
+        if (lane == 0) s.last = everything;
+      }
+      __syncthreads();
+      at = begin_chunk * chunk;
+      upto = min(at + chunk, vocab);
+      before = begin_sum;
+      total = s.last;
+    }
+  }
+  // Tokens that are kept, a run for each wave; the first whose running sum passes
+  // u times the whole lies in one wave's.
+  const int run = (upto - at + LAST_WAVES * 64 - 1) / (LAST_WAVES * 64) * 64;
+  const int begin = at + wave * run, end = min(begin + run, upto);
+  auto token = [&](int i) { return WHOLE ? list[WHOLE ? i : 0] : logit<DT>(logits, i); };
   uint64_t sum = 0;
-  double w;
-  for (int i = begin + lane; i < end; i += 64) sum += kept(i, &w);
-  const uint64_t total = group_sum(s, sum);
-  const double target = fmin(fmax(r.u, 0.0), 1.0 - 0x1p-53) * (double)total;
-  uint64_t before = 0;
+  for (int i = begin + lane; i < end; i += 64) sum += kept(token(i), i, &x);
+  sum = wave_sum_u64(sum);
+  __syncthreads();
+  if (lane == 0) s.waves[wave] = sum;
+  __syncthreads();
+  if (searched) {
+    for (int v = 0; v < LAST_WAVES; ++v) total += s.waves[v];
+  }
   for (int v = 0; v < wave; ++v) before += s.waves[v];
-  // The first token whose running sum passes the target lies in one wave's run.
-  if (!((double)before <= target && (double)(before + s.waves[wave]) > target)) return;
+  const double target = fmin(fmax(r.u, 0.0), 1.0 - 0x1p-53) * (double)total;
+  if (!((double)before <= target && (double)(before + sum) > target)) return;
   for (int i0 = begin; i0 < end; i0 += 64) {
     const int i = i0 + lane;
-    const uint64_t own = i < end ? kept(i, &w) : 0;
-    uint64_t upto = own;
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint64_t v = __shfl_up(upto, o);
-      if (lane >= o) upto += v;
-    }
-    const uint64_t here = __ballot((double)(before + upto) > target);
+    const uint64_t upto_here = before + wave_upto_u64(i < end ? kept(token(i), i, &x) : 0, lane);
+    const uint64_t here = __ballot((double)upto_here > target);
     if (here) {
-      if (lane == __builtin_ctzll(here)) {
-        a.tokens[row] = i;
-        if (a.logprobs) a.logprobs[row] = (float)(log(w) - log(ldexp((double)total, -shift)));
-      }
+      if (lane == __builtin_ctzll(here)) answer(i, (float)(log(x) - log(ldexp((double)total, -shift))));
       return;
     }
-    before += __shfl(upto, 63);
+    before = __shfl(upto_here, 63);
   }
 }
 
+struct Cut {
+  int chunk, chunks;
+};
+// Chunks of a row: enough workgroups to fill the chip, of 2048 tokens at least.
+Cut cut_of(int64_t rows, int64_t vocab) {
+  int64_t chunks = 1024 / (rows < 1 ? 1 : rows);
+  chunks = chunks < 1 ? 1 : chunks > MAX_CHUNKS ? MAX_CHUNKS : chunks;
+  const int64_t each = (vocab + chunks - 1) / chunks;
+  const int64_t chunk = (each + STEP - 1) / STEP * STEP;
+  return {(int)chunk, (int)((vocab + chunk - 1) / chunk)};
+}
+
 template <int DT>
-hipError_t launch(const SampleArgs& a) {
+hipError_t launch(const SampleArgs& all, RowWork* work) {
   int shift = 62;
-  while (((int64_t)1 << (62 - shift)) < a.vocab) --shift;
-  sample_row_kernel<DT><<<dim3((uint32_t)a.rows), THREADS, 0, a.stream>>>(a, shift);
-  return hipGetLastError();
+  while (((int64_t)1 << (62 - shift)) < all.vocab) --shift;
+  if (all.vocab <= LIST) {
+    last_kernel<DT, true><<<dim3((uint32_t)all.rows), LAST_THREADS, 0, all.stream>>>(all, nullptr, all.vocab, 1, shift);
+    return hipGetLastError();
+  }
+  for (int64_t r0 = 0; r0 < all.rows; r0 += BATCH) {
+    SampleArgs a = all;
+    a.rows = std::min<int64_t>(BATCH, all.rows - r0);
+    a.logits += r0 * a.stride * (int64_t)sizeof(typename dt<DT>::T);
+    a.temperature = a.temperature ? a.temperature + r0 : nullptr;
+    a.top_k = a.top_k ? a.top_k + r0 : nullptr;
+    a.top_p = a.top_p ? a.top_p + r0 : nullptr;
+    a.min_p = a.min_p ? a.min_p + r0 : nullptr;
+    a.uniform += r0;
+    a.tokens += r0;
+    a.logprobs = a.logprobs ? a.logprobs + r0 : nullptr;
+    const Cut c = cut_of(a.rows, a.vocab);
+    const dim3 grid((uint32_t)(a.rows * c.chunks));
+    first_kernel<DT><<<grid, PASS_THREADS, 0, a.stream>>>(a, work, c.chunk, c.chunks);
+    if (a.top_k != nullptr || a.top_p != nullptr)
+      bucket_kernel<DT><<<grid, PASS_THREADS, 0, a.stream>>>(a, work, c.chunk, c.chunks, shift);
+    list_kernel<DT><<<grid, PASS_THREADS, 0, a.stream>>>(a, work, c.chunk, c.chunks, shift);
+    last_kernel<DT, false><<<dim3((uint32_t)a.rows), LAST_THREADS, 0, a.stream>>>(a, work, c.chunk, c.chunks, shift);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
 
-size_t sample_workspace_bytes(int64_t, int64_t) { return 256; }
+size_t sample_workspace_bytes(int64_t rows, int64_t vocab) {
+  return vocab <= LIST ? 256 : 256 + (size_t)std::min(rows, BATCH) * sizeof(RowWork);
+}
 
-hipError_t launch_sample(const SampleArgs& a, char*) {
+hipError_t launch_sample(const SampleArgs& a, char* workspace) {
+  RowWork* work = (RowWork*)workspace;
   switch (a.dtype) {
-    case DT_F32: return launch<DT_F32>(a);
-    case DT_F16: return launch<DT_F16>(a);
-    default: return launch<DT_BF16>(a);
+    case DT_F32: return launch<DT_F32>(a, work);
+    case DT_F16: return launch<DT_F16>(a, work);
+    default: return launch<DT_BF16>(a, work);
   }
 }
 

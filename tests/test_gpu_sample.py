@@ -253,3 +253,10 @@ def test_no_rows(qmm):
     z = torch.empty(0, 50, device=DEV)
     qmm.qmm_sample(z, torch.empty(0, device=DEV), torch.empty(0, dtype=torch.int32, device=DEV),
                    torch.empty(256, dtype=torch.uint8, device=DEV))
+
+
+def test_more_rows_than_the_workspace_holds_at_once(qmm):
+    z, u = draw(2500, 4200, torch.bfloat16, seed=40)
+    g = np.random.default_rng(41)
+    check(qmm, z, u, temperature=g.choice([0.0, 0.7, 1.3], 2500), top_k=g.choice([0, 5, 300], 2500),
+          top_p=g.choice([0.5, 0.95, 1.0], 2500), min_p=g.choice([0.0, 0.1], 2500))
