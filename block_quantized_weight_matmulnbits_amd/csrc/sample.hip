@@ -29,15 +29,35 @@ namespace {
 
 constexpr int BUCKETS = 1024, PER_UNIT = 32;   // buckets of 1 / 32 of a nat
 constexpr int LIST = 4096;                     // tokens of a list
-constexpr int STEP = 2048;                     // chunks are a multiple of this
-constexpr int MAX_CHUNKS = 64;
+constexpr int RANKED = 256;                    // so many are compared each with each
+constexpr int STEP = 2048;                     // tokens that a workgroup reads at once
+constexpr int MAX_TILES = 64;
 constexpr int64_t BATCH = 2048;                // rows that the workspace holds at once
 constexpr int PASS_THREADS = 256, LAST_THREADS = 1024, LAST_WAVES = LAST_THREADS / 64;
 
+// How a row is cut: tiles, of which sums are kept, and chunks of whole tiles, a
+// workgroup's in the passes.
+struct Cut {
+  int tile, tiles, chunk, chunks;
+};
+
+// Where top-k and top-p end, as far as the buckets tell.
+struct Ends {
+  int k_bucket;                  // top-k's (BUCKETS: it keeps all)
+  int p_from, p_upto;            // top-p's is one of these (BUCKETS: it keeps all)
+  uint32_t listed;               // tokens in these buckets
+  uint64_t k_count, k_weight;    // tokens and weight before k_bucket
+  uint64_t p_weight;             // weight before p_from
+  // Kept for certain; to be looked at.
+  __device__ __forceinline__ bool before(int b) const { return b < (p_from < k_bucket ? p_from : k_bucket); }
+  __device__ __forceinline__ bool at(int b) const { return b == k_bucket || (b >= p_from && b <= p_upto); }
+};
+
 // What the passes leave of a row.
 struct RowWork {
-  uint64_t first[MAX_CHUNKS];    // the place of each chunk's first token
-  uint64_t sums[MAX_CHUNKS];     // weight of each chunk's tokens before the listed ones
+  Ends ends;
+  uint64_t first[MAX_TILES];     // the place of each chunk's first token
+  uint64_t sums[MAX_TILES];      // weight of each tile's tokens before the listed ones
   uint64_t bucket_weight[BUCKETS];
   uint32_t bucket_count[BUCKETS];
   uint32_t listed;               // tokens in the list
@@ -69,21 +89,28 @@ __device__ __forceinline__ uint64_t place_of(float v, int i) {
   }
   return (uint64_t)b << INDEX_BITS | (uint32_t)((1 << INDEX_BITS) - 1 - i);
 }
+template <int DT> __device__ __forceinline__ float value_of(uint64_t place) {
+  uint32_t b = (uint32_t)(place >> INDEX_BITS);
+  if constexpr (DT == DT_F16)
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)(b & 0x8000u ? b & 0x7FFFu : ~b));
+  if (DT == DT_BF16) b <<= 16;
+  b = b & 0x80000000u ? b & 0x7FFFFFFFu : ~b;
+  return __uint_as_float(DT == DT_BF16 ? b & 0xFFFF0000u : b);
+}
 __device__ __forceinline__ int index_of(uint64_t place) {
   return (1 << INDEX_BITS) - 1 - (int)(place & ((1 << INDEX_BITS) - 1));
 }
 
-// exp(x) for x <= 0 in 64 bits: 2^n times a Taylor polynomial of 13 terms in
-// |r| <= ln 2 / 2 (its rest is below 2^-54 of the value).  Where the result would
-// leave the whole numbers' range it is 0.
-__device__ __forceinline__ double exp_f64(double x) {
+// exp(x) 2^shift for x <= 0 in 64 bits: 2^n times a Taylor polynomial of 12 terms in
+// |r| <= ln 2 / 2 (its rest is below 2^-52 of the value).  Where the result would
+// be far below 1 it is 0.
+__device__ __forceinline__ double exp_f64(double x, int shift) {
   if (!(x > -700.0)) return 0.0;
   const double n = rint(x * 1.4426950408889634074);
   // ln 2 in two parts, the first of 31 bits, so that n times it is exact.
   double r = __builtin_fma(n, -0x1.62e42ff000000p-1, x);
   r = __builtin_fma(n, 0x1.718432a1b0e26p-35, r);
-  double p = 1.0 / 6227020800.0;
-  p = __builtin_fma(p, r, 1.0 / 479001600.0);
+  double p = 1.0 / 479001600.0;
   p = __builtin_fma(p, r, 1.0 / 39916800.0);
   p = __builtin_fma(p, r, 1.0 / 3628800.0);
   p = __builtin_fma(p, r, 1.0 / 362880.0);
@@ -96,24 +123,30 @@ __device__ __forceinline__ double exp_f64(double x) {
   p = __builtin_fma(p, r, 0.5);
   p = __builtin_fma(p, r, 1.0);
   p = __builtin_fma(p, r, 1.0);
-  return ldexp(p, (int)n);
+  return ldexp(p, (int)n + shift);
 }
 
 // A row's settings and the weights of its tokens.
 struct Row {
   float top;
-  double t;
+  double over_t;         // 1 / T
   float per_bucket;      // buckets a unit of the logit
   int shift, k;          // k >= vocab: all
-  double p, min_p, u;
+  double p, min_units, u;
   bool one;              // only the first token
 
+  // The weight in units of 2^-shift, before it is rounded to a whole number.
   __device__ __forceinline__ double weight(float l) const {
     // Infinite logits share everything equally.
-    if (top == INFINITY) return l == INFINITY ? 1.0 : 0.0;
-    return exp_f64(((double)l - (double)top) / t);
+    if (top == INFINITY) return l == INFINITY ? ldexp(1.0, shift) : 0.0;
+    return exp_f64(((double)l - (double)top) * over_t, shift);
   }
-  __device__ __forceinline__ uint64_t units(double w) const { return (uint64_t)rint(ldexp(w, shift)); }
+  // The nearest whole number of a w <= 2^62: its upper and lower 32 bits.
+  static __device__ __forceinline__ uint64_t units(double w) {
+    w = rint(w);
+    const double hi = floor(w * 0x1p-32);
+    return (uint64_t)(uint32_t)hi << 32 | (uint32_t)__builtin_fma(hi, -0x1p32, w);
+  }
   // Does not fall as the logit does: a difference and a product, both rounded.
   __device__ __forceinline__ int bucket(float l) const {
     if (l == top) return 0;
@@ -128,15 +161,15 @@ __device__ Row row_of(const SampleArgs& a, int64_t row, float top, int shift) {
   r.top = top;
   const float t = a.temperature ? a.temperature[row] : 1.f;
   const bool greedy = !(t > 0.f);
-  r.t = greedy ? 1.0 : t;
-  r.per_bucket = (float)PER_UNIT / (float)r.t;
+  r.over_t = greedy ? 1.0 : 1.0 / (double)t;
+  r.per_bucket = greedy ? (float)PER_UNIT : (float)PER_UNIT / t;
   r.shift = shift;
   r.k = a.top_k ? a.top_k[row] : 0;
   if (r.k <= 0 || r.k > a.vocab) r.k = a.vocab;
   if (greedy) r.k = 1;
   const float p = a.top_p ? a.top_p[row] : 1.f, m = a.min_p ? a.min_p[row] : 0.f;
   r.p = p < 1.f ? (p > 0.f ? p : 0.0) : 1.0;
-  r.min_p = m > 0.f ? (m < 1.f ? m : 1.0) : 0.0;
+  r.min_units = ldexp(m > 0.f ? (m < 1.f ? (double)m : 1.0) : 0.0, shift);
   r.u = a.uniform[row];
   r.one = r.k == 1;
   return r;
@@ -165,22 +198,39 @@ __device__ __forceinline__ uint64_t wave_upto_u64(uint64_t v, int lane) {
   return v;
 }
 
-// body(i, logit) for the tokens [begin, end) of a row, eight side by side a thread.
-template <int DT, typename Body>
-__device__ __forceinline__ void each_token(const char* row, int begin, int end, Body body) {
+// body(i, logit) for the tokens [begin, end) of a row, eight side by side a thread,
+// and after(i0) for every STEP of them; AHEAD steps are loaded at once.
+template <int DT, int AHEAD, typename Body, typename After>
+__device__ __forceinline__ void each_token(const char* row, int begin, int end, Body body, After after) {
   using T = typename dt<DT>::T;
-  for (int i0 = begin + (int)threadIdx.x * 8; i0 < end; i0 += PASS_THREADS * 8) {
-    T e[8];
-    if (i0 + 8 <= end) {
-      __builtin_memcpy(e, (const T*)row + i0, sizeof(e));   // at any address
-    } else {
+  for (int i0 = begin; i0 < end; i0 += STEP * AHEAD) {
+    T e[AHEAD][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = ((const T*)row)[i0 + j < end ? i0 + j : end - 1];
+    for (int v = 0; v < AHEAD; ++v) {
+      const int i = i0 + v * STEP + (int)threadIdx.x * 8;
+      if (i + 8 <= end) {
+        __builtin_memcpy(e[v], (const T*)row + i, sizeof(e[v]));   // at any address
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[v][j] = ((const T*)row)[i + j < end ? i + j : end - 1];
+      }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float v = dt<DT>::to_f32(e[j]);
-      if (i0 + j < end) body(i0 + j, v != v ? -INFINITY : v);
+    for (int v = 0; v < AHEAD; ++v) {
+      const int i = i0 + v * STEP + (int)threadIdx.x * 8;
+      auto one = [&](int j) {
+        const float l = dt<DT>::to_f32(e[v][j]);
+        body(i + j, l != l ? -INFINITY : l);
+      };
+      if (i + 8 <= end) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) one(j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (i + j < end) one(j);
+      }
+      if (i0 + v * STEP < end) after(i0 + v * STEP);
     }
   }
 }
@@ -197,19 +247,22 @@ __device__ __forceinline__ uint64_t first_of(const RowWork& w, int chunks) {
 
 // The first pass: the first token of each chunk, and a clean slate.
 template <int DT>
-__global__ __launch_bounds__(PASS_THREADS) void first_kernel(SampleArgs a, RowWork* work, int chunk, int chunks) {
-  const int64_t row = blockIdx.x / chunks;
-  const int c = blockIdx.x % chunks, begin = c * chunk, end = min(begin + chunk, a.vocab);
+__global__ __launch_bounds__(PASS_THREADS) void first_kernel(SampleArgs a, RowWork* work, Cut cut) {
+  const int64_t row = blockIdx.x / cut.chunks;
+  const int c = blockIdx.x % cut.chunks, begin = c * cut.chunk, end = min(begin + cut.chunk, a.vocab);
   RowWork& w = work[row];
-  uint64_t best = 0;
-  each_token<DT>(row_at<DT>(a, row), begin, end, [&](int i, float l) {
-    const uint64_t at = place_of<DT>(l, i);
-    best = at > best ? at : best;
-  });
+  // A thread meets its tokens in their order: the first of equal ones stays.
+  float top = -INFINITY;
+  int at = begin;
+  each_token<DT, 4>(row_at<DT>(a, row), begin, end, [&](int i, float l) {
+    at = l > top ? i : at;
+    top = fmaxf(top, l);
+  }, [](int) {});
+  uint64_t best = top == -INFINITY ? place_of<DT>(top, begin) : place_of<DT>(top, at);
   __shared__ uint64_t waves[PASS_THREADS / 64];
   best = wave_max_u64(best);
   if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = best;
-  for (int b = c * PASS_THREADS + threadIdx.x; b < BUCKETS; b += chunks * PASS_THREADS) {
+  for (int b = c * PASS_THREADS + threadIdx.x; b < BUCKETS; b += cut.chunks * PASS_THREADS) {
     w.bucket_weight[b] = 0;
     w.bucket_count[b] = 0;
   }
@@ -223,13 +276,12 @@ __global__ __launch_bounds__(PASS_THREADS) void first_kernel(SampleArgs a, RowWo
 
 // The second pass: the buckets, where a row is filtered.
 template <int DT>
-__global__ __launch_bounds__(PASS_THREADS) void bucket_kernel(SampleArgs a, RowWork* work, int chunk, int chunks,
-                                                             int shift) {
-  const int64_t row = blockIdx.x / chunks;
-  const int c = blockIdx.x % chunks, begin = c * chunk, end = min(begin + chunk, a.vocab);
+__global__ __launch_bounds__(PASS_THREADS) void bucket_kernel(SampleArgs a, RowWork* work, Cut cut, int shift) {
+  const int64_t row = blockIdx.x / cut.chunks;
+  const int c = blockIdx.x % cut.chunks, begin = c * cut.chunk, end = min(begin + cut.chunk, a.vocab);
   RowWork& w = work[row];
   const char* logits = row_at<DT>(a, row);
-  const Row r = row_of(a, row, logit<DT>(logits, index_of(first_of(w, chunks))), shift);
+  const Row r = row_of(a, row, value_of<DT>(first_of(w, cut.chunks)), shift);
   if (r.top == -INFINITY || r.one || r.all(a.vocab)) return;
   __shared__ uint64_t weight[BUCKETS];
   __shared__ uint32_t count[BUCKETS];
@@ -239,14 +291,14 @@ __global__ __launch_bounds__(PASS_THREADS) void bucket_kernel(SampleArgs a, RowW
   }
   __syncthreads();
   const bool weigh = r.p < 1.0;
-  each_token<DT>(logits, begin, end, [&](int, float l) {
+  each_token<DT, 2>(logits, begin, end, [&](int, float l) {
     const int b = r.bucket(l);
     atomicAdd(&count[b], 1u);
     if (weigh) {
       const uint64_t n = r.units(r.weight(l));
       if (n) atomicAdd((unsigned long long*)&weight[b], (unsigned long long)n);
     }
-  });
+  }, [](int) {});
   __syncthreads();
   for (int b = threadIdx.x; b < BUCKETS; b += PASS_THREADS) {
     if (count[b]) atomicAdd(&w.bucket_count[b], count[b]);
@@ -254,43 +306,37 @@ __global__ __launch_bounds__(PASS_THREADS) void bucket_kernel(SampleArgs a, RowW
   }
 }
 
-// Where top-k and top-p end, as far as the buckets tell.
-struct Ends {
-  int k_bucket;                  // top-k's (BUCKETS: it keeps all)
-  int p_from, p_upto;            // top-p's is one of these (BUCKETS: it keeps all)
-  uint64_t k_count, k_weight;    // tokens and weight before k_bucket
-  uint64_t p_weight;             // weight before p_from
-  uint64_t weight;               // of all
-  uint32_t listed;               // tokens in these buckets
-  // Kept for certain; to be looked at.
-  __device__ __forceinline__ bool before(int b) const { return b < (p_from < k_bucket ? p_from : k_bucket); }
-  __device__ __forceinline__ bool at(int b) const { return b == k_bucket || (b >= p_from && b <= p_upto); }
-};
-
-// A workgroup of `threads`; BUCKETS / 256 buckets each of its first 256 threads.
+// By a workgroup of the passes, BUCKETS / 256 buckets a thread.
 __device__ Ends ends_of(const RowWork& w, const Row& r, int vocab) {
-  constexpr int EACH = BUCKETS / 256;
-  __shared__ uint64_t wave_n[4], wave_w[4], say[8];
-  __shared__ int where[4];
+  constexpr int EACH = BUCKETS / PASS_THREADS, WAVES = PASS_THREADS / 64;
+  __shared__ uint64_t wave_n[WAVES], wave_w[WAVES], say[3][3];
+  __shared__ int where[3];
+  __shared__ uint32_t listed[WAVES];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   uint64_t n[EACH], v[EACH], sum_n = 0, sum_w = 0;
-  if (t < 256) {
 #pragma unroll
-    for (int j = 0; j < EACH; ++j) {
-      sum_n += n[j] = w.bucket_count[t * EACH + j];
-      sum_w += v[j] = w.bucket_weight[t * EACH + j];
-    }
+  for (int j = 0; j < EACH; ++j) {
+    n[j] = w.bucket_count[t * EACH + j];
+    v[j] = w.bucket_weight[t * EACH + j];
+  }
+#pragma unroll
+  for (int j = 0; j < EACH; ++j) {
+    sum_n += n[j];
+    sum_w += v[j];
   }
   uint64_t upto_n = wave_upto_u64(sum_n, lane), upto_w = wave_upto_u64(sum_w, lane);
-  if (t < 256 && lane == 63) {
+  if (lane == 63) {
     wave_n[wave] = upto_n;
     wave_w[wave] = upto_w;
   }
-  if (t < 4) where[t] = BUCKETS;
-  if (t < 8) say[t] = 0;
+  if (t < 3) {
+    where[t] = BUCKETS;
+    say[t][0] = say[t][1] = say[t][2] = 0;
+  }
   __syncthreads();
   uint64_t all = 0;
-  for (int k = 0; k < 4; ++k) {
+#pragma unroll
+  for (int k = 0; k < WAVES; ++k) {
     if (k < wave) {
       upto_n += wave_n[k];
       upto_w += wave_w[k];
@@ -298,91 +344,99 @@ __device__ Ends ends_of(const RowWork& w, const Row& r, int vocab) {
     all += wave_w[k];
   }
   const uint64_t from_n = upto_n - sum_n, from_w = upto_w - sum_w;
-  // The bucket in which a running sum (of counts or weights) reaches `want`.
+  // The bucket in which a running sum (of counts or weights) reaches `want`; what
+  // lies before it, and its weight.
   auto reach = [&](const uint64_t (&x)[EACH], uint64_t from, uint64_t upto, uint64_t want, int slot) {
-    if (t >= 256 || !(from < want && upto >= want)) return;
+    if (!(from < want && upto >= want)) return;
     uint64_t at_n = from_n, at_w = from_w;
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
       if (from < want && from + x[j] >= want) {
         where[slot] = t * EACH + j;
-        say[2 * slot] = at_n;
-        say[2 * slot + 1] = at_w;
+        say[slot][0] = at_n;
+        say[slot][1] = at_w;
+        say[slot][2] = v[j];
       }
       from += x[j];
       at_n += n[j];
       at_w += v[j];
     }
   };
-  if (r.k < vocab) reach(n, from_n, upto_n, r.k, 0);
-  __syncthreads();
+  if (r.k < vocab) {
+    reach(n, from_n, upto_n, r.k, 0);
+    __syncthreads();
+  }
   Ends e;
   e.k_bucket = where[0];
-  e.k_count = say[0];
-  e.k_weight = e.k_bucket < BUCKETS ? say[1] : all;
-  e.weight = all;
+  e.k_count = say[0][0];
+  e.k_weight = e.k_bucket < BUCKETS ? say[0][1] : all;
   e.p_from = e.p_upto = BUCKETS;
   e.p_weight = 0;
   if (r.p < 1.0) {
     // top-k's own sum lies between the weight before its bucket and with it.
-    const uint64_t most = e.k_bucket < BUCKETS ? e.k_weight + w.bucket_weight[e.k_bucket] : all;
-    const double lo = ceil(r.p * (double)e.k_weight), hi = ceil(r.p * (double)most);
+    const double lo = ceil(r.p * (double)e.k_weight);
+    const double hi = ceil(r.p * (double)(e.k_bucket < BUCKETS ? e.k_weight + say[0][2] : all));
     reach(v, from_w, upto_w, lo < 1.0 ? 1 : (uint64_t)lo, 1);
     reach(v, from_w, upto_w, hi < 1.0 ? 1 : (uint64_t)hi, 2);
     __syncthreads();
     e.p_from = where[1];
     e.p_upto = where[2];
-    e.p_weight = say[3];
+    e.p_weight = say[1][1];
   }
-  uint64_t listed = 0;
-  if (t < 256) {
+  uint32_t sum = 0;
 #pragma unroll
-    for (int j = 0; j < EACH; ++j) listed += e.at(t * EACH + j) ? n[j] : 0;
-  }
-  listed = wave_sum_u64(listed);
+  for (int j = 0; j < EACH; ++j) sum += e.at(t * EACH + j) ? (uint32_t)n[j] : 0u;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
+  if (lane == 0) listed[wave] = sum;
   __syncthreads();
-  if (t < 256 && lane == 0) wave_n[wave] = listed;
-  __syncthreads();
-  e.listed = (uint32_t)(wave_n[0] + wave_n[1] + wave_n[2] + wave_n[3]);
-  __syncthreads();
+  e.listed = 0;
+#pragma unroll
+  for (int k = 0; k < WAVES; ++k) e.listed += listed[k];
   return e;
 }
 
 // The third pass: the weight of each chunk before the ends, and the list.
 template <int DT>
-__global__ __launch_bounds__(PASS_THREADS) void list_kernel(SampleArgs a, RowWork* work, int chunk, int chunks,
-                                                           int shift) {
-  const int64_t row = blockIdx.x / chunks;
-  const int c = blockIdx.x % chunks, begin = c * chunk, end = min(begin + chunk, a.vocab);
+__global__ __launch_bounds__(PASS_THREADS) void list_kernel(SampleArgs a, RowWork* work, Cut cut, int shift) {
+  const int64_t row = blockIdx.x / cut.chunks;
+  const int c = blockIdx.x % cut.chunks, begin = c * cut.chunk, end = min(begin + cut.chunk, a.vocab);
   RowWork& w = work[row];
   const char* logits = row_at<DT>(a, row);
-  const Row r = row_of(a, row, logit<DT>(logits, index_of(first_of(w, chunks))), shift);
+  const Row r = row_of(a, row, value_of<DT>(first_of(w, cut.chunks)), shift);
   if (r.top == -INFINITY || r.one) return;
   const bool all = r.all(a.vocab);
   Ends e;
   if (!all) {
     e = ends_of(w, r, a.vocab);
+    if (c == 0 && threadIdx.x == 0) w.ends = e;
     if (e.listed > LIST) return;   // the row is searched as a whole
   }
+  __shared__ uint64_t waves[MAX_TILES][PASS_THREADS / 64];
   uint64_t sum = 0;
-  each_token<DT>(logits, begin, end, [&](int i, float l) {
+  each_token<DT, 2>(logits, begin, end, [&](int i, float l) {
     const int b = all ? 0 : r.bucket(l);
     if (all || e.before(b)) {
       const double x = r.weight(l);
-      if (x >= r.min_p) sum += r.units(x);
+      if (x >= r.min_units) sum += Row::units(x);
     } else if (e.at(b)) {
       // In any order: the list is a set.
       const uint32_t at = atomicAdd(&w.listed, 1u);
       if (at < LIST) w.list[at] = i;
     }
+  }, [&](int i0) {
+    // The end of a tile, or of the row.
+    if ((i0 - begin + STEP) % cut.tile != 0 && i0 + STEP < end) return;
+    sum = wave_sum_u64(sum);
+    if ((threadIdx.x & 63) == 0) waves[(i0 - begin) / cut.tile][threadIdx.x >> 6] = sum;
+    sum = 0;
   });
-  __shared__ uint64_t waves[PASS_THREADS / 64];
-  sum = wave_sum_u64(sum);
-  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int v = 1; v < PASS_THREADS / 64; ++v) sum += waves[v];
-    w.sums[c] = sum;
+  const int t0 = begin / cut.tile, t = threadIdx.x;
+  if (t < cut.chunk / cut.tile && t0 + t < cut.tiles) {
+    uint64_t s = 0;
+    for (int v = 0; v < PASS_THREADS / 64; ++v) s += waves[t][v];
+    w.sums[t0 + t] = s;
   }
 }
 
@@ -453,14 +507,14 @@ __device__ uint64_t threshold(Search& s, uint64_t from, uint64_t want, Each each
 // The last launch, a workgroup a row.  WHOLE: the only one, for rows that fit the
 // list.
 template <int DT, bool WHOLE>
-__global__ __launch_bounds__(LAST_THREADS) void last_kernel(SampleArgs a, RowWork* work, int chunk, int chunks,
-                                                           int shift) {
+__global__ __launch_bounds__(LAST_THREADS) void last_kernel(SampleArgs a, RowWork* work, Cut cut, int shift) {
   __shared__ Search s;
   __shared__ float list[LIST];       // the logits of the listed tokens,
   __shared__ int index[WHOLE ? 1 : LIST];   // and their indices
-  __shared__ uint64_t sums[MAX_CHUNKS];
+  __shared__ uint64_t list_weight[WHOLE ? 1 : RANKED], list_place[WHOLE ? 1 : RANKED];
+  __shared__ uint64_t sums[MAX_TILES];
   __shared__ uint64_t begin_sum;
-  __shared__ int begin_chunk;
+  __shared__ int begin_tile;
   const int64_t row = blockIdx.x;
   const char* logits = row_at<DT>(a, row);
   const int vocab = a.vocab, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -480,9 +534,9 @@ __global__ __launch_bounds__(LAST_THREADS) void last_kernel(SampleArgs a, RowWor
     for (int v = 0; v < LAST_WAVES; ++v) first = s.waves[v] > first ? s.waves[v] : first;
     __syncthreads();
   } else {
-    first = first_of(work[row], chunks);
+    first = first_of(work[row], cut.chunks);
   }
-  const Row r = row_of(a, row, logit<DT>(logits, index_of(first)), shift);
+  const Row r = row_of(a, row, value_of<DT>(first), shift);
   auto answer = [&](int token, float logprob) {
     a.tokens[row] = token;
     if (a.logprobs) a.logprobs[row] = logprob;
@@ -541,7 +595,7 @@ __global__ __launch_bounds__(LAST_THREADS) void last_kernel(SampleArgs a, RowWor
   auto kept = [&](float l, int i, double* x) {
     if (place_of<DT>(l, i) < from) return (uint64_t)0;
     *x = r.weight(l);
-    return *x >= r.min_p ? r.units(*x) : 0;
+    return *x >= r.min_units ? Row::units(*x) : 0;
   };
   double x;
   int at = 0, upto = vocab;          // where the token is looked for
@@ -553,48 +607,99 @@ __global__ __launch_bounds__(LAST_THREADS) void last_kernel(SampleArgs a, RowWor
     RowWork& w = work[row];
     const bool all = r.all(vocab);
     Ends e;
-    if (!all) e = ends_of(w, r, vocab);
+    if (!all) e = w.ends;
     if (!all && e.listed > LIST) {
       filter(whole_row, always, always, r.k, 0, 0);
       searched = true;
     } else {
-      if ((int)threadIdx.x < chunks) sums[threadIdx.x] = w.sums[threadIdx.x];
+      if ((int)threadIdx.x < cut.tiles) sums[threadIdx.x] = w.sums[threadIdx.x];
       if (!all) {
         const int n = (int)e.listed;
         for (int j = threadIdx.x; j < n; j += LAST_THREADS) {
-          index[j] = w.list[j];
-          list[j] = logit<DT>(logits, index[j]);
+          const int i = w.list[j];
+          const float l = logit<DT>(logits, i);
+          index[j] = i;
+          list[j] = l;
+          if (n <= RANKED) {
+            list_place[j] = place_of<DT>(l, i);
+            list_weight[j] = Row::units(r.weight(l));
+          }
         }
+        if (threadIdx.x == 0) s.left = s.last = 0;
         __syncthreads();
         auto listed = [&](auto body) {
           for (int j = threadIdx.x; j < n; j += LAST_THREADS) body(index[j], list[j]);
         };
-        // The weight that the listed tokens of top-k's bucket add to is what lies
-        // before it.
-        filter(listed, [&](float l) { return r.bucket(l) == e.k_bucket; },
-               [&](float l) { const int b = r.bucket(l); return b >= e.p_from && b <= e.p_upto; },
-               r.k - e.k_count, e.k_weight, e.p_weight);
+        auto in_k = [&](float l) { return r.bucket(l) == e.k_bucket; };
+        auto in_p = [&](float l) { const int b = r.bucket(l); return b >= e.p_from && b <= e.p_upto; };
+        if (n <= RANKED) {
+          // Few: how many come before a token, and how much, counted one by one, by
+          // as many neighbouring threads a token as there are.
+          int group = 1;
+          while (group < 64 && 2 * group * n <= LAST_THREADS) group *= 2;
+          const int j = threadIdx.x / group, part = threadIdx.x % group;
+          const bool mine = j < n;
+          const float l = mine ? list[j] : 0.f;
+          const uint64_t own = mine ? list_place[j] : 0;
+          const bool k_mine = mine && in_k(l), p_mine = mine && in_p(l);
+          uint32_t count = 0;
+          uint64_t weight = 0;
+          for (int o = part; o < n; o += group) {
+            // Larger places lie in the same bucket or before it.
+            const bool more = list_place[o] > own;
+            count += more;
+            weight += more ? list_weight[o] : 0;
+          }
+          for (int d = 1; d < group; d <<= 1) {
+            count += __shfl_xor(count, d);
+            weight += __shfl_xor(weight, d);
+          }
+          // Of a token in top-k's bucket, those in top-p's before it were counted, too.
+          uint64_t p_count = 0;
+          if (e.k_bucket < BUCKETS && e.p_from < e.k_bucket) {
+            const bool one = mine && part == 0 && p_mine && !k_mine;
+            p_count = sum_all(one ? 1 : 0);
+          }
+          const bool k_keep = !mine ? false : k_mine ? e.k_count + count - p_count < (uint64_t)r.k : true;
+          const bool chosen = mine && part == 0;
+          const uint64_t whole = e.k_weight + sum_all(chosen && k_mine && k_keep ? list_weight[j] : 0);
+          const double want = ceil(r.p * (double)whole);
+          const uint64_t reach = want < 1.0 ? 1 : (uint64_t)want;
+          const bool keep = k_keep && (r.p < 1.0 ? p_mine && e.p_weight + weight < reach : k_mine);
+          // The last place that is kept; all that are larger are, too.
+          uint64_t least = chosen && keep ? ~own : 0, most = mine ? own : 0;
+          least = wave_max_u64(least);
+          most = wave_max_u64(most);
+          if (lane == 0) {
+            atomicMax((unsigned long long*)&s.left, (unsigned long long)least);
+            atomicMax((unsigned long long*)&s.last, (unsigned long long)most);
+          }
+          __syncthreads();
+          from = s.left ? ~s.left : s.last + 1;
+        } else {
+          filter(listed, in_k, in_p, r.k - e.k_count, e.k_weight, e.p_weight);
+        }
         listed([&](int i, float l) {
           const uint64_t n = kept(l, i, &x);
-          if (n) atomicAdd((unsigned long long*)&sums[i / chunk], (unsigned long long)n);
+          if (n) atomicAdd((unsigned long long*)&sums[i / cut.tile], (unsigned long long)n);
         });
       }
       __syncthreads();
-      // The chunk that u falls on.
+      // The tile that u falls on.
       if (wave == 0) {
-        const uint64_t own = lane < chunks ? sums[lane] : 0, upto_here = wave_upto_u64(own, lane);
+        const uint64_t own = lane < cut.tiles ? sums[lane] : 0, upto_here = wave_upto_u64(own, lane);
         const uint64_t everything = __shfl(upto_here, 63);
         const double target = fmin(fmax(r.u, 0.0), 1.0 - 0x1p-53) * (double)everything;
         const uint64_t here = __ballot((double)upto_here > target);
         if (lane == __builtin_ctzll(here)) {
-          begin_chunk = lane;
+          begin_tile = lane;
           begin_sum = upto_here - own;
         }
         if (lane == 0) s.last = everything;
       }
       __syncthreads();
-      at = begin_chunk * chunk;
-      upto = min(at + chunk, vocab);
+      at = begin_tile * cut.tile;
+      upto = min(at + cut.tile, vocab);
       before = begin_sum;
       total = s.last;
     }
@@ -621,23 +726,23 @@ __global__ __launch_bounds__(LAST_THREADS) void last_kernel(SampleArgs a, RowWor
     const uint64_t upto_here = before + wave_upto_u64(i < end ? kept(token(i), i, &x) : 0, lane);
     const uint64_t here = __ballot((double)upto_here > target);
     if (here) {
-      if (lane == __builtin_ctzll(here)) answer(i, (float)(log(x) - log(ldexp((double)total, -shift))));
+      if (lane == __builtin_ctzll(here)) answer(i, (float)(log(x) - log((double)total)));
       return;
     }
     before = __shfl(upto_here, 63);
   }
 }
 
-struct Cut {
-  int chunk, chunks;
-};
-// Chunks of a row: enough workgroups to fill the chip, of 2048 tokens at least.
+// Tiles of 2048 tokens where 64 of them hold the row.  Chunks: some four
+// workgroups a compute unit, since each has to clear, add and read the buckets.
 Cut cut_of(int64_t rows, int64_t vocab) {
-  int64_t chunks = 1024 / (rows < 1 ? 1 : rows);
-  chunks = chunks < 1 ? 1 : chunks > MAX_CHUNKS ? MAX_CHUNKS : chunks;
-  const int64_t each = (vocab + chunks - 1) / chunks;
-  const int64_t chunk = (each + STEP - 1) / STEP * STEP;
-  return {(int)chunk, (int)((vocab + chunk - 1) / chunk)};
+  Cut c;
+  c.tile = (int)((vocab + MAX_TILES * STEP - 1) / (MAX_TILES * STEP) * STEP);
+  c.tiles = (int)((vocab + c.tile - 1) / c.tile);
+  const int64_t each = std::max<int64_t>(1, rows * c.tiles / 1024);
+  c.chunk = (int)std::min<int64_t>(each, c.tiles) * c.tile;
+  c.chunks = (int)((vocab + c.chunk - 1) / c.chunk);
+  return c;
 }
 
 template <int DT>
@@ -645,7 +750,7 @@ hipError_t launch(const SampleArgs& all, RowWork* work) {
   int shift = 62;
   while (((int64_t)1 << (62 - shift)) < all.vocab) --shift;
   if (all.vocab <= LIST) {
-    last_kernel<DT, true><<<dim3((uint32_t)all.rows), LAST_THREADS, 0, all.stream>>>(all, nullptr, all.vocab, 1, shift);
+    last_kernel<DT, true><<<dim3((uint32_t)all.rows), LAST_THREADS, 0, all.stream>>>(all, nullptr, Cut{}, shift);
     return hipGetLastError();
   }
   for (int64_t r0 = 0; r0 < all.rows; r0 += BATCH) {
@@ -661,11 +766,11 @@ hipError_t launch(const SampleArgs& all, RowWork* work) {
     a.logprobs = a.logprobs ? a.logprobs + r0 : nullptr;
     const Cut c = cut_of(a.rows, a.vocab);
     const dim3 grid((uint32_t)(a.rows * c.chunks));
-    first_kernel<DT><<<grid, PASS_THREADS, 0, a.stream>>>(a, work, c.chunk, c.chunks);
+    first_kernel<DT><<<grid, PASS_THREADS, 0, a.stream>>>(a, work, c);
     if (a.top_k != nullptr || a.top_p != nullptr)
-      bucket_kernel<DT><<<grid, PASS_THREADS, 0, a.stream>>>(a, work, c.chunk, c.chunks, shift);
-    list_kernel<DT><<<grid, PASS_THREADS, 0, a.stream>>>(a, work, c.chunk, c.chunks, shift);
-    last_kernel<DT, false><<<dim3((uint32_t)a.rows), LAST_THREADS, 0, a.stream>>>(a, work, c.chunk, c.chunks, shift);
+      bucket_kernel<DT><<<grid, PASS_THREADS, 0, a.stream>>>(a, work, c, shift);
+    list_kernel<DT><<<grid, PASS_THREADS, 0, a.stream>>>(a, work, c, shift);
+    last_kernel<DT, false><<<dim3((uint32_t)a.rows), LAST_THREADS, 0, a.stream>>>(a, work, c, shift);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
