@@ -140,8 +140,10 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
 
   __shared__ float part_sum[MOE_WAVES][8][64];
 
-  // The expert's weights (the host keeps their offsets below 2^31), and this
-  // lane's rows; those past the last one are read as it and dropped.
+  // The expert's weights (the host keeps their offsets below 2^31).  Four
+  // neighbouring lanes load 64 bytes of a row side by side (lanes 16 apart, as the
+  // matrix cores want them, are each a request of their own); LDS's crossbar hands
+  // them on.  Rows past the last one are read as it and dropped.
   const int64_t first = (int64_t)act.expert * m.rows;
   const char* const codes = (const char*)m.codes + first * m.row_bytes;
   const char* const scales = m.scales + first * m.blocks * (int64_t)sizeof(ST);
@@ -149,7 +151,7 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
   uint32_t row[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    int n = n0 + l15 + (up ? 0 : 16 * t);
+    int n = n0 + lane / 4 + (up ? 0 : 16 * t);
     n = n < width ? n : width - 1;
     row[t] = up ? t * a.inter + n : n;
   }
@@ -162,6 +164,11 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
   // Which eight of a unit's 32 codes a lane holds after the swaps.
   const int chunk = BITS == 4 ? g : (g >> 1) | (g & 1) << 1;
   const V8 ones = __builtin_bit_cast(V8, ONE * u32x4{1u, 1u, 1u, 1u});
+
+  // Word i of the lane that loaded row l15's bytes from 16 g on; of any that loaded
+  // the row.
+  const int codes_from = (4 * l15 + g) * 4, row_from = 4 * l15 * 4;
+  auto hand_on = [](int from, uint32_t v) { return (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v); };
 
   // An and-or takes one scalar operand at most.
   uint32_t mask = 0x000F000Fu << PLACE, offset = OFFSET;
@@ -186,7 +193,7 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
         const uint32_t from = row[t] * row_bytes;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const uint32_t at = step * 128 + 64 * k + 16 * g;
+          const uint32_t at = step * 128 + 64 * k + 16 * (lane % 4);
           if constexpr (WHOLE_STEP) {
             __builtin_memcpy(&d.c[t][k], codes + (from + at), 16);
           } else if constexpr (BITS == 4 && HALVES == 2) {
@@ -237,15 +244,15 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
 
     // A token takes a row for each of its parts.  Row r of a tile is place (r % 4) *
     // 4 + r / 4, so that the first places stand in the first of a lane's four
-    // results; places beyond the last token repeat the first.
+    // results; places beyond the last token repeat one of these.
     const uint16_t* x[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int place = (l15 % 4) * 4 + l15 / 4;
-      int j = place / parts, p = place - j * parts;
-      const bool there = j < fit && r0 + rt * fit + j < act.count;
-      j = there ? r0 + rt * fit + j : r0;
-      p = there ? p : 0;
+      auto there = [&](int at) { return at / parts < fit && r0 + rt * fit + at / parts < act.count; };
+      // Neighbouring lanes ask for the same row where there are no more than four.
+      const int at = there(place) ? place : there(l15 / 4) ? l15 / 4 : 0;
+      const int j = there(at) ? r0 + rt * fit + at / parts : r0, p = there(at) ? at % parts : 0;
       const int pair = w.order[act.start + j];
       x[rt] = side.x + p * side.x_part + (int64_t)(up ? pair / a.top_k : pair) * side.x_cols + 8 * chunk;
     }
@@ -271,10 +278,19 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
     auto compute = [&](int step, const Raw& d, const Inputs& in, auto results) {
       constexpr int RESULTS = decltype(results)::value;
       constexpr f32x4 ZERO = {0.f, 0.f, 0.f, 0.f};
-      uint32_t c[2][4];
+      uint32_t c[2][4], sw[2][S_WORDS], zw[2][Z_WORDS];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int k = 0; k < S_WORDS; ++k) sw[t][k] = hand_on(row_from, d.s[t][k]);
+        if constexpr (ZP) {
+#pragma unroll
+          for (int k = 0; k < Z_WORDS; ++k) zw[t][k] = hand_on(row_from, d.z[t][k]);
+        }
+      }
       auto zero_bits = [&](int t, int b) {
         const int odd = BITS == 4 && NS == 1 ? 4 * ((step * CODES) >> log_block & 1) : 0;
-        return d.z[t][b * BITS / 32] >> (BITS * b % 32 + odd) & ((1u << BITS) - 1u);
+        return zw[t][b * BITS / 32] >> (BITS * b % 32 + odd) & ((1u << BITS) - 1u);
       };
       auto zero = [&](int t, int b) { return ZP ? (float)zero_bits(t, b) : (float)(1 << (BITS - 1)); };
       // 16 + z: a float of 16 whose last bit is 2^-19.
@@ -319,7 +335,7 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) c[t][i] = d.c[t][u / HALF][i];
+            for (int i = 0; i < 4; ++i) c[t][i] = hand_on(codes_from, d.c[t][u / HALF][i]);
             swap_halves(c[t][0], c[t][2]);
             swap_halves(c[t][1], c[t][3]);
             if constexpr (BITS == 4) {
@@ -353,7 +369,7 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int b = HALVES == 2 ? 2 * u + h : u / PER;
-            const uint32_t raw = d.s[t][b * sizeof(ST) / 4] >> (8 * (b * sizeof(ST) % 4));
+            const uint32_t raw = sw[t][b * sizeof(ST) / 4] >> (8 * (b * sizeof(ST) % 4));
             float s;
             if constexpr (SDT == DT_F32) s = __uint_as_float(raw);
             else s = bits16_to_f32<SDT>((uint16_t)raw);
