@@ -118,6 +118,7 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
   constexpr int HALVES = NS == 2 * UNITS ? 2 : 1;            // blocks of 16: two a unit
   constexpr int PER = HALVES == 2 ? 1 : UNITS / NS;          // units a block
   constexpr bool EARLY = RT == 1;            // a step's inputs fit beside its weights
+  constexpr int AHEAD = EARLY ? 2 : 0;       // units whose inputs are loaded a step ahead
   constexpr int S_WORDS = (NS * (SDT == DT_F32 ? 4 : 2) + 3) / 4;
   constexpr int Z_BYTES = (NS * BITS + 7) / 8, Z_WORDS = (Z_BYTES + 3) / 4;
   // 1 and 16 of XDT, twice, and the place of a code's lowest bit in 16 + code.
@@ -269,7 +270,13 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
     };
     auto load_x = [&](int step, Inputs& in) {
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u)
+      for (int u = AHEAD; u < UNITS; ++u)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) in.v[EARLY ? u : 0][rt] = x_at(step, u, rt);
+    };
+    auto load_x_ahead = [&](int step, Inputs& in) {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) in.v[EARLY ? u : 0][rt] = x_at(step, u, rt);
     };
@@ -390,15 +397,26 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
       Inputs in;
       int step = own;
       if (step < whole_steps) {
+        if constexpr (EARLY) load_x_ahead(step, in);
         for (; step + MOE_WAVES < whole_steps; step += MOE_WAVES) {
-          // Loads are waited for in their order: inputs before weights ahead.
-          if constexpr (EARLY) load_x(step, in);
+          // Loads are waited for in their order: inputs before weights ahead, and the
+          // first inputs of a step before it, to cover for the others.
+          Inputs next_in;
+          if constexpr (EARLY) {
+            load_x(step, in);
+            __builtin_amdgcn_sched_barrier(0);
+            load_x_ahead(step + MOE_WAVES, next_in);
+          }
           __builtin_amdgcn_sched_barrier(0);
           Raw next;
           load(step + MOE_WAVES, next, std::true_type{});
           __builtin_amdgcn_sched_barrier(0);
           compute(step, d, in, results);
           d = next;
+          if constexpr (EARLY) {
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) in.v[u][0] = next_in.v[u][0];
+          }
         }
         if constexpr (EARLY) load_x(step, in);
         compute(step, d, in, results);
@@ -406,7 +424,10 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
       if (whole_steps < steps && wave == whole_steps % MOE_WAVES) {
         int last = whole_steps;
         asm volatile("" : "+s"(last));
-        if constexpr (EARLY) load_x(last, in);
+        if constexpr (EARLY) {
+          load_x_ahead(last, in);
+          load_x(last, in);
+        }
         load(last, d, std::false_type{});
         compute(last, d, in, results);
       }

@@ -51,20 +51,16 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
-__device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    const uint64_t u = __shfl_xor(v, o);
-    v = u > v ? u : v;
-  }
-  return v;
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  auto over = [&](uint32_t u) { v = u > v ? u : v; };
+  over((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));    // quad_perm 1,0,3,2
+  over((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));    // quad_perm 2,3,0,1
+  over((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));   // row_half_mirror
+  over((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));   // row_mirror
+  over((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));   // row_bcast:15
+  over((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));   // row_bcast:31
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
-__device__ __forceinline__ float wave_add(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-
 // One wave: token t's experts and their weights in lanes 0 .. top_k - 1; at most
 // 64 PER experts.
 template <int PER>
@@ -78,47 +74,52 @@ __device__ void choose(const MoeArgs& a, int t, int lane, int* id, float* weight
     }
   } else {
     float v[PER];
-    uint64_t best = 0;
+    uint32_t key[PER], best = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int e = lane + 64 * i;
-      v[i] = 64 * i < a.experts && e < a.experts ? load_logit(a, t * a.logits_stride + e) : -INFINITY;
+      const bool there = 64 * i < a.experts && e < a.experts;
+      v[i] = there ? load_logit(a, t * a.logits_stride + e) : -INFINITY;
+      key[i] = there ? order_key(v[i]) : 0u;    // a key of a value is above 0
+      best = key[i] > best ? key[i] : best;
     }
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) top = fmaxf(top, v[i]);
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    best = wave_max_u32(best);
+    auto value = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); };
+    const float top = value(best);
     // Infinite logits share everything equally.
     auto part = [&](float l) { return top == INFINITY ? (l == INFINITY ? 1.f : 0.f) : expf(l - top); };
-    float sum = 0.f;
     if (top > -INFINITY) {
+      float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; ++i)
-        if (64 * i < a.experts && v[i] > -INFINITY) sum += part(v[i]);
-      sum = wave_add(sum);
+        if (v[i] > -INFINITY) sum += part(v[i]);
+      sum = wave_sum(sum);
       float chosen = 0.f, mine = 0.f;
-      uint32_t taken = 0;
       for (int j = 0; j < a.top_k; ++j) {
-        best = 0;
+        // The lowest index that has the largest key, which is then taken away.
+        int e = 0;
+        bool found = false;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          const int e = lane + 64 * i;
-          if (64 * i >= a.experts || e >= a.experts || (taken >> i & 1)) continue;
-          const uint64_t at = (uint64_t)order_key(v[i]) << 32 | (uint32_t)~e;
-          best = at > best ? at : best;
+          const uint64_t has = __ballot(key[i] == best);
+          if (!found && has) {
+            found = true;
+            e = 64 * i + __builtin_ctzll(has);
+          }
         }
-        best = wave_max_u64(best);
-        const int e = (int)~(uint32_t)best;
-        const uint32_t key = (uint32_t)(best >> 32);
-        const float l = __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
-        if ((e & 63) == lane) taken |= 1u << (e >> 6);
-        const float p = l > -INFINITY ? part(l) : 0.f;
+        const float l = value(best), p = l > -INFINITY ? part(l) : 0.f;
         chosen += p;
         if (lane == j) {
           *id = e;
           mine = p;
         }
+        best = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          key[i] = lane + 64 * i == e ? 0u : key[i];
+          best = key[i] > best ? key[i] : best;
+        }
+        best = wave_max_u32(best);
       }
       *weight = mine / (a.normalize ? chosen : sum);
     }
@@ -156,10 +157,13 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
     }
     return;
   }
-  __shared__ int ids[MAX_PAIRS];
-  __shared__ int upto[ROUTE_WAVES], counts[ROUTE_THREADS];
+  __shared__ __attribute__((aligned(16))) int ids[MAX_PAIRS];
+  __shared__ int upto[ROUTE_WAVES];
+  __shared__ __attribute__((aligned(16))) int counts[ROUTE_THREADS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int pairs = a.tokens * a.top_k;
+  if (threadIdx.x < 4 && pairs + threadIdx.x < MAX_PAIRS) ids[pairs + threadIdx.x] = -1;   // four are read at once
+  for (int i = threadIdx.x; i < w.max_active; i += ROUTE_THREADS) w.active[i] = MoeActive{0, 0, 0, 0};
   for (int t = wave; t < a.tokens; t += ROUTE_WAVES) {
     int id;
     float weight;
@@ -176,8 +180,11 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
   // Thread e counts expert e's pairs and lists them in order.
   const int e = threadIdx.x;
   int count = 0;
-  if (e < a.experts)
-    for (int p = 0; p < pairs; ++p) count += ids[p] == e;
+  for (int p = 0; p < pairs; p += 4) {
+    const i32x4 four = *(const i32x4*)(ids + p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) count += four[i] == e;
+  }
   // Pairs before this expert's.
   int sum = count;
 #pragma unroll
@@ -188,13 +195,17 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
   if (lane == 63) upto[wave] = sum;
   counts[e] = count;
   __syncthreads();
+  if (count == 0) return;
   int start = sum - count;
   for (int v = 0; v < wave; ++v) start += upto[v];
   // The place among the active ones: after those with more.
   int place = 0;
-  for (int o = 0; o < a.experts; ++o) place += counts[o] > count || (counts[o] == count && o < e);
-  if (e < a.experts && place < w.max_active) w.active[place] = MoeActive{e, start, count, 0};
-  if (count == 0) return;
+  for (int o = 0; o < a.experts; o += 4) {
+    const i32x4 four = *(const i32x4*)(counts + o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) place += four[i] > count || (four[i] == count && o + i < e);
+  }
+  w.active[place] = MoeActive{e, start, count, 0};
   for (int p = 0; p < pairs; ++p)
     if (ids[p] == e) w.order[start++] = p;
 }
@@ -205,9 +216,12 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a, MoeWork w) {
   const int t = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
   if (n >= a.hidden) return;
   float sum = 0.f;
+#pragma unroll 8
   for (int j = 0; j < a.top_k; ++j) {
+    // What stands there for a pair without an expert is loaded and not used.
     const int pair = t * a.top_k + j;
-    if (w.ids[pair] >= 0) sum += w.out[(int64_t)pair * a.hidden + n];
+    const float v = w.out[(int64_t)pair * a.hidden + n];
+    sum += w.ids[pair] >= 0 ? v : 0.f;
   }
   ((typename dt<DT>::T*)a.y)[t * a.y_stride + n] = dt<DT>::from_f32(sum);
 }
