@@ -738,11 +738,11 @@ def _apart(**tensors):
     return ValueError(f"{name} is on {t.device}, {first} on {x.device}: pass tensors of one GPU")
 
 
-def _matrix(name, t, shape, dtype):
-    """The struct of rows of ``shape`` [rows, cols]."""
+def _matrix(name, t, like, dtype):
+    """The struct of the rows of a matrix t, of the shape of ``like``."""
     strides = t.stride()
-    if t.shape != shape or t.dtype is not dtype or (strides[1] != 1 and shape[1] > 1):
-        raise ValueError(f"{name} must be {dtype} {list(shape)} with a dense last dimension, got {t.dtype} "
+    if not t.is_same_size(like) or t.dtype is not dtype or (strides[1] != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be {dtype} {list(like.shape)} with a dense last dimension, got {t.dtype} "
                          f"{list(t.shape)} with strides {list(strides)}")
     return _pack_rows(t.data_ptr(), strides[0])
 
@@ -782,23 +782,23 @@ def _norm_args(x, weight, residual, h, y, eps, offset, codes, scales, fmt, layou
     if x.dim() != 2 or x.dtype not in _TORCH_TO_QMM:
         raise ValueError(f"x must be [rows, cols] of float32, float16 or bfloat16, got {x.dtype} "
                          f"{list(x.shape)}")
-    shape, dtype, gpu = x.shape, x.dtype, x.get_device()
-    rows, cols = shape
-    quant = None if codes is None else _quant_struct(codes, scales, rows, cols, fmt, layout, block_size)
-    w = None
+    dtype, gpu = x.dtype, x.get_device()
+    rows, cols = x.shape
+    quant = w = None
+    w_dtype = 0
+    if codes is not None:
+        quant = _quant_struct(codes, scales, rows, cols, fmt, layout, block_size)
     if weight is not None:
         if weight.dtype not in _TORCH_TO_QMM:
             raise ValueError(f"weight must be float32, float16 or bfloat16, got {weight.dtype}")
-        w = _dense("weight", weight, (cols,), weight.dtype)
+        w, w_dtype = _dense("weight", weight, (cols,), weight.dtype), _TORCH_TO_QMM[weight.dtype]
     for t in (weight, residual, h, y, codes, scales):
         if t is not None and t.get_device() != gpu or gpu < 0:
             raise _apart(x=x, weight=weight, residual=residual, h=h, y=y, codes=codes, scales=scales)
-    return gpu, (_matrix("x", x, shape, dtype),
-                 None if residual is None else _matrix("residual", residual, shape, dtype),
-                 None if h is None else _matrix("h", h, shape, dtype), w,
-                 0 if weight is None else _TORCH_TO_QMM[weight.dtype], offset, eps,
-                 None if y is None else _matrix("y", y, shape, dtype), quant, _TORCH_TO_QMM[dtype],
-                 rows, cols)
+    return gpu, (_matrix("x", x, x, dtype),
+                 None if residual is None else _matrix("residual", residual, x, dtype),
+                 None if h is None else _matrix("h", h, x, dtype), w, w_dtype, offset, eps,
+                 None if y is None else _matrix("y", y, x, dtype), quant, _TORCH_TO_QMM[dtype], rows, cols)
 
 
 def qmm_rms_norm(x, weight, residual=None, h=None, y=None, eps=1e-5, offset=0.0, codes=None, scales=None,
@@ -882,11 +882,10 @@ def qmm_moe_workspace_size(weights, tokens, top_k) -> int:
 
 
 def _moe_args(x, weights, y, workspace, logits, top_k, normalize, ids, expert_weights):
-    if x.dim() != 2 or x.dtype not in _TORCH_TO_QMM:
-        raise ValueError(f"x must be [tokens, hidden] of float32, float16 or bfloat16, got {x.dtype} "
+    if x.dim() != 2 or x.dtype not in _TORCH_TO_QMM or x.shape[1] != weights.hidden:
+        raise ValueError(f"x must be [tokens, {weights.hidden}] of float32, float16 or bfloat16, got {x.dtype} "
                          f"{list(x.shape)}")
     tokens, gpu = x.shape[0], weights.gpu
-    shape = (tokens, weights.hidden)
     if (logits is None) == (ids is None) or (ids is None) != (expert_weights is None):
         raise ValueError("pass logits and top_k, or ids and expert_weights")
     if ids is None:
@@ -905,7 +904,7 @@ def _moe_args(x, weights, y, workspace, logits, top_k, normalize, ids, expert_we
         if t is not None and t.get_device() != gpu:
             raise _apart(weights=weights.tensors["gate_up"], x=x, y=y, workspace=workspace, logits=logits,
                          ids=ids, expert_weights=expert_weights)
-    return gpu, (_matrix("x", x, shape, x.dtype), weights._ref, route, _matrix("y", y, shape, x.dtype),
+    return gpu, (_matrix("x", x, x, x.dtype), weights._ref, route, _matrix("y", y, x, x.dtype),
                  _TORCH_TO_QMM[x.dtype], tokens, workspace.data_ptr(), workspace.nbytes)
 
 

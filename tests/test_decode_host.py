@@ -1,0 +1,343 @@
+"""The operators around a decode step's projections without a GPU: the plain
+forms against worked values, the refusals at the C boundary and in the binding,
+and the sizes of workspaces."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import decode_ref as ref
+
+FAKE = 0x10000   # never dereferenced: validation fails before any device work
+
+
+@pytest.fixture(scope="module")
+def qmm():
+    from block_quantized_weight_matmulnbits_amd import qmm as q
+    return q
+
+
+# -- the plain forms ---------------------------------------------------------
+
+def test_norm_worked_values():
+    x = torch.tensor([[3.0, -4.0]])
+    h, y = ref.norm32(x, torch.tensor([2.0, 1.0]), None, 0.0, 0.0)
+    np.testing.assert_allclose(y, [[6 / math.sqrt(12.5), -4 / math.sqrt(12.5)]], rtol=1e-6)
+    h, y = ref.norm32(x, torch.tensor([1.0, 0.0]), torch.tensor([[-3.0, 5.0]]), 0.5, 1.0)
+    assert h.tolist() == [[0.0, 1.0]] and y.tolist() == [[0.0, 1.0]]
+    q, s = ref.int8_of(torch.tensor([[127.0, 63.5, -127.0, 0.5, 1.5] + [0.0] * 12]), 16)
+    assert s.tolist() == [[float(np.float32(127) * np.float32(1 / 127)), 0.0]]
+    assert q[0, :5].tolist() == [127, 64, -127, 0, 2] and q.shape == (1, 32) and not q[0, 5:].any()
+    c, e = ref.mx_of(torch.tensor([[448.0, 1.0, -2.0]]), "e4m3")
+    assert e.tolist() == [[127]] and c.view(torch.float8_e4m3fn).float().tolist() == [[448.0, 1.0, -2.0]]
+    c, e = ref.mx_of(torch.tensor([[0.0, 0.0], [500.0, math.nan]]), "e4m3")
+    assert e.tolist() == [[127], [127]] and c.tolist() == [[0, 0], [0x7E, 0x7F]]    # saturated; a nan
+
+
+def test_sampling_worked_values():
+    z = np.log(np.array([1.0, 4.0, 3.0, 2.0]))
+    assert [ref.sample_row(z, 1, 0, 1, 0, u)[0] for u in (0.0, 0.09, 0.11, 0.49, 0.51, 0.79, 0.81)] == [0, 0, 1, 1, 2, 2, 3]
+    assert [ref.sample_row(z, 1, 2, 1, 0, u)[0] for u in (0.0, 0.56, 0.58)] == [1, 1, 2]
+    # 0.5 of 10 is reached by 4 and 3; 0.3 by 4 alone.
+    assert [ref.sample_row(z, 1, 0, p, 0, 0.99)[0] for p in (0.3, 0.5, 0.75, 1.0)] == [1, 2, 3, 3]
+    assert [ref.sample_row(z, 1, 0, 1, m, 0.99)[0] for m in (1.0, 0.7, 0.5, 0.2)] == [1, 2, 3, 3]
+    assert ref.sample_row(z, 1, 0, 1, 0.7, 0.99)[1] == pytest.approx(math.log(3 / 7))
+    assert ref.sample_row(z, 0, 0, 1, 0, 0.99) == (1, 0.0)
+    assert ref.sample_row(np.full(3, -np.inf), 1, 0, 1, 0, 0.5)[0] == -1
+    assert ref.sample_row(np.zeros(4), 1, 2, 1, 0, 0.99)[0] == 1
+
+
+def test_experts_worked_values():
+    ex = ref.Experts(2, 1, 1, 16, 4, zero_points=False, s_dtype=torch.float32)
+    for w, (codes, scales, _) in enumerate(ex.parts):
+        codes.zero_()
+        scales.fill_(1.0)
+        codes[0, :, 0, 0] = 10 if w == 0 else 11      # 2 and 3 above the middle
+        codes[1, :, 0, 0] = 7                         # -1
+    x = torch.tensor([[1.5]])
+    silu = 3 / (1 + math.exp(-3))
+    one, two = 3 * silu * 3, -(-1.5 / (1 + math.exp(1.5)) * -1.5)
+    y, bound = ref.moe(x, ex, np.array([[0, 1]]), np.array([[0.25, 0.75]]), torch.float32)
+    assert y[0, 0] == pytest.approx(0.25 * one + 0.75 * two)
+    # The bound's largest part: 10 steps of 32 bits of (10 + 8) 1.5 in gate and up
+    # (3.3e-5 each), through 2.86 and 1.1 3, times 3 of down and 0.25: 1.5e-4; then
+    # 10 steps of (11 + 8) 8.57 in down, times 0.25: 4.9e-5; the other expert's are
+    # of (7 + 8) in each, below half of these.
+    assert 1.9e-4 < bound[0, 0] < 2 * 2e-4
+    ids, w = ref.route(torch.tensor([[0.0, math.log(3.0)], [-math.inf, math.nan]]), 2, True)
+    assert ids.tolist() == [[1, 0], [-1, -1]] and np.allclose(w[0], [0.75, 0.25])
+    assert np.allclose(ref.route(torch.log(torch.tensor([[1.0, 2, 5]])), 1, False)[1], [[5 / 8]])
+
+
+# -- refusals at the C boundary ----------------------------------------------
+
+def rows(qmm, data=FAKE, stride=512):
+    return qmm._pack_rows(data or 0, stride)
+
+
+def norm(qmm, x="x", residual=None, h=None, weight=FAKE, wt=2, offset=0.0, eps=1e-5, y="y", quant=None, dtype=2,
+         n=4, cols=512):
+    def r(v):
+        return rows(qmm) if isinstance(v, str) else v
+    return qmm.lib.qmm_rms_norm(r(x), r(residual), r(h), weight, wt, offset, eps, r(y), quant, dtype, n, cols, None)
+
+
+def quant(qmm, kind=0, fmt=0, block=32, codes=FAKE, scales=FAKE):
+    return qmm._pack_quant(kind, fmt, block, codes or 0, scales or 0)
+
+
+def test_norm_refuses(qmm):
+    r, q = (lambda *a: rows(qmm, *a)), (lambda **k: quant(qmm, **k))
+    for kw, code, needle in [
+            (dict(dtype=7), -1, "not a qmm_dtype"), (dict(wt=9), -1, "not a qmm_dtype"),
+            (dict(n=-1), -1, "rows must be >= 0"), (dict(cols=0), -1, "cols positive"),
+            (dict(cols=(1 << 20) + 1), -2, "cols at most 2^20"), (dict(n=1 << 40), -2, "below 2^40"),
+            (dict(eps=-1e-5), -1, "eps must be finite"), (dict(eps=math.nan), -1, "eps must be finite"),
+            (dict(eps=math.inf), -1, "eps must be finite"), (dict(offset=math.inf), -1, "offset finite"),
+            (dict(y=None), -1, "all NULL"), (dict(x=None), -1, "x is NULL"),
+            (dict(x=r(None)), -1, "x.data must be a non-null"), (dict(x=r(FAKE + 1)), -1, "aligned to its element size"),
+            (dict(residual=r(FAKE, 511)), -1, "residual.stride=511 does not hold a row"),
+            (dict(h=r(FAKE, -512)), -1, "h.stride"), (dict(y=r(FAKE, 1 << 40)), -1, "y.stride"),
+            (dict(weight=FAKE + 1), -1, "weight must be aligned"), (dict(h="h"), -1, "cannot be the same rows"),
+            (dict(quant=q(kind=3)), -1, "not a qmm_quant_kind"), (dict(quant=q(block=24)), -1, "power of two"),
+            (dict(quant=q(block=8)), -1, "power of two"), (dict(quant=q(block=1 << 21)), -1, "power of two"),
+            (dict(quant=q(kind=1, fmt=2)), -1, "QMM_LOWP_E4M3 or QMM_LOWP_E5M2"),
+            (dict(quant=q(codes=None)), -1, "codes and quant.scales"), (dict(quant=q(scales=None)), -1, "quant.scales"),
+            (dict(quant=q(scales=FAKE + 2)), -1, "4-byte aligned"),
+            (dict(quant=q(kind=2, scales=FAKE + 2)), -1, "4-byte aligned")]:
+        assert norm(qmm, **kw) == code, kw
+        assert needle in qmm.qmm_last_error(), (kw, qmm.qmm_last_error())
+    assert norm(qmm, n=0) == 0 and norm(qmm, n=0, quant=q(codes=None)) == 0
+
+
+def product(qmm, qa=FAKE, sa=FAKE, B=FAKE, layout=0, scales=FAKE, M=4, K=512, N=64, bs=32, bits=4, Y=FAKE):
+    return qmm.lib.qmm_gemm_compint8_quantized(qa, sa, B, layout, scales, 0, None, None, Y, 2, M, K, N, bs, bits, None)
+
+
+@pytest.mark.parametrize("kw,code,needle", [
+    (dict(qa=None), -1, "non-null"), (dict(sa=None), -1, "qa must be 16-byte aligned and sa"),
+    (dict(qa=FAKE + 8), -1, "16-byte aligned"), (dict(sa=FAKE + 2), -1, "4-byte"), (dict(bits=5), -1, "bits must be"),
+    (dict(bs=24), -1, "power of two"), (dict(M=-1), -1, "M must be >= 0"), (dict(Y=None), -1, "non-null"),
+    (dict(layout=1, scales=None, bs=16), -2, "block_size >= 32"), (dict(layout=1), -1, "must be NULL")])
+def test_the_quantized_product_refuses(qmm, kw, code, needle):
+    assert product(qmm, **kw) == code
+    assert needle in qmm.qmm_last_error()
+
+
+def test_the_quantized_product_of_no_rows(qmm):
+    assert product(qmm, M=0, qa=None, sa=None, Y=None) == 0
+
+
+def moe_weights(qmm, up=FAKE, up_s=FAKE, down=FAKE, down_s=FAKE, hidden=256, inter=128, experts=4, s_dtype=2, bs=32, bits=4):
+    return qmm._MoeWeights(up, up_s, None, down, down_s, None, hidden, inter, experts, s_dtype, bs, bits)
+
+
+def moe(qmm, x="x", y="y", w=None, logits=FAKE, lstride=4, ldt=0, ids=0, weights=0, top_k=2, dtype=2, tokens=3, ws=FAKE,
+        ws_bytes=1 << 30, route=True):
+    def r(v):
+        return rows(qmm) if isinstance(v, str) else v
+    import ctypes
+    w = w or moe_weights(qmm)
+    packed = qmm._pack_route(logits, lstride, ldt, 1, ids, weights, top_k)
+    return qmm.lib.qmm_moe(r(x), ctypes.byref(w) if w != "null" else None, packed if route else None, r(y), dtype, tokens, ws,
+                           ws_bytes, None)
+
+
+def test_experts_refuse(qmm):
+    r, w = (lambda *a: rows(qmm, *a)), (lambda **k: moe_weights(qmm, **k))
+    for kw, code, needle in [
+            (dict(x=None), -1, "must be non-null"), (dict(y=None), -1, "must be non-null"),
+            (dict(w="null"), -1, "must be non-null"), (dict(route=False), -1, "must be non-null"),
+            (dict(dtype=4), -1, "not a qmm_dtype"), (dict(w=w(bits=3)), -2, "4 or 8 bits"), (dict(w=w(bits=5)), -1, "4 or 8 bits"),
+            (dict(w=w(bs=8)), -1, "power of two"), (dict(w=w(bs=48)), -1, "power of two"), (dict(w=w(s_dtype=3)), -1, "s_dtype=3"),
+            (dict(w=w(hidden=0)), -1, "must be positive"), (dict(w=w(inter=-1)), -1, "must be positive"),
+            (dict(w=w(experts=0)), -1, "must be positive"), (dict(w=w(experts=1025)), -2, "at most 1024 experts"),
+            (dict(w=w(hidden=1 << 19)), -2, "at most 2^18"), (dict(w=w(hidden=1 << 18, inter=1 << 15)), -2, "below 2^31"),
+            (dict(tokens=-1), -1, "tokens must be >= 0"), (dict(tokens=257), -2, "at most 256 tokens"),
+            (dict(top_k=0), -1, "top_k must be from 1"), (dict(top_k=33), -1, "top_k must be from 1"),
+            (dict(top_k=5), -1, "no more than the experts"),
+            (dict(x=r(None)), -1, "x.data"), (dict(x=r(FAKE, 255)), -1, "x.stride=255"), (dict(y=r(FAKE + 1)), -1, "y.data"),
+            (dict(w=w(up=None)), -1, "codes must be non-null"), (dict(w=w(down=FAKE + 8)), -1, "16-byte aligned"),
+            (dict(w=w(down_s=None)), -1, "non-null"), (dict(w=w(up_s=FAKE + 1)), -1, "aligned to their element size"),
+            (dict(ldt=5), -1, "route.logits"), (dict(logits=FAKE + 2), -1, "route.logits"),
+            (dict(lstride=3), -1, "logits_stride=3"), (dict(logits=0), -1, "logits, or ids and weights"),
+            (dict(logits=0, ids=FAKE), -1, "logits, or ids and weights"),
+            (dict(logits=0, ids=FAKE + 1, weights=FAKE), -1, "logits, or ids and weights"),
+            (dict(ws=None), -3, "qmm_moe_workspace_size"), (dict(ws_bytes=100), -3, "are needed"),
+            (dict(ws=FAKE + 128), -3, "256-byte aligned")]:
+        assert moe(qmm, **kw) == code, kw
+        assert needle in qmm.qmm_last_error(), (kw, qmm.qmm_last_error())
+    assert moe(qmm, tokens=0, ws=None) == 0
+
+
+def sample(qmm, logits=FAKE, dtype=2, n=4, vocab=5000, stride=5000, t=FAKE, k=FAKE, p=FAKE, m=FAKE, u=FAKE, tokens=FAKE,
+           logprobs=FAKE, ws=FAKE, ws_bytes=1 << 30):
+    return qmm.lib.qmm_sample(logits, dtype, n, vocab, stride, t, k, p, m, u, tokens, logprobs, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code,needle", [
+    (dict(dtype=3), -1, "not a qmm_dtype"), (dict(n=-1), -1, "rows must be >= 0"), (dict(vocab=0), -1, "vocab positive"),
+    (dict(n=1 << 21), -2, "below 2^21"), (dict(vocab=(1 << 22) + 1, stride=1 << 23), -2, "at most 2^22"),
+    (dict(logits=None), -1, "non-null"), (dict(u=None), -1, "non-null"), (dict(tokens=None), -1, "non-null"),
+    (dict(logits=FAKE + 1), -1, "aligned"), (dict(t=FAKE + 2), -1, "aligned"), (dict(k=FAKE + 2), -1, "aligned"),
+    (dict(p=FAKE + 1), -1, "aligned"), (dict(m=FAKE + 3), -1, "aligned"), (dict(u=FAKE + 2), -1, "aligned"),
+    (dict(tokens=FAKE + 2), -1, "aligned"), (dict(logprobs=FAKE + 2), -1, "aligned"),
+    (dict(stride=4999), -1, "row_stride=4999"), (dict(stride=-5000), -1, "row_stride"),
+    (dict(ws=None), -3, "qmm_sample_workspace_size"), (dict(ws_bytes=16), -3, "are needed"),
+    (dict(ws=FAKE + 64), -3, "256-byte aligned")])
+def test_sampling_refuses(qmm, kw, code, needle):
+    assert sample(qmm, **kw) == code
+    assert needle in qmm.qmm_last_error()
+
+
+def test_sampling_of_no_rows(qmm):
+    assert sample(qmm, n=0, logits=None, ws=None) == 0
+
+
+def test_recorded_calls_are_checked_when_the_step_is_finalized(qmm):
+    import ctypes
+    s = ctypes.c_void_p()
+    assert qmm.lib.qmm_step_create(ctypes.byref(s)) == 0
+    r, w = rows(qmm), moe_weights(qmm)
+    assert qmm.lib.qmm_step_add_rms_norm(s, r, None, None, None, 0, 0.0, 1e-5, None, None, 2, 4, 512) == 0
+    assert qmm.lib.qmm_step_add_moe(s, r, ctypes.byref(w), None, r, 2, 1, None, 0) == 0
+    assert qmm.lib.qmm_step_add_sample(s, FAKE, 2, 1, 100, 100, *([None] * 4), FAKE, FAKE, None, FAKE, 256) == 0
+    assert qmm.lib.qmm_step_add_gemm_compint8_quantized(s, FAKE, FAKE, FAKE, 0, FAKE, 0, None, None, FAKE, 2, 1, 64, 64, 32,
+                                                        4) == 0
+    assert qmm.lib.qmm_step_size(s) == 4
+    qmm.lib.qmm_step_destroy(s)
+    assert qmm.lib.qmm_step_add_moe(None, r, ctypes.byref(w), None, r, 2, 1, None, 0) == -1
+
+
+# -- workspaces --------------------------------------------------------------
+
+def test_workspaces_grow_with_what_they_hold(qmm):
+    import ctypes
+    w = moe_weights(qmm)
+
+    def size(tokens, top_k, **kw):
+        return qmm.lib.qmm_moe_workspace_size(ctypes.byref(moe_weights(qmm, **kw)), tokens, top_k)
+    assert size(0, 1) > 0 or size(0, 1) == 0
+    last = 0
+    for tokens in (1, 2, 16, 17, 255, 256):
+        now = size(tokens, 2)
+        # Both projections' inputs and the pairs' outputs at least.
+        assert now >= last and now >= tokens * 256 * 2 + 2 * tokens * (128 * 4 + 256 * 4) and now % 256 == 0
+        last = now
+    assert size(257, 2) == 0 and size(4, 33) == 0 and size(4, 0) == 0 and size(4, 2, bits=2) == 0
+    assert qmm.lib.qmm_moe_workspace_size(None, 4, 2) == 0
+    assert qmm.lib.qmm_sample_workspace_size(64, 131072) >= qmm.lib.qmm_sample_workspace_size(1, 131072) > 0
+    assert qmm.lib.qmm_sample_workspace_size(1 << 21, 100) == 0 and qmm.lib.qmm_sample_workspace_size(1, 0) == 0
+    # A batch of any size takes no more than what is held of 2048 rows.
+    assert qmm.lib.qmm_sample_workspace_size((1 << 21) - 1, 1 << 22) == qmm.lib.qmm_sample_workspace_size(2048, 1 << 22)
+
+
+# -- refusals in the binding -------------------------------------------------
+
+class OnGpu(torch.Tensor):
+    """A host tensor that says it is on GPU 0 (its memory is never used: every
+    call here is refused first)."""
+
+    def get_device(self):
+        return 0
+
+
+def there(t):
+    return t.as_subclass(OnGpu)
+
+
+def calls(qmm, put):
+    def i32(*s):
+        return torch.zeros(*s, dtype=torch.int32)
+
+    def bf(*s):
+        return torch.zeros(*s, dtype=torch.bfloat16)
+    t = {n: put(n, x) for n, x in dict(
+        x=bf(4, 64), weight=bf(64), residual=bf(4, 64), h=bf(4, 64), y=bf(4, 64), codes=torch.zeros(4, 64, dtype=torch.int8),
+        scales=torch.zeros(4, 2), qa=torch.zeros(4, 64, dtype=torch.int8), sa=torch.zeros(4, 2),
+        B=torch.zeros(32, 2, 16, dtype=torch.uint8), Y=bf(4, 32), logits=torch.zeros(4, 3), uniform=torch.zeros(4),
+        tokens=i32(4), temperature=torch.ones(4), top_k=i32(4), top_p=torch.ones(4), min_p=torch.ones(4),
+        logprobs=torch.zeros(4), workspace=torch.zeros(1 << 16, dtype=torch.uint8), ids=i32(4, 2),
+        expert_weights=torch.zeros(4, 2)).items()}
+    # Experts on GPU 0, but for the test that says otherwise.
+    e = [put("experts", x) for x in (torch.zeros(3, 32, 2, 16, dtype=torch.uint8), bf(3, 32, 2),
+                                     torch.zeros(3, 64, 1, 16, dtype=torch.uint8), bf(3, 64, 1))]
+    w = qmm.MoeWeights(e[0], e[1], None, e[2], e[3], None, 64, 16, 32, 4)
+    return {
+        "norm": lambda **k: qmm.qmm_rms_norm(**{**dict(x=t["x"], weight=t["weight"], residual=t["residual"], h=t["h"],
+                                                       y=t["y"], codes=t["codes"], scales=t["scales"], block_size=32), **k}),
+        "product": lambda **k: qmm.qmm_gemm_compint8_quantized(t["qa"], t["sa"], t["B"], t["scales"], None, None, t["Y"], 4,
+                                                               64, 32, 32, 4),
+        "moe": lambda **k: qmm.qmm_moe(**{**dict(x=t["x"], weights=w, y=t["y"], workspace=t["workspace"],
+                                                 logits=t["logits"], top_k=2), **k}),
+        "given": lambda **k: qmm.qmm_moe(t["x"], w, t["y"], t["workspace"], ids=t["ids"], expert_weights=t["expert_weights"]),
+        "sample": lambda **k: qmm.qmm_sample(**{**dict(logits=t["logits"], uniform=t["uniform"], tokens=t["tokens"],
+                                                       workspace=t["workspace"], temperature=t["temperature"],
+                                                       top_k=t["top_k"], top_p=t["top_p"], min_p=t["min_p"],
+                                                       logprobs=t["logprobs"]), **k}),
+    }
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c, names in [
+    ("norm", "weight residual h y codes scales"), ("product", "sa B scales Y"), ("moe", "x y workspace logits"),
+    ("given", "x ids expert_weights"), ("sample", "uniform tokens workspace temperature top_k top_p min_p logprobs")]
+    for n in names.split()])
+def test_a_tensor_on_another_device_is_refused(qmm, call, name):
+    c = calls(qmm, lambda n, x: x if n == name else there(x))
+    with pytest.raises(ValueError, match=f"{name} is on cpu, "):
+        c[call]()
+
+
+@pytest.mark.parametrize("call,first", [("norm", "x"), ("product", "qa"), ("sample", "logits")])
+def test_tensors_on_the_host_are_refused(qmm, call, first):
+    c = calls(qmm, lambda n, x: there(x) if n == "experts" else x)
+    with pytest.raises(ValueError, match=f"{first} must be on a GPU"):
+        c[call]()
+
+
+def test_experts_on_the_host_are_refused(qmm):
+    with pytest.raises(ValueError, match="gate_up must be on a GPU"):
+        calls(qmm, lambda n, x: x)
+
+
+def test_shapes_and_types_are_refused(qmm):
+    c = calls(qmm, lambda n, x: there(x))
+
+    def bad(call, match, **kw):
+        with pytest.raises(ValueError, match=match):
+            c[call](**{k: there(v) if isinstance(v, torch.Tensor) else v for k, v in kw.items()})
+
+    bf = torch.bfloat16
+    bad("norm", r"x must be \[rows, cols\]", x=torch.zeros(4, 64, dtype=torch.int32))
+    bad("norm", r"x must be \[rows, cols\]", x=torch.zeros(64, dtype=bf))
+    bad("norm", "residual must be", residual=torch.zeros(4, 63, dtype=bf))
+    bad("norm", "h must be", h=torch.zeros(4, 64))
+    bad("norm", "y must be", y=torch.zeros(64, 4, dtype=bf).t())
+    bad("norm", "weight must be", weight=torch.zeros(65, dtype=bf))
+    bad("norm", "codes must be", codes=torch.zeros(4, 32, dtype=torch.int8))
+    bad("norm", "scales must be", scales=torch.zeros(4, 3))
+    bad("norm", "pass scales", scales=None)
+    bad("norm", "block_size=0", block_size=0)
+    bad("norm", "fmt=", fmt="e4m3")
+    bad("norm", '"e4m3" or "e5m2"', fmt="int8", layout="mx")
+    bad("norm", "E8M0 bytes", fmt="e4m3", layout="mx", codes=torch.zeros(4, 64, dtype=torch.uint8))
+    bad("norm", "uint8 or an 8-bit float", fmt="e4m3", layout="tensor", scales=torch.ones(1))
+    bad("moe", r"x must be \[tokens, 64\]", x=torch.zeros(4, 60, dtype=bf))
+    bad("moe", "y must be", y=torch.zeros(3, 64, dtype=bf))
+    bad("moe", "logits must be", logits=torch.zeros(4, 4))
+    bad("moe", "pass logits and top_k, or ids", logits=None)
+    bad("moe", "pass logits and top_k, or ids", ids=torch.zeros(4, 2, dtype=torch.int32))
+    bad("moe", "ids must be", logits=None, ids=torch.zeros(4, 2, dtype=torch.int64), expert_weights=torch.zeros(4, 2))
+    bad("moe", "expert_weights must be", logits=None, ids=torch.zeros(4, 2, dtype=torch.int32), expert_weights=torch.zeros(4, 3))
+    bad("sample", r"logits must be \[rows, vocab\]", logits=torch.zeros(4, 3, dtype=torch.int32))
+    bad("sample", r"logits must be \[rows, vocab\]", logits=torch.zeros(3, 4).t())
+    bad("sample", "uniform must be", uniform=torch.zeros(5))
+    bad("sample", "top_k must be", top_k=torch.zeros(4, dtype=torch.int64))
+    bad("sample", "temperature must be", temperature=torch.zeros(4, dtype=torch.float64))
+    e = (torch.zeros(3, 32, 2, 16, dtype=torch.uint8), torch.zeros(3, 32, 2), None,
+         torch.zeros(3, 64, 1, 16, dtype=torch.uint8), torch.zeros(3, 64, 1), None)
+    for i, t in ((0, torch.zeros(3, 31, 2, 16, dtype=torch.uint8)), (1, torch.zeros(3, 32, 3)), (1, torch.zeros(3, 32, 2, dtype=bf)),
+                 (2, torch.zeros(3, 32, 2, dtype=torch.uint8)), (3, torch.zeros(2, 64, 1, 16, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            qmm.MoeWeights(*[there(t) if j == i else None if v is None else there(v) for j, v in enumerate(e)], 64, 16, 32, 4)
