@@ -133,6 +133,7 @@ struct Row {
   float per_bucket;      // buckets a unit of the logit
   int shift, k;          // k >= vocab: all
   double p, min_units, u;
+  float little;          // logits below have less than min_p of the first's weight
   bool one;              // only the first token
 
   // The weight in units of 2^-shift, before it is rounded to a whole number.
@@ -172,6 +173,16 @@ __device__ Row row_of(const SampleArgs& a, int64_t row, float top, int shift) {
   r.min_units = ldexp(m > 0.f ? (m < 1.f ? (double)m : 1.0) : 0.0, shift);
   r.u = a.uniform[row];
   r.one = r.k == 1;
+  // exp((l - top) / T) < min_p without the exp: l below top + T log min_p, by more
+  // than the roundings of either side (2^-49 of a weight near 1, a few of the log's 24
+  // bits, of top and of T log min_p in 64 bits, of the bound in 32).  Infinities leave
+  // all to the exp.  256 rows of 32000 with min_p alone: 36 us without, 30 with it.
+  r.little = -INFINITY;
+  if (a.min_p && m > 0.f) {
+    const double off = (double)t * (double)logf(fminf(m, 1.f));
+    const double bound = (double)top + off - 1e-6 * (fabs((double)top) + fabs(off)) - 1e-12 * (double)t;
+    if (top < INFINITY && bound > -1e30) r.little = (float)bound;
+  }
   return r;
 }
 
@@ -417,6 +428,7 @@ __global__ __launch_bounds__(PASS_THREADS) void list_kernel(SampleArgs a, RowWor
   each_token<DT, 2>(logits, begin, end, [&](int i, float l) {
     const int b = all ? 0 : r.bucket(l);
     if (all || e.before(b)) {
+      if (l < r.little) return;
       const double x = r.weight(l);
       if (x >= r.min_units) sum += Row::units(x);
     } else if (e.at(b)) {
@@ -593,7 +605,7 @@ __global__ __launch_bounds__(LAST_THREADS) void last_kernel(SampleArgs a, RowWor
     for (int i = threadIdx.x; i < vocab; i += LAST_THREADS) body(i, WHOLE ? list[WHOLE ? i : 0] : logit<DT>(logits, i));
   };
   auto kept = [&](float l, int i, double* x) {
-    if (place_of<DT>(l, i) < from) return (uint64_t)0;
+    if (l < r.little || place_of<DT>(l, i) < from) return (uint64_t)0;
     *x = r.weight(l);
     return *x >= r.min_units ? Row::units(*x) : 0;
   };
