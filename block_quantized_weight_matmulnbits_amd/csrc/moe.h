@@ -96,6 +96,8 @@ __device__ __forceinline__ void split_bf16(float v, uint16_t (&part)[PARTS]) {
 #ifdef __HIPCC__
 
 constexpr int MOE_WAVES = 4, MOE_THREADS = 64 * MOE_WAVES;
+// Workgroups of a compute unit, as far as registers go.
+constexpr int moe_resident(int rt, int ns) { return rt == 1 && ns <= 8 ? 3 : 2; }
 
 __device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
   const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
@@ -111,7 +113,7 @@ __device__ __forceinline__ void swap_rows(uint32_t& a, uint32_t& b) {
 // Inputs of XDT (16-bit).  WHOLE: weights enter as c - z.  NS blocks a step of 128
 // bytes (1 also where a block is longer).  RT tiles of 16 rows of inputs at once.
 template <int XDT, int BITS, bool WHOLE, int SDT, bool ZP, int NS, int RT>
-__global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_project_kernel(
+__global__ __launch_bounds__(MOE_THREADS, moe_resident(RT, NS)) void moe_project_kernel(
     MoeArgs a, MoeWork w, MoeSide side, int least, int most) {
   constexpr int CODES = 128 * 8 / BITS, UNITS = CODES / 32;  // a step's, 32 a unit
   constexpr int HALF = UNITS / 2;                            // units of 64 bytes
@@ -129,33 +131,14 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
   using Op = MfmaOp<XDT>;
   using V8 = typename Op::V;
 
-  const int tile = blockIdx.x % side.tiles, number = blockIdx.x / side.tiles;
-  const MoeActive act = w.active[number];
-  if (act.count < least || act.count > most) return;
   const bool up = side.up;
   const MoeProj& m = up ? a.up : a.down;
   const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int width = up ? a.inter : a.hidden;   // outputs
-  const int n0 = tile * (up ? 16 : 32);
 
   __shared__ float part_sum[MOE_WAVES][8][64];
 
-  // The expert's weights (the host keeps their offsets below 2^31).  Four
-  // neighbouring lanes load 64 bytes of a row side by side (lanes 16 apart, as the
-  // matrix cores want them, are each a request of their own); LDS's crossbar hands
-  // them on.  Rows past the last one are read as it and dropped.
-  const int64_t first = (int64_t)act.expert * m.rows;
-  const char* const codes = (const char*)m.codes + first * m.row_bytes;
-  const char* const scales = m.scales + first * m.blocks * (int64_t)sizeof(ST);
-  const char* const zps = (const char*)m.zp + first * m.zp_row_bytes;
-  uint32_t row[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    int n = n0 + lane / 4 + (up ? 0 : 16 * t);
-    n = n < width ? n : width - 1;
-    row[t] = up ? t * a.inter + n : n;
-  }
   const uint32_t row_bytes = (uint32_t)m.row_bytes, zp_row_bytes = (uint32_t)m.zp_row_bytes;
   const int blocks = m.blocks;
   const int log_block = 31 - __builtin_clz(a.block);
@@ -176,7 +159,66 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
   asm("" : "+s"(mask));
   asm("" : "+v"(offset));
 
-  for (int r0 = 0; r0 < act.count; r0 += fit * RT) {
+  // The item at hand: 32 rows of an expert for its tokens from r0 on.
+  const int items = side.tiles * w.max_active;
+  int item = blockIdx.x, r0 = 0, start = 0, count = 0, n0 = 0;
+  const char *codes = nullptr, *scales = nullptr, *zps = nullptr;
+  uint32_t row[2];
+  int x_pair[RT], x_at_part[RT], pair[RT];
+
+  // The next item, r0 after the one at hand; false: there is none.
+  auto enter = [&](int at_r0) {
+    r0 = at_r0;
+    if (r0 >= count) {
+      if (count > 0) item += gridDim.x;
+      r0 = 0;
+      for (;; item += gridDim.x) {
+        if (item >= items) return false;
+        const MoeActive act = w.active[item / side.tiles];
+        if (act.count == 0) return false;
+        start = act.start;
+        count = act.count;
+        if (count < least || count > most) continue;
+        n0 = item % side.tiles * (up ? 16 : 32);
+        // The expert's weights (the host keeps their offsets below 2^31).  Four
+        // neighbouring lanes load 64 bytes of a row side by side (lanes 16 apart, as
+        // the matrix cores want them, are each a request of their own); LDS's crossbar
+        // hands them on.  Rows past the last one are read as it and dropped.
+        const int64_t first = (int64_t)act.expert * m.rows;
+        codes = (const char*)m.codes + first * m.row_bytes;
+        scales = m.scales + first * m.blocks * (int64_t)sizeof(ST);
+        zps = (const char*)m.zp + first * m.zp_row_bytes;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          int n = n0 + lane / 4 + (up ? 0 : 16 * t);
+          n = n < width ? n : width - 1;
+          row[t] = up ? t * a.inter + n : n;
+        }
+        break;
+      }
+    }
+    // A token takes a row for each of its parts.  Row r of a tile is place (r % 4) *
+    // 4 + r / 4, so that the first places stand in the first of a lane's four
+    // results; places beyond the last token repeat one of these.
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int place = (l15 % 4) * 4 + l15 / 4;
+      auto there = [&](int at) { return at / parts < fit && r0 + rt * fit + at / parts < count; };
+      // Neighbouring lanes ask for the same row where there are no more than four.
+      const int at = there(place) ? place : there(l15 / 4) ? l15 / 4 : 0;
+      const int j = there(at) ? r0 + rt * fit + at / parts : r0;
+      x_at_part[rt] = there(at) ? at % parts : 0;
+      x_pair[rt] = w.order[start + j];
+      // The token that this thread sums up at the end.
+      const int own = r0 + rt * fit + (int)(threadIdx.x >> 4);
+      pair[rt] = w.order[start + (own < count ? own : r0)];
+    }
+    return true;
+  };
+
+    struct Inputs {
+      u32x4 v[EARLY ? UNITS : 1][RT];
+    };
     // A step's weights: two times 16 bytes of each row, its scales and zero points.
     struct Raw {
       u32x4 c[2][2];
@@ -235,28 +277,22 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
       }
     };
 
-    // The first step is on its way before anything else is looked up.
+    // An item's first step is on its way while the one before it is summed up.
     Raw d;
-    // Opaque, or its addresses would be kept in registers over all of the expert's
-    // tiles of tokens.
+    // Opaque, or its addresses would be kept in registers over all items.
     int own = wave;
     asm volatile("" : "+s"(own));
-    if (own < whole_steps) load(own, d, std::true_type{});
+    auto begin_item = [&](int at_r0) {
+      if (!enter(at_r0)) return false;
+      if (own < whole_steps) load(own, d, std::true_type{});
+      return true;
+    };
 
-    // A token takes a row for each of its parts.  Row r of a tile is place (r % 4) *
-    // 4 + r / 4, so that the first places stand in the first of a lane's four
-    // results; places beyond the last token repeat one of these.
+  for (bool more = begin_item(0); more;) {
     const uint16_t* x[RT];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int place = (l15 % 4) * 4 + l15 / 4;
-      auto there = [&](int at) { return at / parts < fit && r0 + rt * fit + at / parts < act.count; };
-      // Neighbouring lanes ask for the same row where there are no more than four.
-      const int at = there(place) ? place : there(l15 / 4) ? l15 / 4 : 0;
-      const int j = there(at) ? r0 + rt * fit + at / parts : r0, p = there(at) ? at % parts : 0;
-      const int pair = w.order[act.start + j];
-      x[rt] = side.x + p * side.x_part + (int64_t)(up ? pair / a.top_k : pair) * side.x_cols + 8 * chunk;
-    }
+    for (int rt = 0; rt < RT; ++rt)
+      x[rt] = side.x + x_at_part[rt] * side.x_part + (int64_t)(up ? x_pair[rt] / a.top_k : x_pair[rt]) * side.x_cols + 8 * chunk;
 
     f32x4 out[2][RT];
 #pragma unroll
@@ -265,9 +301,6 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
       for (int rt = 0; rt < RT; ++rt) out[t][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     auto x_at = [&](int step, int u, int rt) { return *(const u32x4*)(x[rt] + step * CODES + 32 * u); };
-    struct Inputs {
-      u32x4 v[EARLY ? UNITS : 1][RT];
-    };
     auto load_x = [&](int step, Inputs& in) {
 #pragma unroll
       for (int u = AHEAD; u < UNITS; ++u)
@@ -432,10 +465,8 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
         compute(last, d, in, results);
       }
     };
-    const int places = (act.count - r0) * parts;
-    if (n0 >= width) {
-      // Beyond the last column: zeros, which pad h.
-    } else if (RT == 1 && places <= 4) {
+    const int places = (count - r0) * parts;
+    if (RT == 1 && places <= 4) {
       walk(std::integral_constant<int, 1>{});
     } else if (RT == 1 && places <= 8) {
       walk(std::integral_constant<int, 2>{});
@@ -443,10 +474,21 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
       walk(std::integral_constant<int, 4>{});
     }
 
+    // The sums' places and weights, before the next item's loads.
+    const int from = r0, upto = count, at_n0 = n0;
+    int to_pair[RT];
+    float weight[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int first_token = r0 + rt * fit;
-      if (first_token >= act.count) break;
+      to_pair[rt] = pair[rt];
+      weight[rt] = up ? 0.f : w.weights[pair[rt]];
+    }
+    more = begin_item(r0 + fit * RT);
+
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int first_token = from + rt * fit;
+      if (first_token >= upto) break;
       __syncthreads();
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -454,8 +496,8 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
         for (int i = 0; i < 4; ++i) part_sum[wave][4 * t + i][lane] = out[t][rt][i];
       __syncthreads();
       // This thread's sums: column l15 of both tiles for one token.
-      const int j = threadIdx.x >> 4, n = n0 + l15;
-      if (j >= fit || first_token + j >= act.count) continue;
+      const int j = threadIdx.x >> 4, n = at_n0 + l15;
+      if (j >= fit || first_token + j >= upto) continue;
       float v[2] = {0.f, 0.f};
       for (int p = parts - 1; p >= 0; --p) {
         const int place = j * parts + p, at = place % 4 * 16 + l15;
@@ -468,20 +510,20 @@ __global__ __launch_bounds__(MOE_THREADS, RT == 1 && NS <= 8 ? 3 : 2) void moe_p
         v[0] += s[0];
         v[1] += s[1];
       }
-      const int pair = w.order[act.start + first_token + j];
       if (up) {
-        if (n >= w.h_cols) continue;
         float h = n < a.inter ? v[0] / (1.f + expf(-v[0])) * v[1] : 0.f;
-        uint16_t* to = w.h + (int64_t)pair * w.h_cols + (n & ~7) + place_of_code<WHOLE>(n & 7);
+        uint16_t* to = w.h + (int64_t)to_pair[rt] * w.h_cols + (n & ~7) + place_of_code<WHOLE>(n & 7);
         for (int p = 0; p < side.h_parts; ++p, to += side.h_part) {
           *to = MfmaOp<DT_BF16>::round(h);
           h -= bits16_to_f32<DT_BF16>(*to);
+          // The last tile's pads the row with zeros.
+          if (at_n0 + 16 >= width)
+            for (int k = 16; at_n0 + k < w.h_cols; k += 16) to[k] = 0;
         }
       } else {
-        const float weight = w.weights[pair];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (n + 16 * t < a.hidden) w.out[(int64_t)pair * a.hidden + n + 16 * t] = v[t] * weight;
+          if (n + 16 * t < a.hidden) w.out[(int64_t)to_pair[rt] * a.hidden + n + 16 * t] = v[t] * weight[rt];
       }
     }
   }
@@ -495,11 +537,13 @@ hipError_t launch_rows(const MoeArgs& a, const MoeWork& w, const MoeSide& side) 
   // another costs less than the launch.)
   const int fit = 16 / side.parts, pairs = a.tokens * a.top_k;
   const int many = pairs > fit * a.experts ? std::min(w.max_active, pairs / (fit + 1)) : 0;
+  // As many workgroups as are resident, which go from item to item.
+  auto grid = [&](int experts, int resident) { return dim3((uint32_t)std::min(side.tiles * experts, 256 * resident)); };
   if (many > 0)
     moe_project_kernel<XDT, BITS, WHOLE, SDT, ZP, NS, 4>
-        <<<dim3((uint32_t)side.tiles * many), MOE_THREADS, 0, a.stream>>>(a, w, side, fit + 1, INT32_MAX);
+        <<<grid(many, moe_resident(4, NS)), MOE_THREADS, 0, a.stream>>>(a, w, side, fit + 1, INT32_MAX);
   moe_project_kernel<XDT, BITS, WHOLE, SDT, ZP, NS, 1>
-      <<<dim3((uint32_t)side.tiles * w.max_active), MOE_THREADS, 0, a.stream>>>(a, w, side, 1, many > 0 ? fit : INT32_MAX);
+      <<<grid(w.max_active, moe_resident(1, NS)), MOE_THREADS, 0, a.stream>>>(a, w, side, 1, many > 0 ? fit : INT32_MAX);
   return hipGetLastError();
 }
 

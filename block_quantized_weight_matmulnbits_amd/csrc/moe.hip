@@ -134,19 +134,25 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
   constexpr int PARTS = moe_x_parts(DT);
   if (blockIdx.x > 0) {
     const int chunks = w.x_cols / 8;
-    const int64_t all = (int64_t)a.tokens * chunks;
-    for (int64_t i = (int64_t)(blockIdx.x - 1) * ROUTE_THREADS + threadIdx.x; i < all;
-         i += (int64_t)(gridDim.x - 1) * ROUTE_THREADS) {
-      const int t = (int)(i / chunks), c = (int)(i % chunks) * 8;
+    const int all = a.tokens * chunks;   // at most 2^23
+    for (int i = ((int)blockIdx.x - 1) * ROUTE_THREADS + (int)threadIdx.x; i < all;
+         i += ((int)gridDim.x - 1) * ROUTE_THREADS) {
+      const int t = i / chunks, c = i % chunks * 8;
       const T* from = (const T*)a.x + t * a.x_stride;
+      T v[8];
+      if (c + 8 <= a.hidden) {
+        __builtin_memcpy(v, from + c, sizeof(v));   // at any address
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c + j < a.hidden ? from[c + j] : T(0);
+      }
       uint16_t e[PARTS][8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int k = c + code_at<moe_whole(BITS, DT)>(j);
+        const int k = code_at<moe_whole(BITS, DT)>(j);
         uint16_t part[PARTS];
-        const T v = k < a.hidden ? from[k] : T(0);
-        if constexpr (DT == DT_F32) split_bf16<PARTS>(v, part);
-        else part[0] = __builtin_bit_cast(uint16_t, v);
+        if constexpr (DT == DT_F32) split_bf16<PARTS>(v[k], part);
+        else part[0] = __builtin_bit_cast(uint16_t, v[k]);
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) e[p][j] = part[p];
       }
@@ -158,11 +164,12 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
     return;
   }
   __shared__ __attribute__((aligned(16))) int ids[MAX_PAIRS];
-  __shared__ int upto[ROUTE_WAVES];
+  __shared__ int upto[ROUTE_WAVES], starts[ROUTE_THREADS];
   __shared__ __attribute__((aligned(16))) int counts[ROUTE_THREADS];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int pairs = a.tokens * a.top_k;
   if (threadIdx.x < 4 && pairs + threadIdx.x < MAX_PAIRS) ids[pairs + threadIdx.x] = -1;   // four are read at once
+  counts[threadIdx.x] = 0;
   for (int i = threadIdx.x; i < w.max_active; i += ROUTE_THREADS) w.active[i] = MoeActive{0, 0, 0, 0};
   for (int t = wave; t < a.tokens; t += ROUTE_WAVES) {
     int id;
@@ -177,14 +184,12 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
     }
   }
   __syncthreads();
-  // Thread e counts expert e's pairs and lists them in order.
+  // How many pairs expert e, this thread's, has.
   const int e = threadIdx.x;
-  int count = 0;
-  for (int p = 0; p < pairs; p += 4) {
-    const i32x4 four = *(const i32x4*)(ids + p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) count += four[i] == e;
-  }
+  for (int p = e; p < pairs; p += ROUTE_THREADS)
+    if (ids[p] >= 0) atomicAdd(&counts[ids[p]], 1);
+  __syncthreads();
+  const int count = counts[e];
   // Pairs before this expert's.
   int sum = count;
 #pragma unroll
@@ -193,21 +198,35 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_kernel(MoeArgs a, MoeWork
     if (lane >= o) sum += v;
   }
   if (lane == 63) upto[wave] = sum;
-  counts[e] = count;
   __syncthreads();
-  if (count == 0) return;
   int start = sum - count;
   for (int v = 0; v < wave; ++v) start += upto[v];
-  // The place among the active ones: after those with more.
-  int place = 0;
-  for (int o = 0; o < a.experts; o += 4) {
-    const i32x4 four = *(const i32x4*)(counts + o);
+  starts[e] = start;
+  if (count > 0) {
+    // The place among the active ones: after those with more.
+    int place = 0;
+#pragma unroll 4
+    for (int o = 0; o < a.experts; o += 4) {
+      const i32x4 four = *(const i32x4*)(counts + o);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) place += four[i] > count || (four[i] == count && o + i < e);
+      for (int i = 0; i < 4; ++i) place += four[i] > count || (four[i] == count && o + i < e);
+    }
+    w.active[place] = MoeActive{e, start, count, 0};
   }
-  w.active[place] = MoeActive{e, start, count, 0};
-  for (int p = 0; p < pairs; ++p)
-    if (ids[p] == e) w.order[start++] = p;
+  __syncthreads();
+  // A pair's place: after the same expert's pairs before it.
+  for (int p = threadIdx.x; p < pairs; p += ROUTE_THREADS) {
+    const int id = ids[p];
+    if (id < 0) continue;
+    int place = starts[id];
+#pragma unroll 4
+    for (int q = 0; q < p; q += 4) {
+      const i32x4 four = *(const i32x4*)(ids + q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) place += four[i] == id && q + i < p;
+    }
+    w.order[place] = p;
+  }
 }
 
 // y: the sum of a token's pairs, in their order.
@@ -216,12 +235,19 @@ __global__ __launch_bounds__(256) void combine_kernel(MoeArgs a, MoeWork w) {
   const int t = blockIdx.y, n = blockIdx.x * 256 + threadIdx.x;
   if (n >= a.hidden) return;
   float sum = 0.f;
-#pragma unroll 8
-  for (int j = 0; j < a.top_k; ++j) {
-    // What stands there for a pair without an expert is loaded and not used.
-    const int pair = t * a.top_k + j;
-    const float v = w.out[(int64_t)pair * a.hidden + n];
-    sum += w.ids[pair] >= 0 ? v : 0.f;
+  // Eight at once; what stands there for a pair without an expert is loaded and not
+  // used.
+  for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+    float v[8];
+    int id[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int pair = t * a.top_k + min(j0 + j, a.top_k - 1);
+      v[j] = w.out[(int64_t)pair * a.hidden + n];
+      id[j] = w.ids[pair];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += j0 + j < a.top_k && id[j] >= 0 ? v[j] : 0.f;
   }
   ((typename dt<DT>::T*)a.y)[t * a.y_stride + n] = dt<DT>::from_f32(sum);
 }
@@ -233,7 +259,7 @@ hipError_t launch(const MoeArgs& a, const MoeWork& w) {
   route_kernel<DT, BITS><<<dim3(1 + stage), ROUTE_THREADS, 0, a.stream>>>(a, w);
   hipError_t e = hipGetLastError();
   const int64_t x_part = (int64_t)a.tokens * w.x_cols, h_part = (int64_t)a.tokens * a.top_k * w.h_cols;
-  const MoeSide up{true, w.h_cols / 16, moe_x_parts(DT), moe_h_parts(DT), w.x, x_part, h_part, w.x_cols};
+  const MoeSide up{true, (a.inter + 15) / 16, moe_x_parts(DT), moe_h_parts(DT), w.x, x_part, h_part, w.x_cols};
   const MoeSide down{false, (a.hidden + 31) / 32, moe_h_parts(DT), 0, w.h, h_part, 0, w.h_cols};
   // h is bf16 in every layer.
   if (e == hipSuccess)
