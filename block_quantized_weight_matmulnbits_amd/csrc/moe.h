@@ -5,7 +5,17 @@
 // 16 of the up projection, or 32 of the down projection) for all of the expert's
 // tokens, up to 16 RT at a time; its four waves split K step by step (128 bytes of
 // codes a row, a line of the caches) and join through LDS.  Weights are read once, straight into
-// registers, 16 bytes a lane; HBM is the bound.
+// registers, 16 bytes a lane.  As many workgroups as are resident (three a compute
+// unit, by the registers) go from item to item, and an item's first step is loaded
+// while the one before it is joined: against a workgroup an item, one token over
+// two experts took 52 us instead of 55, six of 64 narrow experts 68 instead of 72.
+//
+// HBM is the bound, at 0.81 of a large copy's rate where every weight of eight wide
+// experts is read (hidden 4096, inter 14336, 16 tokens of f16, blocks of 32: up 135 us
+// = 3.9 TB/s, down 75 us = 3.5), 0.7 for one token (29 us = 4.2 TB/s and 18 to 20 us
+// = 3.2: 256 workgroups, whose beginning and end weigh more; K cut in three filled the
+// chip and changed nothing), 0.5 for narrow ones (rows of 5 to 8 steps: two for
+// a wave, so that joins and the wait for inputs show; 33 and 23 us).
 //
 // The matrix cores multiply x (an f32 one in three bf16 parts, h in two or three:
 // a row each, so that few tokens fill the instruction's 16) with whole numbers,

@@ -1,6 +1,12 @@
 // moe.hip -- a layer of experts on block-quantized weights for a few tokens:
 // the router's choice, the gate and up projections with SiLU, the down
 // projection, and the sum over a token's experts.
+//
+// Four launches: the sum needs all of a token's experts, the down projection all of
+// h, both projections the list of pairs by expert.  The first (4 to 8 us) and the
+// last (3 to 5 us) are chains of dependent loads on a few workgroups; the first
+// lays x out for the matrix cores beside the choice, which would otherwise be
+// done by every workgroup again.
 #include <algorithm>
 
 #include "moe.h"

@@ -13,7 +13,10 @@
 // Bound by HBM: x and the residual in, h and the codes out.  A row is read
 // once and stays in registers, eight elements of a thread side by side, so that
 // the blocks that share a scale are groups of neighbouring lanes and their
-// maxima a few cross-lane steps.
+// maxima a few cross-lane steps.  Workgroups of a row's width go from row to row,
+// the next one loaded ahead: 16384 rows of 4096 bf16 with residual and MX codes take
+// 111 us (4.25 TB/s; 158 with a workgroup a row), 777 f32 rows of 5001 12.4 us (2.8 TB/s).
+// One row takes 3.4 us on the device, of which most is the launch.
 #include <algorithm>
 #include <type_traits>
 

@@ -19,6 +19,14 @@
 // the list, and the chunk and the token that u falls on.  The list is long only
 // where thousands of logits are nearly equal; such a row is searched as a whole.
 // Rows that fit the list are done in one launch.
+//
+// The bound is not memory: one row of 131072 (0.26 MB) takes 3.8 + 6.9 + 7.0 + 11.0
+// us in its four launches, each a chain of dependent loads, scans and barriers; 64
+// rows with settings of their own take 10 (1.7 TB/s) + 20 + 23 + 17 us, where the
+// rows that filter by top-p or not at all need a 64-bit exp for every token and
+// come to lie on the same compute units.  An exp with half of the 64-bit operations
+// (32 roots of 2 in LDS and 6 terms) and lists gathered in LDS before one atomic were
+// each slower by their own start.
 #include <algorithm>
 
 #include "decode.h"

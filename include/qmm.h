@@ -501,7 +501,8 @@ typedef struct qmm_quant {
  * bit.
  *   residual   or NULL: h = x
  *   h, y, quant  outputs, each or NULL (one at least is wanted); h and y may be
- *              x's or residual's own rows (same address and stride)
+ *              x's or residual's own rows (same address and stride); nothing
+ *              else may overlap
  *   weight     [cols] of weight_dtype, or NULL: ones; offset is added to it
  *   cols       1 .. 2^20;  rows = 0 is a no-op
  */
@@ -566,8 +567,9 @@ typedef struct qmm_moe_route {
 /*
  * y[t] = sum_j w_tj down_e(silu(gate_e x_t) * (up_e x_t)),   e = id_tj,
  * silu(a) = a / (1 + exp(-a)), for x and y [tokens, hidden] of dtype (rows with
- * strides; y may be x).  Only the chosen experts' weights are read, once for all
- * of up to 64 tokens of an expert.  Products are of x and whole codes, summed in
+ * strides; y may be x).  Only the chosen experts' weights are read, once for 16
+ * tokens of an expert (8 in the down projection, 5 in f32 layers), or four times
+ * as many where experts have more than those on the average.  Products are of x and whole codes, summed in
  * fp32, each block's sum then scaled; between the projections an f32 layer keeps
  * 24 bits and a 16-bit one 16 bits of every value; y is rounded once.  A token
  * without experts gets 0.  Values of x that are not finite make the token's own
