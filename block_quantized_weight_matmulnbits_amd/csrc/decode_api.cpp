@@ -148,6 +148,13 @@ int qmm_rms_norm(const qmm_rows* x, const qmm_rows* residual, const qmm_rows* h,
     return fail(QMM_ERR_INVALID_ARG, "%s: weight must be aligned to its element size.", fn);
   if (h != nullptr && y != nullptr && h->data == y->data)
     return fail(QMM_ERR_INVALID_ARG, "%s: h and y are two outputs and cannot be the same rows.", fn);
+  for (const qmm_rows* in : {x, residual})
+    for (const qmm_rows* out : {h, y})
+      if (in != nullptr && out != nullptr && in->data == out->data && in->stride != out->stride && rows > 1)
+        return fail(QMM_ERR_INVALID_ARG, "%s: an output begins where an input does, with rows of stride "
+                    "%lld over rows of stride %lld. Why: rows would be written before they are read. How "
+                    "to fix: pass the input's own rows, or rows apart from it.", fn,
+                    (long long)out->stride, (long long)in->stride);
   a.x = (const char*)x->data;
   a.x_stride = x->stride;
   if (residual) a.residual = (const char*)residual->data, a.residual_stride = residual->stride;

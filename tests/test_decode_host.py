@@ -100,6 +100,8 @@ def test_norm_refuses(qmm):
             (dict(residual=r(FAKE, 511)), -1, "residual.stride=511 does not hold a row"),
             (dict(h=r(FAKE, -512)), -1, "h.stride"), (dict(y=r(FAKE, 1 << 40)), -1, "y.stride"),
             (dict(weight=FAKE + 1), -1, "weight must be aligned"), (dict(h="h"), -1, "cannot be the same rows"),
+            (dict(y=r(FAKE, 520)), -1, "rows of stride 520 over rows of stride 512"),
+            (dict(x=r(2 * FAKE), residual="r", h=r(FAKE, 640), y=None), -1, "rows of stride 640 over"),
             (dict(quant=q(kind=3)), -1, "not a qmm_quant_kind"), (dict(quant=q(block=24)), -1, "power of two"),
             (dict(quant=q(block=8)), -1, "power of two"), (dict(quant=q(block=1 << 21)), -1, "power of two"),
             (dict(quant=q(kind=1, fmt=2)), -1, "QMM_LOWP_E4M3 or QMM_LOWP_E5M2"),
