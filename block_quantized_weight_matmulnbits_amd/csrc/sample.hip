@@ -20,9 +20,9 @@
 // where thousands of logits are nearly equal; such a row is searched as a whole.
 // Rows that fit the list are done in one launch.
 //
-// The bound is not memory: one row of 131072 (0.26 MB) takes 3.8 + 6.9 + 7.0 + 11.0
+// The bound is not memory: one row of 131072 (0.26 MB) takes 3.5 + 6.8 + 7.6 + 10.6
 // us in its four launches, each a chain of dependent loads, scans and barriers; 64
-// rows with settings of their own take 10 (1.7 TB/s) + 20 + 23 + 17 us, where the
+// rows with settings of their own take 10 (1.7 TB/s) + 20 + 22 + 16 us, where the
 // rows that filter by top-p or not at all need a 64-bit exp for every token and
 // come to lie on the same compute units.  An exp with half of the 64-bit operations
 // (32 roots of 2 in LDS and 6 terms) and lists gathered in LDS before one atomic were
@@ -113,7 +113,8 @@ __device__ __forceinline__ int index_of(uint64_t place) {
 // |r| <= ln 2 / 2 (its rest is below 2^-52 of the value).  Where the result would
 // be far below 1 it is 0.
 __device__ __forceinline__ double exp_f64(double x, int shift) {
-  if (!(x > -700.0)) return 0.0;
+  const bool far = !(x > -700.0);
+  x = far ? 0.0 : x;
   const double n = rint(x * 1.4426950408889634074);
   // ln 2 in two parts, the first of 31 bits, so that n times it is exact.
   double r = __builtin_fma(n, -0x1.62e42ff000000p-1, x);
@@ -131,7 +132,7 @@ __device__ __forceinline__ double exp_f64(double x, int shift) {
   p = __builtin_fma(p, r, 0.5);
   p = __builtin_fma(p, r, 1.0);
   p = __builtin_fma(p, r, 1.0);
-  return ldexp(p, (int)n + shift);
+  return far ? 0.0 : ldexp(p, (int)n + shift);
 }
 
 // A row's settings and the weights of its tokens.
@@ -147,8 +148,8 @@ struct Row {
   // The weight in units of 2^-shift, before it is rounded to a whole number.
   __device__ __forceinline__ double weight(float l) const {
     // Infinite logits share everything equally.
-    if (top == INFINITY) return l == INFINITY ? ldexp(1.0, shift) : 0.0;
-    return exp_f64(((double)l - (double)top) * over_t, shift);
+    const double d = l == top ? 0.0 : (double)l - (double)top;
+    return exp_f64(d * over_t, shift);
   }
   // The nearest whole number of a w <= 2^62: its upper and lower 32 bits.
   static __device__ __forceinline__ uint64_t units(double w) {
@@ -217,37 +218,37 @@ __device__ __forceinline__ uint64_t wave_upto_u64(uint64_t v, int lane) {
   return v;
 }
 
-// body(i, logit) for the tokens [begin, end) of a row, eight side by side a thread,
-// and after(i0) for every STEP of them; AHEAD steps are loaded at once.
+// body(i, logits, n) for the tokens [begin, end) of a row, n <= EIGHT side by side a
+// thread (past n: minus infinity), and after(i0) for every STEP of them; AHEAD steps
+// are loaded at once.
+constexpr int EIGHT = 8;
 template <int DT, int AHEAD, typename Body, typename After>
-__device__ __forceinline__ void each_token(const char* row, int begin, int end, Body body, After after) {
+__device__ __forceinline__ void each_eight(const char* row, int begin, int end, Body body, After after) {
   using T = typename dt<DT>::T;
   for (int i0 = begin; i0 < end; i0 += STEP * AHEAD) {
-    T e[AHEAD][8];
+    T e[AHEAD][EIGHT];
 #pragma unroll
     for (int v = 0; v < AHEAD; ++v) {
-      const int i = i0 + v * STEP + (int)threadIdx.x * 8;
-      if (i + 8 <= end) {
+      const int i = i0 + v * STEP + (int)threadIdx.x * EIGHT;
+      if (i + EIGHT <= end) {
         __builtin_memcpy(e[v], (const T*)row + i, sizeof(e[v]));   // at any address
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) e[v][j] = ((const T*)row)[i + j < end ? i + j : end - 1];
+        for (int j = 0; j < EIGHT; ++j) e[v][j] = ((const T*)row)[i + j < end ? i + j : end - 1];
       }
     }
 #pragma unroll
     for (int v = 0; v < AHEAD; ++v) {
-      const int i = i0 + v * STEP + (int)threadIdx.x * 8;
-      auto one = [&](int j) {
-        const float l = dt<DT>::to_f32(e[v][j]);
-        body(i + j, l != l ? -INFINITY : l);
-      };
-      if (i + 8 <= end) {
+      const int i = i0 + v * STEP + (int)threadIdx.x * EIGHT;
+      const int n = min(EIGHT, end - i);
+      if (n > 0) {
+        float l[EIGHT];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) one(j);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (i + j < end) one(j);
+        for (int j = 0; j < EIGHT; ++j) {
+          l[j] = dt<DT>::to_f32(e[v][j]);
+          l[j] = j < n && l[j] == l[j] ? l[j] : -INFINITY;
+        }
+        body(i, l, n);
       }
       if (i0 + v * STEP < end) after(i0 + v * STEP);
     }
@@ -273,9 +274,12 @@ __global__ __launch_bounds__(PASS_THREADS) void first_kernel(SampleArgs a, RowWo
   // A thread meets its tokens in their order: the first of equal ones stays.
   float top = -INFINITY;
   int at = begin;
-  each_token<DT, 4>(row_at<DT>(a, row), begin, end, [&](int i, float l) {
-    at = l > top ? i : at;
-    top = fmaxf(top, l);
+  each_eight<DT, 4>(row_at<DT>(a, row), begin, end, [&](int i, const float (&l)[EIGHT], int) {
+#pragma unroll
+    for (int j = 0; j < EIGHT; ++j) {
+      at = l[j] > top ? i + j : at;
+      top = fmaxf(top, l[j]);
+    }
   }, [](int) {});
   uint64_t best = top == -INFINITY ? place_of<DT>(top, begin) : place_of<DT>(top, at);
   __shared__ uint64_t waves[PASS_THREADS / 64];
@@ -310,13 +314,22 @@ __global__ __launch_bounds__(PASS_THREADS) void bucket_kernel(SampleArgs a, RowW
   }
   __syncthreads();
   const bool weigh = r.p < 1.0;
-  each_token<DT, 2>(logits, begin, end, [&](int, float l) {
-    const int b = r.bucket(l);
-    atomicAdd(&count[b], 1u);
-    if (weigh) {
-      const uint64_t n = r.units(r.weight(l));
-      if (n) atomicAdd((unsigned long long*)&weight[b], (unsigned long long)n);
-    }
+  // Eight exps at once: one after another, each waited for the last one's steps (7 f32
+  // rows of 50021: 17.0 us, 15.9 so).
+  each_eight<DT, 2>(logits, begin, end, [&](int, const float (&l)[EIGHT], int n) {
+    int b[EIGHT];
+#pragma unroll
+    for (int j = 0; j < EIGHT; ++j) b[j] = r.bucket(l[j]);
+#pragma unroll
+    for (int j = 0; j < EIGHT; ++j)
+      if (j < n) atomicAdd(&count[b[j]], 1u);
+    if (!weigh) return;
+    uint64_t units[EIGHT];
+#pragma unroll
+    for (int j = 0; j < EIGHT; ++j) units[j] = Row::units(r.weight(l[j]));
+#pragma unroll
+    for (int j = 0; j < EIGHT; ++j)
+      if (units[j]) atomicAdd((unsigned long long*)&weight[b[j]], (unsigned long long)units[j]);
   }, [](int) {});
   __syncthreads();
   for (int b = threadIdx.x; b < BUCKETS; b += PASS_THREADS) {
@@ -433,16 +446,35 @@ __global__ __launch_bounds__(PASS_THREADS) void list_kernel(SampleArgs a, RowWor
   }
   __shared__ uint64_t waves[MAX_TILES][PASS_THREADS / 64];
   uint64_t sum = 0;
-  each_token<DT, 2>(logits, begin, end, [&](int i, float l) {
-    const int b = all ? 0 : r.bucket(l);
-    if (all || e.before(b)) {
-      if (l < r.little) return;
-      const double x = r.weight(l);
-      if (x >= r.min_units) sum += Row::units(x);
-    } else if (e.at(b)) {
-      // In any order: the list is a set.
-      const uint32_t at = atomicAdd(&w.listed, 1u);
-      if (at < LIST) w.list[at] = i;
+  each_eight<DT, 2>(logits, begin, end, [&](int i, const float (&l)[EIGHT], int n) {
+    bool weigh[EIGHT], any = false;
+#pragma unroll
+    for (int j = 0; j < EIGHT; ++j) {
+      const int b = all ? 0 : r.bucket(l[j]);
+      const bool before = all || e.before(b);
+      weigh[j] = before && l[j] > -INFINITY && !(l[j] < r.little);
+      any |= weigh[j];
+      if (!before && e.at(b) && j < n) {
+        // In any order: the list is a set.
+        const uint32_t at = atomicAdd(&w.listed, 1u);
+        if (at < LIST) w.list[at] = i + j;
+      }
+    }
+    if (!any) return;
+    if (r.min_units > 0.0) {
+      // Few of them: 256 rows with min_p take 34 us with eight exps at once, 30 so.
+#pragma unroll
+      for (int j = 0; j < EIGHT; ++j)
+        if (weigh[j]) {
+          const double x = r.weight(l[j]);
+          if (x >= r.min_units) sum += Row::units(x);
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < EIGHT; ++j) {
+        const uint64_t n_units = Row::units(r.weight(l[j]));
+        sum += weigh[j] ? n_units : 0;
+      }
     }
   }, [&](int i0) {
     // The end of a tile, or of the row.
@@ -754,7 +786,9 @@ __global__ __launch_bounds__(LAST_THREADS) void last_kernel(SampleArgs a, RowWor
 }
 
 // Tiles of 2048 tokens where 64 of them hold the row.  Chunks: some four
-// workgroups a compute unit, since each has to clear, add and read the buckets.
+// workgroups a compute unit, since each has to clear, add and read the buckets (64
+// rows of 131072 with two, four, eight: 87, 70, 69 us under the profiler; 256 of 32000:
+// 34, 32, 33).
 Cut cut_of(int64_t rows, int64_t vocab) {
   Cut c;
   c.tile = (int)((vocab + MAX_TILES * STEP - 1) / (MAX_TILES * STEP) * STEP);

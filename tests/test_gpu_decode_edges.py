@@ -71,6 +71,17 @@ def test_min_p_next_to_a_weight(qmm, top, temperature):
         u = (u + 0.37) % 1
 
 
+def test_min_p_under_a_temperature_beyond_logits(qmm):
+    """T log min_p past 1e30: weights of 1, 0.14 and 0, of which min_p leaves the first."""
+    z = torch.full((3, 5000), -2e31)
+    z[:, 17] = z[:, 4000] = 0.0
+    z[1] = -3e38
+    z[1, 40] = 1.0
+    u = torch.tensor([0.3, 0.9, 0.7])
+    tokens = check_tokens(qmm, z, u, temperature=1e31, min_p=[0.5, 0.5, 0.1])
+    assert tokens[:2].tolist() == [17, 40]
+
+
 def test_recorded_steps_share_workspaces(qmm):
     ex = ref.Experts(6, 128, 96, 32, 4, seed=24)
     w = on_gpu(qmm, ex)
