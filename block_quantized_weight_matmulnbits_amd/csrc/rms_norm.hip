@@ -231,21 +231,22 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rms_norm_kernel(NormArgs 
         for (int j = 0; j < CHUNK; ++j) y[j] = c + j < a.cols ? y[j] : 0.f;
       }
     };
+    // The largest magnitude, as the bits that order so, a NaN's above infinity's:
+    // a code is a whole number, so that only the scale can say of a NaN.
     auto chunk_top = [&](const float (&y)[CHUNK]) {
-      float m = 0.f;
+      uint32_t m = 0u;
 #pragma unroll
-      for (int j = 0; j < CHUNK; ++j) m = fmaxf(m, fabsf(y[j]));
+      for (int j = 0; j < CHUNK; ++j) m = max(m, __float_as_uint(y[j]) & 0x7FFFFFFFu);
       return m;
     };
     if constexpr (WAVES > 1) {
-      // Blocks that several waves share: their maxima meet in LDS (the bits of
-      // floats that are not negative order as they do).
+      // Blocks that several waves share: their maxima meet in LDS.
       if (wide) {
         each_piece<NP>(pieces, [&](int p) {
           const int c = (p * RT + t) * CHUNK;
           float y[CHUNK];
           normed(p, y);
-          if (c < a.code_cols) atomicMax(&tops[c >> log_block], __float_as_uint(chunk_top(y)));
+          if (c < a.code_cols) atomicMax(&tops[c >> log_block], chunk_top(y));
         });
         __syncthreads();
       }
@@ -260,26 +261,29 @@ __global__ __launch_bounds__(RT < 256 ? 256 : RT) void rms_norm_kernel(NormArgs 
       if constexpr (KIND == QUANT_NONE) return;
       uint32_t word[2] = {0u, 0u};
       if constexpr (KIND == QUANT_INT8) {
-        float top = chunk_top(y);
+        uint32_t most = chunk_top(y);
         if (wide) {
-          top = __uint_as_float(c < a.code_cols ? tops[c >> log_block] : 0u);
+          most = c < a.code_cols ? tops[c >> log_block] : 0u;
         } else {
-          for (int o = 1; o < a.block / CHUNK; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+          for (int o = 1; o < a.block / CHUNK; o <<= 1) most = max(most, (uint32_t)__shfl_xor((int)most, o));
         }
-        const float s = top * (1.f / 127.f);
+        const float s = __uint_as_float(most) * (1.f / 127.f);
         if (c < a.code_cols && (c & (a.block - 1)) == 0)
           ((float*)a.scales)[row * a.blocks + (c >> log_block)] = s;
+        const bool coded = s > 0.f && s < INFINITY;
 #pragma unroll
         for (int j = 0; j < CHUNK; ++j) {
           const float q = fminf(fmaxf(rintf(y[j] / s), -127.f), 127.f);
-          word[j / 4] |= (s != 0.f ? (uint32_t)(int)q & 0xFFu : 0u) << (8 * (j % 4));
+          word[j / 4] |= (coded ? (uint32_t)(int)q & 0xFFu : 0u) << (8 * (j % 4));
         }
       } else {
         float q[CHUNK];
         // A sum is NaN where one of its terms is (or infinities meet).
         float sum = 0.f;
         if constexpr (KIND == QUANT_MX) {
-          float top = chunk_top(y);
+          float top = 0.f;                            // skips NaN, which has a code
+#pragma unroll
+          for (int j = 0; j < CHUNK; ++j) top = fmaxf(top, fabsf(y[j]));
           top = fmaxf(top, neighbour<0xB1>(top));     // four lanes a block
           top = fmaxf(top, neighbour<0x4E>(top));
           // The exponent of the scale that would put the maximum on the

@@ -806,7 +806,7 @@ def qmm_rms_norm(x, weight, residual=None, h=None, y=None, eps=1e-5, offset=0.0,
     """h = x + residual and y = h / rms(h) * (weight + offset) for x [rows, cols],
     each where its tensor is given, and y in 8 bits: ``codes`` and ``scales`` with
     layout "block" ("int8" codes [rows, kb * block_size], float32 scales [rows, kb],
-    for qmm_gemm_compint8_quantized), "mx" ("e4m3" / "e5m2" codes [rows, cols], E8M0
+    nan or infinite where a block holds one, for qmm_gemm_compint8_quantized), "mx" ("e4m3" / "e5m2" codes [rows, cols], E8M0
     scales [rows, ceil(cols / 32)], for qmm_lowp_matmul) or "tensor" (FP8 codes by
     the float32 scale [1] given)."""
     gpu, args = _norm_args(x, weight, residual, h, y, eps, offset, codes, scales, fmt, layout, block_size)

@@ -470,7 +470,9 @@ typedef enum qmm_quant_kind {
     /* int8 codes [rows, kb * block_size] and f32 scales [rows, kb], kb =
      * ceil(cols / block_size), block_size a power of two from 16 to 2^20, as
      * qmm_gemm_compint8_quantized reads them: scale = amax * (1 / 127), code =
-     * y / scale rounded half to even (0 where the scale is 0, and past cols). */
+     * y / scale rounded half to even (0 where the scale is 0, and past cols).  A
+     * nan in a block makes its scale nan, else an infinity makes it infinite; the
+     * codes of such a block are 0, and a product that reads them is nan. */
     QMM_QUANT_INT8 = 0,
     /* FP8 codes [rows, cols] and E8M0 scales [rows, ceil(cols / 32)], as
      * qmm_lowp_matmul reads them with QMM_LOWP_MX: the scale is the exponent field
@@ -496,9 +498,9 @@ typedef struct qmm_quant {
  *   i = 1 / sqrt(sum(h^2) / cols + eps).
  * h is formed in fp32, the sum and i in 64 bits; i is rounded to fp32 and each
  * product to fp32.  The outputs h and y are rounded once to dtype; quant's codes
- * are made of the unrounded fp32 y (reciprocals and products of scales in fp32,
- * maxima skip nan), so that they and their scales are the definition's bit for
- * bit.
+ * are made of the unrounded fp32 y (reciprocals and products of scales in fp32;
+ * MX's maxima skip nan, which has a code), so that they and their scales are the
+ * definition's bit for bit.
  *   residual   or NULL: h = x
  *   h, y, quant  outputs, each or NULL (one at least is wanted); h and y may be
  *              x's or residual's own rows (same address and stride); nothing
