@@ -22,6 +22,7 @@ struct NormArgs {
   float offset = 0.f;
   double eps = 0.0;
   int kind = QUANT_NONE, format = 0, block = 0;   // block: codes that share a scale
+  float top_factor = 0.f;                         // MX: the scale is the exponent of it times the maximum
   uint8_t* codes = nullptr;                       // rows of code_cols bytes
   void* scales = nullptr;
   int code_cols = 0, blocks = 0;                  // of a row

@@ -113,7 +113,8 @@ int qmm_rms_norm(const qmm_rows* x, const qmm_rows* residual, const qmm_rows* h,
   if (x == nullptr) return fail(QMM_ERR_INVALID_ARG, "%s: x is NULL.", fn);
   qmm::NormArgs a;
   if (quant != nullptr) {
-    if (quant->kind != QMM_QUANT_INT8 && quant->kind != QMM_QUANT_MX && quant->kind != QMM_QUANT_TENSOR)
+    const bool ocp = quant->kind == QMM_QUANT_MX_OCP, mx = quant->kind == QMM_QUANT_MX || ocp;
+    if (quant->kind != QMM_QUANT_INT8 && !mx && quant->kind != QMM_QUANT_TENSOR)
       return fail(QMM_ERR_INVALID_ARG, "%s: quant.kind=%d is not a qmm_quant_kind.", fn, quant->kind);
     const bool ints = quant->kind == QMM_QUANT_INT8;
     if (ints && (quant->block_size < 16 || quant->block_size > qmm::NORM_MAX_COLS ||
@@ -125,11 +126,13 @@ int qmm_rms_norm(const qmm_rows* x, const qmm_rows* residual, const qmm_rows* h,
       return fail(QMM_ERR_INVALID_ARG, "%s: quant.format=%d must be QMM_LOWP_E4M3 or QMM_LOWP_E5M2. "
                   "Why: the output holds 8 bits an element.", fn, quant->format);
     if (rows > 0 && (quant->codes == nullptr || quant->scales == nullptr ||
-                     (quant->kind != QMM_QUANT_MX && !aligned(quant->scales, 4))))
+                     (!mx && !aligned(quant->scales, 4))))
       return fail(QMM_ERR_INVALID_ARG, "%s: quant.codes and quant.scales must be non-null device "
                   "pointers (float32 scales 4-byte aligned).", fn);
-    a.kind = quant->kind;
+    a.kind = mx ? qmm::QUANT_MX : quant->kind;
     a.format = quant->format;
+    if (mx)
+      a.top_factor = a.format == QMM_LOWP_E4M3 ? (ocp ? 0x1p-8f : 1.f / 448.f) : (ocp ? 0x1p-15f : 1.f / 57344.f);
     a.block = ints ? quant->block_size : 32;
     a.blocks = (int)((cols + a.block - 1) / a.block);
     a.code_cols = ints ? a.blocks * a.block : (int)cols;

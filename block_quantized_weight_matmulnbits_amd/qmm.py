@@ -724,8 +724,8 @@ def qmm_pages_compact(pool, refs_out, table_out, live, workspace, stream=None):
 _pack_rows = struct.Struct("@Pq").pack
 _pack_quant = struct.Struct("@iii4xPP").pack
 
-QMM_QUANT_INT8, QMM_QUANT_MX, QMM_QUANT_TENSOR = 0, 1, 2
-QUANT_LAYOUTS = {"block": QMM_QUANT_INT8, "mx": QMM_QUANT_MX, "tensor": QMM_QUANT_TENSOR}
+QMM_QUANT_INT8, QMM_QUANT_MX, QMM_QUANT_TENSOR, QMM_QUANT_MX_OCP = 0, 1, 2, 4
+QUANT_LAYOUTS = {"block": QMM_QUANT_INT8, "mx": QMM_QUANT_MX, "tensor": QMM_QUANT_TENSOR, "mx_ocp": QMM_QUANT_MX_OCP}
 _BYTES = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
 
 
@@ -769,7 +769,7 @@ def _quant_struct(codes, scales, rows, cols, fmt, layout, block_size):
         raise ValueError(f'fmt must be "e4m3" or "e5m2" with layout {layout!r}, got {fmt!r}')
     if codes.dtype not in _BYTES:
         raise ValueError(f"codes must be uint8 or an 8-bit float, got {codes.dtype}")
-    if kind == QMM_QUANT_MX:
+    if kind in (QMM_QUANT_MX, QMM_QUANT_MX_OCP):
         if scales.dtype not in (torch.uint8, torch.float8_e8m0fnu):
             raise ValueError(f"scales must be E8M0 bytes (uint8 or float8_e8m0fnu), got {scales.dtype}")
         s = _dense("scales", scales, (rows, -(-cols // 32)), scales.dtype)
@@ -807,8 +807,10 @@ def qmm_rms_norm(x, weight, residual=None, h=None, y=None, eps=1e-5, offset=0.0,
     each where its tensor is given, and y in 8 bits: ``codes`` and ``scales`` with
     layout "block" ("int8" codes [rows, kb * block_size], float32 scales [rows, kb],
     nan or infinite where a block holds one, for qmm_gemm_compint8_quantized), "mx" ("e4m3" / "e5m2" codes [rows, cols], E8M0
-    scales [rows, ceil(cols / 32)], for qmm_lowp_matmul) or "tensor" (FP8 codes by
-    the float32 scale [1] given)."""
+    scales [rows, ceil(cols / 32)], for qmm_lowp_matmul; the scale that
+    qmm_lowp_quantize takes, which clips a block's largest values), "mx_ocp" (the same
+    with the Microscaling formats' scale, which keeps them: a fifth to a third of the
+    error) or "tensor" (FP8 codes by the float32 scale [1] given)."""
     gpu, args = _norm_args(x, weight, residual, h, y, eps, offset, codes, scales, fmt, layout, block_size)
     _check(lib.qmm_rms_norm(*args, _stream_at(gpu, stream)))
 
