@@ -830,7 +830,8 @@ def _quantized_args(qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size
 def qmm_gemm_compint8_quantized(qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size, bits,
                                 stream=None):
     """qmm_gemm_compint8 on int8 activations ``qa`` [M, kb * block_size] and their
-    scales ``sa`` [M, kb] float32, as qmm_rms_norm writes them."""
+    scales ``sa`` [M, kb] float32, as qmm_rms_norm writes them: its result bit for
+    bit, or for one row of a repacked weight to within the order of fp32 sums."""
     gpu, args = _quantized_args(qa, sa, B, scales, zero_points, bias, Y, M, K, N, block_size, bits)
     _check(lib.qmm_gemm_compint8_quantized(*args, _stream_at(gpu, stream)))
 

@@ -526,9 +526,11 @@ int qmm_rms_norm(const qmm_rows *x, const qmm_rows *residual, const qmm_rows *h,
  * qmm_gemm_compint8 on activations that are quantized already: qa [M, kb *
  * block_size] int8 (16-byte aligned) and sa [M, kb] float32, as QMM_QUANT_INT8
  * writes them with the weight's block_size; y_dtype is the dtype of bias and Y.
- * The other arguments, the kernels and the result are qmm_gemm_compint8's on the
- * same codes and scales; no workspace, no group indices, and on the tiled layout
- * block_size >= 32 for every M.
+ * The other arguments are qmm_gemm_compint8's, and so are the kernels and, bit for
+ * bit, the result on the same codes and scales; but for M = 1 on the tiled layout,
+ * where qmm_gemm_compint8 quantizes within a kernel of its own that adds in another
+ * order (either is off by roundings of fp32).  No workspace, no group indices, and
+ * on the tiled layout block_size >= 32 for every M.
  */
 int qmm_gemm_compint8_quantized(const int8_t *qa, const float *sa, const uint8_t *B,
                                 int b_layout, const void *scales, int s_dtype,
