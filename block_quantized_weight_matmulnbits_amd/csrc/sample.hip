@@ -109,14 +109,14 @@ __device__ __forceinline__ int index_of(uint64_t place) {
   return (1 << INDEX_BITS) - 1 - (int)(place & ((1 << INDEX_BITS) - 1));
 }
 
-// exp(x) 2^shift for x <= 0 in 64 bits: 2^n times a Taylor polynomial of 12 terms in
-// |r| <= ln 2 / 2 (its rest is below 2^-52 of the value).  Where the result would
-// be far below 1 it is 0.
+// exp(x) 2^shift for x <= 0 in 64 bits: 2^n times the Taylor polynomial of degree 12
+// in |r| <= ln 2 / 2 (its rest is at most 1.04 2^-52 of the value).  Where the result
+// would be far below 1 it is 0.
 __device__ __forceinline__ double exp_f64(double x, int shift) {
   const bool far = !(x > -700.0);
   x = far ? 0.0 : x;
   const double n = rint(x * 1.4426950408889634074);
-  // ln 2 in two parts, the first of 31 bits, so that n times it is exact.
+  // ln 2 in two parts, the first of 29 bits, so that n times it is exact.
   double r = __builtin_fma(n, -0x1.62e42ff000000p-1, x);
   r = __builtin_fma(n, 0x1.718432a1b0e26p-35, r);
   double p = 1.0 / 479001600.0;
