@@ -726,7 +726,8 @@ _pack_quant = struct.Struct("@iii4xPP").pack
 
 QMM_QUANT_INT8, QMM_QUANT_MX, QMM_QUANT_TENSOR, QMM_QUANT_MX_OCP = 0, 1, 2, 4
 QUANT_LAYOUTS = {"block": QMM_QUANT_INT8, "mx": QMM_QUANT_MX, "tensor": QMM_QUANT_TENSOR, "mx_ocp": QMM_QUANT_MX_OCP}
-_BYTES = (torch.uint8, torch.float8_e4m3fn, torch.float8_e5m2)
+# The formats that a tensor of 8-bit codes may hold.
+_BYTES = {torch.uint8: ("e4m3", "e5m2"), torch.float8_e4m3fn: ("e4m3",), torch.float8_e5m2: ("e5m2",)}
 
 
 def _apart(**tensors):
@@ -765,10 +766,12 @@ def _quant_struct(codes, scales, rows, cols, fmt, layout, block_size):
         kb = -(-cols // block_size)
         return _pack_quant(kind, 0, block_size, _dense("codes", codes, (rows, kb * block_size), torch.int8),
                            _dense("scales", scales, (rows, kb), torch.float32))
-    if fmt not in LOWP_FORMATS:
+    if fmt not in _BYTES[torch.uint8]:
         raise ValueError(f'fmt must be "e4m3" or "e5m2" with layout {layout!r}, got {fmt!r}')
     if codes.dtype not in _BYTES:
         raise ValueError(f"codes must be uint8 or an 8-bit float, got {codes.dtype}")
+    if fmt not in _BYTES[codes.dtype]:
+        raise ValueError(f"codes of {codes.dtype} hold another format than fmt={fmt!r}: pass the format's own type or uint8")
     if kind in (QMM_QUANT_MX, QMM_QUANT_MX_OCP):
         if scales.dtype not in (torch.uint8, torch.float8_e8m0fnu):
             raise ValueError(f"scales must be E8M0 bytes (uint8 or float8_e8m0fnu), got {scales.dtype}")
