@@ -17,12 +17,14 @@
 // chunk before those buckets and a list of what is in them.  One workgroup a row
 // then finds the last token that is kept, digit by digit of (logit, index) over
 // the list, and the chunk and the token that u falls on.  The list is long only
-// where thousands of logits are nearly equal; such a row is searched as a whole.
+// where thousands of logits are nearly equal; such a row is searched as a whole,
+// eight bits of the places a scan (a flat row of 131072 under top-p 520 us, one of
+// equal logits 1010; 64 of them 590 and 1130).
 // Rows that fit the list are done in one launch.
 //
-// The bound is not memory: one row of 131072 (0.26 MB) takes 3.5 + 6.8 + 7.6 + 10.6
+// The bound is not memory: one row of 131072 (0.26 MB) takes 3.4 + 6.5 + 7.5 + 10.4
 // us in its four launches, each a chain of dependent loads, scans and barriers; 64
-// rows with settings of their own take 10 (1.7 TB/s) + 20 + 22 + 16 us, where the
+// rows with settings of their own take 10 (1.7 TB/s) + 20 + 22 + 17 us, where the
 // rows that filter by top-p or not at all need a 64-bit exp for every token and
 // come to lie on the same compute units.  An exp with half of the 64-bit operations
 // (32 roots of 2 in LDS and 6 terms) and lists gathered in LDS before one atomic were

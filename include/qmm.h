@@ -588,8 +588,12 @@ typedef struct qmm_moe_route {
  * without experts gets 0.  Values of x that are not finite make the token's own
  * y nan.
  * tokens 0 .. 256 (split larger batches, or group the tokens by expert for
- * qmm_gemm); workspace: qmm_moe_workspace_size bytes, 256-byte aligned; calls on
- * one stream may share it.
+ * qmm_gemm).  Where experts have more than a tile of 16 tokens on the average (8 in
+ * the down projection, 5 in f32 layers), a call is slow so far on 4-bit blocks of 64
+ * and less (of any size in f32 layers) and 8-bit ones of 16: 64 tokens, two each of
+ * eight experts in blocks of 32, take five times what four calls of 16 take.
+ * workspace: qmm_moe_workspace_size bytes, 256-byte aligned; calls on one stream may
+ * share it.
  */
 size_t qmm_moe_workspace_size(const qmm_moe_weights *w, int64_t tokens, int top_k);
 
