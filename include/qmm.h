@@ -477,11 +477,10 @@ typedef enum qmm_quant_kind {
     /* FP8 codes [rows, cols] and E8M0 scales [rows, ceil(cols / 32)], as
      * qmm_lowp_matmul reads them with QMM_LOWP_MX: the scale is the exponent field
      * of amax * (1 / max_finite) (of 1 where amax is 0), the codes as in
-     * qmm_lowp_quantize.  A block's largest value then lies at or above the
-     * format's and is clipped, by up to a half of it, as is all that lies within
-     * a factor of two of it: of normally distributed y 10 %, which makes the
-     * codes' error 16 % of y (root mean square).  QMM_QUANT_MX_OCP has 2.9 %
-     * (E4M3) and 5.4 % (E5M2). */
+     * qmm_lowp_quantize.  A block's largest value then lies above the format's (but
+     * where it equals it) and is clipped, by up to a half, as are others that do: of
+     * normally distributed y 10 %, which makes the codes' error 16 % of y (root
+     * mean square).  QMM_QUANT_MX_OCP has 2.9 % (E4M3) and 5.4 % (E5M2). */
     QMM_QUANT_MX = 1,
     /* FP8 codes [rows, cols] with one scale for all, which is given: scales[0],
      * an f32 that is read (codes of y / scale; 0 where the scale is 0). */
